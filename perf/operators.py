@@ -259,7 +259,8 @@ def _prepared(s):
     if c["op"] == "qk_norm_rope":
         return csa.csa_qk_norm_rope(
             q=s["q"], k=s["k"] if c["kv_heads"] else None, q_out=s["q_out"], k_out=s["k_out"] if c["kv_heads"] else None,
-            row_pos=s["pos"], q_gamma=s["q_gamma"], k_gamma=s["k_gamma"], eps=EPS, rope_cos=s["cos"], rope_sin=s["sin"],
+            row_pos=s["pos"], q_gamma=s["q_gamma"],
+            k_gamma=s["k_gamma"] if c["kv_heads"] else None, eps=EPS, rope_cos=s["cos"], rope_sin=s["sin"],
             rope_layout=c["layout"], prepare=True)
     if c["op"] == "kv_append":
         return csa.csa_kv_append(
