@@ -497,6 +497,252 @@ CSA_API csa_status_t csa_sparse_attn_decode(csa_attn_args *args, csa_stream_t st
 CSA_API csa_status_t csa_sparse_attn_prefill(csa_attn_args *args, csa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Paged key/value caches of ordinary attention layers, and the rows that the
+ * calls above read.  No counterpart on the pages: they hand this library
+ * finished RoPE tables ("DeepSeek V4.1 Flash", "Serving-owned full RoPE
+ * tables"), normed queries and window rows published upstream; the four calls
+ * below are that upstream part, and the attention of the layers (or draft
+ * heads) of the same model whose caches hold separate keys and values for
+ * groups of query heads.
+ *
+ * Rotation, as csa_qk_norm_rope and csa_kv_append apply it: the channels
+ * [rope_start, rope_start + rope_dim) of a vector of `head_dim` channels are
+ * turned at the row's position by FP32 tables [rope_cap, rope_dim / 2].
+ * Pair i is (x[2i], x[2i+1]) (CSA_ROPE_ADJACENT, the layout of the calls
+ * above) or (x[i], x[i + rope_dim/2]) (CSA_ROPE_HALF).  rope_cos == NULL: no
+ * rotation.  A negative position is the identity; a position >= rope_cap too,
+ * and raises CSA_DEV_POS_GE_CAP.  rope_start must be a multiple of 8, rope_dim
+ * of 8 (adjacent) or 16 (half), rope_start + rope_dim <= head_dim.  Tables
+ * must be 16-byte aligned.
+ * Norm, ditto: y = x * gamma / sqrt(mean(x^2) + eps) over the head_dim channels
+ * of one head (gamma bf16 [head_dim], NULL: all ones).  Norm and rotation are
+ * computed in FP32 and rounded once, where the result is stored.
+ * Row strides are in bytes, multiples of 16, 0 meaning dense; the heads of a
+ * row are contiguous.
+ * ---------------------------------------------------------------------- */
+
+typedef enum { CSA_ROPE_ADJACENT = 0, CSA_ROPE_HALF = 1 } csa_rope_layout_t;
+typedef enum {
+  CSA_ROPE_NONE = 0,   /* f_i = theta^(-2i/rope_dim) */
+  CSA_ROPE_LINEAR = 1, /* f_i / factor */
+  CSA_ROPE_NTK = 2,    /* theta * factor^(rope_dim/(rope_dim-2)) in the place of theta */
+  CSA_ROPE_YARN = 3    /* f_i * (1 - r_i) + f_i / factor * r_i, see csa_rope_table */
+} csa_rope_scaling_t;
+
+/* ------------------------------------------------------------------------
+ * csa_rope_table - FP32 half-width cos/sin tables, plain or stretched.
+ *
+ * cos[j, i] = attn_factor * cos((pos0 + j) * f_i), sin alike, for j < n_pos and
+ * i < rope_dim / 2, f_i as csa_rope_scaling_t says.  YARN's ramp r_i =
+ * clamp((i - lo) / max(hi - lo, 0.001), 0, 1) runs from the pair that turns
+ * beta_fast times over orig_len positions (and faster ones: r = 0) to the one
+ * that turns beta_slow times (r = 1): lo = max(floor(c(beta_fast)), 0), hi =
+ * min(ceil(c(beta_slow)), rope_dim - 1), c(b) = rope_dim * ln(orig_len / (2 pi
+ * b)) / (2 ln theta).
+ * The angle is reduced exactly (the turns per position as a 64-bit fraction,
+ * multiplied by the position modulo 1), so far positions are as accurate as
+ * near ones: within 2e-7 of the 64-bit value times attn_factor.
+ *
+ * rope_dim even, 2 .. 512 (NTK: at least 4); theta > 1, finite; factor >= 1
+ * (LINEAR, NTK, YARN); orig_len > 0 and beta_fast >= beta_slow > 0 (YARN);
+ * attn_factor > 0; pos0 >= 0; pos0 + n_pos <= 2^31.  cos and sin f32
+ * [n_pos, rope_dim / 2], dense, 4-byte aligned.  n_pos == 0 does nothing.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;
+  int32_t rope_dim;
+  int32_t n_pos;
+  int32_t pos0;
+  int32_t scaling; /* csa_rope_scaling_t */
+  int32_t orig_len;
+  double theta;
+  double factor;
+  double beta_fast;
+  double beta_slow;
+  double attn_factor;
+  float *cos;
+  float *sin;
+} csa_rope_table_args;
+
+CSA_API csa_status_t csa_rope_table(csa_rope_table_args *args, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * csa_qk_norm_rope - the norm of every query and key head and its rotation,
+ * one pass over the rows.
+ *
+ * q bf16 [n_rows, n_q_heads, head_dim] -> q_out, k bf16 [n_rows, n_k_heads,
+ * head_dim] -> k_out (n_k_heads == 0: no keys, k and k_out unused).  q and k
+ * may be row-strided views (of one QKV projection, say).  An output may be its
+ * own input (same pointer and stride: in place); no other overlap.  norm = 0
+ * rotates only.  row_pos i32 [n_rows]; row_req i32 [n_rows] or NULL: a row
+ * with row_req < 0 is padding, neither read nor written.
+ * Supported: head_dim a multiple of 8, 8 .. 512; q, k, q_out, k_out and the
+ * gammas 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;
+  int32_t n_rows;
+  int32_t n_q_heads;
+  int32_t n_k_heads;
+  int32_t head_dim;
+  int32_t norm; /* 1: normalise every head */
+  float eps;
+  int32_t rope_layout; /* csa_rope_layout_t */
+  int32_t rope_start;
+  int32_t rope_dim;
+  int32_t rope_cap;
+  const void *q;
+  const void *k;
+  void *q_out;
+  void *k_out;
+  int64_t q_row_stride;
+  int64_t k_row_stride;
+  int64_t q_out_row_stride;
+  int64_t k_out_row_stride;
+  const void *q_gamma;
+  const void *k_gamma;
+  const int32_t *row_pos;
+  const int32_t *row_req;
+  const float *rope_cos;
+  const float *rope_sin;
+  uint32_t *status_dev;
+} csa_qk_norm_rope_args;
+
+CSA_API csa_status_t csa_qk_norm_rope(csa_qk_norm_rope_args *args, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * csa_kv_append - new keys (normed and rotated on the way) and values into
+ * paged caches.
+ *
+ * Row t of request b = row_req[t] at p = row_pos[t] is written to row p % 128
+ * of page block_table[b, p / 128]: k[t], normed over each head when `norm` and
+ * rotated when rope tables are given, and v[t] as it is (v == NULL: the keys
+ * alone, such as the shared key/value rows [*, 1, 512] that the window of
+ * csa_sparse_attn_* reads).  Rows with row_req < 0 or p < 0 are skipped; a
+ * request >= n_req raises CSA_DEV_BAD_POS, a page outside the table or the pool
+ * CSA_DEV_BAD_BLOCK, and the row is skipped.  Every other row of the pools is
+ * left as it was.  Two rows of one call must not share a slot (what such a slot
+ * holds afterwards is unspecified).
+ *
+ * k, v bf16 [n_rows, n_heads, head_dim], row-strided.  fmt CSA_FMT_BF16:
+ * k_pool, v_pool bf16 [n_blocks, 128, n_heads, head_dim] with page, row and
+ * head strides in bytes (0: dense; multiples of 16; so [n_blocks, n_heads, 128,
+ * head_dim] and pools of several layers or of keys beside values are views).
+ * fmt CSA_FMT_MXFP8: codes uint8 of the same shape and scale bytes uint8
+ * [n_blocks, 128, n_heads, head_dim / 32], dense, head_dim a multiple of 32;
+ * the row as it would be stored in FP32 is quantised as csa_compress publishes
+ * MXFP8.  The slots of different rows must not overlap in memory.
+ * Supported: head_dim a multiple of 8, 8 .. 512; tensors 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;
+  int32_t n_rows;
+  int32_t n_heads;
+  int32_t head_dim;
+  int32_t fmt; /* csa_cache_fmt_t: CSA_FMT_BF16 or CSA_FMT_MXFP8 */
+  int32_t norm;
+  float eps;
+  int32_t rope_layout;
+  int32_t rope_start;
+  int32_t rope_dim;
+  int32_t rope_cap;
+  int32_t n_req;
+  int32_t max_blocks;
+  int32_t n_blocks;
+  const void *k;
+  const void *v;
+  int64_t k_row_stride;
+  int64_t v_row_stride;
+  const void *k_gamma;
+  const int32_t *row_req;
+  const int32_t *row_pos;
+  const float *rope_cos;
+  const float *rope_sin;
+  const int32_t *block_table;
+  void *k_pool;
+  void *v_pool;
+  uint8_t *k_scale_pool;
+  uint8_t *v_scale_pool;
+  int64_t k_page_stride; /* bytes; 0: dense (BF16 pools only, as the next five) */
+  int64_t k_token_stride;
+  int64_t k_head_stride;
+  int64_t v_page_stride;
+  int64_t v_token_stride;
+  int64_t v_head_stride;
+  uint32_t *status_dev;
+} csa_kv_append_args;
+
+CSA_API csa_status_t csa_kv_append(csa_kv_append_args *args, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * csa_paged_attn - attention of a chunk of new tokens, or of single tokens,
+ * over a paged cache of separate keys and values.
+ *
+ * Row t of request b at p sees position j of the request iff 0 <= j <
+ * min(kv_len[b], 128 max_blocks), j <= p when `causal`, and j > p - window when window > 0.  Head
+ * h reads key/value head h / (n_heads / n_kv_heads).  With the visible j:
+ *   l_j = softmax_scale * q[t,h] . k_j
+ *   out[t,h] = sum_j e^{l_j} v_j / (sum_j e^{l_j} + e^{sink_h})
+ *   lse[t,h] = log(sum_j e^{l_j} + e^{sink_h})
+ * sink == NULL means -inf.  A row that sees nothing gets out = 0 and lse =
+ * sink_h.  Keys, values and rows that a row does not see have no effect on it,
+ * whatever they hold (infinities and NaN included).  q is used as it is
+ * (csa_qk_norm_rope rotates it).  Rows may come in any order; rows of one
+ * request that follow one another in ascending position share their reads.
+ * A page outside the pool raises CSA_DEV_BAD_BLOCK and its positions are not
+ * seen; a request >= n_req raises CSA_DEV_BAD_POS and the row is skipped.
+ *
+ * q bf16 [n_rows, n_heads, head_dim], row-strided; k_pool, v_pool bf16
+ * [n_blocks, 128, n_kv_heads, head_dim] with strides as in csa_kv_append; out
+ * bf16 [n_rows, n_heads, head_dim] dense; lse f32 [n_rows, n_heads] or NULL;
+ * block_table i32 [n_req, max_blocks]; kv_len i32 [n_req].  Supported:
+ * head_dim 64 or 128; n_kv_heads a divisor of n_heads, n_heads / n_kv_heads <=
+ * 128.  softmax_scale > 0, finite.  Tensors 16-byte aligned.
+ * `mode` (csa_mode_t) chooses between the kernel for few rows per request
+ * (CSA_MODE_DECODE) and the one for chunks (CSA_MODE_PREFILL); CSA_MODE_AUTO
+ * goes by the sizes.  Both compute the same function; they round differently.
+ * The workspace (size query) holds partial results of split rows; nothing in
+ * it has to be set or kept between calls.  256-byte aligned.  Calls that may
+ * run at the same time need workspaces of their own.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;
+  int32_t n_rows;
+  int32_t n_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t causal; /* 0: every cached position; 1: positions <= the row's */
+  int32_t window; /* 0: none */
+  int32_t mode;   /* csa_mode_t */
+  float softmax_scale;
+  int32_t n_req;
+  int32_t max_blocks;
+  int32_t n_blocks;
+  const void *q;
+  int64_t q_row_stride;
+  const int32_t *row_req;
+  const int32_t *row_pos;
+  const int32_t *kv_len;
+  const int32_t *block_table;
+  const void *k_pool;
+  const void *v_pool;
+  int64_t k_page_stride;
+  int64_t k_token_stride;
+  int64_t k_head_stride;
+  int64_t v_page_stride;
+  int64_t v_token_stride;
+  int64_t v_head_stride;
+  const float *sink;
+  void *out;
+  float *lse;
+  uint32_t *status_dev;
+  void *workspace;
+  size_t workspace_bytes;
+} csa_paged_attn_args;
+
+CSA_API csa_status_t csa_paged_attn(csa_paged_attn_args *args, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Library information and measurement hooks (no counterpart on the pages).
  * ---------------------------------------------------------------------- */
 
@@ -517,7 +763,12 @@ typedef enum {
   CSA_K_ATTN_DECODE = 5,
   CSA_K_ATTN_PREFILL = 6,
   CSA_K_DEQUANT = 7,        /* low-bit pools into the prefill call's BF16 arena */
-  CSA_K_COUNT = 8
+  CSA_K_ROPE_TABLE = 8,
+  CSA_K_NORM_ROPE = 9,      /* csa_qk_norm_rope */
+  CSA_K_KV_APPEND = 10,
+  CSA_K_PAGED_ATTN = 11,    /* csa_paged_attn: the attention itself */
+  CSA_K_PAGED_MERGE = 12,   /* csa_paged_attn: joining the parts of split rows */
+  CSA_K_COUNT = 13
 } csa_kernel_id_t;
 
 /* Time every launch of kernel `kernel_id` (up to `max_launches` launches)

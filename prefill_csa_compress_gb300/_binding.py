@@ -26,6 +26,7 @@ CSA_MODE_AUTO, CSA_MODE_DECODE, CSA_MODE_PREFILL = 0, 1, 2
 KERNEL_IDS = {
     "compress_gate": 0, "compress_pool": 1, "compress_fused": 2, "index_score": 3,
     "index_topk": 4, "attn_decode": 5, "attn_prefill": 6, "dequant": 7,
+    "rope_table": 8, "norm_rope": 9, "kv_append": 10, "paged_attn": 11, "paged_merge": 12,
 }
 
 

@@ -137,6 +137,15 @@ void attn_decode_geometry(const csa_attn_args &a, int *n_splits, int *tiles_per_
 size_t attn_decode_workspace(const csa_attn_args &a);
 cudaError_t launch_attn_decode(const csa_attn_args &a, cudaStream_t s);
 
+// RoPE tables (k_rope_table.cu); head norms with rotation and publication
+// into paged key/value caches (k_norm_rope.cu).
+cudaError_t launch_rope_table(const csa_rope_table_args &a, cudaStream_t s);
+cudaError_t launch_qk_norm_rope(const csa_qk_norm_rope_args &a, cudaStream_t s);
+cudaError_t launch_kv_append(const csa_kv_append_args &a, cudaStream_t s);
+// Attention over a paged key/value cache (k_paged_attn.cu).
+size_t paged_attn_workspace(const csa_paged_attn_args &a);
+cudaError_t launch_paged_attn(const csa_paged_attn_args &a, cudaStream_t s);
+
 // ---------------------------------------------------------------- device side
 
 __device__ __forceinline__ void flag(uint32_t *status, uint32_t bit) {
