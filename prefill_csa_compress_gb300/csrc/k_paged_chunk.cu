@@ -1,0 +1,676 @@
+// Attention of a chunk of rows over a paged key/value cache (csa_paged_attn):
+// tcgen05 tiles of 128 (row, head) pairs against one page of 128 keys.
+//
+// With the query heads of a group stacked under their row, a tile of R rows x G
+// heads (R G <= 128) reads one key/value head:
+//   S[m, c] = q_m . k_c      (128 x 128 x D, both operands K-major)
+//   O[m, :] += P[m, c] v_c   (128 x D x 128, P from tensor memory, V MN-major)
+// with P = 2^(S scale log2(e) - ref_m).  A page is exactly one key tile, so a
+// page costs one block-table look-up and D / 64 TMA boxes for K and V each.
+//
+// A CTA owns two tiles of consecutive rows, so that one tile's products run
+// while the other's softmax does, and both read each page once.  Roles:
+//   warp 0      walks the requests of the CTA's rows and their pages, loads Q, K
+//               and V by TMA (a ring of stages), and describes each page to the rest;
+//   warp 1      issues the MMAs;
+//   warp 2      looks through V on pages that some row does not see whole: rows
+//               that no one sees are zeroed, values that are not finite are
+//               zeroed and reported, since a zero probability times them is not zero;
+//   warps 4..11 softmax, one thread a (row, head) pair: the thread holds its
+//               128 logits, so row maxima and sums need no exchange.  Its
+//               reference only moves (and O is rescaled in tensor memory) when
+//               a logit exceeds it by more than 2^8.
+// Tensor memory: S0, S1 (128 columns each; P over S in BF16), O0, O1 (D each).
+// Rows of several requests in one CTA take turns: a page of another request is
+// masked for the whole row.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
+#include "attn_common.cuh"
+#include "csa_internal.cuh"
+#include "paged_common.cuh"
+#include "tc.cuh"
+
+namespace csa {
+namespace {
+
+using paged::Parts;
+
+constexpr int PC_THREADS = 384;
+constexpr int PC_LOAD = 0, PC_MMA = 1, PC_CLEAN = 2, PC_SOFT0 = 4;
+constexpr int PC_META = 8;  // pages described ahead (the ring holds at most 4 of them)
+constexpr float kMove = 8.f;
+
+template <int D>
+struct Cfg {
+  static constexpr int CHUNKS = D / 64;                // 128-byte column groups of a row
+  static constexpr int TILE = CHUNKS * 16384;          // bytes of a 128-row tile
+  static constexpr int STAGES = D == 128 ? 5 : 8;      // K and V tiles in flight
+  static constexpr int OFF_KV = 2 * TILE;
+  static constexpr int OFF_MISC = OFF_KV + STAGES * TILE;
+  static constexpr int O_COL = 256;
+};
+
+// One page as the consumers need it.
+struct Page {
+  int base;        // position of its first key
+  int req;         // request it belongs to
+  int r0, r1;      // the CTA's rows that read it (a request may have several runs)
+  int mixed;       // some row of the CTA does not see all of it
+  int lo, hi;      // columns [lo, hi) that at least one row sees
+  uint32_t bad[4]; // columns whose values are not finite (mixed pages only)
+};
+
+struct Misc {
+  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full, v_clean[4], drained;
+  uint32_t tmem;
+  int abort;
+  int n_it;        // pages this CTA works through
+  int first_page;  // skipped before them (another part's)
+  int many;        // rows of several requests
+  Page page[PC_META];
+};
+static_assert(Cfg<128>::OFF_MISC + sizeof(Misc) + 1024 <= 227 * 1024, "shared memory");
+
+// Bounded wait that also gives up when another role has.
+__device__ __forceinline__ bool pc_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                        uint32_t *status) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = tc::global_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*abort) return false;
+      if (tc::global_ns() - t0 > 2000000000ull) {
+        *abort = 1;
+        flag(status, CSA_DEV_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool pc_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                             uint32_t *status) {
+  return __all_sync(0xffffffffu, pc_wait(bar, parity, abort, status));
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w,
+                                            uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w),
+      "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+// Consecutive rows of one request among the CTA's rows [0, n): what they see.
+struct Run {
+  int req, end;
+  int lo, hi;          // positions [lo, hi) that at least one of them sees
+  int all_lo, all_hi;  // positions that every one of them sees
+};
+
+// The run that starts at row r0 (whole warp; req < 0: padding).
+__device__ __forceinline__ Run next_run(const csa_paged_attn_args &a, int t0, int r0, int n) {
+  const int lane = threadIdx.x & 31;
+  Run R;
+  R.req = a.row_req[t0 + r0];
+  R.lo = R.all_hi = 0x7FFFFFFF;
+  R.hi = R.all_lo = 0;
+  R.end = n;
+  const bool ok = R.req >= 0 && R.req < a.n_req;
+  for (int base = r0; base < n; base += 32) {
+    const int r = base + lane;
+    const bool same = r < n && a.row_req[t0 + r] == R.req;
+    const uint32_t other = __ballot_sync(0xffffffffu, !same);
+    const int stop = other ? __ffs(other) - 1 : 32;
+    if (ok && lane < stop) {
+      int lo, hi;
+      paged::visible_range(a, R.req, a.row_pos[t0 + r], lo, hi);
+      if (lo < hi) {
+        R.lo = min(R.lo, lo);
+        R.hi = max(R.hi, hi);
+        R.all_lo = max(R.all_lo, lo);
+        R.all_hi = min(R.all_hi, hi);
+      } else {
+        R.all_lo = 0x7FFFFFFF;  // a row that sees nothing
+      }
+    }
+    if (other) {
+      R.end = min(n, base + stop);
+      break;
+    }
+  }
+  R.lo = __reduce_min_sync(0xffffffffu, R.lo);
+  R.hi = __reduce_max_sync(0xffffffffu, R.hi);
+  R.all_lo = __reduce_max_sync(0xffffffffu, R.all_lo);
+  R.all_hi = __reduce_min_sync(0xffffffffu, R.all_hi);
+  return R;
+}
+
+__device__ __forceinline__ int run_pages(const Run &R) {
+  return R.lo < R.hi ? (R.hi - 1) / kBlock - R.lo / kBlock + 1 : 0;
+}
+
+// Bit 15 or 31 of the result: that half of the BF16 pair is not finite.
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
+  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+
+struct ChunkGrid {
+  int n_tiles;    // row tiles (of 2 R rows)
+  int rows_tile;  // R
+  int n_parts;    // parts of a tile's pages
+};
+
+template <int D>
+__global__ void __launch_bounds__(PC_THREADS, 1)
+    paged_chunk_kernel(csa_paged_attn_args a, Parts parts, ChunkGrid G,
+                       const __grid_constant__ CUtensorMap qmap,
+                       const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                            ~uintptr_t(1023));
+  Misc *M = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int *abort = &M->abort;
+
+  // the CTA's item: key/value head fastest, parts next, the last rows (which
+  // see the most) first
+  const int kvh = blockIdx.x % a.n_kv_heads;
+  const int part = blockIdx.x / a.n_kv_heads % G.n_parts;
+  const int tile = G.n_tiles - 1 - blockIdx.x / a.n_kv_heads / G.n_parts;
+  const int g = a.n_heads / a.n_kv_heads;
+  const int t0 = tile * 2 * G.rows_tile;
+  const int n_rows = min(2 * G.rows_tile, a.n_rows - t0);
+  const int n_sub = n_rows > G.rows_tile ? 2 : 1;  // tiles with rows
+
+  if (warp == PC_LOAD) {
+    // how many pages there are, and this part's share of them
+    int total = 0, valid = 0;
+    for (int r = 0; r < n_rows;) {
+      const Run R = next_run(a, t0, r, n_rows);
+      if (R.req >= a.n_req && lane == 0) flag(a.status_dev, CSA_DEV_BAD_POS);
+      if (R.req >= 0 && R.req < a.n_req) {
+        total += run_pages(R);
+        ++valid;
+      }
+      r = R.end;
+    }
+    const int u0 = (int)((long long)total * part / G.n_parts);
+    const int u1 = (int)((long long)total * (part + 1) / G.n_parts);
+    if (lane == 0) {
+      M->first_page = u0;
+      M->n_it = u1 - u0;
+      M->many = valid > 1;
+    }
+  } else if (warp == PC_MMA) {
+    tc::tmem_alloc(&M->tmem, 512);
+  } else if (tid == PC_CLEAN * 32) {
+    tc::mbar_init(&M->q_full, 1);
+    for (int i = 0; i < C::STAGES; ++i) {
+      tc::mbar_init(&M->kv_full[i], 1);
+      tc::mbar_init(&M->kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&M->s_full[i], 2);
+      tc::mbar_init(&M->p_full[i], 128);
+    }
+    tc::mbar_init(&M->o_full, 1);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&M->v_clean[i], 1);
+    tc::mbar_init(&M->drained, 1);
+    M->abort = 0;
+    tc::mbar_fence_init();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = M->tmem;
+  const int n_it = M->n_it;
+
+  if (warp == PC_LOAD && n_it > 0) {
+    // ================================================================ loads
+    uint32_t it = 0;  // tiles loaded
+    bool ok = true;
+    if (lane == 0) {
+      const uint32_t box = (uint32_t)(G.rows_tile * g * 128);
+      tc::mbar_arrive_expect_tx(&M->q_full, n_sub * C::CHUNKS * box);
+      for (int s = 0; s < n_sub; ++s)
+        for (int c = 0; c < C::CHUNKS; ++c)
+          tc::tma_load_3d(sm + s * C::TILE + c * 16384, &qmap, c * 64, kvh * g,
+                          t0 + s * G.rows_tile, &M->q_full);
+    }
+    const bool many = M->many != 0;
+    int skip = M->first_page, left = n_it;
+    for (int r = 0; r < n_rows && left > 0 && ok;) {
+      const int r0 = r;
+      const Run R = next_run(a, t0, r, n_rows);
+      r = R.end;
+      if (R.req < 0 || R.req >= a.n_req) continue;
+      const int np = run_pages(R);
+      if (skip >= np) {
+        skip -= np;
+        continue;
+      }
+      const int pg0 = R.lo / kBlock + skip, n = min(np - skip, left);
+      skip = 0;
+      left -= n;
+      int entry = 0;
+      for (int i = 0; i < n && ok; ++i) {
+        if ((i & 31) == 0)
+          entry = i + lane < n
+                      ? a.block_table[(long long)R.req * a.max_blocks + pg0 + i + lane]
+                      : 0;
+        const int phys = __shfl_sync(0xffffffffu, entry, i & 31);
+        const bool there = phys >= 0 && phys < a.n_blocks;
+        const int base = (pg0 + i) * kBlock;
+        // K, then V
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int st = it % C::STAGES;
+          ok = ok && pc_wait_warp(&M->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, abort, a.status_dev);
+          if (!ok) break;
+          if (lane == 0) {
+            if (kv == 0) {
+              Page &P = M->page[(it >> 1) % PC_META];
+              P.base = base;
+              P.req = R.req;
+              P.r0 = r0;
+              P.r1 = there ? R.end : r0;  // an unmapped page is seen by no row
+              P.mixed = many || !there || base < R.all_lo || base + kBlock > R.all_hi;
+              P.lo = there ? max(R.lo - base, 0) : 0;
+              P.hi = there ? min(R.hi - base, kBlock) : 0;
+              if (!there) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
+            }
+            uint8_t *dst = sm + C::OFF_KV + st * C::TILE;
+            if (there) {
+              tc::mbar_arrive_expect_tx(&M->kv_full[st], C::TILE);
+              for (int c = 0; c < C::CHUNKS; ++c)
+                tma_load_4d(dst + c * 16384, kv ? &vmap : &kmap, c * 64, kvh, 0, phys,
+                            &M->kv_full[st]);
+            } else {
+              tc::mbar_arrive(&M->kv_full[st]);
+            }
+          }
+          __syncwarp();
+          ++it;
+        }
+      }
+    }
+    // whatever was asked for has landed before the CTA retires
+    if (*abort) {
+      tc::mbar_wait(&M->q_full, 0, 50000000ull);
+      for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
+        tc::mbar_wait(&M->kv_full[k % C::STAGES], (k / C::STAGES) & 1, 50000000ull);
+    }
+  } else if (warp == PC_MMA && n_it > 0) {
+    // ================================================================ MMA
+    constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128);
+    constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
+    const uint32_t qs = tc::smem_u32(sm), kvs = qs + C::OFF_KV;
+    auto issue_s = [&](int s, uint32_t ks) {
+#pragma unroll
+      for (int c = 0; c < C::CHUNKS; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc::mma_ss_elect(tmem + s * 128, tc::desc_sw128(qs + s * C::TILE + c * 16384 + k * 32),
+                           tc::desc_sw128(ks + c * 16384 + k * 32), idesc_s, (c | k) != 0);
+      tc::mma_commit_elect(&M->s_full[s]);
+      if (lane == 0) tc::mbar_arrive(&M->s_full[s]);  // hands on the page's description
+      __syncwarp();
+    };
+    bool ok = pc_wait_warp(&M->q_full, 0, abort, a.status_dev) &&
+              pc_wait_warp(&M->kv_full[0], 0, abort, a.status_dev);
+    if (ok) {
+      tc::tc_fence_after();
+      for (int s = 0; s < n_sub; ++s) issue_s(s, kvs);
+      tc::mma_commit_elect(&M->kv_empty[0]);
+    }
+    for (int j = 0; j < n_it && ok; ++j) {
+      const uint32_t iv = 2 * j + 1, ik = 2 * j + 2;
+      const int sv = iv % C::STAGES, sk = ik % C::STAGES;
+      const bool more = j + 1 < n_it;
+      ok = pc_wait_warp(&M->kv_full[sv], (iv / C::STAGES) & 1, abort, a.status_dev) &&
+           pc_wait_warp(&M->v_clean[j & 3], (j >> 2) & 1, abort, a.status_dev);
+      if (ok && more) ok = pc_wait_warp(&M->kv_full[sk], (ik / C::STAGES) & 1, abort, a.status_dev);
+      for (int s = 0; s < n_sub && ok; ++s) {
+        ok = pc_wait_warp(&M->p_full[s], j & 1, abort, a.status_dev);
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc::mma_f16_ta_elect(tmem + C::O_COL + s * D, tmem + s * 128 + k * 8,
+                               tc::desc_sw128_mn(kvs + sv * C::TILE + k * 2048, 16384, 1024), idesc_o,
+                               1u);
+        if (more) issue_s(s, kvs + sk * C::TILE);
+      }
+      if (!ok) break;
+      tc::mma_commit_elect(&M->kv_empty[sv]);
+      if (more) tc::mma_commit_elect(&M->kv_empty[sk]);
+    }
+    if (ok) tc::mma_commit_elect(&M->o_full);
+    // every issued MMA has completed before tensor memory is released
+    tc::mma_commit_elect(&M->drained);
+    tc::mbar_wait(&M->drained, 0, 100000000ull);
+  } else if (warp == PC_CLEAN && n_it > 0) {
+    // ================================================================ V on mixed pages
+    bool ok = true;
+    for (int j = 0; j < n_it && ok; ++j) {
+      const uint32_t iv = 2 * j + 1;
+      const int sv = iv % C::STAGES;
+      ok = pc_wait_warp(&M->kv_full[sv], (iv / C::STAGES) & 1, abort, a.status_dev);
+      if (!ok) break;
+      Page &P = M->page[j % PC_META];
+      if (P.mixed) {
+        uint8_t *v = sm + C::OFF_KV + sv * C::TILE;
+        bool wrote = false;
+        for (int k = 0; k < 4; ++k) {
+          const int row = k * 32 + lane;
+          uint4 *p = reinterpret_cast<uint4 *>(v + row * 128);
+          uint32_t bad = 0;
+          for (int c = 0; c < C::CHUNKS; ++c)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const uint4 w = p[c * 1024 + ((q + lane) & 7)];
+              bad |= not_finite2(w.x) | not_finite2(w.y) | not_finite2(w.z) | not_finite2(w.w);
+            }
+          const bool seen = row >= P.lo && row < P.hi;
+          if (bad) {
+            for (int c = 0; c < C::CHUNKS; ++c)
+              for (int q = 0; q < 8; ++q) p[c * 1024 + q] = make_uint4(0, 0, 0, 0);
+            wrote = true;
+          }
+          const uint32_t word = __ballot_sync(0xffffffffu, bad != 0 && seen);
+          if (lane == 0) P.bad[k] = word;
+        }
+        if (wrote) tc::fence_async_shared();
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&M->v_clean[j & 3]);
+    }
+  } else if (warp >= PC_SOFT0) {
+    // ================================================================ softmax
+    const int s = (warp - PC_SOFT0) >> 2;
+    const int m = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + s * 128 + lane_off, to = tmem + C::O_COL + s * D + lane_off;
+    const float sl2 = a.softmax_scale * paged::kLog2e;
+    const int rr = s * G.rows_tile + m / g, t = t0 + rr, h = kvh * g + m % g;
+    int req = -1, lo = 0, hi = 0;
+    if (m < G.rows_tile * g && rr < n_rows) {
+      req = a.row_req[t];
+      if (req >= a.n_req) req = -1;
+      if (req >= 0) paged::visible_range(a, req, a.row_pos[t], lo, hi);
+    }
+    float ref = -INFINITY, l = 0.f;
+    bool ok = true;
+    if (s < n_sub && n_it > 0) {
+      {
+        uint32_t z[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = 0;
+        for (int c = 0; c < D; c += 32) tc::tmem_st32u(to + c, z);
+        tc::tmem_wait_st();
+      }
+      for (int j = 0; j < n_it; ++j) {
+        ok = pc_wait_warp(&M->s_full[s], j & 1, abort, a.status_dev);
+        if (!ok) break;
+        tc::tc_fence_after();
+        Page &P = M->page[j % PC_META];
+        float x[128];
+        tc::tmem_ld64(ts, reinterpret_cast<float(&)[64]>(x[0]));
+        tc::tmem_ld64(ts + 64, reinterpret_cast<float(&)[64]>(x[64]));
+        int c_lo = 0, c_hi = 128;
+        const bool mixed = P.mixed != 0;
+        if (mixed) {
+          c_lo = max(lo - P.base, 0);
+          c_hi = rr >= P.r0 && rr < P.r1 ? min(hi - P.base, kBlock) : 0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i < c_lo || i >= c_hi) x[i] = -INFINITY;
+        }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        const bool move = top > ref + kMove || (ref == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xffffffffu, move)) {
+          const float f = move && ref > -INFINITY ? exp2f(ref - top) : 1.f;
+          if (__any_sync(0xffffffffu, f != 1.f)) {
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tc::tmem_ld32(to + c, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f;
+              tc::tmem_st32(to + c, o);
+            }
+          }
+          l *= f;
+          if (move) ref = top;
+        }
+        const float r0 = ref == -INFINITY ? 0.f : ref;
+        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+        for (int i = 0; i < 128; i += 2) {
+          const float2 y = tc::ffma2(make_float2(x[i], x[i + 1]), make_float2(sl2, sl2),
+                                     make_float2(-r0, -r0));
+          x[i] = attn::exp2_sfu(y.x);
+          x[i + 1] = attn::exp2_sfu(y.y);
+          float2 &u = sum[(i >> 1) & 1];
+          u = tc::ffma2(make_float2(x[i], x[i + 1]), make_float2(1.f, 1.f), u);
+        }
+        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+        if (mixed) {
+          // values that are not finite: their columns leave the product, and
+          // the rows that see them add them here
+          ok = pc_wait_warp(&M->v_clean[j & 3], (j >> 2) & 1, abort, a.status_dev);
+          if (!ok) break;
+          const uint32_t bad[4] = {P.bad[0], P.bad[1], P.bad[2], P.bad[3]};
+          if (bad[0] | bad[1] | bad[2] | bad[3]) {
+            const int phys = a.block_table[(long long)P.req * a.max_blocks + P.base / kBlock];
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w)
+#pragma unroll 1
+              for (uint32_t b = bad[w]; b; b &= b - 1) {
+                const int c = 32 * w + __ffs(b) - 1;
+                const bool sees = c >= c_lo && c < c_hi;
+                uint32_t raw;
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+                             : "=r"(raw)
+                             : "r"(ts + c));
+                asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(raw)::"memory");
+                const float p = exp2f(__uint_as_float(raw) * sl2 - r0);
+                const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(
+                    static_cast<const uint8_t *>(a.v_pool) + phys * a.v_page_stride +
+                    c * a.v_token_stride + kvh * a.v_head_stride);
+                for (int d = 0; d < D; d += 32) {
+                  float o[32];
+                  tc::tmem_ld32(to + d, o);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (sees) o[i] += p * __bfloat162float(v[d + i]);
+                  tc::tmem_st32(to + d, o);
+                }
+              }
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (bad[i >> 5] >> (i & 31) & 1u) x[i] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = attn::pack2(x[64 * c + 2 * i], x[64 * c + 2 * i + 1]);
+          tc::tmem_st32u(ts + 32 * c, w);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        tc::mbar_arrive(&M->p_full[s]);
+      }
+      if (ok) ok = pc_wait_warp(&M->o_full, 0, abort, a.status_dev);
+      tc::tc_fence_after();
+    }
+    // ---- the row's result, or its part
+    const long long row = (long long)t * a.n_heads + h;
+    const bool mine = req >= 0 && ok;
+    float scale = 0.f;
+    if (G.n_parts > 1) {
+      if (mine) parts.ml[(long long)part * a.n_rows * a.n_heads + row] = make_float2(ref, l);
+      scale = 1.f;
+    } else {
+      const float s2 = mine && a.sink ? a.sink[h] * paged::kLog2e : -INFINITY;
+      const paged::Joined J = paged::finish(ref, l, s2);
+      scale = J.inv;
+      if (mine && a.lse) a.lse[row] = J.lse;
+    }
+    const bool zero = ref == -INFINITY && l == 0.f;  // nothing seen: O may hold nothing
+    if (s < n_sub && ok) {
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (n_it > 0)
+          tc::tmem_ld32(to + c, o);
+        else
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        if (!mine) continue;
+        if (G.n_parts > 1) {
+          if (zero) continue;
+          float4 *dst = reinterpret_cast<float4 *>(
+              parts.o + ((long long)part * a.n_rows * a.n_heads + row) * D + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              w[q] = zero ? 0u
+                          : attn::pack2(o[8 * i + 2 * q] * scale, o[8 * i + 2 * q + 1] * scale);
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == PC_MMA) tc::tmem_dealloc(tmem, 512);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    cudaDriverEntryPointQueryResult q;
+    void *fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  return encode;
+}
+
+// BF16 tensor map of up to 4 dimensions, 128-byte swizzle; strides (bytes) of
+// dimensions 1...
+bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  memset(map, 0, sizeof(*map));
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims,
+                  strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+                   CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const csa_paged_attn_args &a, const Parts &parts, cudaStream_t s) {
+  using C = Cfg<D>;
+  const int g = a.n_heads / a.n_kv_heads;
+  ChunkGrid G;
+  G.rows_tile = 128 / g;
+  G.n_tiles = (a.n_rows + 2 * G.rows_tile - 1) / (2 * G.rows_tile);
+  G.n_parts = parts.n;
+  CUtensorMap qmap, kmap, vmap;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.n_heads, (cuuint64_t)a.n_rows};
+    const cuuint64_t st[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_row_stride};
+    const cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)G.rows_tile};
+    if (!encode(&qmap, a.q, 3, dims, st, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.n_kv_heads, (cuuint64_t)kBlock,
+                                (cuuint64_t)a.n_blocks};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)kBlock, 1};
+    const cuuint64_t ks[3] = {(cuuint64_t)a.k_head_stride, (cuuint64_t)a.k_token_stride,
+                              (cuuint64_t)a.k_page_stride};
+    const cuuint64_t vs[3] = {(cuuint64_t)a.v_head_stride, (cuuint64_t)a.v_token_stride,
+                              (cuuint64_t)a.v_page_stride};
+    if (!encode(&kmap, a.k_pool, 4, dims, ks, box) || !encode(&vmap, a.v_pool, 4, dims, vs, box))
+      return cudaErrorInvalidValue;
+  }
+  const size_t smem = C::OFF_MISC + sizeof(Misc) + 1024;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static bool attr[64] = {};
+  if (dev < 0 || dev >= 64 || !attr[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        paged_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr[dev] = true;
+  }
+  const long long grid = (long long)G.n_tiles * a.n_kv_heads * G.n_parts;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  launch_begin(CSA_K_PAGED_ATTN, s);
+  const cudaError_t e = launch_kernel(paged_chunk_kernel<D>, dim3((unsigned)grid), dim3(PC_THREADS),
+                                      smem, s, 0, false, a, parts, G, qmap, kmap, vmap);
+  launch_end(CSA_K_PAGED_ATTN, s);
+  return e;
+}
+
+}  // namespace
+
+// Parts that a tile's pages are split into: as many as shorten the longest of
+// the waves of CTAs (each page one unit, a CTA's fixed cost about four).
+int paged_chunk_parts(const csa_paged_attn_args &a, int sms) {
+  const int rows = 2 * (128 / (a.n_heads / a.n_kv_heads));
+  const long long items = (long long)((a.n_rows + rows - 1) / rows) * a.n_kv_heads;
+  long long pages = a.max_blocks;
+  if (a.window > 0) {
+    const long long seen = ((long long)a.window + rows + kBlock - 1) / kBlock + 1;
+    pages = pages < seen ? pages : seen;
+  }
+  int best = 1;
+  double cost = 1e30;
+  for (int p = 1; p <= 64 && p <= pages; ++p) {
+    const long long waves = (items * p + sms - 1) / sms;
+    const double c = (double)waves * ((double)((pages + p - 1) / p) + 4.0) + (p > 1 ? 2.0 : 0.0);
+    if (c < cost * 0.97) {
+      cost = c;
+      best = p;
+    }
+    if (waves > 8) break;
+  }
+  return best;
+}
+
+cudaError_t launch_paged_chunk(const csa_paged_attn_args &a, const Parts &parts, int /*sms*/,
+                               cudaStream_t s) {
+  return a.head_dim == 64 ? launch<64>(a, parts, s) : launch<128>(a, parts, s);
+}
+
+}  // namespace csa
