@@ -1,4 +1,9 @@
 // csa_paged_attn: which kernel, how many parts, and the join of the parts.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
 #include "csa_internal.cuh"
 #include "paged_common.cuh"
 #include "tc.cuh"
@@ -56,13 +61,55 @@ int sm_count() {
   return sms;
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    cudaDriverEntryPointQueryResult q;
+    void *fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  return encode;
+}
+
+// BF16 tensor map of up to 4 dimensions, 128-byte swizzle; strides (bytes) of
+// dimensions 1...
+bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  memset(map, 0, sizeof(*map));
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims,
+                  strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+                   CUDA_SUCCESS;
+}
+
+// Few rows per request: the decode kernel.  (Rows per request as the caller's
+// block table has requests; results do not depend on the choice but for
+// rounding.)
+bool use_decode(const csa_paged_attn_args &a) {
+  if (a.mode == CSA_MODE_PREFILL || a.n_rows > paged::kDecodeRows) return false;
+  if (a.mode == CSA_MODE_DECODE) return true;
+  const int g = a.n_heads / a.n_kv_heads, per = (a.n_rows + a.n_req - 1) / a.n_req;
+  return g * per <= 16;
+}
+
 struct Layout {
+  bool decode;
   int parts;
   size_t ml, total;  // parts' statistics after their outputs
 };
 
 Layout layout(const csa_paged_attn_args &a, int sms) {
-  Layout L{paged_chunk_parts(a, sms), 0, 0};
+  Layout L{use_decode(a), 1, 0, 0};
+  if (L.decode) {
+    L.total = paged_decode_workspace(a, sms);
+    return L;
+  }
+  L.parts = paged_chunk_parts(a, sms);
   if (L.parts > 1) {
     const size_t rows = (size_t)a.n_rows * a.n_heads * L.parts;
     L.ml = align_up(rows * a.head_dim * sizeof(float), 256);
@@ -73,11 +120,37 @@ Layout layout(const csa_paged_attn_args &a, int sms) {
 
 }  // namespace
 
+namespace paged {
+
+bool encode_pools(const csa_paged_attn_args &a, CUtensorMap *k, CUtensorMap *v) {
+  const cuuint64_t dims[4] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_kv_heads, (cuuint64_t)kBlock,
+                              (cuuint64_t)a.n_blocks};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)kBlock, 1};
+  const cuuint64_t ks[3] = {(cuuint64_t)a.k_head_stride, (cuuint64_t)a.k_token_stride,
+                            (cuuint64_t)a.k_page_stride};
+  const cuuint64_t vs[3] = {(cuuint64_t)a.v_head_stride, (cuuint64_t)a.v_token_stride,
+                            (cuuint64_t)a.v_page_stride};
+  return encode(k, a.k_pool, 4, dims, ks, box) && encode(v, a.v_pool, 4, dims, vs, box);
+}
+
+bool encode_q(const csa_paged_attn_args &a, int rows, CUtensorMap *q) {
+  const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_heads, (cuuint64_t)a.n_rows};
+  const cuuint64_t st[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)a.q_row_stride};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(a.n_heads / a.n_kv_heads), (cuuint32_t)rows};
+  return encode(q, a.q, 3, dims, st, box);
+}
+
+}  // namespace paged
+
 size_t paged_attn_workspace(const csa_paged_attn_args &a) { return layout(a, sm_count()).total; }
 
 cudaError_t launch_paged_attn(const csa_paged_attn_args &a, cudaStream_t s) {
   const int sms = sm_count();
   const Layout L = layout(a, sms);
+  if (L.decode) {
+    const cudaError_t e = launch_paged_decode(a, sms, s);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   const Parts parts{reinterpret_cast<float *>(ws), reinterpret_cast<float2 *>(ws + L.ml), L.parts};
   cudaError_t e = launch_paged_chunk(a, parts, sms, s);

@@ -24,9 +24,6 @@
 // Rows of several requests in one CTA take turns: a page of another request is
 // masked for the whole row.
 #include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <cstring>
 
 #include "attn_common.cuh"
 #include "csa_internal.cuh"
@@ -96,16 +93,6 @@ __device__ __forceinline__ bool pc_wait_warp(uint64_t *bar, uint32_t parity, vol
   return __all_sync(0xffffffffu, pc_wait(bar, parity, abort, status));
 }
 
-__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w,
-                                            uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(tc::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w),
-      "r"(tc::smem_u32(bar))
-      : "memory");
-}
-
 // Consecutive rows of one request among the CTA's rows [0, n): what they see.
 struct Run {
   int req, end;
@@ -153,11 +140,6 @@ __device__ __forceinline__ Run next_run(const csa_paged_attn_args &a, int t0, in
 
 __device__ __forceinline__ int run_pages(const Run &R) {
   return R.lo < R.hi ? (R.hi - 1) / kBlock - R.lo / kBlock + 1 : 0;
-}
-
-// Bit 15 or 31 of the result: that half of the BF16 pair is not finite.
-__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
-  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
 struct ChunkGrid {
@@ -293,7 +275,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             if (there) {
               tc::mbar_arrive_expect_tx(&M->kv_full[st], C::TILE);
               for (int c = 0; c < C::CHUNKS; ++c)
-                tma_load_4d(dst + c * 16384, kv ? &vmap : &kmap, c * 64, kvh, 0, phys,
+                paged::tma_load_4d(dst + c * 16384, kv ? &vmap : &kmap, c * 64, kvh, 0, phys,
                             &M->kv_full[st]);
             } else {
               tc::mbar_arrive(&M->kv_full[st]);
@@ -379,7 +361,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
               const uint4 w = p[c * 1024 + ((q + lane) & 7)];
-              bad |= not_finite2(w.x) | not_finite2(w.y) | not_finite2(w.z) | not_finite2(w.w);
+              bad |= paged::not_finite2(w.x) | paged::not_finite2(w.y) | paged::not_finite2(w.z) | paged::not_finite2(w.w);
             }
           const bool seen = row >= P.lo && row < P.hi;
           if (bad) {
@@ -468,8 +450,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         }
         l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
         if (mixed) {
-          // values that are not finite: their columns leave the product, and
-          // the rows that see them add them here
+          // values that are not finite are zero in the product; the rows that
+          // see them add them here
           ok = pc_wait_warp(&M->v_clean[j & 3], (j >> 2) & 1, abort, a.status_dev);
           if (!ok) break;
           const uint32_t bad[4] = {P.bad[0], P.bad[1], P.bad[2], P.bad[3]};
@@ -499,9 +481,6 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
                   tc::tmem_st32(to + d, o);
                 }
               }
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (bad[i >> 5] >> (i & 31) & 1u) x[i] = 0.f;
           }
         }
 #pragma unroll
@@ -571,32 +550,6 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   if (warp == PC_MMA) tc::tmem_dealloc(tmem, 512);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-    cudaDriverEntryPointQueryResult q;
-    void *fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      fn = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }();
-  return encode;
-}
-
-// BF16 tensor map of up to 4 dimensions, 128-byte swizzle; strides (bytes) of
-// dimensions 1...
-bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
-            const cuuint64_t *strides, const cuuint32_t *box) {
-  const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
-  memset(map, 0, sizeof(*map));
-  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims,
-                  strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-                   CUDA_SUCCESS;
-}
-
 template <int D>
 cudaError_t launch(const csa_paged_attn_args &a, const Parts &parts, cudaStream_t s) {
   using C = Cfg<D>;
@@ -606,23 +559,8 @@ cudaError_t launch(const csa_paged_attn_args &a, const Parts &parts, cudaStream_
   G.n_tiles = (a.n_rows + 2 * G.rows_tile - 1) / (2 * G.rows_tile);
   G.n_parts = parts.n;
   CUtensorMap qmap, kmap, vmap;
-  {
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.n_heads, (cuuint64_t)a.n_rows};
-    const cuuint64_t st[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_row_stride};
-    const cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)G.rows_tile};
-    if (!encode(&qmap, a.q, 3, dims, st, box)) return cudaErrorInvalidValue;
-  }
-  {
-    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)a.n_kv_heads, (cuuint64_t)kBlock,
-                                (cuuint64_t)a.n_blocks};
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)kBlock, 1};
-    const cuuint64_t ks[3] = {(cuuint64_t)a.k_head_stride, (cuuint64_t)a.k_token_stride,
-                              (cuuint64_t)a.k_page_stride};
-    const cuuint64_t vs[3] = {(cuuint64_t)a.v_head_stride, (cuuint64_t)a.v_token_stride,
-                              (cuuint64_t)a.v_page_stride};
-    if (!encode(&kmap, a.k_pool, 4, dims, ks, box) || !encode(&vmap, a.v_pool, 4, dims, vs, box))
-      return cudaErrorInvalidValue;
-  }
+  if (!paged::encode_q(a, G.rows_tile, &qmap) || !paged::encode_pools(a, &kmap, &vmap))
+    return cudaErrorInvalidValue;
   const size_t smem = C::OFF_MISC + sizeof(Misc) + 1024;
   int dev = 0;
   cudaGetDevice(&dev);
