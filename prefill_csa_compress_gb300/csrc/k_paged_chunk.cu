@@ -16,10 +16,14 @@
 //   warp 2      looks through V on pages that some row does not see whole: rows
 //               that no one sees are zeroed, values that are not finite are
 //               zeroed and reported, since a zero probability times them is not zero;
-//   warps 4..11 softmax, one thread a (row, head) pair: the thread holds its
-//               128 logits, so row maxima and sums need no exchange.  Its
-//               reference only moves (and O is rescaled in tensor memory) when
-//               a logit exceeds it by more than 2^8.
+//   warps 4..19 softmax, eight warps a tile, two threads a (row, head) pair with
+//               64 logits each.  P is computed with the reference as it is; only
+//               when some P of the tile reaches 2 (the references are set so
+//               that the largest is 2^-7) are the maxima taken, references moved
+//               and O rescaled in tensor memory.  Bit 14 of a positive BF16 says
+//               that it is 2 or more, so the test is an OR of the packed P, and
+//               it rides on the barrier that both halves of S need before P
+//               goes over them.
 // Tensor memory: S0, S1 (128 columns each; P over S in BF16), O0, O1 (D each).
 // Rows of several requests in one CTA take turns: a page of another request is
 // masked for the whole row.
@@ -35,10 +39,10 @@ namespace {
 
 using paged::Parts;
 
-constexpr int PC_THREADS = 384;
+constexpr int PC_THREADS = 640;
 constexpr int PC_LOAD = 0, PC_MMA = 1, PC_CLEAN = 2, PC_SOFT0 = 4;
 constexpr int PC_META = 8;  // pages described ahead (the ring holds at most 4 of them)
-constexpr float kMove = 8.f;
+constexpr float kLift = 7.f;  // log2 of the room below P = 2, where a reference moves
 
 template <int D>
 struct Cfg {
@@ -68,8 +72,12 @@ struct Misc {
   int first_page;  // skipped before them (another part's)
   int many;        // rows of several requests
   Page page[PC_META];
+  float top[2][2][128];  // a pair's largest logit, or sum, of each half
 };
-static_assert(Cfg<128>::OFF_MISC + sizeof(Misc) + 1024 <= 227 * 1024, "shared memory");
+// All of it but for a few hundred bytes, so nothing is set aside for aligning
+// the start: a kernel without static shared memory gets it 1024-byte aligned,
+// and one that did not would stop before touching it.
+static_assert(Cfg<128>::OFF_MISC + sizeof(Misc) <= 227 * 1024, "shared memory");
 
 // Bounded wait that also gives up when another role has.
 __device__ __forceinline__ bool pc_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
@@ -155,13 +163,15 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
                        const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                            ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   Misc *M = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
   tc::griddep_wait();
   tc::griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tc::smem_u32(sm) & 1023u) {
+    if (tid == 0) flag(a.status_dev, CSA_DEV_TIMEOUT);
+    return;
+  }
   volatile int *abort = &M->abort;
 
   // the CTA's item: key/value head fastest, parts next, the last rows (which
@@ -203,7 +213,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&M->s_full[i], 2);
-      tc::mbar_init(&M->p_full[i], 128);
+      tc::mbar_init(&M->p_full[i], 8);
     }
     tc::mbar_init(&M->o_full, 1);
     for (int i = 0; i < 4; ++i) tc::mbar_init(&M->v_clean[i], 1);
@@ -379,10 +389,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     }
   } else if (warp >= PC_SOFT0) {
     // ================================================================ softmax
-    const int s = (warp - PC_SOFT0) >> 2;
+    const int s = (warp - PC_SOFT0) >> 3, half = ((warp - PC_SOFT0) >> 2) & 1;
     const int m = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + s * 128 + lane_off, to = tmem + C::O_COL + s * D + lane_off;
+    const uint32_t ts = tmem + s * 128 + lane_off;                         // S, and P over it
+    const uint32_t to = tmem + C::O_COL + s * D + half * (D / 2) + lane_off;  // this half of O
+    const int bar = 1 + s;
     const float sl2 = a.softmax_scale * paged::kLog2e;
     const int rr = s * G.rows_tile + m / g, t = t0 + rr, h = kvh * g + m % g;
     int req = -1, lo = 0, hi = 0;
@@ -391,6 +403,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       if (req >= a.n_req) req = -1;
       if (req >= 0) paged::visible_range(a, req, a.row_pos[t], lo, hi);
     }
+    // P = 2^(x - ref): ref is kLift above the largest logit when it is set
     float ref = -INFINITY, l = 0.f;
     bool ok = true;
     if (s < n_sub && n_it > 0) {
@@ -398,71 +411,109 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         uint32_t z[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) z[i] = 0;
-        for (int c = 0; c < D; c += 32) tc::tmem_st32u(to + c, z);
+        for (int c = 0; c < D / 2; c += 32) tc::tmem_st32u(to + c, z);
         tc::tmem_wait_st();
       }
       for (int j = 0; j < n_it; ++j) {
         ok = pc_wait_warp(&M->s_full[s], j & 1, abort, a.status_dev);
-        if (!ok) break;
-        tc::tc_fence_after();
+        // the tile's eight warps go on or stop together
         Page &P = M->page[j % PC_META];
-        float x[128];
-        tc::tmem_ld64(ts, reinterpret_cast<float(&)[64]>(x[0]));
-        tc::tmem_ld64(ts + 64, reinterpret_cast<float(&)[64]>(x[64]));
-        int c_lo = 0, c_hi = 128;
         const bool mixed = P.mixed != 0;
+        int c_lo = 0, c_hi = 64;  // this half's columns that the row sees
         if (mixed) {
-          c_lo = max(lo - P.base, 0);
-          c_hi = rr >= P.r0 && rr < P.r1 ? min(hi - P.base, kBlock) : 0;
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i < c_lo || i >= c_hi) x[i] = -INFINITY;
+          c_lo = max(lo - P.base, 0) - 64 * half;
+          c_hi = (rr >= P.r0 && rr < P.r1 ? min(hi - P.base, kBlock) : 0) - 64 * half;
         }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
+        uint32_t w[32];
+        float sum;
+        auto logits = [&](float(&x)[64]) {
+          tc::tc_fence_after();
+          tc::tmem_ld64(ts + 64 * half, x);
+          if (mixed) {
 #pragma unroll
-        for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-        const bool move = top > ref + kMove || (ref == -INFINITY && top > -INFINITY);
-        if (__any_sync(0xffffffffu, move)) {
-          const float f = move && ref > -INFINITY ? exp2f(ref - top) : 1.f;
-          if (__any_sync(0xffffffffu, f != 1.f)) {
-            for (int c = 0; c < D; c += 32) {
+            for (int i = 0; i < 64; ++i)
+              if (i < c_lo || i >= c_hi) x[i] = -INFINITY;
+          }
+        };
+        // P of this half and its sum; bit 14 or 30 of the result: some P >= 2
+        auto probabilities = [&](float(&x)[64]) {
+          // with nothing seen yet, any logit makes an infinite P
+          const float r0 = ref == -INFINITY ? 1e30f : -ref;
+          float2 sums[2] = {{0.f, 0.f}, {0.f, 0.f}};
+          uint32_t any = 0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float2 y = tc::ffma2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(sl2, sl2),
+                                 make_float2(r0, r0));
+            y.x = attn::exp2_sfu(y.x);
+            y.y = attn::exp2_sfu(y.y);
+            w[i] = attn::pack2(y.x, y.y);
+            any |= w[i];
+            sums[i & 1] = tc::ffma2(y, make_float2(1.f, 1.f), sums[i & 1]);
+          }
+          sum = (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
+          return any;
+        };
+        bool move = j == 0 || !ok;
+        if (!move) {
+          float x[64];
+          logits(x);
+          move = probabilities(x) & 0x40004000u;
+        }
+        if (tc::bar_or(bar, 256, move)) {
+          // some reference of the tile moves (or a wait gave up): largest logits
+          float x[64];
+          logits(x);
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+          M->top[s][half][m] = top;
+          if (tc::bar_or(bar, 256, !ok)) {
+            ok = false;
+            break;
+          }
+          top = fmaxf(top, M->top[s][half ^ 1][m]);
+          if (top > ref + 1.f) {
+            const float f = ref == -INFINITY ? 1.f : exp2f(ref - (top + kLift));
+            ref = top + kLift;
+            l *= f;
+            sum = f;
+          } else {
+            sum = 1.f;
+          }
+          if (__any_sync(0xffffffffu, sum != 1.f)) {
+            for (int c = 0; c < D / 2; c += 32) {
               float o[32];
               tc::tmem_ld32(to + c, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= f;
+              for (int i = 0; i < 32; ++i) o[i] *= sum;
               tc::tmem_st32(to + c, o);
             }
           }
-          l *= f;
-          if (move) ref = top;
+          logits(x);
+          probabilities(x);
+          tc::bar_sync(bar, 256);  // both halves have read S before P goes over it
         }
-        const float r0 = ref == -INFINITY ? 0.f : ref;
-        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-        for (int i = 0; i < 128; i += 2) {
-          const float2 y = tc::ffma2(make_float2(x[i], x[i + 1]), make_float2(sl2, sl2),
-                                     make_float2(-r0, -r0));
-          x[i] = attn::exp2_sfu(y.x);
-          x[i + 1] = attn::exp2_sfu(y.y);
-          float2 &u = sum[(i >> 1) & 1];
-          u = tc::ffma2(make_float2(x[i], x[i + 1]), make_float2(1.f, 1.f), u);
-        }
-        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+        l += sum;
         if (mixed) {
           // values that are not finite are zero in the product; the rows that
           // see them add them here
           ok = pc_wait_warp(&M->v_clean[j & 3], (j >> 2) & 1, abort, a.status_dev);
-          if (!ok) break;
+          if (tc::bar_or(bar, 256, !ok)) {
+            ok = false;
+            break;
+          }
           const uint32_t bad[4] = {P.bad[0], P.bad[1], P.bad[2], P.bad[3]};
           if (bad[0] | bad[1] | bad[2] | bad[3]) {
             const int phys = a.block_table[(long long)P.req * a.max_blocks + P.base / kBlock];
+            const float r0 = ref == -INFINITY ? 0.f : ref;
 #pragma unroll 1
-            for (int w = 0; w < 4; ++w)
+            for (int k = 0; k < 4; ++k)
 #pragma unroll 1
-              for (uint32_t b = bad[w]; b; b &= b - 1) {
-                const int c = 32 * w + __ffs(b) - 1;
-                const bool sees = c >= c_lo && c < c_hi;
+              for (uint32_t b = bad[k]; b; b &= b - 1) {
+                const int c = 32 * k + __ffs(b) - 1;
+                const bool sees = c - 64 * half >= c_lo && c - 64 * half < c_hi;
                 uint32_t raw;
                 asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
                              : "=r"(raw)
@@ -470,9 +521,11 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
                 asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(raw)::"memory");
                 const float p = exp2f(__uint_as_float(raw) * sl2 - r0);
                 const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(
-                    static_cast<const uint8_t *>(a.v_pool) + phys * a.v_page_stride +
-                    c * a.v_token_stride + kvh * a.v_head_stride);
-                for (int d = 0; d < D; d += 32) {
+                                             static_cast<const uint8_t *>(a.v_pool) +
+                                             phys * a.v_page_stride + c * a.v_token_stride +
+                                             kvh * a.v_head_stride) +
+                                         half * (D / 2);
+                for (int d = 0; d < D / 2; d += 32) {
                   float o[32];
                   tc::tmem_ld32(to + d, o);
 #pragma unroll
@@ -481,39 +534,39 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
                   tc::tmem_st32(to + d, o);
                 }
               }
+            tc::bar_sync(bar, 256);  // both halves have read S before P goes over it
           }
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = attn::pack2(x[64 * c + 2 * i], x[64 * c + 2 * i + 1]);
-          tc::tmem_st32u(ts + 32 * c, w);
-        }
+        tc::tmem_st32u(ts + 32 * half, w);
         tc::tmem_wait_st();
         tc::tc_fence_before();
-        tc::mbar_arrive(&M->p_full[s]);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&M->p_full[s]);
       }
       if (ok) ok = pc_wait_warp(&M->o_full, 0, abort, a.status_dev);
       tc::tc_fence_after();
+      // the row's sum over both halves
+      M->top[s][half][m] = l;
+      if (tc::bar_or(bar, 256, !ok)) ok = false;
+      l = half ? M->top[s][0][m] + l : l + M->top[s][1][m];
     }
     // ---- the row's result, or its part
     const long long row = (long long)t * a.n_heads + h;
     const bool mine = req >= 0 && ok;
-    float scale = 0.f;
+    float scale = 1.f;
     if (G.n_parts > 1) {
-      if (mine) parts.ml[(long long)part * a.n_rows * a.n_heads + row] = make_float2(ref, l);
-      scale = 1.f;
+      if (mine && half == 0)
+        parts.ml[(long long)part * a.n_rows * a.n_heads + row] = make_float2(ref, l);
     } else {
       const float s2 = mine && a.sink ? a.sink[h] * paged::kLog2e : -INFINITY;
       const paged::Joined J = paged::finish(ref, l, s2);
       scale = J.inv;
-      if (mine && a.lse) a.lse[row] = J.lse;
+      if (mine && half == 0 && a.lse) a.lse[row] = J.lse;
     }
     const bool zero = ref == -INFINITY && l == 0.f;  // nothing seen: O may hold nothing
     if (s < n_sub && ok) {
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < D / 2; c += 32) {
         float o[32];
         if (n_it > 0)
           tc::tmem_ld32(to + c, o);
@@ -521,23 +574,23 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         if (!mine) continue;
+        const int d = half * (D / 2) + c;
         if (G.n_parts > 1) {
           if (zero) continue;
           float4 *dst = reinterpret_cast<float4 *>(
-              parts.o + ((long long)part * a.n_rows * a.n_heads + row) * D + c);
+              parts.o + ((long long)part * a.n_rows * a.n_heads + row) * D + d);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         } else {
-          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + c);
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+            uint32_t q[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              w[q] = zero ? 0u
-                          : attn::pack2(o[8 * i + 2 * q] * scale, o[8 * i + 2 * q + 1] * scale);
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 4; ++e)
+              q[e] = zero ? 0u : attn::pack2(o[8 * i + 2 * e] * scale, o[8 * i + 2 * e + 1] * scale);
+            dst[i] = make_uint4(q[0], q[1], q[2], q[3]);
           }
         }
       }
@@ -561,7 +614,7 @@ cudaError_t launch(const csa_paged_attn_args &a, const Parts &parts, cudaStream_
   CUtensorMap qmap, kmap, vmap;
   if (!paged::encode_q(a, G.rows_tile, &qmap) || !paged::encode_pools(a, &kmap, &vmap))
     return cudaErrorInvalidValue;
-  const size_t smem = C::OFF_MISC + sizeof(Misc) + 1024;
+  const size_t smem = C::OFF_MISC + sizeof(Misc);
   int dev = 0;
   cudaGetDevice(&dev);
   static bool attr[64] = {};
