@@ -24,7 +24,8 @@
 //               that it is 2 or more, so the test is an OR of the packed P, and
 //               it rides on the barrier that both halves of S need before P
 //               goes over them.
-// Tensor memory: S0, S1 (128 columns each; P over S in BF16), O0, O1 (D each).
+// Tensor memory: two logit buffers of 128 columns (three for D = 64; P over S in
+// BF16), taken in turn by the tiles, and O0, O1 (D columns each).
 // Rows of several requests in one CTA take turns: a page of another request is
 // masked for the whole row.
 #include <cuda.h>
@@ -51,7 +52,9 @@ struct Cfg {
   static constexpr int STAGES = D == 128 ? 5 : 8;      // K and V tiles in flight
   static constexpr int OFF_KV = 2 * TILE;
   static constexpr int OFF_MISC = OFF_KV + STAGES * TILE;
-  static constexpr int O_COL = 256;
+  // logit buffers in tensor memory: what the outputs of two tiles leave
+  static constexpr int BUFS = D == 128 ? 2 : 3;
+  static constexpr int O_COL = BUFS * 128;
 };
 
 // One page as the consumers need it.
@@ -65,7 +68,8 @@ struct Page {
 };
 
 struct Misc {
-  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full, v_clean[4], drained;
+  uint64_t q_full, kv_full[8], kv_empty[8], s_full[3], p_full[3], o_full, v_clean[4];
+  uint64_t drained;
   uint32_t tmem;
   int abort;
   int n_it;        // pages this CTA works through
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       tc::mbar_init(&M->kv_full[i], 1);
       tc::mbar_init(&M->kv_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::BUFS; ++i) {
       tc::mbar_init(&M->s_full[i], 2);
       tc::mbar_init(&M->p_full[i], 8);
     }
@@ -307,45 +311,63 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128);
     constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
     const uint32_t qs = tc::smem_u32(sm), kvs = qs + C::OFF_KV;
-    auto issue_s = [&](int s, uint32_t ks) {
+    // descriptors of the first tiles; an address further on adds its sixteenths
+    const uint64_t dq = tc::desc_sw128(qs), dk = tc::desc_sw128(kvs);
+    const uint64_t dv = tc::desc_sw128_mn(kvs, 16384, 1024);
+    // Step q is page q / n_sub of tile q % n_sub; its logits, and P after
+    // them, sit in buffer q % BUFS.  Logits run BUFS steps ahead of P V, which
+    // frees the buffer (MMAs complete in order).
+    const int n_steps = n_it * n_sub;
+    int sk = 0, wk = 0, sub = 0;  // next logits: stage, its use's parity, tile
+    auto issue_s = [&](int buf) {
+      if (sub == 0 && !pc_wait_warp(&M->kv_full[sk], wk, abort, a.status_dev)) return false;
+      const uint64_t q0 = dq + sub * (C::TILE >> 4), k0 = dk + sk * (C::TILE >> 4);
 #pragma unroll
       for (int c = 0; c < C::CHUNKS; ++c)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc::mma_ss_elect(tmem + s * 128, tc::desc_sw128(qs + s * C::TILE + c * 16384 + k * 32),
-                           tc::desc_sw128(ks + c * 16384 + k * 32), idesc_s, (c | k) != 0);
-      tc::mma_commit_elect(&M->s_full[s]);
-      if (lane == 0) tc::mbar_arrive(&M->s_full[s]);  // hands on the page's description
-      __syncwarp();
+          tc::mma_ss_elect(tmem + buf * 128, q0 + c * 1024 + k * 2, k0 + c * 1024 + k * 2, idesc_s,
+                           (c | k) != 0);
+      return true;
     };
-    bool ok = pc_wait_warp(&M->q_full, 0, abort, a.status_dev) &&
-              pc_wait_warp(&M->kv_full[0], 0, abort, a.status_dev);
-    if (ok) {
-      tc::tc_fence_after();
-      for (int s = 0; s < n_sub; ++s) issue_s(s, kvs);
-      tc::mma_commit_elect(&M->kv_empty[0]);
+    // after the logits of `buf` (or without any, at the end): everything
+    // issued so far, the tile's last product among it, and the page's description
+    auto hand_on = [&](int buf, bool issued) {
+      tc::mma_commit_elect(&M->s_full[buf]);
+      if (lane == 0) tc::mbar_arrive(&M->s_full[buf]);
+      if (issued && ++sub == n_sub) {
+        tc::mma_commit_elect(&M->kv_empty[sk]);
+        sub = 0;
+        sk += 2;
+        if (sk >= C::STAGES) sk -= C::STAGES, wk ^= 1;
+      }
+    };
+    bool ok = pc_wait_warp(&M->q_full, 0, abort, a.status_dev);
+    for (int q = 0; q < C::BUFS && q < n_steps && ok; ++q) {
+      ok = issue_s(q);
+      hand_on(q, true);
     }
-    for (int j = 0; j < n_it && ok; ++j) {
-      const uint32_t iv = 2 * j + 1, ik = 2 * j + 2;
-      const int sv = iv % C::STAGES, sk = ik % C::STAGES;
-      const bool more = j + 1 < n_it;
-      ok = pc_wait_warp(&M->kv_full[sv], (iv / C::STAGES) & 1, abort, a.status_dev) &&
+    int buf = 0, wp = 0, sv = 1, wv = 0;
+    for (int j = 0, q = 0; j < n_it && ok; ++j) {
+      ok = pc_wait_warp(&M->kv_full[sv], wv, abort, a.status_dev) &&
            pc_wait_warp(&M->v_clean[j & 3], (j >> 2) & 1, abort, a.status_dev);
-      if (ok && more) ok = pc_wait_warp(&M->kv_full[sk], (ik / C::STAGES) & 1, abort, a.status_dev);
-      for (int s = 0; s < n_sub && ok; ++s) {
-        ok = pc_wait_warp(&M->p_full[s], j & 1, abort, a.status_dev);
+      for (int s = 0; s < n_sub && ok; ++s, ++q) {
+        ok = pc_wait_warp(&M->p_full[buf], wp, abort, a.status_dev);
         if (!ok) break;
         tc::tc_fence_after();
+        const uint64_t v0 = dv + sv * (C::TILE >> 4);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          tc::mma_f16_ta_elect(tmem + C::O_COL + s * D, tmem + s * 128 + k * 8,
-                               tc::desc_sw128_mn(kvs + sv * C::TILE + k * 2048, 16384, 1024), idesc_o,
-                               1u);
-        if (more) issue_s(s, kvs + sk * C::TILE);
+          tc::mma_f16_ta_elect(tmem + C::O_COL + s * D, tmem + buf * 128 + k * 8, v0 + k * 128,
+                               idesc_o, 1u);
+        if (s == n_sub - 1) tc::mma_commit_elect(&M->kv_empty[sv]);
+        const bool more = q + C::BUFS < n_steps;
+        if (more) ok = issue_s(buf);
+        hand_on(buf, more);
+        if (++buf == C::BUFS) buf = 0, wp ^= 1;
       }
-      if (!ok) break;
-      tc::mma_commit_elect(&M->kv_empty[sv]);
-      if (more) tc::mma_commit_elect(&M->kv_empty[sk]);
+      sv += 2;
+      if (sv >= C::STAGES) sv -= C::STAGES, wv ^= 1;
     }
     if (ok) tc::mma_commit_elect(&M->o_full);
     // every issued MMA has completed before tensor memory is released
@@ -355,9 +377,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     // ================================================================ V on mixed pages
     bool ok = true;
     for (int j = 0; j < n_it && ok; ++j) {
-      const uint32_t iv = 2 * j + 1;
+      const uint32_t ik = 2 * j, iv = ik + 1;
       const int sv = iv % C::STAGES;
-      ok = pc_wait_warp(&M->kv_full[sv], (iv / C::STAGES) & 1, abort, a.status_dev);
+      // in the order of the loads: only then does a stage's parity tell this
+      // load from the stage's one before
+      ok = pc_wait_warp(&M->kv_full[ik % C::STAGES], (ik / C::STAGES) & 1, abort, a.status_dev) &&
+           pc_wait_warp(&M->kv_full[sv], (iv / C::STAGES) & 1, abort, a.status_dev);
       if (!ok) break;
       Page &P = M->page[j % PC_META];
       if (P.mixed) {
@@ -392,7 +417,6 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     const int s = (warp - PC_SOFT0) >> 3, half = ((warp - PC_SOFT0) >> 2) & 1;
     const int m = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + s * 128 + lane_off;                         // S, and P over it
     const uint32_t to = tmem + C::O_COL + s * D + half * (D / 2) + lane_off;  // this half of O
     const int bar = 1 + s;
     const float sl2 = a.softmax_scale * paged::kLog2e;
@@ -414,8 +438,17 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         for (int c = 0; c < D / 2; c += 32) tc::tmem_st32u(to + c, z);
         tc::tmem_wait_st();
       }
+      // the tile's previous product, step q - n_sub, is complete: the logits
+      // that follow it into its buffer are
+      auto o_settled = [&](int q) {
+        const int next = q - n_sub + C::BUFS;
+        pc_wait_warp(&M->s_full[next % C::BUFS], (next / C::BUFS) & 1, abort, a.status_dev);
+        tc::tc_fence_after();
+      };
       for (int j = 0; j < n_it; ++j) {
-        ok = pc_wait_warp(&M->s_full[s], j & 1, abort, a.status_dev);
+        const int q = j * n_sub + s, buf = q % C::BUFS;
+        const uint32_t ts = tmem + buf * 128 + lane_off;  // S, and P over it
+        ok = pc_wait_warp(&M->s_full[buf], (q / C::BUFS) & 1, abort, a.status_dev);
         // the tile's eight warps go on or stop together
         Page &P = M->page[j % PC_META];
         const bool mixed = P.mixed != 0;
@@ -483,6 +516,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             sum = 1.f;
           }
           if (__any_sync(0xffffffffu, sum != 1.f)) {
+            o_settled(q);
             for (int c = 0; c < D / 2; c += 32) {
               float o[32];
               tc::tmem_ld32(to + c, o);
@@ -506,6 +540,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           }
           const uint32_t bad[4] = {P.bad[0], P.bad[1], P.bad[2], P.bad[3]};
           if (bad[0] | bad[1] | bad[2] | bad[3]) {
+            if (j > 0) o_settled(q);
             const int phys = a.block_table[(long long)P.req * a.max_blocks + P.base / kBlock];
             const float r0 = ref == -INFINITY ? 0.f : ref;
 #pragma unroll 1
@@ -541,7 +576,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&M->p_full[s]);
+        if (lane == 0) tc::mbar_arrive(&M->p_full[buf]);
       }
       if (ok) ok = pc_wait_warp(&M->o_full, 0, abort, a.status_dev);
       tc::tc_fence_after();
