@@ -13,7 +13,7 @@
 //   warp 0      walks the requests of the CTA's rows and their pages, loads Q, K
 //               and V by TMA (a ring of stages), and describes each page to the rest;
 //   warp 1      issues the MMAs;
-//   warp 2      looks through V on pages that some row does not see whole: rows
+//   warp 3      looks through V on pages that some row does not see whole: rows
 //               that no one sees are zeroed, values that are not finite are
 //               zeroed and reported, since a zero probability times them is not zero;
 //   warps 4..19 softmax, eight warps a tile, two threads a (row, head) pair with
@@ -24,8 +24,9 @@
 //               that it is 2 or more, so the test is an OR of the packed P, and
 //               it rides on the barrier that both halves of S need before P
 //               goes over them.
-// Tensor memory: two logit buffers of 128 columns (three for D = 64; P over S in
-// BF16), taken in turn by the tiles, and O0, O1 (D columns each).
+// Tensor memory, a tile: S (128 columns), O (D), and P in BF16: over S for D =
+// 128, which fills the 512 columns; apart from it for D = 64, where the next
+// page's logits then need not wait for this page's product.
 // Rows of several requests in one CTA take turns: a page of another request is
 // masked for the whole row.
 #include <cuda.h>
@@ -41,7 +42,8 @@ namespace {
 using paged::Parts;
 
 constexpr int PC_THREADS = 640;
-constexpr int PC_LOAD = 0, PC_MMA = 1, PC_CLEAN = 2, PC_SOFT0 = 4;
+constexpr int PC_LOAD = 0, PC_MMA = 1, PC_CLEAN = 3, PC_SOFT0 = 4;  // first warps
+constexpr int PC_BAR_START = 3;  // named barriers: 1 and 2 are the tiles'
 constexpr int PC_META = 8;  // pages described ahead (the ring holds at most 4 of them)
 constexpr float kLift = 7.f;  // log2 of the room below P = 2, where a reference moves
 
@@ -52,9 +54,11 @@ struct Cfg {
   static constexpr int STAGES = D == 128 ? 5 : 8;      // K and V tiles in flight
   static constexpr int OFF_KV = 2 * TILE;
   static constexpr int OFF_MISC = OFF_KV + STAGES * TILE;
-  // logit buffers in tensor memory: what the outputs of two tiles leave
-  static constexpr int BUFS = D == 128 ? 2 : 3;
-  static constexpr int O_COL = BUFS * 128;
+  // tensor memory columns of a tile s: S at s * S_STEP, P and O
+  static constexpr bool P_APART = D == 64;  // there is room for P beside S
+  static constexpr int S_STEP = P_APART ? 256 : 128;
+  static constexpr int P_COL = P_APART ? 128 : 0;
+  static constexpr int O_COL = P_APART ? 192 : 256, O_STEP = P_APART ? 256 : 128;
 };
 
 // One page as the consumers need it.
@@ -68,13 +72,11 @@ struct Page {
 };
 
 struct Misc {
-  uint64_t q_full, kv_full[8], kv_empty[8], s_full[3], p_full[3], o_full, v_clean[4];
-  uint64_t drained;
+  uint64_t q_full, kv_full[8], kv_empty[8], ready[4];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_full[2], drained;
   uint32_t tmem;
   int abort;
-  int n_it;        // pages this CTA works through
-  int first_page;  // skipped before them (another part's)
-  int many;        // rows of several requests
+  int n_it;  // pages this CTA works through
   Page page[PC_META];
   float top[2][2][128];  // a pair's largest logit, or sum, of each half
 };
@@ -105,42 +107,63 @@ __device__ __forceinline__ bool pc_wait_warp(uint64_t *bar, uint32_t parity, vol
   return __all_sync(0xffffffffu, pc_wait(bar, parity, abort, status));
 }
 
-// Consecutive rows of one request among the CTA's rows [0, n): what they see.
+// The CTA's rows in the load warp's registers: lane i holds rows 32 k + i.
+// Read at once, so that the walk over them waits for memory twice, not once a row.
+constexpr int PC_K = 8;
+struct Rows {
+  int req[PC_K], lo[PC_K], hi[PC_K];  // -2 past the last row; what a row sees
+};
+
+__device__ __forceinline__ void read_rows(const csa_paged_attn_args &a, int t0, int n, Rows &W) {
+  const int lane = threadIdx.x & 31;
+  int pos[PC_K];
+#pragma unroll
+  for (int k = 0; k < PC_K; ++k) {
+    const int r = 32 * k + lane;
+    W.req[k] = r < n ? a.row_req[t0 + r] : -2;
+    pos[k] = r < n ? a.row_pos[t0 + r] : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < PC_K; ++k) {
+    W.lo[k] = W.hi[k] = 0;
+    if (W.req[k] >= 0 && W.req[k] < a.n_req)
+      paged::visible_range(a, W.req[k], pos[k], W.lo[k], W.hi[k]);
+  }
+}
+
+// Consecutive rows of one request: what they see.
 struct Run {
   int req, end;
   int lo, hi;          // positions [lo, hi) that at least one of them sees
   int all_lo, all_hi;  // positions that every one of them sees
 };
 
-// The run that starts at row r0 (whole warp; req < 0: padding).
-__device__ __forceinline__ Run next_run(const csa_paged_attn_args &a, int t0, int r0, int n) {
+// The run that starts at row r0 < n (whole warp; req < 0: padding).
+__device__ __forceinline__ Run next_run(const Rows &W, int r0, int n) {
   const int lane = threadIdx.x & 31;
   Run R;
-  R.req = a.row_req[t0 + r0];
+  int mine = 0;
+#pragma unroll
+  for (int k = 0; k < PC_K; ++k)
+    if (r0 >> 5 == k) mine = W.req[k];
+  R.req = __shfl_sync(0xffffffffu, mine, r0 & 31);
   R.lo = R.all_hi = 0x7FFFFFFF;
   R.hi = R.all_lo = 0;
   R.end = n;
-  const bool ok = R.req >= 0 && R.req < a.n_req;
-  for (int base = r0; base < n; base += 32) {
-    const int r = base + lane;
-    const bool same = r < n && a.row_req[t0 + r] == R.req;
-    const uint32_t other = __ballot_sync(0xffffffffu, !same);
-    const int stop = other ? __ffs(other) - 1 : 32;
-    if (ok && lane < stop) {
-      int lo, hi;
-      paged::visible_range(a, R.req, a.row_pos[t0 + r], lo, hi);
-      if (lo < hi) {
-        R.lo = min(R.lo, lo);
-        R.hi = max(R.hi, hi);
-        R.all_lo = max(R.all_lo, lo);
-        R.all_hi = min(R.all_hi, hi);
+#pragma unroll
+  for (int k = 0; k < PC_K; ++k) {
+    const int r = 32 * k + lane;
+    const uint32_t other = __ballot_sync(0xffffffffu, r >= r0 && W.req[k] != R.req);
+    if (other && R.end == n) R.end = min(n, 32 * k + __ffs(other) - 1);
+    if (r >= r0 && r < R.end) {
+      if (W.lo[k] < W.hi[k]) {
+        R.lo = min(R.lo, W.lo[k]);
+        R.hi = max(R.hi, W.hi[k]);
+        R.all_lo = max(R.all_lo, W.lo[k]);
+        R.all_hi = min(R.all_hi, W.hi[k]);
       } else {
         R.all_lo = 0x7FFFFFFF;  // a row that sees nothing
       }
-    }
-    if (other) {
-      R.end = min(n, base + stop);
-      break;
     }
   }
   R.lo = __reduce_min_sync(0xffffffffu, R.lo);
@@ -152,6 +175,50 @@ __device__ __forceinline__ Run next_run(const csa_paged_attn_args &a, int t0, in
 
 __device__ __forceinline__ int run_pages(const Run &R) {
   return R.lo < R.hi ? (R.hi - 1) / kBlock - R.lo / kBlock + 1 : 0;
+}
+
+// The MMAs of one step and the commits behind them, issued by one elected lane
+// in one branch (a branch for each instruction takes longer than its MMA).
+#define PC_MMA_PTX "tcgen05.mma.cta_group::1.kind::f16 "
+#define PC_COMMIT_PTX "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
+#define PC_BEGIN_PTX \
+  "{\n\t.reg .pred e, p, q;\n\t.reg .b32 a;\n\t.reg .b64 x, y;\n\telect.sync _|e, 0xffffffff;\n\t@!e bra DONE;\n\t"
+#define PC_COMMIT_IF_PTX(n) "setp.ne.u32 q, %" #n ", 0;\n\t@q " PC_COMMIT_PTX "[%" #n "];\n\t"
+#define PC_PV_PTX(k) \
+  "add.u32 a, %1, " #k " * 8;\n\tadd.u64 x, %2, " #k " * 128;\n\t" PC_MMA_PTX "[%0], [a], x, %3, p;\n\t"
+#define PC_QK_PTX(c, k)                                                     \
+  "add.u64 x, %1, " #c " * 1024 + " #k " * 2;\n\tadd.u64 y, %2, " #c " * 1024 + " #k " * 2;\n\t" \
+  PC_MMA_PTX "[%0], x, y, %3, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+
+// O += P V over the page's 128 keys; the barriers `freed` and `done` (0: none)
+// are arrived on when everything issued so far has completed.
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p_tmem, uint64_t v, uint32_t idesc,
+                                         uint32_t freed, uint32_t done) {
+  asm volatile(PC_BEGIN_PTX "setp.eq.b32 p, 0, 0;\n\t" PC_PV_PTX(0) PC_PV_PTX(1) PC_PV_PTX(2)
+                   PC_PV_PTX(3) PC_PV_PTX(4) PC_PV_PTX(5) PC_PV_PTX(6) PC_PV_PTX(7)
+                       PC_COMMIT_IF_PTX(4) PC_COMMIT_IF_PTX(5) "DONE:\n\t}" ::"r"(d),
+               "r"(p_tmem), "l"(v), "r"(idesc), "r"(freed), "r"(done)
+               : "memory");
+}
+// S = Q K^T over D / 16 steps; `full` also gets a plain arrival, which hands on
+// what this warp has seen (the page's description).
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc,
+                                         uint32_t full, uint32_t freed) {
+#define PC_QK_END_PTX                                                                      \
+  PC_COMMIT_PTX "[%4];\n\t{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%4];\n\t}\n\t" \
+  PC_COMMIT_IF_PTX(5) "DONE:\n\t}"
+  if constexpr (D == 64)
+    asm volatile(PC_BEGIN_PTX "setp.ne.b32 p, 0, 0;\n\t" PC_QK_PTX(0, 0) PC_QK_PTX(0, 1)
+                     PC_QK_PTX(0, 2) PC_QK_PTX(0, 3) PC_QK_END_PTX ::"r"(d),
+                 "l"(q), "l"(k), "r"(idesc), "r"(full), "r"(freed)
+                 : "memory");
+  else
+    asm volatile(PC_BEGIN_PTX "setp.ne.b32 p, 0, 0;\n\t" PC_QK_PTX(0, 0) PC_QK_PTX(0, 1)
+                     PC_QK_PTX(0, 2) PC_QK_PTX(0, 3) PC_QK_PTX(1, 0) PC_QK_PTX(1, 1)
+                         PC_QK_PTX(1, 2) PC_QK_PTX(1, 3) PC_QK_END_PTX ::"r"(d),
+                 "l"(q), "l"(k), "r"(idesc), "r"(full), "r"(freed)
+                 : "memory");
 }
 
 struct ChunkGrid {
@@ -188,11 +255,34 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   const int n_rows = min(2 * G.rows_tile, a.n_rows - t0);
   const int n_sub = n_rows > G.rows_tile ? 2 : 1;  // tiles with rows
 
+  // Barriers first, by the warp that loads: its loads of the first page need no
+  // other warp, and it joins the others once they are under way.
+  Rows W;
+  int n_pages = 0, many = 0, skip = 0;
   if (warp == PC_LOAD) {
+    if (lane == 0) {
+      tc::mbar_init(&M->q_full, 1);
+      for (int i = 0; i < C::STAGES; ++i) {
+        tc::mbar_init(&M->kv_full[i], 1);
+        tc::mbar_init(&M->kv_empty[i], 1);
+      }
+      for (int i = 0; i < 4; ++i) tc::mbar_init(&M->ready[i], 1);
+      for (int i = 0; i < n_sub; ++i) {
+        tc::mbar_init(&M->s_full[i], 2);
+        tc::mbar_init(&M->s_free[i], 8);
+        tc::mbar_init(&M->p_full[i], 8);
+        tc::mbar_init(&M->pv_done[i], 1);
+        tc::mbar_init(&M->o_full[i], 1);
+      }
+      tc::mbar_init(&M->drained, 1);
+      M->abort = 0;
+      tc::mbar_fence_init();
+    }
     // how many pages there are, and this part's share of them
+    read_rows(a, t0, n_rows, W);
     int total = 0, valid = 0;
     for (int r = 0; r < n_rows;) {
-      const Run R = next_run(a, t0, r, n_rows);
+      const Run R = next_run(W, r, n_rows);
       if (R.req >= a.n_req && lane == 0) flag(a.status_dev, CSA_DEV_BAD_POS);
       if (R.req >= 0 && R.req < a.n_req) {
         total += run_pages(R);
@@ -200,38 +290,27 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       }
       r = R.end;
     }
-    const int u0 = (int)((long long)total * part / G.n_parts);
-    const int u1 = (int)((long long)total * (part + 1) / G.n_parts);
-    if (lane == 0) {
-      M->first_page = u0;
-      M->n_it = u1 - u0;
-      M->many = valid > 1;
+    skip = (int)((long long)total * part / G.n_parts);
+    n_pages = (int)((long long)total * (part + 1) / G.n_parts) - skip;
+    many = valid > 1;
+    if (lane == 0) M->n_it = n_pages;
+    __syncwarp();
+    // its loads begin below; the other warps go on once the first are issued
+  } else {
+    if (warp == PC_MMA) tc::tmem_alloc(&M->tmem, 512);
+    if (tid == PC_CLEAN * 32) {
+      paged::prefetch_map(&qmap);
+      paged::prefetch_map(&kmap);
+      paged::prefetch_map(&vmap);
     }
-  } else if (warp == PC_MMA) {
-    tc::tmem_alloc(&M->tmem, 512);
-  } else if (tid == PC_CLEAN * 32) {
-    tc::mbar_init(&M->q_full, 1);
-    for (int i = 0; i < C::STAGES; ++i) {
-      tc::mbar_init(&M->kv_full[i], 1);
-      tc::mbar_init(&M->kv_empty[i], 1);
-    }
-    for (int i = 0; i < C::BUFS; ++i) {
-      tc::mbar_init(&M->s_full[i], 2);
-      tc::mbar_init(&M->p_full[i], 8);
-    }
-    tc::mbar_init(&M->o_full, 1);
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&M->v_clean[i], 1);
-    tc::mbar_init(&M->drained, 1);
-    M->abort = 0;
-    tc::mbar_fence_init();
+    tc::tc_fence_before();
   }
-  tc::tc_fence_before();
-  __syncthreads();
-  tc::tc_fence_after();
-  const uint32_t tmem = M->tmem;
-  const int n_it = M->n_it;
+  if (warp != PC_LOAD || n_pages == 0) {
+    tc::bar_sync(PC_BAR_START, PC_THREADS);
+    tc::tc_fence_after();
+  }
 
-  if (warp == PC_LOAD && n_it > 0) {
+  if (warp == PC_LOAD && n_pages > 0) {
     // ================================================================ loads
     uint32_t it = 0;  // tiles loaded
     bool ok = true;
@@ -243,11 +322,10 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           tc::tma_load_3d(sm + s * C::TILE + c * 16384, &qmap, c * 64, kvh * g,
                           t0 + s * G.rows_tile, &M->q_full);
     }
-    const bool many = M->many != 0;
-    int skip = M->first_page, left = n_it;
+    int left = n_pages;
     for (int r = 0; r < n_rows && left > 0 && ok;) {
       const int r0 = r;
-      const Run R = next_run(a, t0, r, n_rows);
+      const Run R = next_run(W, r, n_rows);
       r = R.end;
       if (R.req < 0 || R.req >= a.n_req) continue;
       const int np = run_pages(R);
@@ -290,7 +368,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
               tc::mbar_arrive_expect_tx(&M->kv_full[st], C::TILE);
               for (int c = 0; c < C::CHUNKS; ++c)
                 paged::tma_load_4d(dst + c * 16384, kv ? &vmap : &kmap, c * 64, kvh, 0, phys,
-                            &M->kv_full[st]);
+                                   &M->kv_full[st]);
             } else {
               tc::mbar_arrive(&M->kv_full[st]);
             }
@@ -298,6 +376,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           __syncwarp();
           ++it;
         }
+        if (it == 2) tc::bar_sync(PC_BAR_START, PC_THREADS);  // n_it, barriers
       }
     }
     // whatever was asked for has landed before the CTA retires
@@ -306,70 +385,51 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
         tc::mbar_wait(&M->kv_full[k % C::STAGES], (k / C::STAGES) & 1, 50000000ull);
     }
-  } else if (warp == PC_MMA && n_it > 0) {
+  }
+  const int n_it = M->n_it;
+  const uint32_t tmem = __reduce_or_sync(0xffffffffu, M->tmem);  // (into a uniform register)
+  if (warp == PC_MMA && n_it > 0) {
     // ================================================================ MMA
     constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128);
     constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
-    const uint32_t qs = tc::smem_u32(sm), kvs = qs + C::OFF_KV;
+    const uint32_t kvs = tc::smem_u32(sm) + C::OFF_KV;
     // descriptors of the first tiles; an address further on adds its sixteenths
-    const uint64_t dq = tc::desc_sw128(qs), dk = tc::desc_sw128(kvs);
+    const uint64_t dq = tc::desc_sw128(tc::smem_u32(sm)), dk = tc::desc_sw128(kvs);
     const uint64_t dv = tc::desc_sw128_mn(kvs, 16384, 1024);
-    // Step q is page q / n_sub of tile q % n_sub; its logits, and P after
-    // them, sit in buffer q % BUFS.  Logits run BUFS steps ahead of P V, which
-    // frees the buffer (MMAs complete in order).
-    const int n_steps = n_it * n_sub;
-    int sk = 0, wk = 0, sub = 0;  // next logits: stage, its use's parity, tile
-    auto issue_s = [&](int buf) {
-      if (sub == 0 && !pc_wait_warp(&M->kv_full[sk], wk, abort, a.status_dev)) return false;
-      const uint64_t q0 = dq + sub * (C::TILE >> 4), k0 = dk + sk * (C::TILE >> 4);
-#pragma unroll
-      for (int c = 0; c < C::CHUNKS; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc::mma_ss_elect(tmem + buf * 128, q0 + c * 1024 + k * 2, k0 + c * 1024 + k * 2, idesc_s,
-                           (c | k) != 0);
-      return true;
+    const uint32_t bar_s = tc::smem_u32(M->s_full), bar_pv = tc::smem_u32(M->pv_done),
+                   bar_kv = tc::smem_u32(M->kv_empty);
+    int sk = 0, sv = 1;  // stages of the next K and V
+    auto next_s = [&](int s) {
+      issue_qk<D>(tmem + s * C::S_STEP, dq + s * (C::TILE >> 4), dk + sk * (C::TILE >> 4), idesc_s,
+                  bar_s + 8 * s, s == n_sub - 1 ? bar_kv + 8 * sk : 0);
     };
-    // after the logits of `buf` (or without any, at the end): everything
-    // issued so far, the tile's last product among it, and the page's description
-    auto hand_on = [&](int buf, bool issued) {
-      tc::mma_commit_elect(&M->s_full[buf]);
-      if (lane == 0) tc::mbar_arrive(&M->s_full[buf]);
-      if (issued && ++sub == n_sub) {
-        tc::mma_commit_elect(&M->kv_empty[sk]);
-        sub = 0;
-        sk += 2;
-        if (sk >= C::STAGES) sk -= C::STAGES, wk ^= 1;
-      }
-    };
-    bool ok = pc_wait_warp(&M->q_full, 0, abort, a.status_dev);
-    for (int q = 0; q < C::BUFS && q < n_steps && ok; ++q) {
-      ok = issue_s(q);
-      hand_on(q, true);
-    }
-    int buf = 0, wp = 0, sv = 1, wv = 0;
-    for (int j = 0, q = 0; j < n_it && ok; ++j) {
-      ok = pc_wait_warp(&M->kv_full[sv], wv, abort, a.status_dev) &&
-           pc_wait_warp(&M->v_clean[j & 3], (j >> 2) & 1, abort, a.status_dev);
-      for (int s = 0; s < n_sub && ok; ++s, ++q) {
-        ok = pc_wait_warp(&M->p_full[buf], wp, abort, a.status_dev);
+    bool ok = pc_wait_warp(&M->q_full, 0, abort, a.status_dev) &&
+              pc_wait_warp(&M->kv_full[0], 0, abort, a.status_dev);
+    if (ok)
+      for (int s = 0; s < n_sub; ++s) next_s(s);
+    for (int j = 0; j < n_it && ok; ++j) {
+      const bool more = j + 1 < n_it;
+      sk = sk + 2 >= C::STAGES ? sk + 2 - C::STAGES : sk + 2;
+      // the page's V and the next page's K
+      ok = pc_wait_warp(&M->ready[j & 3], (j >> 2) & 1, abort, a.status_dev);
+      for (int s = 0; s < n_sub && ok; ++s) {
+        if (C::P_APART && more) {
+          // the next logits as soon as the softmax holds this page's
+          ok = pc_wait_warp(&M->s_free[s], j & 1, abort, a.status_dev);
+          tc::tc_fence_after();
+          if (ok) next_s(s);
+        }
+        ok = ok && pc_wait_warp(&M->p_full[s], j & 1, abort, a.status_dev);
         if (!ok) break;
         tc::tc_fence_after();
-        const uint64_t v0 = dv + sv * (C::TILE >> 4);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc::mma_f16_ta_elect(tmem + C::O_COL + s * D, tmem + buf * 128 + k * 8, v0 + k * 128,
-                               idesc_o, 1u);
-        if (s == n_sub - 1) tc::mma_commit_elect(&M->kv_empty[sv]);
-        const bool more = q + C::BUFS < n_steps;
-        if (more) ok = issue_s(buf);
-        hand_on(buf, more);
-        if (++buf == C::BUFS) buf = 0, wp ^= 1;
+        issue_pv(tmem + C::O_COL + s * C::O_STEP, tmem + s * C::S_STEP + C::P_COL,
+                 dv + sv * (C::TILE >> 4), idesc_o, s == n_sub - 1 ? bar_kv + 8 * sv : 0,
+                 C::P_APART ? bar_pv + 8 * s : 0);
+        if (!C::P_APART && more) next_s(s);  // over P, behind its product
       }
-      sv += 2;
-      if (sv >= C::STAGES) sv -= C::STAGES, wv ^= 1;
+      sv = sv + 2 >= C::STAGES ? sv + 2 - C::STAGES : sv + 2;
     }
-    if (ok) tc::mma_commit_elect(&M->o_full);
+    for (int s = 0; s < n_sub && ok; ++s) tc::mma_commit_elect(&M->o_full[s]);
     // every issued MMA has completed before tensor memory is released
     tc::mma_commit_elect(&M->drained);
     tc::mbar_wait(&M->drained, 0, 100000000ull);
@@ -381,43 +441,51 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       const int sv = iv % C::STAGES;
       // in the order of the loads: only then does a stage's parity tell this
       // load from the stage's one before
-      ok = pc_wait_warp(&M->kv_full[ik % C::STAGES], (ik / C::STAGES) & 1, abort, a.status_dev) &&
-           pc_wait_warp(&M->kv_full[sv], (iv / C::STAGES) & 1, abort, a.status_dev);
+      if (j == 0) ok = pc_wait_warp(&M->kv_full[0], 0, abort, a.status_dev);
+      ok = ok && pc_wait_warp(&M->kv_full[sv], (iv / C::STAGES) & 1, abort, a.status_dev);
       if (!ok) break;
       Page &P = M->page[j % PC_META];
       if (P.mixed) {
         uint8_t *v = sm + C::OFF_KV + sv * C::TILE;
         bool wrote = false;
+#pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int row = k * 32 + lane;
           uint4 *p = reinterpret_cast<uint4 *>(v + row * 128);
           uint32_t bad = 0;
-          for (int c = 0; c < C::CHUNKS; ++c)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const uint4 w = p[c * 1024 + ((q + lane) & 7)];
-              bad |= paged::not_finite2(w.x) | paged::not_finite2(w.y) | paged::not_finite2(w.z) | paged::not_finite2(w.w);
-            }
-          const bool seen = row >= P.lo && row < P.hi;
+          for (int c = 0; c < C::CHUNKS; ++c) {
+            uint4 w[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) w[q] = p[c * 1024 + ((q + lane) & 7)];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              bad |= paged::not_finite2(w[q].x) | paged::not_finite2(w[q].y) |
+                     paged::not_finite2(w[q].z) | paged::not_finite2(w[q].w);
+          }
           if (bad) {
             for (int c = 0; c < C::CHUNKS; ++c)
               for (int q = 0; q < 8; ++q) p[c * 1024 + q] = make_uint4(0, 0, 0, 0);
             wrote = true;
           }
-          const uint32_t word = __ballot_sync(0xffffffffu, bad != 0 && seen);
-          if (lane == 0) P.bad[k] = word;
+          const uint32_t seen = __ballot_sync(0xffffffffu, bad != 0 && row >= P.lo && row < P.hi);
+          if (lane == 0) P.bad[k] = seen;
         }
         if (wrote) tc::fence_async_shared();
       }
+      if (j + 1 < n_it)  // the MMA warp waits once for both
+        ok = pc_wait_warp(&M->kv_full[(ik + 2) % C::STAGES], ((ik + 2) / C::STAGES) & 1, abort,
+                          a.status_dev);
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&M->v_clean[j & 3]);
+      if (lane == 0 && ok) tc::mbar_arrive(&M->ready[j & 3]);
     }
   } else if (warp >= PC_SOFT0) {
     // ================================================================ softmax
     const int s = (warp - PC_SOFT0) >> 3, half = ((warp - PC_SOFT0) >> 2) & 1;
     const int m = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t to = tmem + C::O_COL + s * D + half * (D / 2) + lane_off;  // this half of O
+    const uint32_t ts = tmem + s * C::S_STEP + lane_off, tp = ts + C::P_COL;
+    const uint32_t to = tmem + C::O_COL + s * C::O_STEP + half * (D / 2) + lane_off;  // this half
     const int bar = 1 + s;
     const float sl2 = a.softmax_scale * paged::kLog2e;
     const int rr = s * G.rows_tile + m / g, t = t0 + rr, h = kvh * g + m % g;
@@ -438,17 +506,13 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         for (int c = 0; c < D / 2; c += 32) tc::tmem_st32u(to + c, z);
         tc::tmem_wait_st();
       }
-      // the tile's previous product, step q - n_sub, is complete: the logits
-      // that follow it into its buffer are
-      auto o_settled = [&](int q) {
-        const int next = q - n_sub + C::BUFS;
-        pc_wait_warp(&M->s_full[next % C::BUFS], (next / C::BUFS) & 1, abort, a.status_dev);
-        tc::tc_fence_after();
+      // the tile's product of the page before is complete
+      auto o_settled = [&](int j) {
+        if (C::P_APART && j > 0) pc_wait_warp(&M->pv_done[s], (j - 1) & 1, abort, a.status_dev);
+        tc::tc_fence_after();  // (else the logits were issued behind it)
       };
       for (int j = 0; j < n_it; ++j) {
-        const int q = j * n_sub + s, buf = q % C::BUFS;
-        const uint32_t ts = tmem + buf * 128 + lane_off;  // S, and P over it
-        ok = pc_wait_warp(&M->s_full[buf], (q / C::BUFS) & 1, abort, a.status_dev);
+        ok = pc_wait_warp(&M->s_full[s], j & 1, abort, a.status_dev);
         // the tile's eight warps go on or stop together
         Page &P = M->page[j % PC_META];
         const bool mixed = P.mixed != 0;
@@ -491,7 +555,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         if (!move) {
           float x[64];
           logits(x);
-          move = probabilities(x) & 0x40004000u;
+          // (a thread without a row has whatever was in shared memory for q)
+          move = (probabilities(x) & 0x40004000u) && req >= 0;
         }
         if (tc::bar_or(bar, 256, move)) {
           // some reference of the tile moves (or a wait gave up): largest logits
@@ -507,7 +572,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             break;
           }
           top = fmaxf(top, M->top[s][half ^ 1][m]);
-          if (top > ref + 1.f) {
+          if (req >= 0 && top > ref + 1.f) {
             const float f = ref == -INFINITY ? 1.f : exp2f(ref - (top + kLift));
             ref = top + kLift;
             l *= f;
@@ -516,7 +581,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             sum = 1.f;
           }
           if (__any_sync(0xffffffffu, sum != 1.f)) {
-            o_settled(q);
+            o_settled(j);
             for (int c = 0; c < D / 2; c += 32) {
               float o[32];
               tc::tmem_ld32(to + c, o);
@@ -533,14 +598,14 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         if (mixed) {
           // values that are not finite are zero in the product; the rows that
           // see them add them here
-          ok = pc_wait_warp(&M->v_clean[j & 3], (j >> 2) & 1, abort, a.status_dev);
+          ok = pc_wait_warp(&M->ready[j & 3], (j >> 2) & 1, abort, a.status_dev);
           if (tc::bar_or(bar, 256, !ok)) {
             ok = false;
             break;
           }
           const uint32_t bad[4] = {P.bad[0], P.bad[1], P.bad[2], P.bad[3]};
           if (bad[0] | bad[1] | bad[2] | bad[3]) {
-            if (j > 0) o_settled(q);
+            o_settled(j);
             const int phys = a.block_table[(long long)P.req * a.max_blocks + P.base / kBlock];
             const float r0 = ref == -INFINITY ? 0.f : ref;
 #pragma unroll 1
@@ -572,13 +637,19 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             tc::bar_sync(bar, 256);  // both halves have read S before P goes over it
           }
         }
-        tc::tmem_st32u(ts + 32 * half, w);
+        if (C::P_APART) {
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&M->s_free[s]);
+          o_settled(j);  // and has read the P that goes now
+        }
+        tc::tmem_st32u(tp + 32 * half, w);
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&M->p_full[buf]);
+        if (lane == 0) tc::mbar_arrive(&M->p_full[s]);
       }
-      if (ok) ok = pc_wait_warp(&M->o_full, 0, abort, a.status_dev);
+      if (ok) ok = pc_wait_warp(&M->o_full[s], 0, abort, a.status_dev);
       tc::tc_fence_after();
       // the row's sum over both halves
       M->top[s][half][m] = l;
@@ -600,6 +671,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     }
     const bool zero = ref == -INFINITY && l == 0.f;  // nothing seen: O may hold nothing
     if (s < n_sub && ok) {
+      // Through shared memory (the tile's Q, which no MMA reads any more), 64
+      // bytes of a row at a time: a thread holds a row, and four lanes store one
+      // row's piece (every lane storing its own row took 3.7 us).
+      const uint32_t rows_here = __ballot_sync(0xffffffffu, mine && !(G.n_parts > 1 && zero));
+      uint4 *stage = reinterpret_cast<uint4 *>(sm + s * C::TILE +
+                                               (half * 4 + (warp & 3)) * (C::TILE / 8));
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 32) {
         float o[32];
@@ -608,24 +685,46 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         else
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        if (!mine) continue;
         const int d = half * (D / 2) + c;
         if (G.n_parts > 1) {
-          if (zero) continue;
-          float4 *dst = reinterpret_cast<float4 *>(
-              parts.o + ((long long)part * a.n_rows * a.n_heads + row) * D + d);
+          // 32 rows of 64 bytes twice: D = 64 has 2 KB a warp
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int u = 0; u < 2; ++u) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              stage[lane * 4 + (i ^ ((lane >> 1) & 3))] = make_uint4(
+                  __float_as_uint(o[16 * u + 4 * i]), __float_as_uint(o[16 * u + 4 * i + 1]),
+                  __float_as_uint(o[16 * u + 4 * i + 2]), __float_as_uint(o[16 * u + 4 * i + 3]));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = i * 8 + (lane >> 2), q = lane & 3;
+              const uint4 v = stage[r * 4 + (q ^ ((r >> 1) & 3))];
+              const long long to_row = __shfl_sync(0xffffffffu, row, r);
+              if (rows_here >> r & 1)
+                reinterpret_cast<uint4 *>(
+                    parts.o + ((long long)part * a.n_rows * a.n_heads + to_row) * D + d + 16 * u)[q] = v;
+            }
+          }
         } else {
-          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d);
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t q[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               q[e] = zero ? 0u : attn::pack2(o[8 * i + 2 * e] * scale, o[8 * i + 2 * e + 1] * scale);
-            dst[i] = make_uint4(q[0], q[1], q[2], q[3]);
+            stage[lane * 4 + (i ^ ((lane >> 1) & 3))] = make_uint4(q[0], q[1], q[2], q[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2), q = lane & 3;
+            const uint4 v = stage[r * 4 + (q ^ ((r >> 1) & 3))];
+            const long long to_row = __shfl_sync(0xffffffffu, row, r);
+            if (rows_here >> r & 1)
+              reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + to_row * D + d)[q] = v;
           }
         }
       }

@@ -58,6 +58,10 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, 
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const void *tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
+
 // Host: tensor maps of the pools [pages, 128, heads, head_dim], one page of one
 // head and 64 channels a box, 128-byte swizzle; and of q, a group's heads of
 // `rows` rows a box.
