@@ -72,8 +72,9 @@ struct Page {
 };
 
 struct Misc {
-  uint64_t q_full, kv_full[8], kv_empty[8], ready[4];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_full[2], drained;
+  // 32 barriers, initialised by a lane each
+  uint64_t q_full, drained, kv_full[8], kv_empty[8], ready[4], pv_done[2], o_full[2];
+  uint64_t s_full[2], s_free[2], p_full[2];
   uint32_t tmem;
   int abort;
   int n_it;  // pages this CTA works through
@@ -116,7 +117,7 @@ struct Rows {
 
 __device__ __forceinline__ void read_rows(const csa_paged_attn_args &a, int t0, int n, Rows &W) {
   const int lane = threadIdx.x & 31;
-  int pos[PC_K];
+  int pos[PC_K], len[PC_K];
 #pragma unroll
   for (int k = 0; k < PC_K; ++k) {
     const int r = 32 * k + lane;
@@ -124,10 +125,12 @@ __device__ __forceinline__ void read_rows(const csa_paged_attn_args &a, int t0, 
     pos[k] = r < n ? a.row_pos[t0 + r] : 0;
   }
 #pragma unroll
+  for (int k = 0; k < PC_K; ++k)  // (one wait for all of them)
+    len[k] = a.kv_len[W.req[k] >= 0 && W.req[k] < a.n_req ? W.req[k] : 0];
+#pragma unroll
   for (int k = 0; k < PC_K; ++k) {
-    W.lo[k] = W.hi[k] = 0;
-    if (W.req[k] >= 0 && W.req[k] < a.n_req)
-      paged::visible_range(a, W.req[k], pos[k], W.lo[k], W.hi[k]);
+    paged::visible_range(a, len[k], pos[k], W.lo[k], W.hi[k]);
+    if (W.req[k] < 0 || W.req[k] >= a.n_req) W.lo[k] = W.hi[k] = 0;
   }
 }
 
@@ -136,40 +139,56 @@ struct Run {
   int req, end;
   int lo, hi;          // positions [lo, hi) that at least one of them sees
   int all_lo, all_hi;  // positions that every one of them sees
+
+  __device__ __forceinline__ void add(int l, int h) {
+    if (l < h) {
+      lo = min(lo, l);
+      hi = max(hi, h);
+      all_lo = max(all_lo, l);
+      all_hi = min(all_hi, h);
+    } else {
+      all_lo = 0x7FFFFFFF;  // a row that sees nothing
+    }
+  }
+  __device__ __forceinline__ void reduce() {
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+  }
 };
+
+// All rows as one run, if they are one request's.
+__device__ __forceinline__ bool one_run(const Rows &W, int n, Run &R) {
+  const int lane = threadIdx.x & 31;
+  R = {__shfl_sync(0xffffffffu, W.req[0], 0), n, 0x7FFFFFFF, 0, 0, 0x7FFFFFFF};
+  bool same = true;
+#pragma unroll
+  for (int k = 0; k < PC_K; ++k)
+    if (32 * k + lane < n) {
+      same = same && W.req[k] == R.req;
+      R.add(W.lo[k], W.hi[k]);
+    }
+  R.reduce();
+  return __all_sync(0xffffffffu, same);
+}
 
 // The run that starts at row r0 < n (whole warp; req < 0: padding).
 __device__ __forceinline__ Run next_run(const Rows &W, int r0, int n) {
   const int lane = threadIdx.x & 31;
-  Run R;
   int mine = 0;
 #pragma unroll
   for (int k = 0; k < PC_K; ++k)
     if (r0 >> 5 == k) mine = W.req[k];
-  R.req = __shfl_sync(0xffffffffu, mine, r0 & 31);
-  R.lo = R.all_hi = 0x7FFFFFFF;
-  R.hi = R.all_lo = 0;
-  R.end = n;
+  Run R = {__shfl_sync(0xffffffffu, mine, r0 & 31), n, 0x7FFFFFFF, 0, 0, 0x7FFFFFFF};
 #pragma unroll
   for (int k = 0; k < PC_K; ++k) {
     const int r = 32 * k + lane;
     const uint32_t other = __ballot_sync(0xffffffffu, r >= r0 && W.req[k] != R.req);
     if (other && R.end == n) R.end = min(n, 32 * k + __ffs(other) - 1);
-    if (r >= r0 && r < R.end) {
-      if (W.lo[k] < W.hi[k]) {
-        R.lo = min(R.lo, W.lo[k]);
-        R.hi = max(R.hi, W.hi[k]);
-        R.all_lo = max(R.all_lo, W.lo[k]);
-        R.all_hi = min(R.all_hi, W.hi[k]);
-      } else {
-        R.all_lo = 0x7FFFFFFF;  // a row that sees nothing
-      }
-    }
+    if (r >= r0 && r < R.end) R.add(W.lo[k], W.hi[k]);
   }
-  R.lo = __reduce_min_sync(0xffffffffu, R.lo);
-  R.hi = __reduce_max_sync(0xffffffffu, R.hi);
-  R.all_lo = __reduce_max_sync(0xffffffffu, R.all_lo);
-  R.all_hi = __reduce_min_sync(0xffffffffu, R.all_hi);
+  R.reduce();
   return R;
 }
 
@@ -221,6 +240,36 @@ __device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k, uin
                  : "memory");
 }
 
+// Bits below n of a word (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t below(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
+}
+
+// 16 consecutive FP32 columns of this thread's lane, and back.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+
 struct ChunkGrid {
   int n_tiles;    // row tiles (of 2 R rows)
   int rows_tile;  // R
@@ -255,65 +304,18 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   const int n_rows = min(2 * G.rows_tile, a.n_rows - t0);
   const int n_sub = n_rows > G.rows_tile ? 2 : 1;  // tiles with rows
 
-  // Barriers first, by the warp that loads: its loads of the first page need no
-  // other warp, and it joins the others once they are under way.
-  Rows W;
-  int n_pages = 0, many = 0, skip = 0;
+  // The warp that loads sets up the barriers and finds the CTA's pages; its
+  // loads of q and of the first page need no other warp, and it joins the others
+  // once they are under way.
   if (warp == PC_LOAD) {
-    if (lane == 0) {
-      tc::mbar_init(&M->q_full, 1);
-      for (int i = 0; i < C::STAGES; ++i) {
-        tc::mbar_init(&M->kv_full[i], 1);
-        tc::mbar_init(&M->kv_empty[i], 1);
-      }
-      for (int i = 0; i < 4; ++i) tc::mbar_init(&M->ready[i], 1);
-      for (int i = 0; i < n_sub; ++i) {
-        tc::mbar_init(&M->s_full[i], 2);
-        tc::mbar_init(&M->s_free[i], 8);
-        tc::mbar_init(&M->p_full[i], 8);
-        tc::mbar_init(&M->pv_done[i], 1);
-        tc::mbar_init(&M->o_full[i], 1);
-      }
-      tc::mbar_init(&M->drained, 1);
-      M->abort = 0;
-      tc::mbar_fence_init();
-    }
-    // how many pages there are, and this part's share of them
-    read_rows(a, t0, n_rows, W);
-    int total = 0, valid = 0;
-    for (int r = 0; r < n_rows;) {
-      const Run R = next_run(W, r, n_rows);
-      if (R.req >= a.n_req && lane == 0) flag(a.status_dev, CSA_DEV_BAD_POS);
-      if (R.req >= 0 && R.req < a.n_req) {
-        total += run_pages(R);
-        ++valid;
-      }
-      r = R.end;
-    }
-    skip = (int)((long long)total * part / G.n_parts);
-    n_pages = (int)((long long)total * (part + 1) / G.n_parts) - skip;
-    many = valid > 1;
-    if (lane == 0) M->n_it = n_pages;
-    __syncwarp();
-    // its loads begin below; the other warps go on once the first are issued
-  } else {
-    if (warp == PC_MMA) tc::tmem_alloc(&M->tmem, 512);
-    if (tid == PC_CLEAN * 32) {
-      paged::prefetch_map(&qmap);
-      paged::prefetch_map(&kmap);
-      paged::prefetch_map(&vmap);
-    }
-    tc::tc_fence_before();
-  }
-  if (warp != PC_LOAD || n_pages == 0) {
-    tc::bar_sync(PC_BAR_START, PC_THREADS);
-    tc::tc_fence_after();
-  }
-
-  if (warp == PC_LOAD && n_pages > 0) {
     // ================================================================ loads
-    uint32_t it = 0;  // tiles loaded
-    bool ok = true;
+    Rows W;
+    read_rows(a, t0, n_rows, W);
+    // (q_full, ..., o_full: one arrival; s_full two; s_free and p_full a warp each)
+    tc::mbar_init(&M->q_full + lane, lane < 26 ? 1 : (lane < 28 ? 2 : 8));
+    if (lane == 0) M->abort = 0;
+    tc::mbar_fence_init();
+    __syncwarp();
     if (lane == 0) {
       const uint32_t box = (uint32_t)(G.rows_tile * g * 128);
       tc::mbar_arrive_expect_tx(&M->q_full, n_sub * C::CHUNKS * box);
@@ -322,13 +324,35 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           tc::tma_load_3d(sm + s * C::TILE + c * 16384, &qmap, c * 64, kvh * g,
                           t0 + s * G.rows_tile, &M->q_full);
     }
-    int left = n_pages;
-    for (int r = 0; r < n_rows && left > 0 && ok;) {
+    // Two walks over the runs of one request, the first (not needed for a
+    // single run) to count the pages: this part takes its share of them.
+    Run R;
+    const bool single = one_run(W, n_rows, R);
+    bool counting = true, many = false, ok = true;
+    int total = 0, valid = 0, skip = 0, n_pages = 0, left = 0;
+    uint32_t it = 0;  // tiles loaded
+    for (int r = 0; ok;) {
+      if (r >= n_rows || (!counting && left == 0)) {
+        if (!counting) break;
+        counting = false;
+        skip = (int)((long long)total * part / G.n_parts);
+        left = n_pages = (int)((long long)total * (part + 1) / G.n_parts) - skip;
+        many = valid > 1;
+        if (lane == 0) M->n_it = n_pages;
+        r = 0;
+        continue;
+      }
       const int r0 = r;
-      const Run R = next_run(W, r, n_rows);
+      if (!single) R = next_run(W, r, n_rows);
       r = R.end;
+      if (counting && R.req >= a.n_req && lane == 0) flag(a.status_dev, CSA_DEV_BAD_POS);
       if (R.req < 0 || R.req >= a.n_req) continue;
       const int np = run_pages(R);
+      if (counting) {
+        total += np;
+        ++valid;
+        continue;
+      }
       if (skip >= np) {
         skip -= np;
         continue;
@@ -346,10 +370,10 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         const bool there = phys >= 0 && phys < a.n_blocks;
         const int base = (pg0 + i) * kBlock;
         // K, then V
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++it) {
           const int st = it % C::STAGES;
-          ok = ok && pc_wait_warp(&M->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, abort, a.status_dev);
+          ok = pc_wait_warp(&M->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, abort, a.status_dev);
           if (!ok) break;
           if (lane == 0) {
             if (kv == 0) {
@@ -374,17 +398,26 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             }
           }
           __syncwarp();
-          ++it;
         }
         if (it == 2) tc::bar_sync(PC_BAR_START, PC_THREADS);  // n_it, barriers
       }
     }
+    if (n_pages == 0) tc::bar_sync(PC_BAR_START, PC_THREADS);
     // whatever was asked for has landed before the CTA retires
-    if (*abort) {
-      tc::mbar_wait(&M->q_full, 0, 50000000ull);
+    if (n_pages == 0 || *abort) tc::mbar_wait(&M->q_full, 0, 50000000ull);
+    if (*abort)
       for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
         tc::mbar_wait(&M->kv_full[k % C::STAGES], (k / C::STAGES) & 1, 50000000ull);
+  } else {
+    if (warp == PC_MMA) tc::tmem_alloc(&M->tmem, 512);
+    if (tid == PC_CLEAN * 32) {
+      paged::prefetch_map(&qmap);
+      paged::prefetch_map(&kmap);
+      paged::prefetch_map(&vmap);
     }
+    tc::tc_fence_before();
+    tc::bar_sync(PC_BAR_START, PC_THREADS);
+    tc::tc_fence_after();
   }
   const int n_it = M->n_it;
   const uint32_t tmem = __reduce_or_sync(0xffffffffu, M->tmem);  // (into a uniform register)
@@ -493,8 +526,9 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     if (m < G.rows_tile * g && rr < n_rows) {
       req = a.row_req[t];
       if (req >= a.n_req) req = -1;
-      if (req >= 0) paged::visible_range(a, req, a.row_pos[t], lo, hi);
+      if (req >= 0) paged::visible_range(a, a.kv_len[req], a.row_pos[t], lo, hi);
     }
+    const float s2 = req >= 0 && a.sink ? a.sink[h] * paged::kLog2e : -INFINITY;
     // P = 2^(x - ref): ref is kLift above the largest logit when it is set
     float ref = -INFINITY, l = 0.f;
     bool ok = true;
@@ -516,24 +550,58 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         // the tile's eight warps go on or stop together
         Page &P = M->page[j % PC_META];
         const bool mixed = P.mixed != 0;
-        int c_lo = 0, c_hi = 64;  // this half's columns that the row sees
+        // this half's columns that the row sees (all of them unless the page is mixed)
+        uint32_t see[2] = {~0u, ~0u};
         if (mixed) {
-          c_lo = max(lo - P.base, 0) - 64 * half;
-          c_hi = (rr >= P.r0 && rr < P.r1 ? min(hi - P.base, kBlock) : 0) - 64 * half;
+          const int c_lo = max(lo - P.base, 0) - 64 * half;
+          const int c_hi = (rr >= P.r0 && rr < P.r1 ? min(hi - P.base, kBlock) : 0) - 64 * half;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            see[k] = below(c_hi - 32 * k) & ~below(c_lo - 32 * k);
         }
+        // P and its sum, with the references as they are; where some P of the
+        // tile comes out at 2 or more (bit 14 or 30), again with moved references.
         uint32_t w[32];
         float sum;
-        auto logits = [&](float(&x)[64]) {
+        for (bool move = j == 0;;) {
+          float x[64];
           tc::tc_fence_after();
           tc::tmem_ld64(ts + 64 * half, x);
           if (mixed) {
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-              if (i < c_lo || i >= c_hi) x[i] = -INFINITY;
+              if (!(see[i >> 5] >> (i & 31) & 1u)) x[i] = -INFINITY;
           }
-        };
-        // P of this half and its sum; bit 14 or 30 of the result: some P >= 2
-        auto probabilities = [&](float(&x)[64]) {
+          if (move) {
+            float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+            float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+            M->top[s][half][m] = top;
+            // (a wait that gave up is known to all eight warps of the tile here)
+            if (tc::bar_or(bar, 256, !ok)) {
+              ok = false;
+              break;
+            }
+            top = fmaxf(top, M->top[s][half ^ 1][m]);
+            float f = 1.f;
+            if (req >= 0 && top > ref + 1.f) {
+              f = ref == -INFINITY ? 1.f : exp2f(ref - (top + kLift));
+              ref = top + kLift;
+              l *= f;
+            }
+            if (__any_sync(0xffffffffu, f != 1.f)) {
+              o_settled(j);
+#pragma unroll 1
+              for (int c = 0; c < D / 2; c += 16) {
+                float o[16];
+                tmem_ld16(to + c, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= f;
+                tmem_st16(to + c, o);
+              }
+            }
+          }
           // with nothing seen yet, any logit makes an infinite P
           const float r0 = ref == -INFINITY ? 1e30f : -ref;
           float2 sums[2] = {{0.f, 0.f}, {0.f, 0.f}};
@@ -549,51 +617,14 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             sums[i & 1] = tc::ffma2(y, make_float2(1.f, 1.f), sums[i & 1]);
           }
           sum = (sums[0].x + sums[1].x) + (sums[0].y + sums[1].y);
-          return any;
-        };
-        bool move = j == 0 || !ok;
-        if (!move) {
-          float x[64];
-          logits(x);
-          // (a thread without a row has whatever was in shared memory for q)
-          move = (probabilities(x) & 0x40004000u) && req >= 0;
+          // Both halves have read S before P goes over it.  (A thread without a
+          // row has whatever was in shared memory for q: it asks for nothing.)
+          const bool again =
+              tc::bar_or(bar, 256, !move && (((any & 0x40004000u) && req >= 0) || !ok));
+          if (!again) break;
+          move = true;
         }
-        if (tc::bar_or(bar, 256, move)) {
-          // some reference of the tile moves (or a wait gave up): largest logits
-          float x[64];
-          logits(x);
-          float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-          for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-          M->top[s][half][m] = top;
-          if (tc::bar_or(bar, 256, !ok)) {
-            ok = false;
-            break;
-          }
-          top = fmaxf(top, M->top[s][half ^ 1][m]);
-          if (req >= 0 && top > ref + 1.f) {
-            const float f = ref == -INFINITY ? 1.f : exp2f(ref - (top + kLift));
-            ref = top + kLift;
-            l *= f;
-            sum = f;
-          } else {
-            sum = 1.f;
-          }
-          if (__any_sync(0xffffffffu, sum != 1.f)) {
-            o_settled(j);
-            for (int c = 0; c < D / 2; c += 32) {
-              float o[32];
-              tc::tmem_ld32(to + c, o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= sum;
-              tc::tmem_st32(to + c, o);
-            }
-          }
-          logits(x);
-          probabilities(x);
-          tc::bar_sync(bar, 256);  // both halves have read S before P goes over it
-        }
+        if (!ok) break;
         l += sum;
         if (mixed) {
           // values that are not finite are zero in the product; the rows that
@@ -613,7 +644,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
 #pragma unroll 1
               for (uint32_t b = bad[k]; b; b &= b - 1) {
                 const int c = 32 * k + __ffs(b) - 1;
-                const bool sees = c - 64 * half >= c_lo && c - 64 * half < c_hi;
+                const bool sees = c + P.base >= lo && c + P.base < hi && rr >= P.r0 && rr < P.r1;
                 uint32_t raw;
                 asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
                              : "=r"(raw)
@@ -625,13 +656,14 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
                                              phys * a.v_page_stride + c * a.v_token_stride +
                                              kvh * a.v_head_stride) +
                                          half * (D / 2);
-                for (int d = 0; d < D / 2; d += 32) {
-                  float o[32];
-                  tc::tmem_ld32(to + d, o);
+#pragma unroll 1
+                for (int d = 0; d < D / 2; d += 16) {
+                  float o[16];
+                  tmem_ld16(to + d, o);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i)
+                  for (int i = 0; i < 16; ++i)
                     if (sees) o[i] += p * __bfloat162float(v[d + i]);
-                  tc::tmem_st32(to + d, o);
+                  tmem_st16(to + d, o);
                 }
               }
             tc::bar_sync(bar, 256);  // both halves have read S before P goes over it
@@ -664,7 +696,6 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       if (mine && half == 0)
         parts.ml[(long long)part * a.n_rows * a.n_heads + row] = make_float2(ref, l);
     } else {
-      const float s2 = mine && a.sink ? a.sink[h] * paged::kLog2e : -INFINITY;
       const paged::Joined J = paged::finish(ref, l, s2);
       scale = J.inv;
       if (mine && half == 0 && a.lse) a.lse[row] = J.lse;

@@ -114,7 +114,7 @@ __device__ __forceinline__ int item_rows(const csa_paged_attn_args &a, int t, in
   int n = 0;
   for (; t + n < end && a.row_req[t + n] == b; ++n) {
     int l, h;
-    paged::visible_range(a, b, a.row_pos[t + n], l, h);
+    paged::visible_range(a, a.kv_len[b], a.row_pos[t + n], l, h);
     if (l < h) {
       lo = min(lo, l);
       hi = max(hi, h);
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     if (tid < PAIRS) {
       const int r = tid / gt, h = tid % gt;
       int lo = 0, hi = 0;
-      if (r < n_rows && h < n_heads) paged::visible_range(a, b, a.row_pos[t + r], lo, hi);
+      if (r < n_rows && h < n_heads) paged::visible_range(a, a.kv_len[b], a.row_pos[t + r], lo, hi);
       M->lo[tid] = lo;
       M->hi[tid] = hi;
       M->ref[tid] = -INFINITY;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     int all_lo = 0, all_hi = 0x7FFFFFFF;
     for (int r = 0; r < n_rows; ++r) {
       int lo, hi;
-      paged::visible_range(a, b, a.row_pos[t + r], lo, hi);
+      paged::visible_range(a, a.kv_len[b], a.row_pos[t + r], lo, hi);
       all_lo = max(all_lo, lo);
       all_hi = min(all_hi, max(lo, hi));
     }

@@ -12,14 +12,13 @@ namespace paged {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Positions [lo, hi) of request b that a row at position p sees.
-__device__ __forceinline__ void visible_range(const csa_paged_attn_args &a, int b, int p, int &lo,
-                                              int &hi) {
-  const long long cap = (long long)a.max_blocks * kBlock;
-  const int len = (int)min((long long)a.kv_len[b], min(cap, 0x7FFFFFFFll));
+// Positions [lo, hi) that a row at position p sees in a cache of kv_len.
+__device__ __forceinline__ void visible_range(const csa_paged_attn_args &a, int kv_len, int p,
+                                              int &lo, int &hi) {
+  const int len = min(kv_len, (int)min((long long)a.max_blocks * kBlock, 0x7FFFFFFFll));
   hi = a.causal && p < len ? p + 1 : len;
   const long long from = a.window > 0 ? (long long)p - a.window + 1 : 0;
-  lo = (int)max(0ll, min(from, 0x7FFFFFFFll));
+  lo = (int)max(0ll, from);
 }
 
 // The parts of split rows, merged by paged_merge_kernel: part s of row t and
