@@ -183,10 +183,19 @@ class _Call(B.PreparedCall):
         self.device = tensors[0].device
 
     def __call__(self, stream=None):
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
-                return super().__call__(stream)
-        return super().__call__(stream)
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"{self.fn_name}: the stream is on {stream.device}, the tensors on "
+                             f"{self.device}")
+        index = self.device.index
+        if torch.cuda.current_device() != index:
+            with torch.cuda.device(index):
+                return self(stream)
+        # (the raw handle: a Stream object costs more than the launch)
+        raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+        st = self.fn(*self._refs, raw)
+        if st != B.CSA_OK:
+            raise B.CsaError(self.fn_name, st)
+        return self.workspace
 
 
 def _launch(fn_name, a, tensors, stream, prepare, workspace=None, sized=False):

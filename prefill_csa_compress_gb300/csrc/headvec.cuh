@@ -1,9 +1,11 @@
-// One head's vector of a row: the RMS norm over its channels and the rotation
-// of part of them, held in registers by a group of lanes.  A vector of
-// head_dim = 8 n channels is n chunks of 16 bytes; lane l of its group of L
-// lanes holds chunks l, l + L, ... (C of them).
+// Heads of one row: the RMS norm over each head's channels and the rotation of
+// part of them, held in registers by groups of lanes.  A head of 8 n channels
+// is n chunks of 16 bytes; lane l of its group of L lanes holds chunks l, l + L,
+// ... (C of them).
 //   y = x gamma / sqrt(mean(x^2) + eps), then pairs turned at the position.
-// FP32 throughout; the caller rounds once.
+// FP32 throughout; the caller rounds once.  A warp takes U heads of 32 / L groups
+// of one row at a time: the row's rotation and gamma are loaded once for all of
+// them, and all heads' loads are in flight together.
 #pragma once
 
 #include <type_traits>
@@ -15,7 +17,7 @@ namespace headvec {
 
 struct Rope {
   const float *cos, *sin;  // [cap, dim / 2], or null: no rotation
-  int start, dim, cap, half_layout;
+  int start, dim, cap;
 };
 
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
@@ -55,100 +57,165 @@ __device__ __forceinline__ int table_row(const Rope &R, int pos, uint32_t *statu
   return pos;
 }
 
-// The normed, rotated vector at `src` (n_chunks chunks) into y.  Every lane of
-// the warp calls it with the same `reduce`; `on` is false for lanes without a
-// vector, and `norm` (which needs `reduce`) may differ between the warp's
-// vectors.  `trow` as table_row gives it.  All loads of the vector happen before it returns and
-// before any lane of the warp leaves it, so the caller may overwrite `src`.
-template <int L, int C>
-__device__ __forceinline__ void load(const uint16_t *src, int n_chunks, bool on, bool reduce,
-                                     bool norm, float eps, const uint16_t *gamma, const Rope &R, int trow,
-                                     float (&y)[C][8]) {
-  const int l = threadIdx.x & (L - 1);
-  const int c_lo = R.start >> 3, c_hi = (R.start + R.dim) >> 3, hop = R.dim >> 4;
-  uint4 raw[C], mate[C];
+// Heads first + u (32 / L) + lane / L, u < U, of a row of `n` heads of 8 n_chunks
+// channels, one after the other.  Every lane of the warp takes part in both
+// steps: load() asks for the row's channels, which needs no position, so that the
+// position, its table row and its page are on their way at the same time; finish()
+// norms and rotates head after head and hands each chunk to store(head, chunk,
+// on, y).  Everything is read before store() runs, so that it may overwrite its
+// own head.
+template <int L, int C, int U, bool HALF>
+struct Heads {
+  static constexpr int PAIRS = HALF ? 8 : 4;  // angles of a chunk
+  // A half-layout chunk's partner: with one chunk a lane, the partner's lane has
+  // it; above 256 channels it comes along.
+  static constexpr bool FETCH = HALF && C > 1;
+  uint4 raw[U][C], mate[FETCH ? U : 1][C];
+  uint4 g[C], gm[HALF ? C : 1];               // gamma of both
+  int h0, n, n_chunks, c_lo, c_hi, hop;
+
+  __device__ __forceinline__ bool turned(int c) const { return c >= c_lo && c < c_hi; }
+  __device__ __forceinline__ int partner(int c) const { return c - c_lo < hop ? c + hop : c - hop; }
+
+  __device__ __forceinline__ void load(const uint16_t *src, int first, int n_heads, int chunks,
+                                       const uint16_t *gamma, const Rope &R) {
+    const int lane = threadIdx.x & 31, l = lane & (L - 1);
+    h0 = first + lane / L;
+    n = n_heads;
+    n_chunks = chunks;
+    c_lo = R.cos ? R.start >> 3 : 0;
+    c_hi = R.cos ? (R.start + R.dim) >> 3 : 0;
+    hop = R.dim >> 4;
+    const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
 #pragma unroll
-  for (int j = 0; j < C; ++j) {
-    const int c = l + L * j;
-    raw[j] = mate[j] = make_uint4(0, 0, 0, 0);
-    if (on && c < n_chunks) {
-      raw[j] = ld16(src + 8 * c);
-      if (R.half_layout && trow >= 0 && c >= c_lo && c < c_hi)
-        mate[j] = ld16(src + 8 * (c - c_lo < hop ? c + hop : c - hop));
-    }
-  }
-  float r = 1.f;
-  if (reduce) {
-    float ss = 0.f;
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int c = l + L * j, h = h0 + u * (32 / L);
+        const uint16_t *head = src + (long long)h * 8 * n_chunks;
+        raw[u][j] = make_uint4(0, 0, 0, 0);
+        if (h < n && c < n_chunks) raw[u][j] = ld16(head + 8 * c);
+        if constexpr (FETCH) {
+          mate[u][j] = make_uint4(0, 0, 0, 0);
+          if (h < n && c < n_chunks && turned(c)) mate[u][j] = ld16(head + 8 * partner(c));
+        }
+      }
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      float x[8];
-      unpack8(raw[j], x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-    }
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    r = rsqrtf(ss / (float)(8 * n_chunks) + eps);
-  }
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < C; ++j) {
-    const int c = l + L * j;
-    unpack8(raw[j], y[j]);
-    if (!on || c >= n_chunks) continue;
-    if (norm) {
-      float g[8];
-      if (gamma) unpack8(ld16(gamma + 8 * c), g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[j][i] *= gamma ? r * g[i] : r;
-    }
-    if (trow < 0 || c < c_lo || c >= c_hi) continue;
-    const long long t = (long long)trow * (R.dim >> 1);
-    if (!R.half_layout) {
-      float cs[4], sn[4];
-      ld4f(R.cos + t + 4 * (c - c_lo), cs);
-      ld4f(R.sin + t + 4 * (c - c_lo), sn);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = y[j][2 * i], b = y[j][2 * i + 1];
-        y[j][2 * i] = a * cs[i] - b * sn[i];
-        y[j][2 * i + 1] = a * sn[i] + b * cs[i];
-      }
-    } else {
-      const bool first = c - c_lo < hop;
-      const int i0 = 8 * (first ? c - c_lo : c - c_lo - hop);
-      float cs[8], sn[8], m[8];
-      ld4f(R.cos + t + i0, cs);
-      ld4f(R.cos + t + i0 + 4, cs + 4);
-      ld4f(R.sin + t + i0, sn);
-      ld4f(R.sin + t + i0 + 4, sn + 4);
-      unpack8(mate[j], m);
-      if (norm) {
-        float g[8];
-        if (gamma) unpack8(ld16(gamma + 8 * (first ? c + hop : c - hop)), g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] *= gamma ? r * g[i] : r;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        y[j][i] = first ? y[j][i] * cs[i] - m[i] * sn[i] : m[i] * sn[i] + y[j][i] * cs[i];
+      const int c = l + L * j;
+      g[j] = gamma && c < n_chunks ? ld16(gamma + 8 * c) : ones;
+      if constexpr (HALF)
+        gm[j] = gamma && c < n_chunks && turned(c) ? ld16(gamma + 8 * partner(c)) : ones;
     }
   }
-}
 
-// Lanes and chunks of a head of `dim` channels: f(L, C) as constants.
-template <typename F>
-auto dispatch(int dim, F &&f) {
+  // `trow` as table_row gives it; `norm` alike in all lanes.
+  template <typename Store>
+  __device__ __forceinline__ void finish(bool norm, float eps, const Rope &R, int trow,
+                                         Store &&store) {
+    const int l = threadIdx.x & (L - 1);
+    float cs[C][PAIRS], sn[C][PAIRS], sign[C];
+    bool rot[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int c = l + L * j;
+      rot[j] = trow >= 0 && c < n_chunks && turned(c);
+      sign[j] = HALF && c - c_lo < hop ? -1.f : 1.f;
+      if (rot[j]) {
+        const long long t = (long long)trow * (R.dim >> 1) +
+                            PAIRS * ((HALF ? min(c, partner(c)) : c) - c_lo);
+#pragma unroll
+        for (int i = 0; i < PAIRS; i += 4) {
+          ld4f(R.cos + t + i, cs[j] + i);
+          ld4f(R.sin + t + i, sn[j] + i);
+        }
+      }
+    }
+    __syncwarp();
+    const float inv_n = 1.f / (float)(8 * n_chunks);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * (32 / L);
+      float r = 1.f;
+      if (norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          float x[8];
+          unpack8(raw[u][j], x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        }
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        r = rsqrtf(fmaf(ss, inv_n, eps));
+      }
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        uint4 other = make_uint4(0, 0, 0, 0);
+        if constexpr (HALF && !FETCH) {
+          const int from = ((threadIdx.x & 31) & ~(L - 1)) + (turned(l) ? partner(l) : l);
+          other.x = __shfl_sync(0xffffffffu, raw[u][j].x, from);
+          other.y = __shfl_sync(0xffffffffu, raw[u][j].y, from);
+          other.z = __shfl_sync(0xffffffffu, raw[u][j].z, from);
+          other.w = __shfl_sync(0xffffffffu, raw[u][j].w, from);
+        }
+        float y[8], w[8];
+        unpack8(raw[u][j], y);
+        unpack8(g[j], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= r * w[i];
+        if (rot[j]) {
+          if constexpr (!HALF) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = y[2 * i], b = y[2 * i + 1];
+              y[2 * i] = a * cs[j][i] - b * sn[j][i];
+              y[2 * i + 1] = a * sn[j][i] + b * cs[j][i];
+            }
+          } else {
+            float m[8];
+            unpack8(FETCH ? mate[FETCH ? u : 0][j] : other, m);
+            unpack8(gm[j], w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              y[i] = y[i] * cs[j][i] + sign[j] * (m[i] * (r * w[i])) * sn[j][i];
+          }
+        }
+        // every lane calls it (it may exchange values with its neighbours)
+        store(h, l + L * j, h < n && l + L * j < n_chunks, y);
+      }
+    }
+  }
+};
+
+// Groups' lanes, chunks a lane and heads at once for n_heads heads of `dim`
+// channels, and the layout: f(L, C, U, HALF) as constants.  Four heads at once
+// where a row has them (two of the half layout above 256 channels, for the
+// registers), else one.
+template <int L, int C, typename F>
+auto dispatch_heads(int n_heads, bool half, F &&f) {
   using std::integral_constant;
+  constexpr integral_constant<int, L> l{};
+  constexpr integral_constant<int, C> c{};
+  constexpr integral_constant<int, 1> one{};
+  if (half) {
+    constexpr integral_constant<int, (C == 1 ? 4 : 2)> many{};
+    return n_heads > 32 / L ? f(l, c, many, std::true_type()) : f(l, c, one, std::true_type());
+  }
+  constexpr integral_constant<int, 4> many{};
+  return n_heads > 32 / L ? f(l, c, many, std::false_type()) : f(l, c, one, std::false_type());
+}
+template <typename F>
+auto dispatch(int dim, int n_heads, bool half, F &&f) {
   const int n = dim / 8;
-  if (n <= 1) return f(integral_constant<int, 1>(), integral_constant<int, 1>());
-  if (n <= 2) return f(integral_constant<int, 2>(), integral_constant<int, 1>());
-  if (n <= 4) return f(integral_constant<int, 4>(), integral_constant<int, 1>());
-  if (n <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
-  if (n <= 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
-  if (n <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
-  return f(integral_constant<int, 32>(), integral_constant<int, 2>());
+  if (n <= 1) return dispatch_heads<1, 1>(n_heads, half, f);
+  if (n <= 2) return dispatch_heads<2, 1>(n_heads, half, f);
+  if (n <= 4) return dispatch_heads<4, 1>(n_heads, half, f);
+  if (n <= 8) return dispatch_heads<8, 1>(n_heads, half, f);
+  if (n <= 16) return dispatch_heads<16, 1>(n_heads, half, f);
+  if (n <= 32) return dispatch_heads<32, 1>(n_heads, half, f);
+  return dispatch_heads<32, 2>(n_heads, half, f);
 }
 
 }  // namespace headvec
