@@ -15,42 +15,46 @@ using paged::Parts;
 
 constexpr int PM_THREADS = 256;
 
-// One warp per (row, head): out and lse from the row's parts.  Part weights
-// 2^(m_s - m) with m the largest reference; their sums in FP32, in part order.
+// D / 4 threads per (row, head), four channels each: out and lse from the row's
+// parts.  Part weights 2^(m_s - m) with m the largest reference; the sums in FP32,
+// in part order.  Latency bounds it, so four parts are in flight at a time.
 template <int D>
 __global__ void __launch_bounds__(PM_THREADS)
     paged_merge_kernel(csa_paged_attn_args a, Parts parts) {
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
+  constexpr int PER = D / 4;
   const long long rows = (long long)a.n_rows * a.n_heads;
-  const long long r = (long long)blockIdx.x * (PM_THREADS / 32) + (threadIdx.x >> 5);
+  const long long r = (long long)blockIdx.x * (PM_THREADS / PER) + threadIdx.x / PER;
   if (r >= rows) return;
+  const int c = threadIdx.x % PER;
   const int t = (int)(r / a.n_heads), h = (int)(r - (long long)t * a.n_heads);
   const int b = a.row_req[t];
   if (b < 0 || b >= a.n_req) return;
   float m = -INFINITY;
-  for (int s = lane; s < parts.n; s += 32) m = fmaxf(m, parts.ml[s * rows + r].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float acc[E] = {}, l = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < parts.n; ++s) m = fmaxf(m, parts.ml[s * rows + r].x);
+  float acc[4] = {}, l = 0.f;
+#pragma unroll 4
   for (int s = 0; s < parts.n; ++s) {
     const float2 ml = parts.ml[s * rows + r];
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing was seen there
+    const float4 o = reinterpret_cast<const float4 *>(parts.o + (s * rows + r) * D)[c];
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing was seen there (o is not set)
     const float w = ml.x == -INFINITY ? ml.y : exp2f(ml.x - m);  // (l is NaN there)
     l += w * ml.y;
-    const float *o = parts.o + (s * rows + r) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += w * o[e];
+    acc[0] += w * o.x, acc[1] += w * o.y, acc[2] += w * o.z, acc[3] += w * o.w;
   }
   const float s2 = a.sink ? a.sink[h] * paged::kLog2e : -INFINITY;
   const paged::Joined J = paged::finish(m, l, s2);
   const bool zero = m == -INFINITY && l == 0.f;
-  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + r * D + lane * E;
+  __nv_bfloat162 out[2];
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = __float2bfloat16_rn(zero ? 0.f : acc[e] * J.inv);
-  if (a.lse && lane == 0) a.lse[r] = J.lse;
+  for (int e = 0; e < 2; ++e)
+    out[e] = zero ? __floats2bfloat162_rn(0.f, 0.f)
+                  : __floats2bfloat162_rn(acc[2 * e] * J.inv, acc[2 * e + 1] * J.inv);
+  reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + r * D)[c] =
+      *reinterpret_cast<const uint2 *>(out);
+  if (a.lse && c == 0) a.lse[r] = J.lse;
 }
 
 int sm_count() {
@@ -156,7 +160,8 @@ cudaError_t launch_paged_attn(const csa_paged_attn_args &a, cudaStream_t s) {
   cudaError_t e = launch_paged_chunk(a, parts, sms, s);
   if (e != cudaSuccess || L.parts == 1) return e != cudaSuccess ? e : cudaGetLastError();
   const long long rows = (long long)a.n_rows * a.n_heads;
-  const dim3 grid((unsigned)((rows + PM_THREADS / 32 - 1) / (PM_THREADS / 32)));
+  const int per_block = PM_THREADS / (a.head_dim / 4);
+  const dim3 grid((unsigned)((rows + per_block - 1) / per_block));
   launch_begin(CSA_K_PAGED_MERGE, s);
   e = a.head_dim == 64
           ? launch_kernel(paged_merge_kernel<64>, grid, dim3(PM_THREADS), 0, s, 0, false, a, parts)
