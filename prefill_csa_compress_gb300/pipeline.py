@@ -23,6 +23,7 @@ from __future__ import annotations
 import torch
 
 from . import _binding as B
+from . import _paged as P
 
 
 class CsaStep:
@@ -40,6 +41,9 @@ class CsaStep:
     ``cand`` (level one), and ``cand_in`` restricts it to given candidate
     blocks (reindex).  ``overlap`` makes both compressors pool each entry
     over the previous group's tokens too (the overlapping ratio-4 layout).
+    With ``win_raw`` (bf16 [rows, 512]) in ``t`` the step first publishes the
+    rows' window entries in kv_pool, rotated at their positions and, with
+    ``win_gamma`` (bf16 [512]), normed; without it kv_pool already holds them.
     """
 
     def __init__(self, t: dict, ratio: int, topk: int, prefill: bool = False,
@@ -108,6 +112,16 @@ class CsaStep:
                         idx_scale_pool=None)
         return main, keys
 
+    def _window_kw(self):
+        t = self.t
+        return dict(k=t["win_raw"].unsqueeze(1), row_req=t["row_req"], row_pos=t["row_pos"],
+                    block_table=t["kv_table"], k_pool=t["kv_pool"], k_scale_pool=t.get("kv_scale"),
+                    norm="win_gamma" in t, k_gamma=t.get("win_gamma"), rope_cos=t["rope_cos"],
+                    rope_sin=t["rope_sin"], status=self.status)
+
+    def publish_window(self, stream=None):
+        P.csa_kv_append(stream=stream, **self._window_kw())
+
     def compress(self, stream=None):
         main, keys = self._compress_kw()
         if self.dense:
@@ -156,6 +170,8 @@ class CsaStep:
         """Marshal the step's calls once (buffers must stay in place)."""
         t = self.t
         calls = []
+        if "win_raw" in t:
+            calls.append(P.csa_kv_append(prepare=True, **self._window_kw()))
         if self.do_compress:
             main, keys = self._compress_kw()
             calls.append(B.csa_compress(prepare=True, **main) if self.dense else
@@ -176,6 +192,8 @@ class CsaStep:
 
     def run(self, stream=None):
         if self._prepared is None:
+            if "win_raw" in self.t:
+                self.publish_window(stream)
             if self.do_compress:
                 self.compress(stream)
             if not self.dense:
@@ -241,6 +259,74 @@ class StepChain:
         for s in self.steps:
             if s._prepared is None:
                 s.prepare()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, capture_error_mode="thread_local"):
+            self.run()
+        self._graph = g
+        return self
+
+    def replay(self):
+        self._graph.replay()
+
+    def drop_graph(self):
+        self._graph = None
+
+
+class PagedAttnStep:
+    """One step of a layer whose paged cache holds keys and values of grouped
+    query heads: the norms of the query heads with their rotation, the rows'
+    keys (normed and rotated) and values into the caches, then attention.
+
+    ``t`` maps names to device tensors: q [rows, heads, dim], k and v [rows,
+    kv_heads, dim] (views of one projection, say), row_req, row_pos, kv_len (the
+    step's rows included), k_pool, v_pool, kv_table, rope_cos, rope_sin, and
+    optionally q_gamma, k_gamma and sink.  It owns the normed queries, out, lse
+    and the attention's workspace; like ``CsaStep`` it computes nothing itself,
+    issues its calls on one stream, and takes its place in a ``StepChain``.
+    """
+
+    before_attention = None
+
+    def __init__(self, t: dict, causal: bool = True, window: int = 0, rope_layout: str = "adjacent",
+                 eps: float = 1e-6, status_buf=None):
+        self.t = t
+        q = t["q"]
+        self.q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        self.out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        self.lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
+        self.status = status_buf if status_buf is not None else torch.zeros(
+            1, dtype=torch.int32, device=q.device)
+        rope = dict(rope_cos=t["rope_cos"], rope_sin=t["rope_sin"], rope_layout=rope_layout, eps=eps,
+                    status=self.status)
+        self._calls = (
+            (P.csa_qk_norm_rope, dict(q=q, q_out=self.q, row_pos=t["row_pos"], row_req=t["row_req"],
+                                      q_gamma=t.get("q_gamma"), **rope)),
+            (P.csa_kv_append, dict(k=t["k"], v=t["v"], row_req=t["row_req"], row_pos=t["row_pos"],
+                                   block_table=t["kv_table"], k_pool=t["k_pool"],
+                                   v_pool=t["v_pool"], norm=True, k_gamma=t.get("k_gamma"), **rope)),
+            (P.csa_paged_attn, dict(q=self.q, row_req=t["row_req"], row_pos=t["row_pos"],
+                                    k_pool=t["k_pool"], v_pool=t["v_pool"],
+                                    block_table=t["kv_table"], kv_len=t["kv_len"], out=self.out,
+                                    lse=self.lse, sink=t.get("sink"), causal=causal,
+                                    window=window, status=self.status)))
+        self._prepared = None
+        self._graph = None
+
+    def prepare(self):
+        """Marshal the step's calls once (buffers must stay in place)."""
+        self._prepared = [fn(prepare=True, **kw) for fn, kw in self._calls]
+        return self
+
+    def run(self, stream=None):
+        if self._prepared is None:
+            self.prepare()
+        for c in self._prepared:
+            c(stream)
+
+    def capture(self):
+        """Record one step into a CUDA graph.  Call after a warm-up ``run``."""
+        if self._prepared is None:
+            self.prepare()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, capture_error_mode="thread_local"):
             self.run()

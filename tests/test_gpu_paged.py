@@ -691,3 +691,108 @@ def test_a_layer_from_prompt_to_tokens(dim, layout, window):
     logit = 2 * H8 * np.abs(q64).max() * np.abs(kk).max() * dim ** 0.5
     assert (np.abs(_np(out) - o) <= H8 * np.abs(o) + (H8 + 2 * logit) * spread + 1e-6).all()
     assert np.abs(_np(out) - o).mean() <= 2 * H8 * np.abs(o).mean() + 1e-3
+
+
+@pytest.mark.parametrize("lowbit", [False, True])
+def test_csa_step_publishes_its_window(lowbit):
+    """A CSA step that publishes its own window rows: the same result as the
+    step on a pool that already holds them, run eagerly, prepared and captured."""
+    from prefill_csa_compress_gb300.pipeline import CsaStep
+    from workloads import make_workload, spec_for
+
+    spec = spec_for("lowbit_decode" if lowbit else "serving_decode", seed=77)
+    t = make_workload(spec).to(DEV)
+    n = t["row_req"].shape[0]
+    t["win_raw"] = _bf(np.random.default_rng(1), n, 512)
+    t["win_gamma"] = _bf(np.random.default_rng(2), 512)
+    names = ["kv_pool", "kv_scale"] if lowbit else ["kv_pool"]
+    before = {k: t[k].clone() for k in names}
+    step = CsaStep(t, spec.ratio, spec.topk)
+    step.publish_window()
+    torch.cuda.synchronize()
+    after = {k: t[k].clone() for k in names}
+    changed = (after["kv_pool"] != before["kv_pool"]).flatten(2).any(-1)
+    assert int(changed.sum()) == n and int(step.status.item()) == 0
+    plain = CsaStep({k: v for k, v in t.items() if not k.startswith("win_")}, spec.ratio, spec.topk)
+    plain.run()
+    torch.cuda.synchronize()
+    want = plain.out.clone(), plain.lse.clone()
+    graph = []
+
+    def captured():
+        if not graph:
+            step.capture()
+            graph.append(1)
+        step.replay()
+
+    for run in (step.run, lambda: step.prepare().run(), captured):
+        for k in names:
+            t[k].copy_(before[k])
+        step.out.zero_()
+        run()
+        torch.cuda.synchronize()
+        assert int(step.status.item()) == 0
+        assert all(torch.equal(t[k], after[k]) for k in names)
+        assert torch.equal(step.out, want[0]) and torch.equal(step.lse, want[1])
+
+
+def test_paged_attn_step():
+    """The step object: a prompt eagerly, then tokens through one captured
+    graph whose inputs change in place, against the calls one by one; and as
+    a layer of a chain with another."""
+    from prefill_csa_compress_gb300.pipeline import PagedAttnStep, StepChain
+
+    rng = np.random.default_rng(9)
+    hq, hk, dim, first = 8, 2, 128, 300
+    cos, sin = torch.empty((512, 64), device=DEV), torch.empty((512, 64), device=DEV)
+    csa.csa_rope_table(cos=cos, sin=sin)
+    table = _i32([[1, 4, 0]])
+    gq, gk = _bf(rng, dim), _bf(rng, dim)
+    sink = torch.zeros(hq, device=DEV)
+
+    def tensors(n, pos, pools):
+        qkv = _bf(rng, n, hq + 2 * hk, dim)
+        return dict(q=qkv[:, :hq], k=qkv[:, hq:hq + hk], v=qkv[:, hq + hk:], row_req=_i32([0] * n),
+                    row_pos=_i32(np.arange(pos, pos + n)), kv_len=_i32([pos + n]), k_pool=pools[0], v_pool=pools[1],
+                    kv_table=table, rope_cos=cos, rope_sin=sin, q_gamma=gq, k_gamma=gk, sink=sink, qkv=qkv)
+
+    def by_hand(t, window):
+        q = torch.empty(t["q"].shape, dtype=torch.bfloat16, device=DEV)
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device=DEV)
+        rope = dict(rope_cos=cos, rope_sin=sin, rope_layout="half")
+        csa.csa_qk_norm_rope(q=t["q"], q_out=q, row_pos=t["row_pos"], q_gamma=gq, **rope)
+        csa.csa_kv_append(k=t["k"], v=t["v"], row_req=t["row_req"], row_pos=t["row_pos"], block_table=table,
+                          k_pool=t["k_pool"], v_pool=t["v_pool"], norm=True, k_gamma=gk, **rope)
+        csa.csa_paged_attn(q=q, row_req=t["row_req"], row_pos=t["row_pos"], k_pool=t["k_pool"], v_pool=t["v_pool"],
+                           block_table=table, kv_len=t["kv_len"], out=out, lse=lse, sink=sink, window=window)
+        torch.cuda.synchronize()
+        return out, lse
+
+    pools = [torch.full((5, 128, hk, dim), NAN, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    mine = [p.clone() for p in pools]
+    t = tensors(first, 0, pools)
+    step = PagedAttnStep(t, rope_layout="half")
+    step.run()
+    want = by_hand({**t, "k_pool": mine[0], "v_pool": mine[1]}, 0)
+    assert torch.equal(step.out, want[0]) and torch.equal(step.lse, want[1])
+    t = tensors(1, first, pools)
+    other = [p.clone() for p in pools]
+    chain = StepChain([PagedAttnStep(t, rope_layout="half"),
+                       PagedAttnStep({**t, "k_pool": other[0], "v_pool": other[1]}, rope_layout="half", window=128)])
+    chain.run()
+    chain.capture()
+    for i in range(3):
+        t["qkv"].copy_(_bf(rng, 1, hq + 2 * hk, dim))
+        t["row_pos"].fill_(first + i)
+        t["kv_len"].fill_(first + i + 1)
+        chain.replay()
+        torch.cuda.synchronize()
+        want = by_hand({**t, "k_pool": mine[0], "v_pool": mine[1]}, 0)
+        assert torch.equal(chain.steps[0].out, want[0]) and torch.equal(chain.steps[0].lse, want[1])
+        if i == 0:
+            windowed = [p.clone() for p in other]
+        want = by_hand({**t, "k_pool": windowed[0], "v_pool": windowed[1]}, 128)
+        assert torch.equal(chain.out, want[0]) and torch.equal(chain.lse, want[1])
+    for p, q in zip(pools, mine):
+        assert torch.equal(p.view(torch.int16), q.view(torch.int16))
+    assert int(chain.status.item()) == 0
