@@ -91,14 +91,20 @@ bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims
                    CUDA_SUCCESS;
 }
 
-// Few rows per request: the decode kernel.  (Rows per request as the caller's
-// block table has requests; results do not depend on the choice but for
-// rounding.)
+// The decode kernel or the chunk kernel.  The decode kernel reads a request's
+// pages once for every item of 16 (row, head) pairs of a key/value head (32 from 17
+// heads on), the chunk kernel once for up to 256 pairs, but works through the
+// requests of a CTA's rows one after the other.  With the average rows of a
+// request: up to two items, decode (8 requests of 8 rows of 4 heads over 1000
+// positions 21 us against 40, 64 requests of 1 row 55 against 239); up to four
+// where several requests have few pages each (8 x 16 rows over 100 positions 17
+// against 24, over 8000 positions 167 against 87); else chunks (8 x 32 rows, 1000
+// positions 56 against 27).  Results do not depend on it but for rounding.
 bool use_decode(const csa_paged_attn_args &a) {
   if (a.mode == CSA_MODE_PREFILL || a.n_rows > paged::kDecodeRows) return false;
   if (a.mode == CSA_MODE_DECODE) return true;
-  const int g = a.n_heads / a.n_kv_heads, per = (a.n_rows + a.n_req - 1) / a.n_req;
-  return g * per <= 16;
+  const int per = (a.n_rows + a.n_req - 1) / a.n_req, items = paged_decode_items(a, per);
+  return items <= 2 || (items <= 4 && a.n_req > 1 && a.max_blocks <= 4);
 }
 
 struct Layout {

@@ -810,6 +810,10 @@ int paged_chunk_parts(const csa_paged_attn_args &a, int sms) {
     const long long seen = ((long long)a.window + rows + kBlock - 1) / kBlock + 1;
     pages = pages < seen ? pages : seen;
   }
+  // the requests that a CTA's rows may belong to, each with pages of its own
+  const long long per = (a.n_rows + a.n_req - 1) / a.n_req;
+  const long long runs = per >= rows ? 1 : (rows + per - 1) / (per > 0 ? per : 1);
+  pages *= runs < a.n_req ? runs : a.n_req;
   int best = 1;
   double cost = 1e30;
   for (int p = 1; p <= 64 && p <= pages; ++p) {

@@ -642,6 +642,11 @@ int pair_tiles(const csa_paged_attn_args &a) {
 
 }  // namespace
 
+int paged_decode_items(const csa_paged_attn_args &a, int rows) {
+  const int pairs = 16 * pair_tiles(a), g = a.n_heads / a.n_kv_heads;
+  return g < pairs ? (rows + pairs / g - 1) / (pairs / g) : rows * ((g + pairs - 1) / pairs);
+}
+
 size_t paged_decode_workspace(const csa_paged_attn_args &a, int sms) {
   const int pairs = 16 * pair_tiles(a);
   const int g = a.n_heads / a.n_kv_heads, gt = g < pairs ? g : pairs;

@@ -88,6 +88,7 @@ cudaError_t launch_paged_chunk(const csa_paged_attn_args &a, const paged::Parts 
                                cudaStream_t s);
 
 // Few rows per request: a stream of pages (k_paged_decode.cu).
+int paged_decode_items(const csa_paged_attn_args &a, int rows);  // per request and kv head
 size_t paged_decode_workspace(const csa_paged_attn_args &a, int sms);
 cudaError_t launch_paged_decode(const csa_paged_attn_args &a, int sms, cudaStream_t s);
 
