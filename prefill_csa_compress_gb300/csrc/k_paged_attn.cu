@@ -15,34 +15,54 @@ using paged::Parts;
 
 constexpr int PM_THREADS = 256;
 
-// D / 4 threads per (row, head), four channels each: out and lse from the row's
-// parts.  Part weights 2^(m_s - m) with m the largest reference; the sums in FP32,
-// in part order.  Latency bounds it, so four parts are in flight at a time.
-template <int D>
+// W groups of D / 4 threads per (row, head), four channels a thread: out and lse
+// from the row's parts.  Part weights 2^(m_s - m) with m the largest reference; sums
+// in FP32, group w adding parts w, w + W, ... and the groups added in order.
+// Latency bounds it: four parts of a group are in flight at a time, and where a row
+// has many parts eight groups share them (63 parts of 8 rows of 16 heads: the whole
+// call 30.1 -> 19.6 us).
+template <int D, int W>
 __global__ void __launch_bounds__(PM_THREADS)
     paged_merge_kernel(csa_paged_attn_args a, Parts parts) {
   tc::griddep_wait();
   tc::griddep_launch_dependents();
-  constexpr int PER = D / 4;
+  constexpr int PER = D / 4, ROWS = PM_THREADS / (PER * W);
+  __shared__ float sums[W > 1 ? W * ROWS : 1][PER][5];
   const long long rows = (long long)a.n_rows * a.n_heads;
-  const long long r = (long long)blockIdx.x * (PM_THREADS / PER) + threadIdx.x / PER;
-  if (r >= rows) return;
-  const int c = threadIdx.x % PER;
-  const int t = (int)(r / a.n_heads), h = (int)(r - (long long)t * a.n_heads);
-  const int b = a.row_req[t];
-  if (b < 0 || b >= a.n_req) return;
-  float m = -INFINITY;
+  const int c = threadIdx.x % PER, w = threadIdx.x / PER % W, i = threadIdx.x / (PER * W);
+  const long long r = (long long)blockIdx.x * ROWS + i;
+  const int t = r < rows ? (int)(r / a.n_heads) : 0;
+  const int h = (int)(r - (long long)t * a.n_heads);
+  const int b = r < rows ? a.row_req[t] : -1;
+  const bool on = b >= 0 && b < a.n_req;
+  if (W == 1 && !on) return;
+  float m = -INFINITY, acc[4] = {}, l = 0.f;
+  if (on) {
+#pragma unroll 8
+    for (int s = 0; s < parts.n; ++s) m = fmaxf(m, parts.ml[s * rows + r].x);
 #pragma unroll 4
-  for (int s = 0; s < parts.n; ++s) m = fmaxf(m, parts.ml[s * rows + r].x);
-  float acc[4] = {}, l = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < parts.n; ++s) {
-    const float2 ml = parts.ml[s * rows + r];
-    const float4 o = reinterpret_cast<const float4 *>(parts.o + (s * rows + r) * D)[c];
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing was seen there (o is not set)
-    const float w = ml.x == -INFINITY ? ml.y : exp2f(ml.x - m);  // (l is NaN there)
-    l += w * ml.y;
-    acc[0] += w * o.x, acc[1] += w * o.y, acc[2] += w * o.z, acc[3] += w * o.w;
+    for (int s = w; s < parts.n; s += W) {
+      const float2 ml = parts.ml[s * rows + r];
+      const float4 o = reinterpret_cast<const float4 *>(parts.o + (s * rows + r) * D)[c];
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing was seen there (o is not set)
+      const float x = ml.x == -INFINITY ? ml.y : exp2f(ml.x - m);  // (l is NaN there)
+      l += x * ml.y;
+      acc[0] += x * o.x, acc[1] += x * o.y, acc[2] += x * o.z, acc[3] += x * o.w;
+    }
+  }
+  if constexpr (W > 1) {
+    float *mine = sums[w * ROWS + i][c];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mine[e] = acc[e];
+    mine[4] = l;
+    __syncthreads();
+    if (w != 0 || !on) return;
+    for (int k = 1; k < W; ++k) {
+      const float *other = sums[k * ROWS + i][c];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] += other[e];
+      l += other[4];
+    }
   }
   const float s2 = a.sink ? a.sink[h] * paged::kLog2e : -INFINITY;
   const paged::Joined J = paged::finish(m, l, s2);
@@ -55,6 +75,14 @@ __global__ void __launch_bounds__(PM_THREADS)
   reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + r * D)[c] =
       *reinterpret_cast<const uint2 *>(out);
   if (a.lse && c == 0) a.lse[r] = J.lse;
+}
+
+template <int D, int W>
+cudaError_t launch_merge(const csa_paged_attn_args &a, const Parts &parts, cudaStream_t s) {
+  constexpr int per_block = PM_THREADS / (D / 4 * W);
+  const long long rows = (long long)a.n_rows * a.n_heads;
+  const dim3 grid((unsigned)((rows + per_block - 1) / per_block));
+  return launch_kernel(paged_merge_kernel<D, W>, grid, dim3(PM_THREADS), 0, s, 0, false, a, parts);
 }
 
 int sm_count() {
@@ -165,13 +193,12 @@ cudaError_t launch_paged_attn(const csa_paged_attn_args &a, cudaStream_t s) {
   const Parts parts{reinterpret_cast<float *>(ws), reinterpret_cast<float2 *>(ws + L.ml), L.parts};
   cudaError_t e = launch_paged_chunk(a, parts, sms, s);
   if (e != cudaSuccess || L.parts == 1) return e != cudaSuccess ? e : cudaGetLastError();
-  const long long rows = (long long)a.n_rows * a.n_heads;
-  const int per_block = PM_THREADS / (a.head_dim / 4);
-  const dim3 grid((unsigned)((rows + per_block - 1) / per_block));
   launch_begin(CSA_K_PAGED_MERGE, s);
-  e = a.head_dim == 64
-          ? launch_kernel(paged_merge_kernel<64>, grid, dim3(PM_THREADS), 0, s, 0, false, a, parts)
-          : launch_kernel(paged_merge_kernel<128>, grid, dim3(PM_THREADS), 0, s, 0, false, a, parts);
+  const bool many = L.parts >= 8;
+  if (a.head_dim == 64)
+    e = many ? launch_merge<64, 8>(a, parts, s) : launch_merge<64, 1>(a, parts, s);
+  else
+    e = many ? launch_merge<128, 8>(a, parts, s) : launch_merge<128, 1>(a, parts, s);
   launch_end(CSA_K_PAGED_MERGE, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

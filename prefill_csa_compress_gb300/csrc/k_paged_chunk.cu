@@ -800,8 +800,12 @@ cudaError_t launch(const csa_paged_attn_args &a, const Parts &parts, cudaStream_
 
 }  // namespace
 
-// Parts that a tile's pages are split into: as many as shorten the longest of
-// the waves of CTAs (each page one unit, a CTA's fixed cost about four).
+// Parts that a tile's pages are split into: as many as make waves x (pages of a
+// part + 4) + 2 + p / 16 smallest, in units of a page: a CTA's fixed cost is about
+// four pages, joining costs two and a sixteenth a part.  (2048 rows of 24 heads over
+// 12345 positions: 1, 2, 3, 4, 8 parts 242, 210, 203, 231, 267 us; 16 rows of 64 heads
+// over 32768: 8, 13, 19, 26 parts 58, 44, 44, 58 us; 8 rows of 16 over 8000: 8, 16, 32,
+// 64 parts 22, 17, 16, 19 us.  The rule takes 3, 19 and 32.)
 int paged_chunk_parts(const csa_paged_attn_args &a, int sms) {
   const int rows = 2 * (128 / (a.n_heads / a.n_kv_heads));
   const long long items = (long long)((a.n_rows + rows - 1) / rows) * a.n_kv_heads;
@@ -818,7 +822,7 @@ int paged_chunk_parts(const csa_paged_attn_args &a, int sms) {
   double cost = 1e30;
   for (int p = 1; p <= 64 && p <= pages; ++p) {
     const long long waves = (items * p + sms - 1) / sms;
-    const double c = (double)waves * ((double)((pages + p - 1) / p) + 4.0) + (p > 1 ? 2.0 : 0.0);
+    const double c = (double)waves * ((double)((pages + p - 1) / p) + 4.0) + (p > 1 ? 2.0 + p / 16.0 : 0.0);
     if (c < cost * 0.97) {
       cost = c;
       best = p;

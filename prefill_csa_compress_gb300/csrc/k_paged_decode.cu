@@ -49,8 +49,10 @@ struct Cfg {
 
 struct Plan {
   long long before[paged::kDecodeRows + 1];  // pages of all items of earlier rows
+  int req[paged::kDecodeRows];               // -1: padding, or no such request
   int pages[paged::kDecodeRows];             // of an item that starts at this row, or 0
   int first[paged::kDecodeRows];             // its first page
+  int lo[paged::kDecodeRows], hi[paged::kDecodeRows];  // positions that the row sees
 };
 
 template <int PAIRS>
@@ -103,26 +105,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The rows of an item that starts at row t: t .. up to the next multiple of
-// `rows`, as long as they are the same request's.  Returns their number and
-// the positions that at least one of them sees.
-__device__ __forceinline__ int item_rows(const csa_paged_attn_args &a, int t, int rows, int b,
-                                         int &lo, int &hi) {
-  const int end = min(a.n_rows, (t / rows + 1) * rows);
-  lo = 0x7FFFFFFF;
-  hi = 0;
-  int n = 0;
-  for (; t + n < end && a.row_req[t + n] == b; ++n) {
-    int l, h;
-    paged::visible_range(a, a.kv_len[b], a.row_pos[t + n], l, h);
-    if (l < h) {
-      lo = min(lo, l);
-      hi = max(hi, h);
-    }
-  }
-  return n;
-}
-
 template <int D, int MT>
 __global__ void __launch_bounds__(PD_THREADS, 1)
     paged_decode_kernel(csa_paged_attn_args a, DecodeParts parts,
@@ -143,14 +125,37 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
   const int gt = min(g, PAIRS), rows = PAIRS / gt;       // heads and rows of an item
   const int head_tiles = (g + gt - 1) / gt, subs = a.n_kv_heads * head_tiles;
 
-  // ---- the list of items, the same in every CTA
+  // ---- the list of items, the same in every CTA: what each row sees ...
   for (int t = tid; t < a.n_rows; t += PD_THREADS) {
-    const int b = a.row_req[t];
-    int n_pages = 0, first = 0;
+    const int b = a.row_req[t], p = a.row_pos[t];
+    int lo = 0, hi = 0;
     if (b >= a.n_req && blockIdx.x == 0) flag(a.status_dev, CSA_DEV_BAD_POS);
-    if (b >= 0 && b < a.n_req && (t % rows == 0 || a.row_req[t - 1] != b)) {
-      int lo, hi;
-      const int n = item_rows(a, t, rows, b, lo, hi);
+    if (b >= 0 && b < a.n_req) paged::visible_range(a, a.kv_len[b], p, lo, hi);
+    plan.req[t] = b < a.n_req ? b : -1;
+    plan.lo[t] = lo;
+    plan.hi[t] = hi;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      tc::mbar_init(&M->full[i], 1);
+      tc::mbar_init(&M->empty[i], PD_WARPS);
+    }
+    M->abort = 0;
+    tc::mbar_fence_init();
+  }
+  __syncthreads();
+  // ... and, for each row t that starts an item, the pages that it and the rows
+  // after it see: up to the next multiple of `rows`, while they are the same request's
+  for (int t = tid; t < a.n_rows; t += PD_THREADS) {
+    const int b = plan.req[t];
+    int n_pages = 0, first = 0;
+    if (b >= 0 && (t % rows == 0 || plan.req[t - 1] != b)) {
+      int lo = 0x7FFFFFFF, hi = 0, n = 0;
+      for (; n == 0 || (t + n < a.n_rows && (t + n) % rows != 0 && plan.req[t + n] == b); ++n)
+        if (plan.lo[t + n] < plan.hi[t + n]) {
+          lo = min(lo, plan.lo[t + n]);
+          hi = max(hi, plan.hi[t + n]);
+        }
       if (lo < hi) {
         first = lo / kBlock;
         n_pages = (hi - 1) / kBlock - first + 1;
@@ -161,14 +166,6 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     }
     plan.pages[t] = n_pages;
     plan.first[t] = first;
-  }
-  if (tid == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
-      tc::mbar_init(&M->full[i], 1);
-      tc::mbar_init(&M->empty[i], PD_WARPS);
-    }
-    M->abort = 0;
-    tc::mbar_fence_init();
   }
   __syncthreads();
   if (warp == 0) {
@@ -217,7 +214,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
       const int pb = (int)min((long long)P, pa + (w1 - w));
       const int kvh = sub / head_tiles;
       const int32_t *table =
-          a.block_table + (long long)a.row_req[t] * a.max_blocks + plan.first[t];
+          a.block_table + (long long)plan.req[t] * a.max_blocks + plan.first[t];
       int entry = 0;
       for (int p = pa; p < pb && ok; ++p, ++it) {
         if (((p - pa) & 31) == 0) entry = p + lane < pb ? table[p + lane] : 0;
@@ -260,45 +257,82 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
   const int mi = lane >> 3, ri = lane & 7;  // ldmatrix: matrix and row of this lane's address
   const int fr = lane >> 2, fc = (lane & 3) * 2;  // fragment row and column
   constexpr int NV = D / 64;  // 8-channel tiles of O per warp
+  // The item that holds page w (row t or a later one), and this thread's 16-byte
+  // pieces of its q; rows and heads that it lacks are zero.
+  struct Item {
+    int t, sub, pa, pb, h0, n_rows, n_heads;
+  };
+  constexpr int QN = PAIRS * (D / 8) / (32 * PD_WARPS);  // pieces a thread
+  auto item_at = [&](long long w, int t) {
+    Item I;
+    while (plan.before[t + 1] <= w) ++t;
+    const int P = plan.pages[t];
+    I.t = t;
+    I.sub = (int)((w - plan.before[t]) / P);
+    I.pa = (int)((w - plan.before[t]) % P);
+    I.pb = (int)min((long long)P, I.pa + (w1 - w));
+    const int kvh = I.sub / head_tiles;
+    I.h0 = kvh * g + I.sub % head_tiles * gt;
+    I.n_heads = min(gt, (kvh + 1) * g - I.h0);  // the last head tile may be short
+    I.n_rows = 1;
+    while (t + I.n_rows < a.n_rows && (t + I.n_rows) % rows != 0 &&
+           plan.req[t + I.n_rows] == plan.req[t])
+      ++I.n_rows;
+    return I;
+  };
+  auto read_q = [&](const Item &I, uint4(&q)[QN > 0 ? QN : 1]) {
+#pragma unroll
+    for (int u = 0; u < (QN > 0 ? QN : 1); ++u) {
+      const int i = u * 32 * PD_WARPS + tid, m = i / (D / 8), c = i % (D / 8);
+      const int r = m / gt, h = m % gt;
+      q[u] = make_uint4(0, 0, 0, 0);
+      if (m < PAIRS && r < I.n_rows && h < I.n_heads)
+        q[u] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) +
+                                                (I.t + r) * a.q_row_stride +
+                                                (long long)(I.h0 + h) * D * 2 + c * 16);
+    }
+  };
   uint32_t it = 0;
   bool ok = true;
-  int t = row0;
+  Item I = item_at(w0, row0);
+  uint4 q_next[QN > 0 ? QN : 1];
+  read_q(I, q_next);
   for (long long w = w0; w < w1 && ok;) {
-    while (plan.before[t + 1] <= w) ++t;
-    const int P = plan.pages[t], first = plan.first[t];
-    const int sub = (int)((w - plan.before[t]) / P), pa = (int)((w - plan.before[t]) % P);
-    const int pb = (int)min((long long)P, pa + (w1 - w));
-    const int kvh = sub / head_tiles, h0 = kvh * g + sub % head_tiles * gt;
-    const int n_heads = min(gt, (kvh + 1) * g - h0);  // the last head tile may be short
-    const int b = a.row_req[t];
-    int n_rows = 1;
-    while (t + n_rows < a.n_rows && (t + n_rows) % rows != 0 && a.row_req[t + n_rows] == b) ++n_rows;
+    const int t = I.t, sub = I.sub, pa = I.pa, pb = I.pb, h0 = I.h0, n_heads = I.n_heads;
+    const int n_rows = I.n_rows, P = plan.pages[t], first = plan.first[t], kvh = sub / head_tiles;
 
     // ---- Q and what each pair (row i / gt, head i % gt) sees
     tc::bar_sync(PD_BAR, 32 * PD_WARPS);  // the previous item is done with Q and the statistics
-    for (int i = tid; i < PAIRS * (D / 8); i += 32 * PD_WARPS) {
-      const int m = i / (D / 8), c = i % (D / 8), r = m / gt, h = m % gt;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < n_rows && h < n_heads)
-        v = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) +
-                                             (t + r) * a.q_row_stride + (h0 + h) * D * 2 + c * 16);
-      *reinterpret_cast<uint4 *>(sm + C::OFF_Q + m * C::Q_STRIDE * 2 + c * 16) = v;
+#pragma unroll
+    for (int u = 0; u < (QN > 0 ? QN : 1); ++u) {
+      const int i = u * 32 * PD_WARPS + tid, m = i / (D / 8), c = i % (D / 8);
+      if (m < PAIRS) *reinterpret_cast<uint4 *>(sm + C::OFF_Q + m * C::Q_STRIDE * 2 + c * 16) = q_next[u];
     }
     if (tid < PAIRS) {
       const int r = tid / gt, h = tid % gt;
-      int lo = 0, hi = 0;
-      if (r < n_rows && h < n_heads) paged::visible_range(a, a.kv_len[b], a.row_pos[t + r], lo, hi);
-      M->lo[tid] = lo;
-      M->hi[tid] = hi;
+      const bool on = r < n_rows && h < n_heads;
+      M->lo[tid] = on ? plan.lo[t + r] : 0;
+      M->hi[tid] = on ? plan.hi[t + r] : 0;
       M->ref[tid] = -INFINITY;
     }
     // positions that every pair of the item sees (padding pairs aside)
     int all_lo = 0, all_hi = 0x7FFFFFFF;
     for (int r = 0; r < n_rows; ++r) {
-      int lo, hi;
-      paged::visible_range(a, a.kv_len[b], a.row_pos[t + r], lo, hi);
-      all_lo = max(all_lo, lo);
-      all_hi = min(all_hi, max(lo, hi));
+      all_lo = max(all_lo, plan.lo[t + r]);
+      all_hi = min(all_hi, max(plan.lo[t + r], plan.hi[t + r]));
+    }
+    float s2[MT][2];  // sinks in log2 units
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int h = (i * 16 + u * 8 + fr) % gt;
+        s2[i][u] = a.sink && h < n_heads ? a.sink[h0 + h] * paged::kLog2e : -INFINITY;
+      }
+    // the next item's q is on its way during this one
+    if (w + (pb - pa) < w1) {
+      I = item_at(w + (pb - pa), t);
+      read_q(I, q_next);
     }
     tc::bar_sync(PD_BAR, 32 * PD_WARPS);
     uint32_t qf[MT == 1 ? D / 16 : 1][4];
@@ -531,8 +565,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
         const bool zero = ref == -INFINITY && sum == 0.f;
         if (whole) {
           const long long row = (long long)(t + r) * a.n_heads + h0 + h;
-          const float s2 = a.sink ? a.sink[h0 + h] * paged::kLog2e : -INFINITY;
-          const paged::Joined J = paged::finish(ref, sum, s2);
+          const paged::Joined J = paged::finish(ref, sum, s2[i][u]);
           uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + row * D +
                                                        warp * (D / 8) + fc);
 #pragma unroll
