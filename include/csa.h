@@ -631,7 +631,7 @@ CSA_API csa_status_t csa_qk_norm_rope(csa_qk_norm_rope_args *args, csa_stream_t 
  * fmt CSA_FMT_MXFP8: codes uint8 of the same shape and scale bytes uint8
  * [n_blocks, 128, n_heads, head_dim / 32], dense, head_dim a multiple of 32;
  * the row as it would be stored in FP32 is quantised as csa_compress publishes
- * MXFP8.  The slots of different rows must not overlap in memory.
+ * MXFP8 (an infinity saturates its group's scale; a NaN stays one).  The slots of different rows must not overlap in memory.
  * Supported: head_dim a multiple of 8, 8 .. 512; tensors 16-byte aligned.
  * ---------------------------------------------------------------------- */
 typedef struct {
@@ -695,12 +695,13 @@ CSA_API csa_status_t csa_kv_append(csa_kv_append_args *args, csa_stream_t stream
  * q bf16 [n_rows, n_heads, head_dim], row-strided; k_pool, v_pool bf16
  * [n_blocks, 128, n_kv_heads, head_dim] with strides as in csa_kv_append; out
  * bf16 [n_rows, n_heads, head_dim] dense; lse f32 [n_rows, n_heads] or NULL;
- * block_table i32 [n_req, max_blocks]; kv_len i32 [n_req].  Supported:
+ * block_table i32 [n_req, max_blocks]; kv_len i32 [n_req].  out and lse must not
+ * overlap the inputs.  Supported: at most 2^24 rows and 2^24 pages a request;
  * head_dim 64 or 128; n_kv_heads a divisor of n_heads, n_heads / n_kv_heads <=
  * 128.  softmax_scale > 0, finite.  Tensors 16-byte aligned.
  * `mode` (csa_mode_t) chooses between the kernel for few rows per request
- * (CSA_MODE_DECODE) and the one for chunks (CSA_MODE_PREFILL); CSA_MODE_AUTO
- * goes by the sizes.  Both compute the same function; they round differently.
+ * (CSA_MODE_DECODE; calls of up to 512 rows) and the one for chunks
+ * (CSA_MODE_PREFILL); CSA_MODE_AUTO goes by the sizes.  Both compute the same function; they round differently.
  * The workspace (size query) holds partial results of split rows; nothing in
  * it has to be set or kept between calls.  256-byte aligned.  Calls that may
  * run at the same time need workspaces of their own.

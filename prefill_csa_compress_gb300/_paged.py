@@ -141,6 +141,13 @@ def _pool_strides(t, name):
     return page * 2, token * 2, head * 2
 
 
+def _int32(x, name):
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def _ptr(tensors, name, t):
     """The address of a checked tensor, noting its device."""
     if t is None:
@@ -166,7 +173,7 @@ def _rope(a, tensors, cos, sin, layout, start, dim):
     a.rope_cap, a.rope_dim = int(cos.shape[0]), 2 * int(cos.shape[1])
     if not 0 < a.rope_dim <= dim:
         raise ValueError(f"the tables rotate {a.rope_dim} channels of a head of {dim}")
-    a.rope_start = dim - a.rope_dim if start is None else int(start)
+    a.rope_start = dim - a.rope_dim if start is None else _int32(start, "rope_start")
     a.rope_cos, a.rope_sin = _ptr(tensors, "rope_cos", cos), _ptr(tensors, "rope_sin", sin)
 
 
@@ -230,8 +237,9 @@ def csa_rope_table(*, cos, sin, theta=10000.0, scaling="none", factor=1.0, orig_
     _dense(sin, "sin", torch.float32, tuple(cos.shape))
     a, tensors = RopeTableArgs(), []
     a.struct_size = ctypes.sizeof(a)
-    a.n_pos, a.rope_dim, a.pos0 = int(cos.shape[0]), 2 * int(cos.shape[1]), int(pos0)
-    a.scaling, a.orig_len = _SCALINGS[scaling], int(orig_len)
+    a.n_pos, a.rope_dim = _int32(cos.shape[0], "cos"), 2 * int(cos.shape[1])
+    a.pos0 = _int32(pos0, "pos0")
+    a.scaling, a.orig_len = _SCALINGS[scaling], _int32(orig_len, "orig_len")
     a.theta, a.factor, a.attn_factor = float(theta), float(factor), float(attn_factor)
     a.beta_fast, a.beta_slow = float(beta_fast), float(beta_slow)
     a.cos, a.sin = _ptr(tensors, "cos", cos), _ptr(tensors, "sin", sin)
@@ -379,7 +387,8 @@ def csa_paged_attn(*, q, row_req, row_pos, k_pool, v_pool, block_table, kv_len, 
                                   ("workspace", workspace, torch.uint8, (None,))):
         if x is not None:
             _dense(x, name, dtype, shape)
-    a.causal, a.window, a.mode = 1 if causal else 0, int(window), int(mode)
+    a.causal, a.window = 1 if causal else 0, _int32(window, "window")
+    a.mode = _int32(mode, "mode")
     a.softmax_scale = float(d ** -0.5 if softmax_scale is None else softmax_scale)
     for name, x in (("q", q), ("row_req", row_req), ("row_pos", row_pos), ("kv_len", kv_len),
                     ("block_table", block_table), ("k_pool", k_pool), ("v_pool", v_pool),

@@ -169,6 +169,7 @@ CSA_API csa_status_t csa_paged_attn(csa_paged_attn_args *user, csa_stream_t stre
   csa_paged_attn_args a = *user;
   if (a.n_rows < 0 || a.n_req <= 0 || a.max_blocks <= 0 || a.n_blocks <= 0)
     return CSA_ERR_INVALID_ARG;
+  if (a.n_rows > (1 << 24)) return CSA_ERR_UNSUPPORTED;
   if (a.max_blocks > (1 << 24) || a.n_heads < 1 || a.n_kv_heads < 1 || a.n_heads > 65536 ||
       a.n_heads % a.n_kv_heads)
     return CSA_ERR_INVALID_ARG;

@@ -536,6 +536,45 @@ def test_hidden_infinities(mode, value, heads, kv_heads, dim, window):
 
 
 @MODES
+@pytest.mark.parametrize("value", [float("inf"), NAN])
+def test_a_broken_query_stays_alone(mode, value):
+    """A query row that is not finite leaves every other row's bits as they were."""
+    b = Batch(chunk(0, 180, 40) + chunk(1, 100, 3), [220, 103], 8, 2, 128)
+    want, wl, _ = b.call(mode)
+    for t in (7, 41):
+        keep = b.q.clone()
+        b.q[t, 3, 5] = value
+        out, lse, _ = b.call(mode)
+        other = torch.ones(43, 8, dtype=torch.bool, device=DEV)
+        other[t, 3] = False
+        assert torch.equal(out[other], want[other]) and torch.equal(lse[other], wl[other])
+        assert out[t, 3].isnan().any()
+        b.q.copy_(keep)
+
+
+@MODES
+@pytest.mark.parametrize("n,heads,kv_heads", [(511, 4, 2), (512, 2, 2), (600, 4, 1)])
+def test_many_single_rows(mode, n, heads, kv_heads):
+    """Requests of one row around the decode kernel's most rows, some of them
+    empty, some long enough for parts."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(1, 40, n)
+    lens[5], lens[300], lens[301] = 700, 0, 400
+    Batch([(b, max(int(k) - 1, 0)) for b, k in enumerate(lens)], lens.tolist(), heads, kv_heads, 64).check(mode)
+
+
+@MODES
+def test_equal_positions_and_far_rows(mode):
+    """Rows that repeat a position, and positions far past the cache."""
+    rows = [(0, 50)] * 5 + [(0, 7)] * 3 + [(0, 10 ** 9)] * 2 + [(1, 3)] * 30
+    b = Batch(rows, [300, 260], 4, 2, 64)
+    out, lse = b.check(mode)
+    b.q[1:5] = b.q[0]
+    out, lse, _ = b.call(mode)
+    assert all(torch.equal(out[0], out[i]) and torch.equal(lse[0], lse[i]) for i in range(1, 5))
+
+
+@MODES
 def test_large_logits(mode):
     """Logits to about +-1000, and their maximum in any page."""
     b = Batch(chunk(0, 300, 20), [320], 4, 2, 128, qk=9.0)

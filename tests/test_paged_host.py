@@ -99,7 +99,7 @@ REFUSED = [
         dict(kv_len=None), dict(block_table=None), dict(k_pool=None), dict(v_pool=None),
         dict(out=None), dict(q=_base + 8), dict(out=_base + 8), dict(k_pool=_base + 8)]),
     ("csa_paged_attn", ATTN, UNSUPPORTED, [
-        dict(head_dim=32), dict(head_dim=256), dict(n_heads=129, n_kv_heads=1)]),
+        dict(head_dim=32), dict(head_dim=256), dict(n_heads=129, n_kv_heads=1), dict(n_rows=(1 << 24) + 1)]),
 ]
 
 
@@ -207,6 +207,11 @@ def test_binding_refusals():
                         (dict(block_table=_i(2, 6)[:, ::2]), "contiguous")]:
         with pytest.raises(ValueError, match=why):
             csa.csa_paged_attn(**{**at, **change})
+    for change in (dict(window=2 ** 32 + 1), dict(mode=2 ** 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            csa.csa_paged_attn(**{**at, **change})
+    with pytest.raises(ValueError, match="32 bits"):
+        csa.csa_rope_table(cos=f32, sin=f32.clone(), pos0=2 ** 32)
     with pytest.raises(TypeError, match="sink must be"):
         csa.csa_paged_attn(**{**at, "sink": torch.zeros(8).double()})
 
