@@ -597,26 +597,31 @@ __global__ void __launch_bounds__(128)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long row = blockIdx.x;
   const int t = (int)(row / a.n_heads), h = (int)(row - (long long)t * a.n_heads);
-  const int b = a.row_req[t];
-  if (b < 0 || b >= a.n_req) return;
   const int g = a.n_heads / a.n_kv_heads, gt = min(g, pairs), kvh = h / g;
   const int head_tiles = (g + gt - 1) / gt, sub = kvh * head_tiles + h % g / gt;
+  // (three waits for memory in all: these, the references, the outputs)
   const int4 it = parts.item[(long long)t * (a.n_kv_heads * head_tiles) + sub];
+  const int b = a.row_req[t];
+  const float s2 = a.sink ? a.sink[h] * paged::kLog2e : -INFINITY;
+  if (b < 0 || b >= a.n_req) return;      // (item is not set there)
   if (it.x == it.y && it.x >= 0) return;  // written whole
   const int m = (t - it.z) * gt + h % g % gt, n = it.x < 0 ? 0 : it.y - it.x + 1;
   auto slot = [&](int s) { return (2ll * (it.x + s) + (s == 0 ? 1 : 0)) * pairs + m; };
   // the part with the largest reference first, then the sums in part order
   float ref = -INFINITY;
-  for (int s = threadIdx.x & 31; s < n; s += 32) ref = fmaxf(ref, parts.ml[slot(s)].x);
+  for (int s = lane; s < n; s += 32) ref = fmaxf(ref, parts.ml[slot(s)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
   float acc[E] = {}, l = 0.f;
+#pragma unroll 4
   for (int s = warp; s < n; s += NW) {
     const float2 ml = parts.ml[slot(s)];
+    float o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = parts.o[slot(s) * D + lane * E + e];
     if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing was seen there
     const float w = ml.x == -INFINITY ? ml.y : exp2f(ml.x - ref);  // (l is NaN there)
     l += w * ml.y;
-    const float *o = parts.o + slot(s) * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] += w * o[e];
   }
@@ -626,7 +631,6 @@ __global__ void __launch_bounds__(128)
   __syncthreads();
   if (warp != 0) return;
   l = (sh_l[0] + sh_l[1]) + (sh_l[2] + sh_l[3]);
-  const float s2 = a.sink ? a.sink[h] * paged::kLog2e : -INFINITY;
   const paged::Joined J = paged::finish(ref, l, s2);
   const bool zero = ref == -INFINITY && l == 0.f;
   __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + row * D + lane * E;
