@@ -158,17 +158,33 @@ struct Run {
   }
 };
 
-// All rows as one run, if they are one request's.
-__device__ __forceinline__ bool one_run(const Rows &W, int n, Run &R) {
+// All rows as one run, if they are one request's (the usual case, without the
+// registers and the code of the walk: that code is fetched cold by every CTA).
+__device__ __forceinline__ bool one_run(const csa_paged_attn_args &a, int t0, int n, Run &R) {
   const int lane = threadIdx.x & 31;
-  R = {__shfl_sync(0xffffffffu, W.req[0], 0), n, 0x7FFFFFFF, 0, 0, 0x7FFFFFFF};
+  R = {0, n, 0x7FFFFFFF, 0, 0, 0x7FFFFFFF};
   bool same = true;
+#pragma unroll 1
+  for (int r = lane; r - lane < n; r += 64) {
+    int req[2], pos[2], len[2];
 #pragma unroll
-  for (int k = 0; k < PC_K; ++k)
-    if (32 * k + lane < n) {
-      same = same && W.req[k] == R.req;
-      R.add(W.lo[k], W.hi[k]);
+    for (int k = 0; k < 2; ++k) {
+      const int t = t0 + min(r + 32 * k, n - 1);  // (past the last row: that row again)
+      req[k] = a.row_req[t];
+      pos[k] = a.row_pos[t];
     }
+    if (r == lane) R.req = __shfl_sync(0xffffffffu, req[0], 0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      len[k] = a.kv_len[req[k] >= 0 && req[k] < a.n_req ? req[k] : 0];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      int lo, hi;
+      paged::visible_range(a, len[k], pos[k], lo, hi);
+      same = same && req[k] == R.req;
+      R.add(lo, hi);
+    }
+  }
   R.reduce();
   return __all_sync(0xffffffffu, same);
 }
@@ -309,8 +325,6 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   // once they are under way.
   if (warp == PC_LOAD) {
     // ================================================================ loads
-    Rows W;
-    read_rows(a, t0, n_rows, W);
     // (q_full, ..., o_full: one arrival; s_full two; s_free and p_full a warp each)
     tc::mbar_init(&M->q_full + lane, lane < 26 ? 1 : (lane < 28 ? 2 : 8));
     if (lane == 0) M->abort = 0;
@@ -324,10 +338,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           tc::tma_load_3d(sm + s * C::TILE + c * 16384, &qmap, c * 64, kvh * g,
                           t0 + s * G.rows_tile, &M->q_full);
     }
-    // Two walks over the runs of one request, the first (not needed for a
-    // single run) to count the pages: this part takes its share of them.
+    // Two walks over the runs of one request, the first to count the pages: this
+    // part takes its share of them.
     Run R;
-    const bool single = one_run(W, n_rows, R);
+    Rows W;
+    const bool single = one_run(a, t0, n_rows, R);
+    if (!single) read_rows(a, t0, n_rows, W);
     bool counting = true, many = false, ok = true;
     int total = 0, valid = 0, skip = 0, n_pages = 0, left = 0;
     uint32_t it = 0;  // tiles loaded

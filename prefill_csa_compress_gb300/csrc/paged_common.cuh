@@ -15,10 +15,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Positions [lo, hi) that a row at position p sees in a cache of kv_len.
 __device__ __forceinline__ void visible_range(const csa_paged_attn_args &a, int kv_len, int p,
                                               int &lo, int &hi) {
-  const int len = min(kv_len, (int)min((long long)a.max_blocks * kBlock, 0x7FFFFFFFll));
+  const int len = min(kv_len, a.max_blocks < 0x7FFFFFFF / kBlock ? a.max_blocks * kBlock : 0x7FFFFFFF);
   hi = a.causal && p < len ? p + 1 : len;
-  const long long from = a.window > 0 ? (long long)p - a.window + 1 : 0;
-  lo = (int)max(0ll, from);
+  lo = a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
 }
 
 // The parts of split rows, merged by paged_merge_kernel: part s of row t and
