@@ -678,6 +678,51 @@ def test_streams_and_graphs(mode):
     assert not torch.equal(new[0], want[0][0]) and torch.equal(calls[0][1], new[0])
 
 
+@MODES
+def test_graphs_that_share_a_workspace(mode):
+    """Two graphs captured on one workspace and replayed in turn, the caller's
+    own references gone."""
+    a = Batch(chunk(0, 2000, 20), [2020], 8, 2, 128, seed=1)
+    b = Batch([(0, 4000), (1, 77)], [4001, 78], 16, 4, 64, seed=2)
+    want = [x.call(mode) for x in (a, b)]
+    ws = torch.zeros(256 << 20, dtype=torch.uint8, device=DEV)
+    runs = []
+    for x in (a, b):
+        call, out, lse, _ = x.call(mode, prepare=True, workspace=ws)
+        call()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        runs.append((g, out, lse, call))
+    del a, b, x, ws
+    junk = [torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    for _ in range(3):
+        for (g, out, lse, _), w in zip(runs, want):
+            out.fill_(1)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
+    del junk
+
+
+def test_no_rows():
+    """Calls with nothing to do launch nothing and touch nothing."""
+    q, k = (torch.zeros((0, h, 64), dtype=torch.bfloat16, device=DEV) for h in (4, 2))
+    none, tab = _i32([]), _i32([[0]])
+    cos, sin = (torch.ones((16, 32), device=DEV) for _ in range(2))
+    pool = torch.full((1, 128, 2, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    before = csa.launch_count()
+    csa.csa_rope_table(cos=cos[:0], sin=sin[:0])
+    csa.csa_qk_norm_rope(q=q, k=k, row_pos=none, rope_cos=cos, rope_sin=sin)
+    csa.csa_kv_append(k=k, v=k, row_req=none, row_pos=none, block_table=tab, k_pool=pool, v_pool=pool.clone(), norm=True,
+                      rope_cos=cos, rope_sin=sin)
+    csa.csa_paged_attn(q=q, row_req=none, row_pos=none, k_pool=pool, v_pool=pool, block_table=tab, kv_len=_i32([5]),
+                       out=q.clone())
+    torch.cuda.synchronize()
+    assert csa.launch_count() == before and (pool == 3).all()
+
+
 def test_both_kernels_agree_with_auto():
     for rows, lens in ((chunk(0, 900, 1) + [(1, 44)], [901, 45]), (chunk(0, 0, 600), [600])):
         b = Batch(rows, lens, 8, 2, 128)
