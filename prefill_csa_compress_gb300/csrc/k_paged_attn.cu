@@ -64,8 +64,7 @@ __global__ void __launch_bounds__(PM_THREADS)
       l += other[4];
     }
   }
-  const float s2 = a.sink ? a.sink[h] * paged::kLog2e : -INFINITY;
-  const paged::Joined J = paged::finish(m, l, s2);
+  const paged::Joined J = paged::finish(m, l, a.sink ? a.sink[h] : -INFINITY);
   const bool zero = m == -INFINITY && l == 0.f;
   __nv_bfloat162 out[2];
 #pragma unroll

@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       if (req >= a.n_req) req = -1;
       if (req >= 0) paged::visible_range(a, a.kv_len[req], a.row_pos[t], lo, hi);
     }
-    const float s2 = req >= 0 && a.sink ? a.sink[h] * paged::kLog2e : -INFINITY;
+    const float sink = req >= 0 && a.sink ? a.sink[h] : -INFINITY;
     // P = 2^(x - ref): ref is kLift above the largest logit when it is set
     float ref = -INFINITY, l = 0.f;
     bool ok = true;
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       if (mine && half == 0)
         parts.ml[(long long)part * a.n_rows * a.n_heads + row] = make_float2(ref, l);
     } else {
-      const paged::Joined J = paged::finish(ref, l, s2);
+      const paged::Joined J = paged::finish(ref, l, sink);
       scale = J.inv;
       if (mine && half == 0 && a.lse) a.lse[row] = J.lse;
     }

@@ -323,13 +323,13 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
       all_lo = max(all_lo, plan.lo[t + r]);
       all_hi = min(all_hi, max(plan.lo[t + r], plan.hi[t + r]));
     }
-    float s2[MT][2];  // sinks in log2 units
+    float sink[MT][2];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int h = (i * 16 + u * 8 + fr) % gt;
-        s2[i][u] = a.sink && h < n_heads ? a.sink[h0 + h] * paged::kLog2e : -INFINITY;
+        sink[i][u] = a.sink && h < n_heads ? a.sink[h0 + h] : -INFINITY;
       }
     // the next item's q is on its way during this one
     if (w + (pb - pa) < w1) {
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
         const bool zero = ref == -INFINITY && sum == 0.f;
         if (whole) {
           const long long row = (long long)(t + r) * a.n_heads + h0 + h;
-          const paged::Joined J = paged::finish(ref, sum, s2[i][u]);
+          const paged::Joined J = paged::finish(ref, sum, sink[i][u]);
           uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + row * D +
                                                        warp * (D / 8) + fc);
 #pragma unroll
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(128)
   // (three waits for memory in all: these, the references, the outputs)
   const int4 it = parts.item[(long long)t * (a.n_kv_heads * head_tiles) + sub];
   const int b = a.row_req[t];
-  const float s2 = a.sink ? a.sink[h] * paged::kLog2e : -INFINITY;
+  const float sink = a.sink ? a.sink[h] : -INFINITY;
   if (b < 0 || b >= a.n_req) return;      // (item is not set there)
   if (it.x == it.y && it.x >= 0) return;  // written whole
   const int m = (t - it.z) * gt + h % g % gt, n = it.x < 0 ? 0 : it.y - it.x + 1;
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(128)
   __syncthreads();
   if (warp != 0) return;
   l = (sh_l[0] + sh_l[1]) + (sh_l[2] + sh_l[3]);
-  const paged::Joined J = paged::finish(ref, l, s2);
+  const paged::Joined J = paged::finish(ref, l, sink);
   const bool zero = ref == -INFINITY && l == 0.f;
   __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + row * D + lane * E;
 #pragma unroll

@@ -70,12 +70,11 @@ bool encode_q(const csa_paged_attn_args &a, int rows, CUtensorMap *q);
 struct Joined {
   float inv, lse;
 };
-__device__ __forceinline__ Joined finish(float m, float l, float s2) {
-  // m = -inf: nothing was seen; s2: the sink in log2 units, -inf for none
-  const float mm = fmaxf(m, s2);
-  if (mm == -INFINITY) return {0.f, l == 0.f ? -INFINITY : l};  // l is NaN if a logit was
-  const float f = m == -INFINITY ? (l == 0.f ? 0.f : l) : exp2f(m - mm);
-  const float L = l * f + exp2f(s2 - mm);
+__device__ __forceinline__ Joined finish(float m, float l, float sink) {
+  // m = -inf: nothing was seen (l = 0; NaN if a logit was); sink = -inf: none
+  if (m == -INFINITY) return {l, l == 0.f ? sink : l};
+  const float s2 = sink * kLog2e, mm = fmaxf(m, s2);
+  const float f = exp2f(m - mm), L = l * f + (s2 == mm ? 1.f : exp2f(s2 - mm));
   return {f / L, (mm + log2f(L)) * kLn2};
 }
 

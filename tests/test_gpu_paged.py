@@ -506,6 +506,20 @@ def test_nothing_is_seen(mode):
 
 
 @MODES
+def test_unbounded_sinks(mode):
+    """A sink of +inf takes everything: out = 0, lse = inf; a row that sees
+    nothing returns its sink's bits.  Whole rows and rows in parts."""
+    for b in (Batch(chunk(0, 30, 6) + [(1, -1)], [36, 0], 8, 2, 128), Batch([(0, 4000), (1, 3)], [4001, 0], 8, 2, 64)):
+        b.sink[::2] = float("inf")
+        out, lse, st = b.call(mode)
+        assert st == 0
+        assert (out[:, ::2] == 0).all() and (lse[:, ::2] == float("inf")).all()
+        assert torch.equal(lse[-1], b.sink) and (out[-1] == 0).all()
+        b.sink[::2] = -float("inf")
+        b.check(mode)
+
+
+@MODES
 @pytest.mark.parametrize("value", [float("inf"), -float("inf"), NAN])
 @pytest.mark.parametrize("heads,kv_heads,dim,window", [(8, 1, 128, 0), (4, 4, 64, 0), (8, 2, 64, 40)])
 def test_hidden_infinities(mode, value, heads, kv_heads, dim, window):
