@@ -130,7 +130,8 @@ bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims
 bool use_decode(const csa_paged_attn_args &a) {
   if (a.mode == CSA_MODE_PREFILL || a.n_rows > paged::kDecodeRows) return false;
   if (a.mode == CSA_MODE_DECODE) return true;
-  const int per = (a.n_rows + a.n_req - 1) / a.n_req, items = paged_decode_items(a, per);
+  const int per = (int)(((long long)a.n_rows + a.n_req - 1) / a.n_req);
+  const int items = paged_decode_items(a, per);
   return items <= 2 || (items <= 4 && a.n_req > 1 && a.max_blocks <= 4);
 }
 

@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
               P.req = R.req;
               P.r0 = r0;
               P.r1 = there ? R.end : r0;  // an unmapped page is seen by no row
-              P.mixed = many || !there || base < R.all_lo || base + kBlock > R.all_hi;
+              P.mixed = many || !there || base < R.all_lo || R.all_hi - base < kBlock;
               P.lo = there ? max(R.lo - base, 0) : 0;
               P.hi = there ? min(R.hi - base, kBlock) : 0;
               if (!there) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
@@ -838,7 +838,7 @@ int paged_chunk_parts(const csa_paged_attn_args &a, int sms) {
     pages = pages < seen ? pages : seen;
   }
   // the requests that a CTA's rows may belong to, each with pages of its own
-  const long long per = (a.n_rows + a.n_req - 1) / a.n_req;
+  const long long per = ((long long)a.n_rows + a.n_req - 1) / a.n_req;
   const long long runs = per >= rows ? 1 : (rows + per - 1) / (per > 0 ? per : 1);
   pages *= runs < a.n_req ? runs : a.n_req;
   int best = 1;

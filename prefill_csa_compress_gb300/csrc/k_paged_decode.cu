@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
       ok = pd_wait(&M->full[st], (it / C::STAGES) & 1, abort, a.status_dev) && ok;
       const uint32_t ks = kv_s + st * 2 * C::TILE, vs = ks + C::TILE;
       const int phys = M->phys[st], base = (first + p) * kBlock;
-      const bool mixed = phys < 0 || base < all_lo || base + kBlock > all_hi;
+      const bool mixed = phys < 0 || base < all_lo || all_hi - base < kBlock;
 
       // ---- S = Q K^T over this warp's 16 keys
       float x[MT][2][4] = {};

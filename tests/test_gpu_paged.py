@@ -520,6 +520,33 @@ def test_unbounded_sinks(mode):
 
 
 @MODES
+def test_last_positions_of_a_table(mode):
+    """A window over the last of 2^31 positions: the one past kv_len lies on
+    the same page and holds NaN."""
+    top, window, heads, kv_heads, dim = 2 ** 31 - 1, 200, 4, 2, 128
+    rng = np.random.default_rng(5)
+    k, v = _bf(rng, 3, 128, kv_heads, dim), _bf(rng, 3, 128, kv_heads, dim)
+    k[2, 127], v[2, 127] = NAN, NAN
+    table = torch.full((1, 1 << 24), -1, dtype=torch.int32, device=DEV)
+    table[0, -3:] = _i32([0, 1, 2])
+    pos = np.array([top - 2, top - 1, top - 130, top], dtype=np.int64)
+    q, sink = _bf(rng, 4, heads, dim), torch.zeros(heads, device=DEV)
+    out, lse, st = torch.empty_like(q), torch.empty((4, heads), device=DEV), _status()
+    csa.csa_paged_attn(q=q, row_req=_i32([0] * 4), row_pos=torch.from_numpy(pos).int().to(DEV), k_pool=k, v_pool=v,
+                       block_table=table, kv_len=_i32([top]), out=out, lse=lse, sink=sink, window=window, mode=mode,
+                       status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    # the same rows over the last three pages alone
+    o, ls, spread = PO.paged_attention(_np(q), np.zeros(4, int), pos - (top + 1 - 384), _np(k), _np(v),
+                                       np.array([[0, 1, 2]]), [383], dim ** -0.5, window=window, sink=np.zeros(heads))
+    # as Batch.compare counts them
+    e = dim * 2.0 ** -24 * np.abs(_np(q)).max() * np.nanmax(np.abs(_np(k))) * dim ** 0.5
+    assert (np.abs(_np(out) - o) <= H8 * np.abs(o) + (H8 + 2 * e + 2.0 ** -12) * spread).all()
+    assert (np.abs(_np(lse) - ls) <= e + 512 * 2.0 ** -24 + 2.0 ** -21 * np.abs(ls) + 2.0 ** -20).all()
+
+
+@MODES
 @pytest.mark.parametrize("value", [float("inf"), -float("inf"), NAN])
 @pytest.mark.parametrize("heads,kv_heads,dim,window", [(8, 1, 128, 0), (4, 4, 64, 0), (8, 2, 64, 40)])
 def test_hidden_infinities(mode, value, heads, kv_heads, dim, window):
