@@ -425,12 +425,17 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         if (it == 2) tc::bar_sync(PC_BAR_START, PC_THREADS);  // n_it, barriers
       }
     }
-    if (n_pages == 0) tc::bar_sync(PC_BAR_START, PC_THREADS);
+    if (n_pages == 0) {
+      // q has landed before the others put their zeros where it goes
+      pc_wait_warp(&M->q_full, 0, abort, a.status_dev);
+      tc::bar_sync(PC_BAR_START, PC_THREADS);
+    }
     // whatever was asked for has landed before the CTA retires
-    if (n_pages == 0 || *abort) tc::mbar_wait(&M->q_full, 0, 50000000ull);
-    if (*abort)
+    if (*abort) {
+      tc::mbar_wait(&M->q_full, 0, 50000000ull);
       for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
         tc::mbar_wait(&M->kv_full[k % C::STAGES], (k / C::STAGES) & 1, 50000000ull);
+    }
   } else {
     if (warp == PC_MMA) tc::tmem_alloc(&M->tmem, 512);
     if (tid == PC_CLEAN * 32) {

@@ -505,6 +505,23 @@ def test_nothing_is_seen(mode):
     b.check(mode, causal=False, window=2147483647)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(64, 1), (32, 8), (2, 2)])
+def test_many_rows_that_see_nothing(heads, kv_heads, dim):
+    """Whole tiles without a page, among tiles with pages: zeros where the
+    queries were on their way, over and over."""
+    n = 3000
+    b = Batch([(t // 1000, t % 1000) for t in range(n)], [0, 40, 0], heads, kv_heads, dim)
+    b.q.fill_(float("inf"))
+    b.q[1000:2000] = 0.5
+    for _ in range(10):
+        out, lse, st = b.call(PREFILL)
+        assert st == 0
+        assert (out[:1000] == 0).all() and (out[2000:] == 0).all()
+        assert torch.equal(lse[:1000], b.sink.expand(1000, heads)) and torch.equal(lse[2000:], lse[:1000])
+        assert out[1000:2000].isfinite().all() and (out[1000:2000] != 0).any()
+
+
 @MODES
 def test_unbounded_sinks(mode):
     """A sink of +inf takes everything: out = 0, lse = inf; a row that sees
