@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
 // One CTA per (row, head): warp s takes every fourth part, lanes the channels.
 template <int D>
 __global__ void __launch_bounds__(128)
-    paged_join_kernel(csa_paged_attn_args a, DecodeParts parts, int pairs) {
+    paged_join_kernel(csa_paged_attn_args a, DecodeParts parts, int pairs, int n_ctas) {
   tc::griddep_wait();
   tc::griddep_launch_dependents();
   constexpr int E = D / 32, NW = 4;
@@ -607,6 +607,8 @@ __global__ void __launch_bounds__(128)
   const float sink = a.sink ? a.sink[h] : -INFINITY;
   if (b < 0 || b >= a.n_req) return;      // (item is not set there)
   if (it.x == it.y && it.x >= 0) return;  // written whole
+  // (an item that its CTA gave up before, after a wait that ran out, is not set)
+  if (it.y >= n_ctas || it.z > t || it.z <= t - pairs / gt) return;
   const int m = (t - it.z) * gt + h % g % gt, n = it.x < 0 ? 0 : it.y - it.x + 1;
   auto slot = [&](int s) { return (2ll * (it.x + s) + (s == 0 ? 1 : 0)) * pairs + m; };
   // the part with the largest reference first, then the sums in part order
@@ -669,7 +671,7 @@ cudaError_t launch(const csa_paged_attn_args &a, const DecodeParts &parts, int s
   if (e != cudaSuccess) return e;
   launch_begin(CSA_K_PAGED_MERGE, s);
   e = launch_kernel(paged_join_kernel<D>, dim3((unsigned)(a.n_rows * a.n_heads)), dim3(128), 0, s, 0,
-                    false, a, parts, C::PAIRS);
+                    false, a, parts, C::PAIRS, sms);
   launch_end(CSA_K_PAGED_MERGE, s);
   return e;
 }
