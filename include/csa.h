@@ -575,7 +575,7 @@ CSA_API csa_status_t csa_rope_table(csa_rope_table_args *args, csa_stream_t stre
  * may be row-strided views (of one QKV projection, say).  An output may be its
  * own input (same pointer and stride: in place); no other overlap.  norm = 0
  * rotates only.  row_pos i32 [n_rows]; row_req i32 [n_rows] or NULL: a row
- * with row_req < 0 is padding, neither read nor written.
+ * with row_req < 0 is padding: nothing is written, whatever it holds.
  * Supported: head_dim a multiple of 8, 8 .. 512; q, k, q_out, k_out and the
  * gammas 16-byte aligned.
  * ---------------------------------------------------------------------- */
@@ -631,7 +631,8 @@ CSA_API csa_status_t csa_qk_norm_rope(csa_qk_norm_rope_args *args, csa_stream_t 
  * fmt CSA_FMT_MXFP8: codes uint8 of the same shape and scale bytes uint8
  * [n_blocks, 128, n_heads, head_dim / 32], dense, head_dim a multiple of 32;
  * the row as it would be stored in FP32 is quantised as csa_compress publishes
- * MXFP8 (an infinity saturates its group's scale; a NaN stays one).  The slots of different rows must not overlap in memory.
+ * MXFP8 (an infinity saturates its group's scale; a NaN stays one).  The slots
+ * of different rows must not overlap in memory.
  * Supported: head_dim a multiple of 8, 8 .. 512; tensors 16-byte aligned.
  * ---------------------------------------------------------------------- */
 typedef struct {
@@ -679,14 +680,17 @@ CSA_API csa_status_t csa_kv_append(csa_kv_append_args *args, csa_stream_t stream
  * over a paged cache of separate keys and values.
  *
  * Row t of request b at p sees position j of the request iff 0 <= j <
- * min(kv_len[b], 128 max_blocks), j <= p when `causal`, and j > p - window when window > 0.  Head
- * h reads key/value head h / (n_heads / n_kv_heads).  With the visible j:
+ * min(kv_len[b], 128 max_blocks), j <= p when `causal`, and j > p - window when
+ * window > 0.  Head h reads key/value head h / (n_heads / n_kv_heads).  With the
+ * visible j:
  *   l_j = softmax_scale * q[t,h] . k_j
  *   out[t,h] = sum_j e^{l_j} v_j / (sum_j e^{l_j} + e^{sink_h})
  *   lse[t,h] = log(sum_j e^{l_j} + e^{sink_h})
  * sink == NULL means -inf.  A row that sees nothing gets out = 0 and lse =
- * sink_h.  Keys, values and rows that a row does not see have no effect on it,
- * whatever they hold (infinities and NaN included).  q is used as it is
+ * sink_h.  Logits are FP32 sums; a (row, head) whose largest reaches 2^29 in size
+ * has an unspecified result (from 2^24 on, FP32 does not resolve them to 1).
+ * Keys, values and rows that a row does not see have no effect on it, whatever
+ * they hold (infinities and NaN included).  q is used as it is
  * (csa_qk_norm_rope rotates it).  Rows may come in any order; rows of one
  * request that follow one another in ascending position share their reads.
  * A page outside the pool raises CSA_DEV_BAD_BLOCK and its positions are not
@@ -701,7 +705,8 @@ CSA_API csa_status_t csa_kv_append(csa_kv_append_args *args, csa_stream_t stream
  * 128.  softmax_scale > 0, finite.  Tensors 16-byte aligned.
  * `mode` (csa_mode_t) chooses between the kernel for few rows per request
  * (CSA_MODE_DECODE; calls of up to 512 rows) and the one for chunks
- * (CSA_MODE_PREFILL); CSA_MODE_AUTO goes by the sizes.  Both compute the same function; they round differently.
+ * (CSA_MODE_PREFILL); CSA_MODE_AUTO goes by the sizes.  Both compute the same
+ * function; they round differently.
  * The workspace (size query) holds partial results of split rows; nothing in
  * it has to be set or kept between calls.  256-byte aligned.  Calls that may
  * run at the same time need workspaces of their own.

@@ -260,7 +260,7 @@ def csa_qk_norm_rope(*, q, row_pos, k=None, q_out=None, k_out=None, row_req=None
     q_out = q if q_out is None else q_out
     a.q_row_stride = _rows(q, "q", (None, None, None))
     n, h, d = (int(x) for x in q.shape)
-    a.n_rows, a.n_q_heads, a.head_dim = n, h, d
+    a.n_rows, a.n_q_heads, a.head_dim = _int32(n, "rows"), h, d
     a.q_out_row_stride = _rows(q_out, "q_out", (n, h, d))
     if k is not None:
         k_out = k if k_out is None else k_out
@@ -303,7 +303,7 @@ def csa_kv_append(*, k, row_req, row_pos, block_table, k_pool, v=None, v_pool=No
     a.struct_size = ctypes.sizeof(a)
     a.k_row_stride = _rows(k, "k", (None, None, None))
     n, h, d = (int(x) for x in k.shape)
-    a.n_rows, a.n_heads, a.head_dim = n, h, d
+    a.n_rows, a.n_heads, a.head_dim = _int32(n, "rows"), h, d
     if (v is None) != (v_pool is None):
         raise ValueError("v and v_pool go together")
     if v is not None:
@@ -367,7 +367,7 @@ def csa_paged_attn(*, q, row_req, row_pos, k_pool, v_pool, block_table, kv_len, 
     a.struct_size = ctypes.sizeof(a)
     a.q_row_stride = _rows(q, "q", (None, None, None))
     n, h, d = (int(x) for x in q.shape)
-    a.n_rows, a.n_heads, a.head_dim = n, h, d
+    a.n_rows, a.n_heads, a.head_dim = _int32(n, "rows"), h, d
     _want(k_pool, "k_pool", torch.bfloat16, (None, PAGE, None, d))
     _want(v_pool, "v_pool", torch.bfloat16, tuple(k_pool.shape))
     a.n_blocks, a.n_kv_heads = int(k_pool.shape[0]), int(k_pool.shape[2])

@@ -644,6 +644,32 @@ def test_large_logits(mode):
 
 
 @MODES
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_logits_of_two_to_the_28(mode, sign):
+    """Powers of two, so that the logits are exact: the positions with the
+    largest share the row evenly, the others get nothing."""
+    b = Batch([(0, 299), (0, 300), (1, 20), (1, 1)], [301, 30], 4, 2, 64)
+    seen = ~b.k.isnan()
+    b.q.zero_()
+    b.q[..., 0] = 2.0 ** 16
+    few = torch.arange(128, device=DEV)[None, :, None] % 16 == 3
+    b.k[..., 0] = torch.where(few.expand(b.k.shape[:3]) == (sign > 0), 2.0 ** 15 * sign, 2.0 ** 14 * sign).bfloat16()
+    b.k.masked_fill_(~seen, NAN)
+    out, lse, st = b.call(mode, sink=False)
+    assert st == 0
+    for t, (r, p) in enumerate(zip(b.req, b.pos)):
+        j = np.arange(p + 1)
+        top = j[j % 16 == 3] if (j % 16 == 3).any() else j
+        # sign < 0: the small ones (2^14) are the largest
+        v = _np(b.v)[b.table[r][top // 128], top % 128]  # [n, kv_heads, dim]
+        o, spread = np.repeat(v.mean(0), 2, 0), np.repeat(np.abs(v).mean(0), 2, 0)
+        assert (np.abs(_np(out)[t] - o) <= H8 * np.abs(o) + (H8 + 2.0 ** -12) * spread).all()
+        x = 2.0 ** 13 * _np(b.k)[b.table[r][top[0] // 128], top[0] % 128, :, 0]
+        ref = np.repeat(x, 2) + np.log(len(top))
+        assert (np.abs(_np(lse)[t] - ref) <= 2.0 ** -21 * np.abs(ref)).all()
+
+
+@MODES
 @pytest.mark.parametrize("n,heads,kv_heads", [(40000, 8, 1), (20001, 16, 2)])
 def test_long_cache(mode, n, heads, kv_heads):
     b = Batch([(0, n - 2), (0, n - 1), (1, 500)], [n, 501], heads, kv_heads, 64, seed=2)
