@@ -18,15 +18,17 @@
 //               zeroed and reported, since a zero probability times them is not zero;
 //   warps 4..19 softmax, eight warps a tile, two threads a (row, head) pair with
 //               64 logits each.  P is computed with the reference as it is; only
-//               when some P of the tile reaches 2 (the references are set so
+//               when some P of 32 pairs reaches 2 (the references are set so
 //               that the largest is 2^-7) are the maxima taken, references moved
 //               and O rescaled in tensor memory.  Bit 14 of a positive BF16 says
 //               that it is 2 or more, so the test is an OR of the packed P, and
 //               it rides on the barrier that both halves of S need before P
 //               goes over them.
-// Tensor memory, a tile: S (128 columns), O (D), and P in BF16: over S for D =
-// 128, which fills the 512 columns; apart from it for D = 64, where the next
-// page's logits then need not wait for this page's product.
+// Tensor memory: O (D columns a tile), and S (128 columns) with P in BF16 over it.
+// D = 128 fills the 512 columns; with D = 64 there is room for a third S, and
+// a tile's next logits then need not wait for its product (304 -> 298 us for a
+// prompt of 8192, 142 -> 138 us for ragged chunks once only the pairs' two warps
+// meet at a barrier and not the tile's eight).
 // Rows of several requests in one CTA take turns: a page of another request is
 // masked for the whole row.
 //
@@ -50,7 +52,7 @@ using paged::Parts;
 
 constexpr int PC_THREADS = 640;
 constexpr int PC_LOAD = 0, PC_MMA = 1, PC_CLEAN = 3, PC_SOFT0 = 4;  // first warps
-constexpr int PC_BAR_START = 3;  // named barriers: 1 and 2 are the tiles'
+constexpr int PC_BAR_START = 9;  // named barriers: 1 .. 8 are the softmax warps'
 constexpr int PC_META = 8;  // pages described ahead (the ring holds at most 4 of them)
 constexpr float kLift = 7.f;  // log2 of the room below P = 2, where a reference moves
 
@@ -61,11 +63,11 @@ struct Cfg {
   static constexpr int STAGES = D == 128 ? 5 : 8;      // K and V tiles in flight
   static constexpr int OFF_KV = 2 * TILE;
   static constexpr int OFF_MISC = OFF_KV + STAGES * TILE;
-  // tensor memory columns of a tile s: S at s * S_STEP, P and O
-  static constexpr bool P_APART = D == 64;  // there is room for P beside S
-  static constexpr int S_STEP = P_APART ? 256 : 128;
-  static constexpr int P_COL = P_APART ? 128 : 0;
-  static constexpr int O_COL = P_APART ? 192 : 256, O_STEP = P_APART ? 256 : 128;
+  // Tensor memory columns: buffers of 128 for S (with P over it), then O.  Two
+  // buffers, one a tile, or with room for a third (ROTATE) three that the tiles
+  // take in turn, so that a tile's next logits do not wait for its product.
+  static constexpr bool ROTATE = D == 64;
+  static constexpr int O_COL = ROTATE ? 384 : 256;
 };
 
 // One page as the consumers need it.
@@ -81,7 +83,7 @@ struct Page {
 struct Misc {
   // 32 barriers, initialised by a lane each
   uint64_t q_full, drained, kv_full[8], kv_empty[8], ready[4], pv_done[2], o_full[2];
-  uint64_t s_full[2], s_free[2], p_full[2];
+  uint64_t s_full[3], p_full[3];  // a buffer each
   uint32_t tmem;
   int abort;
   int n_it;  // pages this CTA works through
@@ -219,12 +221,11 @@ __device__ __forceinline__ int run_pages(const Run &R) {
   return R.lo < R.hi ? (R.hi - 1) / kBlock - R.lo / kBlock + 1 : 0;
 }
 
-// The MMAs of one step and the commits behind them, issued by one elected lane
-// in one branch (a branch for each instruction takes longer than its MMA).
+// The MMAs of one step and the commits behind them, for one elected lane.
 #define PC_MMA_PTX "tcgen05.mma.cta_group::1.kind::f16 "
 #define PC_COMMIT_PTX "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
 #define PC_BEGIN_PTX \
-  "{\n\t.reg .pred e, p, q;\n\t.reg .b32 a;\n\t.reg .b64 x, y;\n\telect.sync _|e, 0xffffffff;\n\t@!e bra DONE;\n\t"
+  "{\n\t.reg .pred p, q;\n\t.reg .b32 a;\n\t.reg .b64 x, y;\n\t"
 #define PC_COMMIT_IF_PTX(n) "setp.ne.u32 q, %" #n ", 0;\n\t@q " PC_COMMIT_PTX "[%" #n "];\n\t"
 #define PC_PV_PTX(k) \
   "add.u32 a, %1, " #k " * 8;\n\tadd.u64 x, %2, " #k " * 128;\n\t" PC_MMA_PTX "[%0], [a], x, %3, p;\n\t"
@@ -238,7 +239,7 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p_tmem, uint64_t v
                                          uint32_t freed, uint32_t done) {
   asm volatile(PC_BEGIN_PTX "setp.eq.b32 p, 0, 0;\n\t" PC_PV_PTX(0) PC_PV_PTX(1) PC_PV_PTX(2)
                    PC_PV_PTX(3) PC_PV_PTX(4) PC_PV_PTX(5) PC_PV_PTX(6) PC_PV_PTX(7)
-                       PC_COMMIT_IF_PTX(4) PC_COMMIT_IF_PTX(5) "DONE:\n\t}" ::"r"(d),
+                       PC_COMMIT_IF_PTX(4) PC_COMMIT_IF_PTX(5) "}" ::"r"(d),
                "r"(p_tmem), "l"(v), "r"(idesc), "r"(freed), "r"(done)
                : "memory");
 }
@@ -249,7 +250,7 @@ __device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k, uin
                                          uint32_t full, uint32_t freed) {
 #define PC_QK_END_PTX                                                                      \
   PC_COMMIT_PTX "[%4];\n\t{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%4];\n\t}\n\t" \
-  PC_COMMIT_IF_PTX(5) "DONE:\n\t}"
+  PC_COMMIT_IF_PTX(5) "}"
   if constexpr (D == 64)
     asm volatile(PC_BEGIN_PTX "setp.ne.b32 p, 0, 0;\n\t" PC_QK_PTX(0, 0) PC_QK_PTX(0, 1)
                      PC_QK_PTX(0, 2) PC_QK_PTX(0, 3) PC_QK_END_PTX ::"r"(d),
@@ -332,8 +333,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   // once they are under way.
   if (warp == PC_LOAD) {
     // ================================================================ loads
-    // (q_full, ..., o_full: one arrival; s_full two; s_free and p_full a warp each)
-    tc::mbar_init(&M->q_full + lane, lane < 26 ? 1 : (lane < 28 ? 2 : 8));
+    // (q_full, ..., o_full: one arrival; s_full two; p_full a warp each)
+    tc::mbar_init(&M->q_full + lane, lane < 26 ? 1 : (lane < 29 ? 2 : 8));
     if (lane == 0) M->abort = 0;
     tc::mbar_fence_init();
     __syncwarp();
@@ -451,49 +452,62 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   const uint32_t tmem = __reduce_or_sync(0xffffffffu, M->tmem);  // (into a uniform register)
   if (warp == PC_MMA && n_it > 0) {
     // ================================================================ MMA
-    constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128);
-    constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
-    const uint32_t kvs = tc::smem_u32(sm) + C::OFF_KV;
-    // descriptors of the first tiles; an address further on adds its sixteenths
-    const uint64_t dq = tc::desc_sw128(tc::smem_u32(sm)), dk = tc::desc_sw128(kvs);
-    const uint64_t dv = tc::desc_sw128_mn(kvs, 16384, 1024);
-    const uint32_t bar_s = tc::smem_u32(M->s_full), bar_pv = tc::smem_u32(M->pv_done),
-                   bar_kv = tc::smem_u32(M->kv_empty);
-    int sk = 0, sv = 1;  // stages of the next K and V
-    auto next_s = [&](int s) {
-      issue_qk<D>(tmem + s * C::S_STEP, dq + s * (C::TILE >> 4), dk + sk * (C::TILE >> 4), idesc_s,
-                  bar_s + 8 * s, s == n_sub - 1 ? bar_kv + 8 * sk : 0);
-    };
-    bool ok = pc_wait_warp(&M->q_full, 0, abort, a.status_dev) &&
-              pc_wait_warp(&M->kv_full[0], 0, abort, a.status_dev);
-    if (ok)
-      for (int s = 0; s < n_sub; ++s) next_s(s);
-    for (int j = 0; j < n_it && ok; ++j) {
-      const bool more = j + 1 < n_it;
-      sk = sk + 2 >= C::STAGES ? sk + 2 - C::STAGES : sk + 2;
-      // the page's V and the next page's K
-      ok = pc_wait_warp(&M->ready[j & 3], (j >> 2) & 1, abort, a.status_dev);
-      for (int s = 0; s < n_sub && ok; ++s) {
-        if (C::P_APART && more) {
-          // the next logits as soon as the softmax holds this page's
-          ok = pc_wait_warp(&M->s_free[s], j & 1, abort, a.status_dev);
-          tc::tc_fence_after();
-          if (ok) next_s(s);
+    // One lane does it all: a wait takes it 90 cycles where the whole warp, which has
+    // to agree on each, takes 160 to 320 (prompt of 8192 with 64 channels a head: 341 ->
+    // 302 us, with 128: 387 -> 381).
+    if (tc::elect_one()) {
+      constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128);
+      constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
+      const uint32_t kvs = tc::smem_u32(sm) + C::OFF_KV;
+      // descriptors of the first tiles; an address further on adds its sixteenths
+      const uint64_t dq = tc::desc_sw128(tc::smem_u32(sm)), dk = tc::desc_sw128(kvs);
+      const uint64_t dv = tc::desc_sw128_mn(kvs, 16384, 1024);
+      const uint32_t bar_s = tc::smem_u32(M->s_full), bar_pv = tc::smem_u32(M->pv_done),
+                     bar_kv = tc::smem_u32(M->kv_empty);
+      int sk = 0, sv = 1;  // stages of the next K and V
+      // The next logits, page qj of tile qs into buffer qb.
+      int qj = 0, qs = 0, qb = 0;
+      auto next_s = [&] {
+        if (C::ROTATE && qs == 0 && !pc_wait(&M->kv_full[sk], (qj >> 2) & 1, abort, a.status_dev))
+          return false;
+        issue_qk<D>(tmem + qb * 128, dq + qs * (C::TILE >> 4), dk + sk * (C::TILE >> 4), idesc_s,
+                    bar_s + 8 * qb, qs == n_sub - 1 ? bar_kv + 8 * sk : 0);
+        if (++qs == n_sub) {
+          qs = 0;
+          ++qj;
+          sk = sk + 2 >= C::STAGES ? sk + 2 - C::STAGES : sk + 2;
         }
-        ok = ok && pc_wait_warp(&M->p_full[s], j & 1, abort, a.status_dev);
-        if (!ok) break;
-        tc::tc_fence_after();
-        issue_pv(tmem + C::O_COL + s * C::O_STEP, tmem + s * C::S_STEP + C::P_COL,
-                 dv + sv * (C::TILE >> 4), idesc_o, s == n_sub - 1 ? bar_kv + 8 * sv : 0,
-                 C::P_APART ? bar_pv + 8 * s : 0);
-        if (!C::P_APART && more) next_s(s);  // over P, behind its product
+        qb = C::ROTATE ? (qb == 2 ? 0 : qb + 1) : qs;
+        return true;
+      };
+      bool ok = pc_wait(&M->q_full, 0, abort, a.status_dev) &&
+                (C::ROTATE || pc_wait(&M->kv_full[0], 0, abort, a.status_dev));
+      for (int n = 0; n < (C::ROTATE ? n_sub + 1 : n_sub) && qj < n_it && ok; ++n) ok = next_s();
+      int pb = 0;  // buffer of the next P, and the parity of its turn
+      uint32_t turn = 0;
+      for (int j = 0; j < n_it && ok; ++j) {
+        // the page's V and the next page's K
+        ok = pc_wait(&M->ready[j & 3], (j >> 2) & 1, abort, a.status_dev);
+        for (int s = 0; s < n_sub && ok; ++s) {
+          ok = pc_wait(&M->p_full[pb], turn, abort, a.status_dev);
+          if (!ok) break;
+          tc::tc_fence_after();
+          issue_pv(tmem + C::O_COL + s * D, tmem + pb * 128, dv + sv * (C::TILE >> 4), idesc_o,
+                   s == n_sub - 1 ? bar_kv + 8 * sv : 0, C::ROTATE ? bar_pv + 8 * s : 0);
+          if (++pb == (C::ROTATE ? 3 : n_sub)) {
+            pb = 0;
+            turn ^= 1;
+          }
+          if (qj < n_it) ok = next_s();  // over P, or over the P before it
+        }
+        sv = sv + 2 >= C::STAGES ? sv + 2 - C::STAGES : sv + 2;
       }
-      sv = sv + 2 >= C::STAGES ? sv + 2 - C::STAGES : sv + 2;
+      for (int s = 0; s < n_sub && ok; ++s) tc::mma_commit(&M->o_full[s]);
+      // every issued MMA has completed before tensor memory is released
+      tc::mma_commit(&M->drained);
+      tc::mbar_wait(&M->drained, 0, 100000000ull);
     }
-    for (int s = 0; s < n_sub && ok; ++s) tc::mma_commit_elect(&M->o_full[s]);
-    // every issued MMA has completed before tensor memory is released
-    tc::mma_commit_elect(&M->drained);
-    tc::mbar_wait(&M->drained, 0, 100000000ull);
+    __syncwarp();
   } else if (warp == PC_CLEAN && n_it > 0) {
     // ================================================================ V on mixed pages
     bool ok = true;
@@ -545,9 +559,9 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     const int s = (warp - PC_SOFT0) >> 3, half = ((warp - PC_SOFT0) >> 2) & 1;
     const int m = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + s * C::S_STEP + lane_off, tp = ts + C::P_COL;
-    const uint32_t to = tmem + C::O_COL + s * C::O_STEP + half * (D / 2) + lane_off;  // this half
-    const int bar = 1 + s;
+    uint32_t ts = tmem + s * 128 + lane_off;
+    const uint32_t to = tmem + C::O_COL + s * D + half * (D / 2) + lane_off;  // this half
+    const int bar = 1 + s * 4 + (warp & 3);  // of the two warps that share 32 rows
     const float sl2 = a.softmax_scale * paged::kLog2e;
     const int rr = s * G.rows_tile + m / g, t = t0 + rr, h = kvh * g + m % g;
     int req = -1, lo = 0, hi = 0;
@@ -560,6 +574,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     // P = 2^(x - ref): ref is kLift above the largest logit when it is set
     float ref = -INFINITY, l = 0.f;
     bool ok = true;
+    int buf = s;  // of the logits, and the parity of its turn
+    uint32_t turn = 0;
     if (s < n_sub && n_it > 0) {
       {
         uint32_t z[32];
@@ -570,12 +586,11 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       }
       // the tile's product of the page before is complete
       auto o_settled = [&](int j) {
-        if (C::P_APART && j > 0) pc_wait_warp(&M->pv_done[s], (j - 1) & 1, abort, a.status_dev);
+        if (C::ROTATE && j > 0) pc_wait_warp(&M->pv_done[s], (j - 1) & 1, abort, a.status_dev);
         tc::tc_fence_after();  // (else the logits were issued behind it)
       };
       for (int j = 0; j < n_it; ++j) {
-        ok = pc_wait_warp(&M->s_full[s], j & 1, abort, a.status_dev);
-        // the tile's eight warps go on or stop together
+        ok = pc_wait_warp(&M->s_full[buf], turn, abort, a.status_dev);
         Page &P = M->page[j % PC_META];
         const bool mixed = P.mixed != 0;
         // this half's columns that the row sees (all of them unless the page is mixed)
@@ -606,8 +621,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
             for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
             float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
             M->top[s][half][m] = top;
-            // (a wait that gave up is known to all eight warps of the tile here)
-            if (tc::bar_or(bar, 256, !ok)) {
+            // (a wait that gave up is known to both warps here)
+            if (tc::bar_or(bar, 64, !ok)) {
               ok = false;
               break;
             }
@@ -648,7 +663,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           // Both halves have read S before P goes over it.  (A thread without a
           // row has whatever was in shared memory for q: it asks for nothing.)
           const bool again =
-              tc::bar_or(bar, 256, !move && (((any & 0x40004000u) && req >= 0) || !ok));
+              tc::bar_or(bar, 64, !move && (((any & 0x40004000u) && req >= 0) || !ok));
           if (!again) break;
           move = true;
         }
@@ -658,7 +673,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           // values that are not finite are zero in the product; the rows that
           // see them add them here
           ok = pc_wait_warp(&M->ready[j & 3], (j >> 2) & 1, abort, a.status_dev);
-          if (tc::bar_or(bar, 256, !ok)) {
+          if (tc::bar_or(bar, 64, !ok)) {
             ok = false;
             break;
           }
@@ -694,26 +709,27 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
                   tmem_st16(to + d, o);
                 }
               }
-            tc::bar_sync(bar, 256);  // both halves have read S before P goes over it
+            tc::bar_sync(bar, 64);  // both halves have read S before P goes over it
           }
         }
-        if (C::P_APART) {
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&M->s_free[s]);
-          o_settled(j);  // and has read the P that goes now
-        }
-        tc::tmem_st32u(tp + 32 * half, w);
+        tc::tmem_st32u(ts + 32 * half, w);
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&M->p_full[s]);
+        if (lane == 0) tc::mbar_arrive(&M->p_full[buf]);
+        // the next page's buffer
+        if (C::ROTATE) buf += n_sub;
+        if (!C::ROTATE || buf >= 3) {
+          if (C::ROTATE) buf -= 3;
+          turn ^= 1;
+        }
+        if (C::ROTATE) ts = tmem + buf * 128 + lane_off;
       }
       if (ok) ok = pc_wait_warp(&M->o_full[s], 0, abort, a.status_dev);
       tc::tc_fence_after();
       // the row's sum over both halves
       M->top[s][half][m] = l;
-      if (tc::bar_or(bar, 256, !ok)) ok = false;
+      if (tc::bar_or(bar, 64, !ok)) ok = false;
       l = half ? M->top[s][0][m] + l : l + M->top[s][1][m];
     }
     // ---- the row's result, or its part

@@ -330,6 +330,14 @@ __device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t adesc, ui
       : "memory");
 }
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+               : "=r"(e));
+  return e != 0;
+}
+
 __device__ __forceinline__ void mma_commit_elect(uint64_t *bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
