@@ -169,7 +169,10 @@ struct Run {
 
 // All rows as one run, if they are one request's (the usual case, without the
 // registers and the code of the walk: that code is fetched cold by every CTA).
-__device__ __forceinline__ bool one_run(const csa_paged_attn_args &a, int t0, int n, Run &R) {
+// meanwhile() runs while the first rows are on their way.
+template <typename F>
+__device__ __forceinline__ bool one_run(const csa_paged_attn_args &a, int t0, int n, Run &R,
+                                        F &&meanwhile) {
   const int lane = threadIdx.x & 31;
   R = {0, n, 0x7FFFFFFF, 0, 0, 0x7FFFFFFF};
   bool same = true;
@@ -182,7 +185,10 @@ __device__ __forceinline__ bool one_run(const csa_paged_attn_args &a, int t0, in
       req[k] = a.row_req[t];
       pos[k] = a.row_pos[t];
     }
-    if (r == lane) R.req = __shfl_sync(0xffffffffu, req[0], 0);
+    if (r == lane) {
+      meanwhile();
+      R.req = __shfl_sync(0xffffffffu, req[0], 0);
+    }
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       len[k] = a.kv_len[req[k] >= 0 && req[k] < a.n_req ? req[k] : 0];
@@ -333,24 +339,25 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   // once they are under way.
   if (warp == PC_LOAD) {
     // ================================================================ loads
-    // (q_full, ..., o_full: one arrival; s_full two; p_full a warp each)
-    tc::mbar_init(&M->q_full + lane, lane < 26 ? 1 : (lane < 29 ? 2 : 8));
-    if (lane == 0) M->abort = 0;
-    tc::mbar_fence_init();
-    __syncwarp();
-    if (lane == 0) {
-      const uint32_t box = (uint32_t)(G.rows_tile * g * 128);
-      tc::mbar_arrive_expect_tx(&M->q_full, n_sub * C::CHUNKS * box);
-      for (int s = 0; s < n_sub; ++s)
-        for (int c = 0; c < C::CHUNKS; ++c)
-          tc::tma_load_3d(sm + s * C::TILE + c * 16384, &qmap, c * 64, kvh * g,
-                          t0 + s * G.rows_tile, &M->q_full);
-    }
     // Two walks over the runs of one request, the first to count the pages: this
     // part takes its share of them.
     Run R;
     Rows W;
-    const bool single = one_run(a, t0, n_rows, R);
+    const bool single = one_run(a, t0, n_rows, R, [&] {
+      // (q_full, ..., o_full: one arrival; s_full two; p_full a warp each)
+      tc::mbar_init(&M->q_full + lane, lane < 26 ? 1 : (lane < 29 ? 2 : 8));
+      if (lane == 0) M->abort = 0;
+      tc::mbar_fence_init();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t box = (uint32_t)(G.rows_tile * g * 128);
+        tc::mbar_arrive_expect_tx(&M->q_full, n_sub * C::CHUNKS * box);
+        for (int s = 0; s < n_sub; ++s)
+          for (int c = 0; c < C::CHUNKS; ++c)
+            tc::tma_load_3d(sm + s * C::TILE + c * 16384, &qmap, c * 64, kvh * g,
+                            t0 + s * G.rows_tile, &M->q_full);
+      }
+    });
     if (!single) read_rows(a, t0, n_rows, W);
     bool counting = true, many = false, ok = true;
     int total = 0, valid = 0, skip = 0, n_pages = 0, left = 0;
@@ -725,8 +732,6 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         }
         if (C::ROTATE) ts = tmem + buf * 128 + lane_off;
       }
-      if (ok) ok = pc_wait_warp(&M->o_full[s], 0, abort, a.status_dev);
-      tc::tc_fence_after();
       // the row's sum over both halves
       M->top[s][half][m] = l;
       if (tc::bar_or(bar, 64, !ok)) ok = false;
@@ -743,6 +748,11 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       const paged::Joined J = paged::finish(ref, l, sink);
       scale = J.inv;
       if (mine && half == 0 && a.lse) a.lse[row] = J.lse;
+    }
+    // (the last product has been under way all the while)
+    if (s < n_sub && n_it > 0) {
+      ok = ok && pc_wait_warp(&M->o_full[s], 0, abort, a.status_dev);
+      tc::tc_fence_after();
     }
     const bool zero = ref == -INFINITY && l == 0.f;  // nothing seen: O may hold nothing
     if (s < n_sub && ok) {
