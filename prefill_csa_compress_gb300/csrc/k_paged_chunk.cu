@@ -32,12 +32,14 @@
 // Rows of several requests in one CTA take turns: a page of another request is
 // masked for the whole row.
 //
-// What bounds it is the chain of one tile: 2,950 cycles a page for both tiles at D
-// = 128, where their MMAs take 2,048 -- the softmax of a tile 1,240 (reading the
-// logits 205, the probabilities 670, the barrier 160, storing them 200), its MMAs
-// 1,024, the rest the way from role to role.  A prompt of 8192 (32 query heads on 8
-// of 128) takes 390 us (1.41 PFLOP/s), 4096 rows of 64 heads over 65,536 positions
-// 5.6 ms (1.53 PFLOP/s).
+// What bounds it is the chain of one tile.  D = 128: 2,900 cycles a page for both
+// tiles, where their MMAs take 2,048 -- the softmax of a tile 1,500 (reading the
+// logits 300, the probabilities 700, the barrier 250, storing them 200), its MMAs
+// 1,024, the rest the way from role to role.  D = 64: 2,330 cycles, all of them the
+// softmax's (the warps issue half of the time, the exponentials' unit is busy for
+// 35 %).  A CTA's start and end take 14,000.  A prompt of 8192 (32 query heads on 8
+// of 128) takes 381 us (1.44 PFLOP/s), of 64 channels 288 us (0.95 PFLOP/s), 4096
+// rows of 64 heads of 128 over 65,536 positions 5.5 ms (1.54 PFLOP/s).
 #include <cuda.h>
 
 #include "attn_common.cuh"
