@@ -8,18 +8,24 @@
 // tcgen05 would be seven eighths padding at 16 pairs):
 //   S = Q K^T   warp w takes keys 16 w .. 16 w + 15 of the page
 //   P = 2^(S scale log2(e) - ref), one reference per pair, shared by the CTA;
-//               it moves (and O is rescaled) only when a logit exceeds it by
-//               more than 2^8, which rides on the barrier before P is written
+//               the item's first page sets it; it moves (and O is rescaled) only
+//               when a logit exceeds it by more than 2^8, which a barrier votes on
 //   O += P V    warp w takes D / 8 output channels, P through shared memory,
 //               so no warp holds a partial O and an item ends without a merge.
 // A ninth warp keeps a ring of pages in flight by TMA.
 //
-// All pages of all items are one list, cut into equal shares, one per CTA (one
-// CTA per SM): ragged contexts and few rows load every SM alike.  A share that
-// starts or ends inside an item leaves a part in the workspace, at most two per
-// CTA, which paged_join_kernel puts together in page order.
+// All pages of all items are one list, cut into equal shares, one per CTA: ragged
+// contexts and few rows load every SM alike.  A share that starts or ends inside an
+// item leaves a part in the workspace, at most two per CTA, which
+// paged_join_kernel puts together in page order.  One CTA per SM keeps 192 KB of
+// pages in flight; for heads of 64, where a page is half as long and latency shows,
+// two keep 96 KB each (64 requests over 1000 positions of 8 x 64 47 -> 38 us, 32
+// to 16,384 of 4 x 64 104 -> 92; 4 x 2 rows at 131,072 194 -> 198).
 // 32 requests of one row with contexts to 16,384 (64 heads on 8 of 128): 207 us, 6.6
-// TB/s; 4 x 2 rows at 131,072 positions: 311 us, 6.9 TB/s, the rate of a plain copy.
+// TB/s; 4 x 2 rows at 131,072 positions: 311 us, 6.9 TB/s, the rate of a plain copy;
+// of 64 channels (rows of 128 bytes, 1 KB apart): 198 us, 5.4 TB/s.  A page takes a CTA
+// 2,400 cycles, an item of one page 6,000 (its logits 900, the references 500, the
+// product 1,100, the sums and the output 1,600).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -37,11 +43,12 @@ constexpr int PD_WARPS = 8, PD_THREADS = 32 * (PD_WARPS + 1);
 constexpr int PD_BAR = 1;
 constexpr float kMove = 8.f;
 
-template <int D, int MT>
+template <int D, int MT, int ST>
 struct Cfg {
   static constexpr int CHUNKS = D / 64;
   static constexpr int TILE = CHUNKS * 16384;  // bytes of a page of K (or V)
-  static constexpr int STAGES = D == 128 ? 3 : 6;
+  static constexpr int STAGES = ST;
+  static constexpr int CTAS = ST * 2 * TILE <= 98304 ? 2 : 1;  // an SM
   static constexpr int PAIRS = 16 * MT;
   static constexpr int Q_STRIDE = D + 8, P_STRIDE = kBlock + 8;  // elements, odd in 16 bytes
   static constexpr int OFF_Q = STAGES * 2 * TILE;
@@ -49,12 +56,23 @@ struct Cfg {
   static constexpr int OFF_MISC = OFF_P + PAIRS * P_STRIDE * 2;
 };
 
+// The list of items, by row, behind everything else in shared memory.
 struct Plan {
-  long long before[paged::kDecodeRows + 1];  // pages of all items of earlier rows
-  int req[paged::kDecodeRows];               // -1: padding, or no such request
-  int pages[paged::kDecodeRows];             // of an item that starts at this row, or 0
-  int first[paged::kDecodeRows];             // its first page
-  int lo[paged::kDecodeRows], hi[paged::kDecodeRows];  // positions that the row sees
+  long long *before;  // pages of all items of earlier rows; and of all rows
+  int *req;           // -1: padding, or no such request
+  int *pages;         // of an item that starts at this row, or 0
+  int *first;         // its first page
+  int *lo, *hi;       // positions that the row sees
+
+  __device__ Plan(void *at, int n) {
+    before = static_cast<long long *>(at);
+    req = reinterpret_cast<int *>(before + n + 1);
+    pages = req + n;
+    first = pages + n;
+    lo = first + n;
+    hi = lo + n;
+  }
+  static constexpr int bytes(int n) { return 8 * (n + 1) + 5 * 4 * n; }
 };
 
 template <int PAIRS>
@@ -63,10 +81,15 @@ struct Misc {
   int phys[6];  // the page in the stage, -1: unmapped
   int abort;
   uint32_t bad[2][4];  // keys of the page whose values are not finite (pages in turn)
-  int lo[PAIRS], hi[PAIRS];
-  float ref[PAIRS], top[PD_WARPS][PAIRS];
-  Plan plan;
+  int lo[2][PAIRS], hi[2][PAIRS];  // what a pair sees (items in turn)
+  float top[PD_WARPS][PAIRS], sum[PD_WARPS][PAIRS];
 };
+
+// Shared memory of a CTA for a call of n rows.
+template <int D, int MT, int ST>
+constexpr int smem_bytes(int n) {
+  return Cfg<D, MT, ST>::OFF_MISC + (int)sizeof(Misc<16 * MT>) + Plan::bytes(n);
+}
 
 __device__ __forceinline__ bool pd_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
                                         uint32_t *status) {
@@ -100,28 +123,32 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
 // c += a b: a 16 x 16 (row major), b 16 x 8, BF16, FP32 sums
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(PD_THREADS, 1)
+template <int D, int MT, int ST>
+__global__ void __launch_bounds__(PD_THREADS, (Cfg<D, MT, ST>::CTAS))
     paged_decode_kernel(csa_paged_attn_args a, DecodeParts parts,
                         const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
-  using C = Cfg<D, MT>;
+  using C = Cfg<D, MT, ST>;
   constexpr int PAIRS = C::PAIRS;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                            ~uintptr_t(1023));
+  // (a kernel without static shared memory gets it 1024-byte aligned; one that did
+  // not would stop before touching it)
+  extern __shared__ __align__(1024) uint8_t sm[];
   auto *M = reinterpret_cast<Misc<PAIRS> *>(sm + C::OFF_MISC);
-  Plan &plan = M->plan;
+  const Plan plan(M + 1, a.n_rows);
   tc::griddep_wait();
   tc::griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tc::smem_u32(sm) & 1023u) {
+    if (tid == 0) flag(a.status_dev, CSA_DEV_TIMEOUT);
+    return;
+  }
   volatile int *abort = &M->abort;
   const int g = a.n_heads / a.n_kv_heads;
   const int gt = min(g, PAIRS), rows = PAIRS / gt;       // heads and rows of an item
@@ -145,6 +172,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     M->abort = 0;
     tc::mbar_fence_init();
   }
+  if (tid < 8) M->bad[tid >> 2][tid & 3] = 0;
   __syncthreads();
   // ... and, for each row t that starts an item, the pages that it and the rows
   // after it see: up to the next multiple of `rows`, while they are the same request's
@@ -203,16 +231,24 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     }
     row0 = l;
   }
+  const int sub0 = (int)((w0 - plan.before[row0]) / plan.pages[row0]);
+  const int pa0 = (int)(w0 - plan.before[row0] - (long long)sub0 * plan.pages[row0]);
+  // the item behind item sub of row t (the last row is followed by none)
+  auto next_item = [&](int &t, int &sub) {
+    if (++sub < subs) return;
+    sub = 0;
+    do
+      ++t;
+    while (t < a.n_rows && plan.pages[t] == 0);
+  };
 
   if (warp == PD_WARPS) {
     // ================================================================ loads
     uint32_t it = 0;
     bool ok = true;
-    int t = row0;
+    int t = row0, sub = sub0, pa = pa0;
     for (long long w = w0; w < w1 && ok;) {
-      while (plan.before[t + 1] <= w) ++t;
       const int P = plan.pages[t];
-      const int sub = (int)((w - plan.before[t]) / P), pa = (int)((w - plan.before[t]) % P);
       const int pb = (int)min((long long)P, pa + (w1 - w));
       const int kvh = sub / head_tiles;
       const int32_t *table =
@@ -244,6 +280,8 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
         __syncwarp();
       }
       w += pb - pa;
+      pa = 0;
+      next_item(t, sub);
     }
     if (*abort)  // whatever was asked for has landed before the CTA retires
       for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
@@ -259,22 +297,20 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
   const int mi = lane >> 3, ri = lane & 7;  // ldmatrix: matrix and row of this lane's address
   const int fr = lane >> 2, fc = (lane & 3) * 2;  // fragment row and column
   constexpr int NV = D / 64;  // 8-channel tiles of O per warp
-  // The item that holds page w (row t or a later one), and this thread's 16-byte
-  // pieces of its q; rows and heads that it lacks are zero.
+  // Item sub of row t, from its page pa (page w of the list) on, and this thread's
+  // 16-byte pieces of its q; rows and heads that it lacks are zero.
   struct Item {
     int t, sub, pa, pb, h0, n_rows, n_heads;
   };
   constexpr int QN = PAIRS * (D / 8) / (32 * PD_WARPS);  // pieces a thread
-  auto item_at = [&](long long w, int t) {
+  auto item_at = [&](long long w, int t, int sub, int pa) {
     Item I;
-    while (plan.before[t + 1] <= w) ++t;
-    const int P = plan.pages[t];
     I.t = t;
-    I.sub = (int)((w - plan.before[t]) / P);
-    I.pa = (int)((w - plan.before[t]) % P);
-    I.pb = (int)min((long long)P, I.pa + (w1 - w));
-    const int kvh = I.sub / head_tiles;
-    I.h0 = kvh * g + I.sub % head_tiles * gt;
+    I.sub = sub;
+    I.pa = pa;
+    I.pb = (int)min((long long)plan.pages[t], pa + (w1 - w));
+    const int kvh = head_tiles == 1 ? sub : sub / head_tiles;
+    I.h0 = kvh * g + (sub - kvh * head_tiles) * gt;
     I.n_heads = min(gt, (kvh + 1) * g - I.h0);  // the last head tile may be short
     I.n_rows = 1;
     while (t + I.n_rows < a.n_rows && (t + I.n_rows) % rows != 0 &&
@@ -294,29 +330,33 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
                                                 (long long)(I.h0 + h) * D * 2 + c * 16);
     }
   };
-  uint32_t it = 0;
-  bool ok = true;
-  Item I = item_at(w0, row0);
-  uint4 q_next[QN > 0 ? QN : 1];
-  read_q(I, q_next);
-  for (long long w = w0; w < w1 && ok;) {
-    const int t = I.t, sub = I.sub, pa = I.pa, pb = I.pb, h0 = I.h0, n_heads = I.n_heads;
-    const int n_rows = I.n_rows, P = plan.pages[t], first = plan.first[t], kvh = sub / head_tiles;
-
-    // ---- Q and what each pair (row i / gt, head i % gt) sees
-    tc::bar_sync(PD_BAR, 32 * PD_WARPS);  // the previous item is done with Q and the statistics
+  // q and what each pair (row i / gt, head i % gt) sees, for the item's first page
+  auto set_item = [&](const Item &I, const uint4(&q)[QN > 0 ? QN : 1], int turn) {
 #pragma unroll
     for (int u = 0; u < (QN > 0 ? QN : 1); ++u) {
       const int i = u * 32 * PD_WARPS + tid, m = i / (D / 8), c = i % (D / 8);
-      if (m < PAIRS) *reinterpret_cast<uint4 *>(sm + C::OFF_Q + m * C::Q_STRIDE * 2 + c * 16) = q_next[u];
+      if (m < PAIRS) *reinterpret_cast<uint4 *>(sm + C::OFF_Q + m * C::Q_STRIDE * 2 + c * 16) = q[u];
     }
     if (tid < PAIRS) {
       const int r = tid / gt, h = tid % gt;
-      const bool on = r < n_rows && h < n_heads;
-      M->lo[tid] = on ? plan.lo[t + r] : 0;
-      M->hi[tid] = on ? plan.hi[t + r] : 0;
-      M->ref[tid] = -INFINITY;
+      const bool on = r < I.n_rows && h < I.n_heads;
+      M->lo[turn][tid] = on ? plan.lo[I.t + r] : 0;
+      M->hi[turn][tid] = on ? plan.hi[I.t + r] : 0;
     }
+  };
+  uint32_t it = 0;
+  bool ok = true;
+  int turn = 0;
+  Item I = item_at(w0, row0, sub0, pa0);
+  uint4 q_next[QN > 0 ? QN : 1];
+  read_q(I, q_next);
+  set_item(I, q_next, turn);
+  tc::bar_sync(PD_BAR, 32 * PD_WARPS);
+  for (long long w = w0; w < w1 && ok; turn ^= 1) {
+    const int t = I.t, sub = I.sub, pa = I.pa, pb = I.pb, h0 = I.h0, n_heads = I.n_heads;
+    const int n_rows = I.n_rows, P = plan.pages[t], first = plan.first[t];
+    const int kvh = head_tiles == 1 ? sub : sub / head_tiles;
+    const bool more = w + (pb - pa) < w1;
     // positions that every pair of the item sees (padding pairs aside)
     int all_lo = 0, all_hi = 0x7FFFFFFF;
     for (int r = 0; r < n_rows; ++r) {
@@ -332,18 +372,21 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
         sink[i][u] = a.sink && h < n_heads ? a.sink[h0 + h] : -INFINITY;
       }
     // the next item's q is on its way during this one
-    if (w + (pb - pa) < w1) {
-      I = item_at(w + (pb - pa), t);
+    if (more) {
+      int t_next = t, sub_next = sub;
+      next_item(t_next, sub_next);
+      I = item_at(w + (pb - pa), t_next, sub_next, 0);
       read_q(I, q_next);
     }
-    tc::bar_sync(PD_BAR, 32 * PD_WARPS);
     uint32_t qf[MT == 1 ? D / 16 : 1][4];
     if constexpr (MT == 1) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
         ldsm4(q_s + (((mi & 1) * 8 + ri) * C::Q_STRIDE + k * 16 + (mi >> 1) * 8) * 2, qf[k]);
     }
-    float o[MT][NV][4] = {}, l[MT][2] = {};
+    float o[MT][NV][4] = {}, l[MT][2] = {}, refs[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) refs[i][0] = refs[i][1] = -INFINITY;
 
     for (int p = pa; p < pb; ++p, ++it) {
       const int st = it % C::STAGES;
@@ -383,11 +426,11 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int m = i * 16 + u * 8 + fr;
-          const float ref = M->ref[m];
+          const float ref = refs[i][u];
           int lo = 0, hi = kBlock;
           if (mixed) {
-            lo = M->lo[m] - base;
-            hi = phys < 0 ? 0 : M->hi[m] - base;
+            lo = M->lo[turn][m] - base;
+            hi = phys < 0 ? 0 : M->hi[turn][m] - base;
           }
 #pragma unroll
           for (int n = 0; n < 2; ++n)
@@ -402,8 +445,6 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
       if (mixed) {
         // this warp's 16 rows of V: rows that nobody sees and values that are
         // not finite become zero, the latter are reported
-        if (tid < 4) M->bad[it & 1][tid] = 0;
-        tc::bar_sync(PD_BAR, 32 * PD_WARPS);
         const int row = warp * 16 + (lane & 15), half = lane >> 4;
         uint4 *v = reinterpret_cast<uint4 *>(sm + st * 2 * C::TILE + C::TILE + row * 128);
         uint32_t bad = 0;
@@ -422,8 +463,10 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
           if (half == 0 && phys >= 0) atomicOr(&M->bad[it & 1][row >> 5], 1u << (row & 31));
         }
       }
-      if (tc::bar_or(PD_BAR, 32 * PD_WARPS, exceeds)) {
-        // ---- some reference moves: the pairs' largest logits of the page
+      // ---- references: set by the item's first page, and moved when a logit
+      // exceeds one by too much, to the pairs' largest logits of the page
+      const bool start = p == pa;
+      if (start || tc::bar_or(PD_BAR, 32 * PD_WARPS, exceeds)) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -443,31 +486,27 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
             float top = M->top[0][m];
 #pragma unroll
             for (int q = 1; q < PD_WARPS; ++q) top = fmaxf(top, M->top[q][m]);
-            const float ref = M->ref[m];
-            const float f = top > ref + kMove && ref > -INFINITY ? exp2f(ref - top) : 1.f;
-            l[i][u] *= f;
+            const float ref = refs[i][u];
+            if (top > ref + kMove) {
+              const float f = ref > -INFINITY ? exp2f(ref - top) : 1.f;
+              refs[i][u] = top;
+              l[i][u] *= f;
 #pragma unroll
-            for (int n = 0; n < NV; ++n) {
-              o[i][n][2 * u] *= f;
-              o[i][n][2 * u + 1] *= f;
+              for (int n = 0; n < NV; ++n) {
+                o[i][n][2 * u] *= f;
+                o[i][n][2 * u + 1] *= f;
+              }
             }
           }
-        tc::bar_sync(PD_BAR, 32 * PD_WARPS);  // everyone has read the old references
-        if (tid < PAIRS) {
-          float top = M->top[0][tid];
-#pragma unroll
-          for (int q = 1; q < PD_WARPS; ++q) top = fmaxf(top, M->top[q][tid]);
-          if (top > M->ref[tid] + kMove) M->ref[tid] = top;
-        }
-        tc::bar_sync(PD_BAR, 32 * PD_WARPS);
       }
+      if (tid < 4) M->bad[~it & 1][tid] = 0;  // for the next page
       // ---- P, rounded to BF16 for the product; the sums take it unrounded
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int m = i * 16 + u * 8 + fr;
-          const float ref = M->ref[m], r0 = ref == -INFINITY ? 0.f : ref;
+          const float ref = refs[i][u], r0 = ref == -INFINITY ? 0.f : ref;
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const float y0 = attn::exp2_sfu(x[i][n][2 * u] - r0);
@@ -520,7 +559,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
                 const int m = i * 16 + u * 8 + fr;
-                if (c + base < M->lo[m] || c + base >= M->hi[m]) continue;
+                if (c + base < M->lo[turn][m] || c + base >= M->hi[turn][m]) continue;
                 const float pr = __bfloat162float(Ps[m * C::P_STRIDE + c]);
 #pragma unroll
                 for (int n = 0; n < NV; ++n)
@@ -536,23 +575,26 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     }
     if (!ok) break;
 
-    // ---- the sums of all warps' keys, then the result or a part of it
+    // ---- the sums of all warps' keys, then the result or a part of it; the next
+    // item's q takes this one's place (all warps are past their last logits)
+    if (more) set_item(I, q_next, turn ^ 1);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         l[i][u] += __shfl_xor_sync(0xffffffffu, l[i][u], 1);
         l[i][u] += __shfl_xor_sync(0xffffffffu, l[i][u], 2);
-        if ((lane & 3) == 0) M->top[warp][i * 16 + u * 8 + fr] = l[i][u];
+        if ((lane & 3) == 0) M->sum[warp][i * 16 + u * 8 + fr] = l[i][u];
       }
     tc::bar_sync(PD_BAR, 32 * PD_WARPS);
     const bool whole = pa == 0 && pb == P;
     const long long slot = 2 * (long long)blockIdx.x + (pa == 0 ? 1 : 0);
     if (pa == 0 && tid < n_rows) {
       // which CTAs hold the item, for the join
-      const long long last = plan.before[t] + (long long)(sub + 1) * P - 1;
-      parts.item[(long long)(t + tid) * subs + sub] =
-          make_int4((int)blockIdx.x, (int)(((last + 1) * N - 1) / W), t, 0);
+      int last = blockIdx.x;
+      if (pb < P)
+        last = (int)(((plan.before[t] + (long long)(sub + 1) * P) * N - 1) / W);
+      parts.item[(long long)(t + tid) * subs + sub] = make_int4((int)blockIdx.x, last, t, 0);
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -560,10 +602,10 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
       for (int u = 0; u < 2; ++u) {
         const int m = i * 16 + u * 8 + fr, r = m / gt, h = m % gt;
         if (r >= n_rows || h >= n_heads) continue;
-        float sum = M->top[0][m];
+        float sum = M->sum[0][m];
 #pragma unroll
-        for (int q = 1; q < PD_WARPS; ++q) sum += M->top[q][m];
-        const float ref = M->ref[m];
+        for (int q = 1; q < PD_WARPS; ++q) sum += M->sum[q][m];
+        const float ref = refs[i][u];
         const bool zero = ref == -INFINITY && sum == 0.f;
         if (whole) {
           const long long row = (long long)(t + r) * a.n_heads + h0 + h;
@@ -647,31 +689,32 @@ __global__ void __launch_bounds__(128)
   if (a.lse && lane == 0) a.lse[row] = J.lse;
 }
 
-template <int D, int MT>
-cudaError_t launch(const csa_paged_attn_args &a, const DecodeParts &parts, int sms,
+template <int D, int MT, int ST>
+cudaError_t launch(const csa_paged_attn_args &a, const DecodeParts &parts, int ctas,
                    cudaStream_t s) {
-  using C = Cfg<D, MT>;
+  using C = Cfg<D, MT, ST>;
   CUtensorMap kmap, vmap;
   if (!paged::encode_pools(a, &kmap, &vmap)) return cudaErrorInvalidValue;
-  const size_t smem = C::OFF_MISC + sizeof(Misc<C::PAIRS>) + 1024;
-  static_assert(C::OFF_MISC + sizeof(Misc<C::PAIRS>) + 1024 <= 227 * 1024, "shared memory");
+  constexpr int most = smem_bytes<D, MT, ST>(paged::kDecodeRows);
+  static_assert(most <= 227 * 1024, "shared memory");
+  static_assert(sizeof(Misc<C::PAIRS>) % 8 == 0 && C::OFF_MISC % 8 == 0, "alignment");
   int dev = 0;
   cudaGetDevice(&dev);
   static bool attr[64] = {};
   if (dev < 0 || dev >= 64 || !attr[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(
-        paged_decode_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        paged_decode_kernel<D, MT, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr[dev] = true;
   }
   launch_begin(CSA_K_PAGED_ATTN, s);
-  cudaError_t e = launch_kernel(paged_decode_kernel<D, MT>, dim3(sms), dim3(PD_THREADS), smem, s, 0,
-                                false, a, parts, kmap, vmap);
+  cudaError_t e = launch_kernel(paged_decode_kernel<D, MT, ST>, dim3(ctas), dim3(PD_THREADS),
+                                smem_bytes<D, MT, ST>(a.n_rows), s, 0, false, a, parts, kmap, vmap);
   launch_end(CSA_K_PAGED_ATTN, s);
   if (e != cudaSuccess) return e;
   launch_begin(CSA_K_PAGED_MERGE, s);
   e = launch_kernel(paged_join_kernel<D>, dim3((unsigned)(a.n_rows * a.n_heads)), dim3(128), 0, s, 0,
-                    false, a, parts, C::PAIRS, sms);
+                    false, a, parts, C::PAIRS, ctas);
   launch_end(CSA_K_PAGED_MERGE, s);
   return e;
 }
@@ -688,27 +731,41 @@ int paged_decode_items(const csa_paged_attn_args &a, int rows) {
   return g < pairs ? (rows + pairs / g - 1) / (pairs / g) : rows * ((g + pairs - 1) / pairs);
 }
 
+namespace {
+
+// Two CTAs an SM for heads of 64, where they fit: up to 330 rows in items of 16
+// pairs, 48 in items of 32 (the figures are at the top).
+bool two_ctas(const csa_paged_attn_args &a) {
+  constexpr int half = 228 * 1024 / 2 - 1024;  // of an SM's shared memory
+  return a.head_dim == 64 && (pair_tiles(a) == 1 ? smem_bytes<64, 1, 3>(a.n_rows)
+                                                 : smem_bytes<64, 2, 3>(a.n_rows)) <= half;
+}
+
+}  // namespace
+
 size_t paged_decode_workspace(const csa_paged_attn_args &a, int sms) {
   const int pairs = 16 * pair_tiles(a);
   const int g = a.n_heads / a.n_kv_heads, gt = g < pairs ? g : pairs;
   const size_t subs = (size_t)a.n_kv_heads * ((g + gt - 1) / gt);
-  const size_t slots = 2 * (size_t)sms * pairs;
+  const size_t slots = 2 * (size_t)sms * (two_ctas(a) ? 2 : 1) * pairs;
   return align_up(slots * a.head_dim * sizeof(float), 256) + align_up(slots * sizeof(float2), 256) +
          align_up((size_t)a.n_rows * subs * sizeof(int4), 256);
 }
 
 cudaError_t launch_paged_decode(const csa_paged_attn_args &a, int sms, cudaStream_t s) {
-  const int mt = pair_tiles(a);
-  const size_t slots = 2 * (size_t)sms * 16 * mt;
+  const int mt = pair_tiles(a), ctas = sms * (two_ctas(a) ? 2 : 1);
+  const size_t slots = 2 * (size_t)ctas * 16 * mt;
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   DecodeParts parts;
   parts.o = reinterpret_cast<float *>(ws);
   ws += align_up(slots * a.head_dim * sizeof(float), 256);
   parts.ml = reinterpret_cast<float2 *>(ws);
   parts.item = reinterpret_cast<int4 *>(ws + align_up(slots * sizeof(float2), 256));
-  if (a.head_dim == 64)
-    return mt == 1 ? launch<64, 1>(a, parts, sms, s) : launch<64, 2>(a, parts, sms, s);
-  return mt == 1 ? launch<128, 1>(a, parts, sms, s) : launch<128, 2>(a, parts, sms, s);
+  if (a.head_dim == 128)
+    return mt == 1 ? launch<128, 1, 3>(a, parts, ctas, s) : launch<128, 2, 3>(a, parts, ctas, s);
+  if (ctas > sms)
+    return mt == 1 ? launch<64, 1, 3>(a, parts, ctas, s) : launch<64, 2, 3>(a, parts, ctas, s);
+  return mt == 1 ? launch<64, 1, 6>(a, parts, ctas, s) : launch<64, 2, 6>(a, parts, ctas, s);
 }
 
 }  // namespace csa

@@ -621,6 +621,29 @@ def test_many_single_rows(mode, n, heads, kv_heads):
     Batch([(b, max(int(k) - 1, 0)) for b, k in enumerate(lens)], lens.tolist(), heads, kv_heads, 64).check(mode)
 
 
+@pytest.mark.parametrize("n,heads,kv_heads", [(30, 40, 2), (48, 17, 1), (49, 17, 1), (330, 4, 2), (345, 4, 2)])
+def test_single_rows_of_narrow_heads(n, heads, kv_heads):
+    """Either side of the row counts up to which two CTAs share an SM; every
+    third context ends inside a page that holds NaN from there on."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(1, 700, n)
+    lens[::7] = 128
+    b = Batch([(i, int(lens[i]) - 1 + (i % 3 == 0)) for i in range(n)], lens, heads, kv_heads, 64, seed=n)
+    b.check(DECODE)
+    b.check(DECODE, window=200)
+
+
+def test_chosen_kernel_agrees():
+    """Sizes around the choice between the two kernels: the chosen one's result
+    is one of the two."""
+    for req, rows, heads, kv, dim in ((4, 16, 32, 8, 128), (24, 8, 64, 8, 64), (3, 8, 32, 1, 128), (2, 12, 16, 4, 64)):
+        b = Batch([r for i in range(req) for r in chunk(i, 90 + 30 * i, rows)],
+                  [90 + 30 * i + rows for i in range(req)], heads, kv, dim)
+        got = b.check(csa.CSA_MODE_AUTO)
+        both = [b.call(m) for m in (DECODE, PREFILL)]
+        assert any(torch.equal(got[0], o) and torch.equal(got[1], l) for o, l, _ in both)
+
+
 @MODES
 def test_equal_positions_and_far_rows(mode):
     """Rows that repeat a position, and positions far past the cache."""
