@@ -124,16 +124,20 @@ bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims
 // heads on), the chunk kernel once for up to 256 pairs, but works through the
 // requests of a CTA's rows one after the other.  With the average rows of a
 // request: up to two items, decode (8 requests of 8 rows of 4 heads over 1000
-// positions 21 us against 40, 64 requests of 1 row 55 against 239); up to four
-// where several requests have few pages each (8 x 16 rows over 100 positions 17
-// against 24, over 8000 positions 167 against 87); else chunks (8 x 32 rows, 1000
-// positions 56 against 27).  Results do not depend on it but for rounding.
-bool use_decode(const csa_paged_attn_args &a) {
+// positions 20 us against 37, 64 requests of 1 row 52 against 165).  Several
+// requests of more items too, while there are at most two an SM, a request's pages
+// are not read too often, and a request does not fill a chunk CTA: 4 x 16 rows of 4
+// heads over 600 positions 18 us against 26, 8 of them over 2000 43 against 44.  Else
+// chunks: 24 of them over 600 (59 us against 37), 8 over 8000 (168 against 91), 12 x
+// 8 rows of 32 heads over 400 (20 against 15).  Results do not depend on it but for
+// rounding.
+bool use_decode(const csa_paged_attn_args &a, int sms) {
   if (a.mode == CSA_MODE_PREFILL || a.n_rows > paged::kDecodeRows) return false;
   if (a.mode == CSA_MODE_DECODE) return true;
   const int per = (int)(((long long)a.n_rows + a.n_req - 1) / a.n_req);
-  const int items = paged_decode_items(a, per);
-  return items <= 2 || (items <= 4 && a.n_req > 1 && a.max_blocks <= 4);
+  const long long items = paged_decode_items(a, per);
+  return items <= 2 || (a.n_req > 1 && items * a.n_req * a.n_kv_heads <= 2 * sms &&
+                        items * a.max_blocks <= 64 && per * (a.n_heads / a.n_kv_heads) < 256);
 }
 
 struct Layout {
@@ -143,7 +147,7 @@ struct Layout {
 };
 
 Layout layout(const csa_paged_attn_args &a, int sms) {
-  Layout L{use_decode(a), 1, 0, 0};
+  Layout L{use_decode(a, sms), 1, 0, 0};
   if (L.decode) {
     L.total = paged_decode_workspace(a, sms);
     return L;
