@@ -15,16 +15,22 @@ namespace {
 using headvec::Rope;
 
 constexpr int NR_THREADS = 256;
-// Blocks an SM: three keep 24 warps' loads in flight within 85 registers a thread
-// (8192 rows of 64 heads of 512: 183 us, 6.0 TB/s; two blocks 223 us, and two heads
-// at once instead of four with four blocks 196 us).  Partners fetched beside their
-// chunks (half layout above 256 channels) need more registers.
+// Blocks an SM, for the loads in flight within the registers that are left to a thread:
+// above 256 channels three (85 registers; 8192 rows of 64 heads of 512: 183 us, 6.0
+// TB/s; two blocks 223 us, and two heads at once instead of four with four blocks 196
+// us), up to 256 five (48 registers; 16384 rows of 32 + 8 heads of 128, adjacent pairs:
+// 64 us, 5.2 TB/s; three blocks 81, four 70, six 67), four for halves, whose partners'
+// angles and gammas come along (85 us; three blocks 91, five 112).  Partners fetched
+// beside their chunks (halves above 256 channels) need more registers.
 template <int C, bool HALF>
-constexpr int kBlocks = C == 1 || !HALF ? 3 : 1;
-// The publication kernel takes more registers; with one head a warp there are
-// many short warps, and more of them help (8192 rows of 512: 10.0 -> 9.3 us).
+constexpr int kBlocks = C == 1 ? (HALF ? 4 : 5) : (HALF ? 1 : 3);
+// The publication kernel.  With one head a warp there are many short warps, and four
+// blocks help (8192 rows of 512: 10.0 -> 9.3 us).  With several heads a warp, of up to 256
+// channels: adjacent pairs four (8192 rows of 8 + 8 heads of 128 17.5 us, 64 rows 2.8;
+// three 19.0 and 2.8, two 23.1 and 2.6), halves two (25.1 and 2.9; three 23.1 and 3.5,
+// one 42.7 and 2.8); above that two (the 8192 of 512: 31.7 us; three 39.0, one 46.6).
 template <int C, int U, bool HALF>
-constexpr int kAppendBlocks = U == 1 && (C == 1 || !HALF) ? 4 : 1;
+constexpr int kAppendBlocks = U == 1 ? (C == 1 || !HALF ? 4 : 1) : (C == 1 && !HALF ? 4 : 2);
 
 __device__ __forceinline__ const uint16_t *at(const void *base, long long bytes) {
   return reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(base) + bytes);
