@@ -282,7 +282,8 @@ class PagedAttnStep:
     step's rows included), k_pool, v_pool, kv_table, rope_cos, rope_sin, and
     optionally q_gamma, k_gamma and sink.  It owns the normed queries, out, lse
     and the attention's workspace; like ``CsaStep`` it computes nothing itself,
-    issues its calls on one stream, and takes its place in a ``StepChain``.
+    issues its calls on one stream, takes its place in a ``StepChain``, and
+    reads ``t``, ``out`` and ``lse`` when it runs, or when it is prepared.
     """
 
     before_attention = None
@@ -296,32 +297,40 @@ class PagedAttnStep:
         self.lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
         self.status = status_buf if status_buf is not None else torch.zeros(
             1, dtype=torch.int32, device=q.device)
-        rope = dict(rope_cos=t["rope_cos"], rope_sin=t["rope_sin"], rope_layout=rope_layout, eps=eps,
-                    status=self.status)
-        self._calls = (
-            (P.csa_qk_norm_rope, dict(q=q, q_out=self.q, row_pos=t["row_pos"], row_req=t["row_req"],
-                                      q_gamma=t.get("q_gamma"), **rope)),
+        self.causal, self.window = bool(causal), int(window)
+        self.rope_layout, self.eps = rope_layout, float(eps)
+        self.ws = None
+        self._prepared = None
+        self._graph = None
+
+    def _calls(self):
+        t = self.t
+        rope = dict(rope_cos=t["rope_cos"], rope_sin=t["rope_sin"], rope_layout=self.rope_layout,
+                    eps=self.eps, status=self.status)
+        return (
+            (P.csa_qk_norm_rope, dict(q=t["q"], q_out=self.q, row_pos=t["row_pos"],
+                                      row_req=t["row_req"], q_gamma=t.get("q_gamma"), **rope)),
             (P.csa_kv_append, dict(k=t["k"], v=t["v"], row_req=t["row_req"], row_pos=t["row_pos"],
                                    block_table=t["kv_table"], k_pool=t["k_pool"],
                                    v_pool=t["v_pool"], norm=True, k_gamma=t.get("k_gamma"), **rope)),
             (P.csa_paged_attn, dict(q=self.q, row_req=t["row_req"], row_pos=t["row_pos"],
                                     k_pool=t["k_pool"], v_pool=t["v_pool"],
                                     block_table=t["kv_table"], kv_len=t["kv_len"], out=self.out,
-                                    lse=self.lse, sink=t.get("sink"), causal=causal,
-                                    window=window, status=self.status)))
-        self._prepared = None
-        self._graph = None
+                                    lse=self.lse, sink=t.get("sink"), causal=self.causal,
+                                    window=self.window, status=self.status, workspace=self.ws)))
 
     def prepare(self):
         """Marshal the step's calls once (buffers must stay in place)."""
-        self._prepared = [fn(prepare=True, **kw) for fn, kw in self._calls]
+        self._prepared = [fn(prepare=True, **kw) for fn, kw in self._calls()]
         return self
 
     def run(self, stream=None):
         if self._prepared is None:
-            self.prepare()
-        for c in self._prepared:
-            c(stream)
+            for fn, kw in self._calls():
+                self.ws = fn(stream=stream, **kw)  # (the attention's is the last)
+        else:
+            for c in self._prepared:
+                c(stream)
 
     def capture(self):
         """Record one step into a CUDA graph.  Call after a warm-up ``run``."""
