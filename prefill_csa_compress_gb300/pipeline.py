@@ -283,10 +283,10 @@ class PagedAttnStep:
     optionally q_gamma, k_gamma and sink.  It owns the normed queries, out, lse
     and the attention's workspace; like ``CsaStep`` it computes nothing itself,
     issues its calls on one stream, takes its place in a ``StepChain``, and
-    reads ``t``, ``out`` and ``lse`` when it runs, or when it is prepared.
+    reads ``t``, ``out`` and ``lse`` when it runs, or when it is prepared.  Its first
+    call reads the queries and its second the keys, so ``before_attention`` (what
+    ``StepIO`` sets to wait for late inputs) is called before all of them.
     """
-
-    before_attention = None
 
     def __init__(self, t: dict, causal: bool = True, window: int = 0, rope_layout: str = "adjacent",
                  eps: float = 1e-6, status_buf=None):
@@ -299,6 +299,7 @@ class PagedAttnStep:
             1, dtype=torch.int32, device=q.device)
         self.causal, self.window = bool(causal), int(window)
         self.rope_layout, self.eps = rope_layout, float(eps)
+        self.before_attention = None
         self.ws = None
         self._prepared = None
         self._graph = None
@@ -325,6 +326,8 @@ class PagedAttnStep:
         return self
 
     def run(self, stream=None):
+        if self.before_attention:
+            self.before_attention(stream)
         if self._prepared is None:
             for fn, kw in self._calls():
                 self.ws = fn(stream=stream, **kw)  # (the attention's is the last)

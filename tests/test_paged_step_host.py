@@ -105,3 +105,17 @@ def test_unprepared_step_runs_on_its_stream(log):
     assert calls[2][1]["window"] == 7 and calls[2][1]["causal"] is False
     for _, kw, _ in calls[:2]:
         assert kw["rope_layout"] == "half" and kw["eps"] == 1e-5
+
+
+@pytest.mark.parametrize("prepared", [False, True])
+def test_late_inputs_are_waited_for(log, prepared):
+    """What StepIO sets to wait for late inputs is called once a run, on the
+    run's stream, before anything reads an input."""
+    step = PL.PagedAttnStep(tensors())
+    if prepared:
+        step.prepare()
+    step.before_attention = lambda stream: log.append(("wait", {}, stream))
+    for stream in (None, "s"):
+        log.clear()
+        step.run(stream)
+        assert [e[0] for e in log if e[0] != "prof_join"] == ["wait", *NAMES] and log[0][2] == stream
