@@ -334,6 +334,7 @@ class PagedAttnStep:
         else:
             for c in self._prepared:
                 c(stream)
+        B.prof_join(stream)
 
     def capture(self):
         """Record one step into a CUDA graph.  Call after a warm-up ``run``."""

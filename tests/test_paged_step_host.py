@@ -119,3 +119,13 @@ def test_late_inputs_are_waited_for(log, prepared):
         log.clear()
         step.run(stream)
         assert [e[0] for e in log if e[0] != "prof_join"] == ["wait", *NAMES] and log[0][2] == stream
+
+
+@pytest.mark.parametrize("prepared", [False, True])
+def test_timing_events_are_joined(log, prepared):
+    """A run ends by joining the timing side stream, as a capture needs."""
+    step = PL.PagedAttnStep(tensors())
+    if prepared:
+        step.prepare()
+    step.run("s")
+    assert [e[0] for e in log] == [*NAMES, "prof_join"] and log[-1][2] == "s"
