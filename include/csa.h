@@ -539,9 +539,9 @@ typedef enum {
  * that turns beta_slow times (r = 1): lo = max(floor(c(beta_fast)), 0), hi =
  * min(ceil(c(beta_slow)), rope_dim - 1), c(b) = rope_dim * ln(orig_len / (2 pi
  * b)) / (2 ln theta).
- * The angle is reduced exactly (the turns per position as a 64-bit fraction,
- * multiplied by the position modulo 1), so far positions are as accurate as
- * near ones: within 2e-7 of the 64-bit value times attn_factor.
+ * The f_i are taken in FP64.  Their product with the position is reduced from a
+ * 64-bit fraction of turns, so far positions are as accurate as near ones: within
+ * 2e-7 attn_factor of the cosine and sine of the exact product, up to position 2^31.
  *
  * rope_dim even, 2 .. 512 (NTK: at least 4); theta > 1, finite; factor >= 1
  * (LINEAR, NTK, YARN); orig_len > 0 and beta_fast >= beta_slow > 0 (YARN);

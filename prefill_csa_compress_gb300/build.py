@@ -25,6 +25,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+    # host arithmetic as written on every machine (RoPE frequencies: no fused products)
+    "-Xcompiler", "-ffp-contract=off",
     "-I", INCLUDE, "-I", CSRC,
 ]
 

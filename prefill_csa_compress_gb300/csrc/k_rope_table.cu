@@ -1,10 +1,10 @@
 // FP32 half-width RoPE tables (csa_rope_table).
 //
 // Entry (p, i) is cos and sin of p * f_i.  The host turns each f_i into turns
-// per position as a 64-bit binary fraction F_i = f_i / (2 pi) * 2^64; p * F_i
-// modulo 2^64 is then the angle modulo one turn, in two integer multiplications.
-// F_i carries the 53 bits of f_i, so the angle of a far position is as exact as
-// p * f_i in 64-bit arithmetic; its top 32 bits are kept (1.5e-9 radians).
+// per position as a 64-bit binary fraction F_i = f_i / (2 pi) * 2^64, rounded once;
+// p * F_i modulo 2^64 is then the angle modulo one turn, in two integer
+// multiplications.  At p = 2^31 the rounding of F_i moves it by 3.7e-10 radians (a
+// quotient of 53 bits would by 2.4e-7); its top 32 bits are kept (1.5e-9 radians).
 #include <math.h>
 
 #include "csa_internal.cuh"
@@ -24,8 +24,10 @@ struct RopeTurns {
 // turn taken off leaves |r| <= pi/4, where
 //   sin r = r + r z (s0 + s1 z + s2 z^2),  cos r = 1 - z/2 + z^2 (c0 + c1 z + c2 z^2)
 // with z = r^2 and the polynomials that interpolate (sin(r)/r - 1)/z and (cos r -
-// 1 + z/2)/z^2 at the three Chebyshev nodes of [0, pi^2/16]: 5e-8 and 8e-8 off
-// in FP32.  The quarter turns swap and negate.
+// 1 + z/2)/z^2 at the three Chebyshev nodes of [0, pi^2/16].  In FP32 they are 0.95e-7
+// and 1.22e-7 off at most, nearly all of it the arithmetic's rounding (a fourth
+// coefficient leaves 0.88e-7 and 1.18e-7); scaled by an FP32 factor 1.82e-7 of it.
+// The quarter turns swap and negate.
 __device__ __forceinline__ float2 cos_sin(uint32_t phase) {
   const uint32_t quarter = (phase + 0x20000000u) >> 30;
   const float r = (float)(int32_t)(phase - (quarter << 30)) * 1.46291807927e-9f;  // 2 pi / 2^32
@@ -100,6 +102,16 @@ void frequencies(const csa_rope_table_args &a, double *f) {
   }
 }
 
+// Turns per position of a rotation of f <= 1 radians, as a 64-bit fraction (below
+// 0.16 * 2^64): 1 / (2 pi) as the sum of two doubles, the product's own rounding taken
+// along, and one rounding at the end.
+uint64_t turn_fraction(double f) {
+  constexpr double kInv = 0x1.45f306dc9c883p-3, kInvLow = -0x1.6b01ec5417056p-57;
+  const double p = f * kInv, low = fma(f, kInvLow, fma(f, kInv, -p));
+  const double s = ldexp(p, 64), whole = floor(s);
+  return (uint64_t)whole + (uint64_t)llrint((s - whole) + ldexp(low, 64));
+}
+
 }  // namespace
 
 cudaError_t launch_rope_table(const csa_rope_table_args &a, cudaStream_t s) {
@@ -107,10 +119,7 @@ cudaError_t launch_rope_table(const csa_rope_table_args &a, cudaStream_t s) {
   double f[RT_MAX_PAIRS];
   frequencies(a, f);
   RopeTurns turns;
-  for (int i = 0; i < RT_MAX_PAIRS; ++i) {
-    // f <= 1, so the fraction is below 0.16 * 2^64
-    turns.f[i] = i < pairs ? (uint64_t)llrint(ldexp(f[i] / 6.283185307179586476925, 62)) << 2 : 0;
-  }
+  for (int i = 0; i < RT_MAX_PAIRS; ++i) turns.f[i] = i < pairs ? turn_fraction(f[i]) : 0;
   const bool wide = pairs % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.cos) |
                                         reinterpret_cast<uintptr_t>(a.sin)) & 15u) == 0;
   const int rows = RT_THREADS / (wide ? pairs / 4 : pairs);

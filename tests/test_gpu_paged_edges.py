@@ -22,6 +22,37 @@ from test_gpu_paged import DEV, MODES, Batch, _bf, _close_vec, _i32, _np, _pool,
 LOWEST = -2 ** 31
 
 
+# ---------------------------------------------------------------- rope tables
+
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+def _exact_angle(pos, f):
+    """pos * f modulo a turn, from the exact product of the two numbers."""
+    x = pos * Fraction(f) / (2 * PI)
+    return float((x - round(x)) * 2 * PI)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(theta=500000.0), dict(theta=1.5), dict(scaling="linear", factor=3.0),
+    dict(scaling="ntk", factor=8.0), dict(scaling="yarn", factor=40.0, orig_len=4096),
+    dict(scaling="yarn", factor=7.0, orig_len=65536, theta=500000.0, beta_fast=16.0, beta_slow=2.0)])
+@pytest.mark.parametrize("pos0", [0, 131071, 2 ** 24 + 12345, 2147308307, 2 ** 31 - 7])
+@pytest.mark.parametrize("rope_dim,amp", [(128, 1.0), (64, 1.3688879454113936), (6, 0.5973347702152793)])
+def test_rope_table_far_positions(kw, pos0, rope_dim, amp):
+    """2e-7 of the FP64 rotation times the position, at any position (the
+    definition's frequencies, and their product with the position exactly; the
+    library's cosine of an FP64 angle adds 2^-52)."""
+    n_pos, pairs = 7, rope_dim // 2
+    cos, sin = torch.empty((n_pos, pairs), device=DEV), torch.empty((n_pos, pairs), device=DEV)
+    csa.csa_rope_table(cos=cos, sin=sin, pos0=pos0, attn_factor=amp, **kw)
+    torch.cuda.synchronize()
+    f = PO.rope_frequencies(rope_dim, **kw)
+    a = np.array([[_exact_angle(pos0 + j, float(f[i])) for i in range(pairs)] for j in range(n_pos)])
+    assert np.abs(_np(cos) - amp * np.cos(a)).max() <= 2e-7 * amp
+    assert np.abs(_np(sin) - amp * np.sin(a)).max() <= 2e-7 * amp
+
+
 # ---------------------------------------------------------------- attention
 
 
