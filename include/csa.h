@@ -515,8 +515,9 @@ CSA_API csa_status_t csa_sparse_attn_prefill(csa_attn_args *args, csa_stream_t s
  * of 8 (adjacent) or 16 (half), rope_start + rope_dim <= head_dim.  Tables
  * must be 16-byte aligned.
  * Norm, ditto: y = x * gamma / sqrt(mean(x^2) + eps) over the head_dim channels
- * of one head (gamma bf16 [head_dim], NULL: all ones).  Norm and rotation are
- * computed in FP32 and rounded once, where the result is stored.
+ * of one head (gamma bf16 [head_dim], NULL: all ones), for finite channels of any
+ * size: a head whose squares leave FP32 is scaled by a power of two first.  Norm and
+ * rotation are computed in FP32 and rounded once, where the result is stored.
  * Row strides are in bytes, multiples of 16, 0 meaning dense; the heads of a
  * row are contiguous.
  * ---------------------------------------------------------------------- */

@@ -19,7 +19,7 @@ constexpr int NR_THREADS = 256;
 // above 256 channels three (85 registers; 8192 rows of 64 heads of 512: 183 us, 6.0
 // TB/s; two blocks 223 us, and two heads at once instead of four with four blocks 196
 // us), up to 256 five (48 registers; 16384 rows of 32 + 8 heads of 128, adjacent pairs:
-// 64 us, 5.2 TB/s; three blocks 81, four 70, six 67), four for halves, whose partners'
+// 66 us, 5.1 TB/s; three blocks 81, four 70, six 67), four for halves, whose partners'
 // angles and gammas come along (85 us; three blocks 91, five 112).  Partners fetched
 // beside their chunks (halves above 256 channels) need more registers.
 template <int C, bool HALF>

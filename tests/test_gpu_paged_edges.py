@@ -53,6 +53,80 @@ def test_rope_table_far_positions(kw, pos0, rope_dim, amp):
     assert np.abs(_np(sin) - amp * np.sin(a)).max() <= 2e-7 * amp
 
 
+# ---------------------------------------------------------------- norms
+
+
+def _extreme_heads(rng, rows, heads, dim):
+    """Heads of one row at very different scales: the squares of the large ones
+    leave FP32 (some only in the sum of 512), those of the small ones vanish."""
+    x = rng.standard_normal((rows, heads, dim))
+    scales = [1.0, 1e18, 3e-38, 1e30, 1e-30, 2.0 ** 125, 2.0 ** -100, 1e19, 3e17]
+    for t in range(rows):
+        for h in range(heads):
+            x[t, h] *= scales[(3 * t + h) % len(scales)]
+    x = torch.from_numpy(x).clamp(-3e38, 3e38).bfloat16()
+    if rows > 1:
+        x[1, 0] = torch.finfo(torch.bfloat16).max
+        x[1, -1] = 2.0 ** -133  # the smallest BF16
+        x[1, -1, 0] = -(2.0 ** -130)
+    return x.to(DEV)
+
+
+@pytest.mark.parametrize("layout", ["adjacent", "half"])
+@pytest.mark.parametrize("heads,dim,rd", [(9, 512, 64), (2, 512, 512), (9, 128, 128), (5, 64, 32), (40, 8, 0), (3, 264, 208)])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+def test_norm_of_extreme_heads(layout, heads, dim, rd, eps):
+    """Finite channels of any size are normed as the formula says, in every head
+    by itself; NaN and infinities stay in their head."""
+    rng = np.random.default_rng(dim + heads)
+    rows = 7
+    x = _extreme_heads(rng, rows, heads, dim)
+    gamma = _bf(rng, dim)
+    pos = rng.integers(0, 50, rows)
+    cos, sin = PO.rope_table(50, rd or 2)
+    tabs = dict(rope_cos=torch.from_numpy(cos).float().to(DEV), rope_sin=torch.from_numpy(sin).float().to(DEV),
+                rope_layout=layout) if rd else {}
+    turn = dict(cos=_np(tabs["rope_cos"]), sin=_np(tabs["rope_sin"]), layout=layout) if rd else {}
+    ref = PO.norm_rotate(_np(x), pos, gamma=_np(gamma), eps=eps, **turn)
+    # below the normal range FP32 and BF16 resolve steps of 2^-149 and 2^-133 of the result
+    out = torch.empty_like(x)
+    csa.csa_qk_norm_rope(q=x, q_out=out, row_pos=_i32(pos), q_gamma=gamma, eps=eps, **tabs)
+    _close_vec(_np(out), ref, extra=2.0 ** -133)
+    pool, _ = _pool(2, heads, dim, "dense")
+    csa.csa_kv_append(k=x, row_req=_i32([0] * rows), row_pos=_i32(np.arange(rows)), block_table=_i32([[1]]),
+                      k_pool=pool, norm=True, k_gamma=gamma, eps=eps)
+    _close_vec(_np(pool[1, :rows]), PO.norm_rotate(_np(x), pos, gamma=_np(gamma), eps=eps), extra=2.0 ** -133)
+    for value in (math.nan, math.inf):
+        y = x.clone()
+        y[2, 0, dim // 2] = value
+        broken = torch.empty_like(x)
+        csa.csa_qk_norm_rope(q=y, q_out=broken, row_pos=_i32(pos), q_gamma=gamma, eps=eps, **tabs)
+        torch.cuda.synchronize()
+        assert broken[2, 0].isnan().any()
+        same = torch.ones((rows, heads), dtype=torch.bool, device=DEV)
+        same[2, 0] = False
+        assert torch.equal(broken[same], out[same])
+
+
+def test_publication_of_extreme_heads():
+    """The same into an MXFP8 pool: codes of values between -gamma sqrt(512) and it."""
+    rng = np.random.default_rng(8)
+    rows, dim = 9, 512
+    x = _extreme_heads(rng, rows, 1, dim)
+    codes = torch.zeros((1, 128, 1, dim), dtype=torch.uint8, device=DEV)
+    scales = torch.zeros((1, 128, 1, dim // 32), dtype=torch.uint8, device=DEV)
+    csa.csa_kv_append(k=x, row_req=_i32([0] * rows), row_pos=_i32(np.arange(rows)), block_table=_i32([[0]]), k_pool=codes,
+                      k_scale_pool=scales, norm=True, eps=0.0)
+    torch.cuda.synchronize()
+    ref = PO.norm_rotate(_np(x), np.zeros(rows), eps=0.0)[:, 0].reshape(rows, 16, 32)
+    got = _np(codes[0, :rows, 0].view(torch.float8_e4m3fn).float()).reshape(rows, 16, 32)
+    got = got * 2.0 ** (_np(scales[0, :rows, 0])[..., None] - 127)
+    # half a step of E4M3, and below its normal range (2^-6) half of 2^-9, times the group's scale, at most
+    # 2 amax / 448; FP32 as _close_vec counts it
+    amax = np.abs(ref).max(-1, keepdims=True)
+    assert (np.abs(got - ref) <= 2.0 ** -4 * np.abs(ref) + 2.0 ** -10 * amax / 224 + 2.0 ** -16 * amax).all()
+
+
 # ---------------------------------------------------------------- attention
 
 
