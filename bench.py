@@ -20,11 +20,11 @@ the host cores instead (a bounded sample of the same workload).
 from __future__ import annotations
 
 import argparse
-import glob
 import hashlib
 import json
 import math
 import os
+import re
 import subprocess
 import sys
 import threading
@@ -38,24 +38,24 @@ METRIC = "CSA decode token-rows/s + % HBM roofline; prefill tokens/s + % tensor 
 L2_FLUSH_BYTES = 256 << 20  # > 129 MB L2
 
 # DRAM traffic per launch from an ncu capture, keyed by kernel; each entry
-# names the source it was taken on (sha1 of the kernel's .cu) so a changed
+# names the sources it was taken on (a sha1 of them) so a changed
 # kernel reports null.  Values are from `ncu --metrics dram__bytes_read.sum,
 # dram__bytes_write.sum` captures of these same bench workloads.
 NCU_TRAFFIC = {
     # dram__bytes_read.sum + dram__bytes_write.sum of one launch (one-kernel ncu
     # captures, profiles/dram_traffic.md), keyed by the hash of the kernel's
-    # source and the shared headers
-    ("tiny_decode", "attn_decode"): {"bytes": 557310, "src": "3c516bde6e00"},
-    ("tiny_decode", "index_score"): {"bytes": 168448, "src": "5a17c226935a"},
-    ("serving_decode", "attn_decode"): {"bytes": 4609280, "src": "3c516bde6e00"},
-    ("serving_decode", "index_score"): {"bytes": 1558784, "src": "5a17c226935a"},
-    ("ratio1_decode", "index_score"): {"bytes": 70123776, "src": "5a17c226935a"},
-    ("ratio1_decode", "index_topk"): {"bytes": 4454144, "src": "4a72031579c9"},
-    ("million_decode", "index_score"): {"bytes": 142287616, "src": "5a17c226935a"},
-    ("million_decode", "attn_decode"): {"bytes": 17844736, "src": "3c516bde6e00"},
-    ("million_decode", "index_topk"): {"bytes": 8648704, "src": "4a72031579c9"},
-    ("chunked_prefill", "attn_prefill"): {"bytes": 1061745408, "src": "6c2a1d534303"},
-    ("chunked_prefill", "index_score"): {"bytes": 151614976, "src": "5a17c226935a"},
+    # source and the headers that it includes
+    ("tiny_decode", "attn_decode"): {"bytes": 557056, "src": "feea71e9003f"},
+    ("tiny_decode", "index_score"): {"bytes": 168704, "src": "3d62599c11ea"},
+    ("serving_decode", "attn_decode"): {"bytes": 4608512, "src": "feea71e9003f"},
+    ("serving_decode", "index_score"): {"bytes": 1560832, "src": "3d62599c11ea"},
+    ("ratio1_decode", "index_score"): {"bytes": 69963776, "src": "3d62599c11ea"},
+    ("ratio1_decode", "index_topk"): {"bytes": 4453888, "src": "b07977dcef29"},
+    ("million_decode", "index_score"): {"bytes": 142465792, "src": "3d62599c11ea"},
+    ("million_decode", "attn_decode"): {"bytes": 17844992, "src": "feea71e9003f"},
+    ("million_decode", "index_topk"): {"bytes": 8649216, "src": "b07977dcef29"},
+    ("chunked_prefill", "attn_prefill"): {"bytes": 1062021120, "src": "3f636bc5677f"},
+    ("chunked_prefill", "index_score"): {"bytes": 152042752, "src": "3d62599c11ea"},
 }
 
 
@@ -404,16 +404,31 @@ def _config(wl, args):
 # ---------------------------------------------------------------- GPU arm
 
 
+CSRC = os.path.join(ROOT, "prefill_csa_compress_gb300", "csrc")
+
+
+def _sources(name):
+    """A kernel's source file and the headers of its folder that it includes,
+    by way of others too."""
+    found, todo = [], [name]
+    while todo:
+        n = todo.pop()
+        path = os.path.join(CSRC, n)
+        if path in found or not os.path.exists(path):  # (the public header is no kernel code)
+            continue
+        found.append(path)
+        with open(path) as f:
+            todo += re.findall(r'^\s*#include "([^"]+)"', f.read(), re.M)
+    return sorted(found)
+
+
 def _src_sha(name):
-    """Hash of a kernel's source file and of every shared header it may
-    include: a stored traffic figure counts only while both are unchanged."""
-    csrc = os.path.join(ROOT, "prefill_csa_compress_gb300", "csrc")
+    """Hash of a kernel's source file and of the headers that it includes: a
+    stored traffic figure counts only while all of them are unchanged."""
     h = hashlib.sha1()
-    try:
-        for path in [os.path.join(csrc, name)] + sorted(glob.glob(os.path.join(csrc, "*.cuh"))):
-            h.update(open(path, "rb").read())
-    except OSError:
-        return None
+    for path in _sources(name):
+        with open(path, "rb") as f:
+            h.update(f.read())
     return h.hexdigest()[:12]
 
 
