@@ -131,8 +131,14 @@ bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims
 // are not read too often, and a request does not fill a chunk CTA: 4 x 16 rows of 4
 // heads over 600 positions 18 us against 26, 8 of them over 2000 43 against 44.  Else
 // chunks: 24 of them over 600 (59 us against 37), 8 over 8000 (168 against 91), 12 x
-// 8 rows of 32 heads over 400 (20 against 15).  Results do not depend on it but for
-// rounding.
+// 8 rows of 32 heads over 400 (20 against 15).  The host does not know how the rows
+// are spread.  With one chunk and single tokens for the rest, decode is the faster one
+// wherever this takes it (64 requests, 512 rows of 32 heads over 600: 107 us against
+// 453) and mostly where this takes chunks (of 64 heads: 162 against 407).  With all rows
+// one request's it is the slower one from some 100,000 rows x positions on (16 rows over
+// 8000: 24 us against 19, 512 over 600: 98 against 22).  Nor does the host know the
+// caches' lengths: max_blocks stands for them.  Results do not depend on the choice but
+// for rounding.
 bool use_decode(const csa_paged_attn_args &a, int sms) {
   if (a.mode == CSA_MODE_PREFILL || a.n_rows > paged::kDecodeRows) return false;
   if (a.mode == CSA_MODE_DECODE) return true;

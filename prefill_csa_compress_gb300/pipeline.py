@@ -286,10 +286,12 @@ class PagedAttnStep:
     reads ``t``, ``out`` and ``lse`` when it runs, or when it is prepared.  Its first
     call reads the queries and its second the keys, so ``before_attention`` (what
     ``StepIO`` sets to wait for late inputs) is called before all of them.
+    ``mode`` is ``csa_paged_attn``'s: what it chooses by itself goes by the rows
+    a request has on average and by the block table's width.
     """
 
     def __init__(self, t: dict, causal: bool = True, window: int = 0, rope_layout: str = "adjacent",
-                 eps: float = 1e-6, status_buf=None):
+                 eps: float = 1e-6, status_buf=None, mode: int = B.CSA_MODE_AUTO):
         self.t = t
         q = t["q"]
         self.q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -299,6 +301,7 @@ class PagedAttnStep:
             1, dtype=torch.int32, device=q.device)
         self.causal, self.window = bool(causal), int(window)
         self.rope_layout, self.eps = rope_layout, float(eps)
+        self.mode = int(mode)
         self.before_attention = None
         self.ws = None
         self._prepared = None
@@ -318,7 +321,8 @@ class PagedAttnStep:
                                     k_pool=t["k_pool"], v_pool=t["v_pool"],
                                     block_table=t["kv_table"], kv_len=t["kv_len"], out=self.out,
                                     lse=self.lse, sink=t.get("sink"), causal=self.causal,
-                                    window=self.window, status=self.status, workspace=self.ws)))
+                                    window=self.window, mode=self.mode, status=self.status,
+                                    workspace=self.ws)))
 
     def prepare(self):
         """Marshal the step's calls once (buffers must stay in place)."""

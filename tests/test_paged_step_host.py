@@ -129,3 +129,13 @@ def test_timing_events_are_joined(log, prepared):
         step.prepare()
     step.run("s")
     assert [e[0] for e in log] == [*NAMES, "prof_join"] and log[-1][2] == "s"
+
+
+def test_mode_reaches_the_attention(log):
+    """The kernel that a caller asks for, where the choice by averages would go
+    wrong (a chunk beside single tokens, a lone chunk in a table of many)."""
+    for mode in (PL.B.CSA_MODE_AUTO, PL.B.CSA_MODE_DECODE, PL.B.CSA_MODE_PREFILL):
+        log.clear()
+        PL.PagedAttnStep(tensors(), mode=mode).run()
+        assert [kw["mode"] for name, kw, _ in log if name == "csa_paged_attn"] == [mode]
+    assert PL.PagedAttnStep(tensors()).mode == PL.B.CSA_MODE_AUTO
