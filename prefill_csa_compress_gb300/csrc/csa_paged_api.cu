@@ -43,11 +43,11 @@ bool pool_strides(int64_t *page, int64_t *token, int64_t *head, int64_t n_pages,
         std::swap(st[i], st[j]);
         std::swap(n[i], n[j]);
       }
-  int64_t reach = bytes;
+  __int128 reach = bytes;  // (to 2^71: 2^31 pages, 2^40 bytes apart)
   for (int i = 0; i < 3; ++i) {
     if (n[i] == 1) continue;
     if (st[i] < reach) return false;
-    reach = st[i] * (n[i] - 1) + reach;
+    reach += (__int128)st[i] * (n[i] - 1);
   }
   return true;
 }
