@@ -170,7 +170,7 @@ def _rope(a, tensors, cos, sin, layout, start, dim):
     _dense(cos, "rope_cos", torch.float32, (None, None))
     _dense(sin, "rope_sin", torch.float32, tuple(cos.shape))
     a.rope_layout = _LAYOUTS[layout]
-    a.rope_cap, a.rope_dim = int(cos.shape[0]), 2 * int(cos.shape[1])
+    a.rope_cap, a.rope_dim = _int32(cos.shape[0], "rope_cos"), _int32(2 * cos.shape[1], "rope_cos")
     if not 0 < a.rope_dim <= dim:
         raise ValueError(f"the tables rotate {a.rope_dim} channels of a head of {dim}")
     a.rope_start = dim - a.rope_dim if start is None else _int32(start, "rope_start")
@@ -237,7 +237,7 @@ def csa_rope_table(*, cos, sin, theta=10000.0, scaling="none", factor=1.0, orig_
     _dense(sin, "sin", torch.float32, tuple(cos.shape))
     a, tensors = RopeTableArgs(), []
     a.struct_size = ctypes.sizeof(a)
-    a.n_pos, a.rope_dim = _int32(cos.shape[0], "cos"), 2 * int(cos.shape[1])
+    a.n_pos, a.rope_dim = _int32(cos.shape[0], "cos"), _int32(2 * cos.shape[1], "cos")
     a.pos0 = _int32(pos0, "pos0")
     a.scaling, a.orig_len = _SCALINGS[scaling], _int32(orig_len, "orig_len")
     a.theta, a.factor, a.attn_factor = float(theta), float(factor), float(attn_factor)
@@ -260,12 +260,12 @@ def csa_qk_norm_rope(*, q, row_pos, k=None, q_out=None, k_out=None, row_req=None
     q_out = q if q_out is None else q_out
     a.q_row_stride = _rows(q, "q", (None, None, None))
     n, h, d = (int(x) for x in q.shape)
-    a.n_rows, a.n_q_heads, a.head_dim = _int32(n, "rows"), h, d
+    a.n_rows, a.n_q_heads, a.head_dim = (_int32(x, "q") for x in (n, h, d))
     a.q_out_row_stride = _rows(q_out, "q_out", (n, h, d))
     if k is not None:
         k_out = k if k_out is None else k_out
         a.k_row_stride = _rows(k, "k", (n, None, d))
-        a.n_k_heads = int(k.shape[1])
+        a.n_k_heads = _int32(k.shape[1], "k")
         a.k_out_row_stride = _rows(k_out, "k_out", tuple(k.shape))
     elif k_out is not None or k_gamma is not None:
         raise ValueError("k_out and k_gamma need k")
@@ -303,7 +303,7 @@ def csa_kv_append(*, k, row_req, row_pos, block_table, k_pool, v=None, v_pool=No
     a.struct_size = ctypes.sizeof(a)
     a.k_row_stride = _rows(k, "k", (None, None, None))
     n, h, d = (int(x) for x in k.shape)
-    a.n_rows, a.n_heads, a.head_dim = _int32(n, "rows"), h, d
+    a.n_rows, a.n_heads, a.head_dim = (_int32(x, "k") for x in (n, h, d))
     if (v is None) != (v_pool is None):
         raise ValueError("v and v_pool go together")
     if v is not None:
@@ -334,11 +334,11 @@ def csa_kv_append(*, k, row_req, row_pos, block_table, k_pool, v=None, v_pool=No
             setattr(a, p + "_token_stride", st[1])
             setattr(a, p + "_head_stride", st[2])
         pages = int(x.shape[0])
-    a.n_blocks = pages
+    a.n_blocks = _int32(pages, "pools")
     _dense(row_req, "row_req", torch.int32, (n,))
     _dense(row_pos, "row_pos", torch.int32, (n,))
     _dense(block_table, "block_table", torch.int32, (None, None))
-    a.n_req, a.max_blocks = int(block_table.shape[0]), int(block_table.shape[1])
+    a.n_req, a.max_blocks = (_int32(x, "block_table") for x in block_table.shape)
     if k_gamma is not None:
         if not norm:
             raise ValueError("k_gamma needs norm")
@@ -367,16 +367,16 @@ def csa_paged_attn(*, q, row_req, row_pos, k_pool, v_pool, block_table, kv_len, 
     a.struct_size = ctypes.sizeof(a)
     a.q_row_stride = _rows(q, "q", (None, None, None))
     n, h, d = (int(x) for x in q.shape)
-    a.n_rows, a.n_heads, a.head_dim = _int32(n, "rows"), h, d
+    a.n_rows, a.n_heads, a.head_dim = (_int32(x, "q") for x in (n, h, d))
     _want(k_pool, "k_pool", torch.bfloat16, (None, PAGE, None, d))
     _want(v_pool, "v_pool", torch.bfloat16, tuple(k_pool.shape))
-    a.n_blocks, a.n_kv_heads = int(k_pool.shape[0]), int(k_pool.shape[2])
+    a.n_blocks, a.n_kv_heads = _int32(k_pool.shape[0], "pools"), _int32(k_pool.shape[2], "pools")
     if a.n_kv_heads < 1 or h % a.n_kv_heads:
         raise ValueError(f"{h} query heads do not divide among {a.n_kv_heads} key/value heads")
     a.k_page_stride, a.k_token_stride, a.k_head_stride = _pool_strides(k_pool, "k_pool")
     a.v_page_stride, a.v_token_stride, a.v_head_stride = _pool_strides(v_pool, "v_pool")
     _dense(block_table, "block_table", torch.int32, (None, None))
-    a.n_req, a.max_blocks = int(block_table.shape[0]), int(block_table.shape[1])
+    a.n_req, a.max_blocks = (_int32(x, "block_table") for x in block_table.shape)
     _dense(kv_len, "kv_len", torch.int32, (a.n_req,))
     _dense(row_req, "row_req", torch.int32, (n,))
     _dense(row_pos, "row_pos", torch.int32, (n,))
