@@ -500,10 +500,10 @@ CSA_API csa_status_t csa_sparse_attn_prefill(csa_attn_args *args, csa_stream_t s
  * Paged key/value caches of ordinary attention layers, and the rows that the
  * calls above read.  No counterpart on the pages: they hand this library
  * finished RoPE tables ("DeepSeek V4.1 Flash", "Serving-owned full RoPE
- * tables"), normed queries and window rows published upstream; the four calls
- * below are that upstream part, and the attention of the layers (or draft
- * heads) of the same model whose caches hold separate keys and values for
- * groups of query heads.
+ * tables"), normed queries and window rows published upstream; the first three
+ * calls below are that upstream part.  The pages describe no layer whose cache
+ * holds separate keys and values for groups of query heads; the fourth call is
+ * for such layers over the same kind of pages.
  *
  * Rotation, as csa_qk_norm_rope and csa_kv_append apply it: the channels
  * [rope_start, rope_start + rope_dim) of a vector of `head_dim` channels are
@@ -632,8 +632,10 @@ CSA_API csa_status_t csa_qk_norm_rope(csa_qk_norm_rope_args *args, csa_stream_t 
  * fmt CSA_FMT_MXFP8: codes uint8 of the same shape and scale bytes uint8
  * [n_blocks, 128, n_heads, head_dim / 32], dense, head_dim a multiple of 32;
  * the row as it would be stored in FP32 is quantised as csa_compress publishes
- * MXFP8 (an infinity saturates its group's scale; a NaN stays one).  The slots
- * of different rows must not overlap in memory.
+ * MXFP8 (an infinity saturates its group's scale; a NaN stays one).  Of this
+ * library's calls, csa_sparse_attn_* reads such rows (one head of 512 channels, as
+ * its window); csa_paged_attn reads BF16 pools only.  The slots of different rows
+ * must not overlap in memory.
  * Supported: head_dim a multiple of 8, 8 .. 512; tensors 16-byte aligned.
  * ---------------------------------------------------------------------- */
 typedef struct {
@@ -690,6 +692,9 @@ CSA_API csa_status_t csa_kv_append(csa_kv_append_args *args, csa_stream_t stream
  * sink == NULL means -inf.  A row that sees nothing gets out = 0 and lse =
  * sink_h.  Logits are FP32 sums; a (row, head) whose largest reaches 2^29 in size
  * has an unspecified result (from 2^24 on, FP32 does not resolve them to 1).
+ * Sums, references and lse are FP32; the probabilities are rounded to BF16 for
+ * the product with the values, as in csa_sparse_attn_*, which moves an output by at
+ * most 2^-8 of its sum of p_j |v_j|.
  * Keys, values and rows that a row does not see have no effect on it, whatever
  * they hold (infinities and NaN included).  q is used as it is
  * (csa_qk_norm_rope rotates it).  Rows may come in any order; rows of one

@@ -362,7 +362,9 @@ def csa_paged_attn(*, q, row_req, row_pos, k_pool, v_pool, block_table, kv_len, 
     """Attention of the rows of ``q`` [rows, heads, dim] over paged keys and
     values [pages, 128, kv_heads, dim] (``include/csa.h``: csa_paged_attn).
     Returns the workspace, which a later call of the same sizes may be given;
-    calls that overlap need one each."""
+    calls that overlap need one each.  ``mode`` (CSA_MODE_*) names the kernel;
+    left to itself the call takes the rows as spread evenly over the block
+    table's requests and the caches as long as its rows."""
     a, tensors = PagedAttnArgs(), []
     a.struct_size = ctypes.sizeof(a)
     a.q_row_stride = _rows(q, "q", (None, None, None))

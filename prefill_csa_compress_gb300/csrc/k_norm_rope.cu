@@ -24,11 +24,15 @@ constexpr int NR_THREADS = 256;
 // beside their chunks (halves above 256 channels) need more registers.
 template <int C, bool HALF>
 constexpr int kBlocks = C == 1 ? (HALF ? 4 : 5) : (HALF ? 1 : 3);
-// The publication kernel.  With one head a warp there are many short warps, and four
-// blocks help (8192 rows of 512: 10.0 -> 9.3 us).  With several heads a warp, of up to 256
-// channels: adjacent pairs four (8192 rows of 8 + 8 heads of 128 17.5 us, 64 rows 2.8;
-// three 19.0 and 2.8, two 23.1 and 2.6), halves two (25.1 and 2.9; three 23.1 and 3.5,
-// one 42.7 and 2.8); above that two (the 8192 of 512: 31.7 us; three 39.0, one 46.6).
+// The publication kernel, its inputs from memory.  With one head a warp there are many
+// short warps, and four blocks help (8192 rows of 512 to MXFP8, with the host's call:
+// 10.0 -> 9.3 us; the kernel alone 8.4, to BF16 7.7).  With several heads a warp, of up
+// to 256 channels: adjacent pairs four (8192 rows of 8 + 8 heads of 128 18.0 us; without
+// the look at a head's scale 17.5, three blocks of that 19.0 and two 23.1), halves two
+// (25.6; without 25.1, three 23.1 but 64 rows 3.5 for 2.9, one 42.7); above that two
+// (8192 rows of 8 heads of 512, keys alone, 33.1 us; without 31.9, three 39.0, one 46.6).
+// At these bounds some instances spill (at most 290 bytes a thread, the halves above
+// 256 channels).
 template <int C, int U, bool HALF>
 constexpr int kAppendBlocks = U == 1 ? (C == 1 || !HALF ? 4 : 1) : (C == 1 && !HALF ? 4 : 2);
 

@@ -38,8 +38,9 @@
 // 1,024, the rest the way from role to role.  D = 64: 2,330 cycles, all of them the
 // softmax's (the warps issue half of the time, the exponentials' unit is busy for
 // 35 %).  A CTA's start and end take 14,000.  A prompt of 8192 (32 query heads on 8
-// of 128) takes 381 us (1.44 PFLOP/s), of 64 channels 288 us (0.95 PFLOP/s), 4096
-// rows of 64 heads of 128 over 65,536 positions 5.5 ms (1.54 PFLOP/s).
+// of 128) takes 381 us from L2 (1.44 PFLOP/s) and 398 from memory, of 64 channels 288
+// us from L2 (0.95 PFLOP/s), 4096 rows of 64 heads of 128 over 65,536 positions 5.5 ms
+// (1.54 PFLOP/s).
 #include <cuda.h>
 
 #include "attn_common.cuh"
