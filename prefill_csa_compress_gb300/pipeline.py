@@ -451,15 +451,19 @@ class StepIO:
         for s_ in (step.steps if isinstance(step, StepChain) else [step]):
             if s_._prepared is None:
                 s_.prepare()
+        before = first.before_attention
         first.before_attention = (lambda stream: torch.cuda.current_stream().wait_event(
             self._late_ev)) if self.split < self.dev_in.numel() else None
-        self._h2d_split()  # creates the side stream and event outside the capture
-        torch.cuda.synchronize()
-        g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g, capture_error_mode="thread_local"):
-            self._h2d_split()
-            step.run()
-            self.d2h()
+        try:
+            self._h2d_split()  # creates the side stream and event outside the capture
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, capture_error_mode="thread_local"):
+                self._h2d_split()
+                step.run()
+                self.d2h()
+        finally:  # outside the graph the event means nothing
+            first.before_attention = before
         return g
 
     def d2h(self):

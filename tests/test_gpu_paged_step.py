@@ -108,3 +108,40 @@ def test_timed_capture(kernel, chained):
         whole.drop_graph()
         csa.prof_disable()
     assert torch.equal(step.out, want[0]) and torch.equal(step.lse, want[1])
+
+
+def _csa():
+    from prefill_csa_compress_gb300.pipeline import CsaStep
+    from workloads import make_workload, spec_for
+
+    spec = spec_for("tiny_decode", seed=5)
+    t = make_workload(spec).to(DEV)
+    return t, lambda: CsaStep(t, spec.ratio, spec.topk), ["q", "row_req", "row_pos", "kv_len"]
+
+
+def _paged():
+    rng = np.random.default_rng(5)
+    t = _tensors(rng, 4, _pools(rng))
+    return t, lambda: PagedAttnStep(t), INPUTS
+
+
+@pytest.mark.parametrize("kind", [_csa, _paged])
+@pytest.mark.parametrize("late", [(), ("q",)])
+@pytest.mark.parametrize("chained", [False, True])
+def test_eager_run_after_a_capture(kind, late, chained):
+    """A step whose graph waits for late inputs still runs by itself, and its
+    graph still replays afterwards."""
+    t, make, inputs = kind()
+    step = make()
+    whole = StepChain([step]) if chained else step
+    io = StepIO(t, inputs, late=late).bind_outputs(whole)
+    whole.run()
+    torch.cuda.synchronize()
+    want = step.out.clone(), step.lse.clone()
+    graph = io.capture(whole)
+    for run in (whole.run, graph.replay, whole.run):
+        step.out.fill_(7)
+        run()
+        torch.cuda.synchronize()
+        assert torch.equal(step.out, want[0]) and torch.equal(step.lse, want[1])
+    assert int(step.status.item()) == 0
