@@ -708,8 +708,12 @@ CSA_API csa_status_t csa_kv_append(csa_kv_append_args *args, csa_stream_t stream
  * 64 channels by 14 %, of 128 by 2 %); out
  * bf16 [n_rows, n_heads, head_dim] dense; lse f32 [n_rows, n_heads] or NULL;
  * block_table i32 [n_req, max_blocks]; kv_len i32 [n_req].  out and lse must not
- * overlap the inputs.  Supported: at most 2^24 rows and 2^24 pages a request;
- * head_dim 64 or 128; n_kv_heads a divisor of n_heads, n_heads / n_kv_heads <=
+ * overlap the inputs.  v_dim (0, or a struct_size that ends before it: head_dim) is
+ * the values' width where it is not the keys': the expanded form of latent attention
+ * has keys of 192 and values of 128 (csa_latent_expand), v_pool [.., v_dim], out
+ * [n_rows, n_heads, v_dim]; such calls run as CSA_MODE_PREFILL whatever `mode` says.
+ * Supported: at most 2^24 rows and 2^24 pages a request;
+ * head_dim = v_dim = 64 or 128, or head_dim 192 with v_dim 128; n_kv_heads a divisor of n_heads, n_heads / n_kv_heads <=
  * 128.  softmax_scale > 0, finite.  Tensors 16-byte aligned.
  * `mode` (csa_mode_t) chooses between the kernel for few rows per request
  * (CSA_MODE_DECODE; calls of up to 512 rows, more run as CSA_MODE_PREFILL) and the
@@ -761,9 +765,271 @@ typedef struct {
   uint32_t *status_dev;
   void *workspace;
   size_t workspace_bytes;
+  int32_t v_dim; /* 0: head_dim */
 } csa_paged_attn_args;
 
 CSA_API csa_status_t csa_paged_attn(csa_paged_attn_args *args, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Latent caches: attention whose keys and values come from one vector a token.
+ *
+ * A cached position holds a latent c_j (512 channels, normed) and a key r_j (64
+ * channels, rotated) that all heads share, 1152 bytes in BF16.  csa_kv_append
+ * publishes both (two calls, c with its norm and r with its rotation).  Head h's key
+ * is [W_uk,h c_j, r_j] and its value W_uv,h c_j.  Two forms read such a cache:
+ *  - absorbed (csa_latent_attn): W_uk goes into the query and W_uv behind the
+ *    output, so that attention runs over the latents themselves, 2176 operations a
+ *    pair of (row, head) and position, 1152 bytes a position;
+ *  - expanded (csa_latent_expand, then csa_paged_attn with keys of 192 and values
+ *    of 128): 640 operations a pair and 131,072 a position and head to expand.
+ * The absorbed form is the one for few rows over long caches, the expanded one for
+ * prompts.
+ *
+ * The pools are BF16: c_pool [n_blocks, 128, 512], r_pool [n_blocks, 128, 64], with
+ * page and token strides in bytes (0: dense; multiples of 16), so one pool of rows of
+ * 576 is two views.
+ * ---------------------------------------------------------------------- */
+#define CSA_LATENT_DIM 512 /* channels of a latent */
+#define CSA_NOPE_DIM 128   /* key channels of a head that come from the latent */
+#define CSA_VALUE_DIM 128  /* value channels of a head */
+
+/* ------------------------------------------------------------------------
+ * csa_latent_attn - absorbed latent attention over a paged latent cache.
+ *
+ * Row t of request b at p sees position j as in csa_paged_attn (kv_len, causal,
+ * window).  With the visible j:
+ *   l_j = softmax_scale * (q[t,h] . c_j + q_rope[t,h] . r_j)
+ *   out[t,h] = sum_j e^{l_j} c_j / (sum_j e^{l_j} + e^{sink_h})
+ *   lse[t,h] = log(sum_j e^{l_j} + e^{sink_h})
+ * q[t,h] is the head's query times its W_uk (512 channels), q_rope its rotated part;
+ * the value of a head is W_uv,h out[t,h].  sink == NULL means -inf.  A row that sees
+ * nothing gets out = 0 and lse = sink_h; rows with row_req < 0 are not written; a
+ * request >= n_req raises CSA_DEV_BAD_POS and the row is skipped; a page outside the
+ * pool raises CSA_DEV_BAD_BLOCK and its positions are not seen.  Logits are FP32 sums;
+ * a (row, head) whose largest reaches 2^29 in size has an unspecified result.
+ * Sums, references and lse are FP32; probabilities are rounded to BF16 for the
+ * product with the latents, which moves an output by at most 2^-8 of its sum of
+ * p_j |c_j|.  Positions that a row does not see have no effect on it, whatever they
+ * hold.  A row that sees a latent with a value that is not finite has outputs that
+ * are not finite in the channels of those values at least.
+ *
+ * q bf16 [n_rows, n_heads, 512] and q_rope bf16 [n_rows, n_heads, 64], with row and
+ * head strides in bytes (0: dense; multiples of 16; so [n_heads, n_rows, 512], the
+ * outcome of a product a head, and halves of rows of 576 are views); out bf16
+ * [n_rows, n_heads, 512] dense; lse f32 [n_rows, n_heads] or NULL; block_table i32
+ * [n_req, max_blocks]; kv_len i32 [n_req].  out and lse must not overlap the inputs.
+ * Rows may come in any order; rows of one request that follow one another share
+ * their reads (64 / n_heads of them).  Supported: 1 .. 128 heads, at most 2^24 rows
+ * and 2^24 pages a request.  softmax_scale > 0, finite.  Tensors 16-byte aligned.
+ * The workspace (size query) holds partial results of split rows; nothing in it has
+ * to be set or kept between calls.  256-byte aligned.  Calls that may run at the same
+ * time need workspaces of their own.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;
+  int32_t n_rows;
+  int32_t n_heads;
+  int32_t causal; /* 0: every cached position; 1: positions <= the row's */
+  int32_t window; /* 0: none */
+  float softmax_scale;
+  int32_t n_req;
+  int32_t max_blocks;
+  int32_t n_blocks;
+  const void *q;
+  const void *q_rope;
+  int64_t q_row_stride;
+  int64_t q_head_stride;
+  int64_t q_rope_row_stride;
+  int64_t q_rope_head_stride;
+  const int32_t *row_req;
+  const int32_t *row_pos;
+  const int32_t *kv_len;
+  const int32_t *block_table;
+  const void *c_pool;
+  const void *r_pool;
+  int64_t c_page_stride;
+  int64_t c_token_stride;
+  int64_t r_page_stride;
+  int64_t r_token_stride;
+  const float *sink;
+  void *out;
+  float *lse;
+  uint32_t *status_dev;
+  void *workspace;
+  size_t workspace_bytes;
+} csa_latent_attn_args;
+
+CSA_API csa_status_t csa_latent_attn(csa_latent_attn_args *args, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * csa_latent_expand - keys and values of every head from a paged latent cache.
+ *
+ * For every request b and position first[b] <= j < min(kv_len[b], 128 max_blocks)
+ * (first == NULL: 0; a negative one counts as 0) and head h, slot j of the request's
+ * expanded cache gets
+ *   k[j,h] = [bf16(w_uk[h] c_j), r_j]   (128 + 64 channels)
+ *   v[j,h] = bf16(w_uv[h] c_j)          (128 channels)
+ * with FP32 sums.  Slot j is row j % 128 of page out_table[b, j / 128] of k_pool and
+ * v_pool; every other row is left as it was.  A source page outside its pool, or a
+ * destination page outside out_table or the pools, raises CSA_DEV_BAD_BLOCK and its
+ * positions are skipped.  A destination page must be one request's alone, and the
+ * expanded pools must not overlap the inputs.
+ *
+ * w_uk, w_uv bf16 [n_heads, 128, 512], a head's rows dense, with head strides in
+ * bytes (0: dense; so the halves of a checkpoint's [n_heads, 256, 512] are views).
+ * k_pool bf16 [n_out_blocks, 128, n_heads, 192], v_pool bf16 [n_out_blocks, 128,
+ * n_heads, 128], page, token and head strides as in csa_kv_append.  block_table i32
+ * [n_req, max_blocks], out_table i32 [n_req, out_max_blocks].  1 .. 65536 heads.
+ * Tensors 16-byte aligned.  No workspace.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;
+  int32_t n_heads;
+  int32_t n_req;
+  int32_t max_blocks;
+  int32_t n_blocks;
+  int32_t out_max_blocks;
+  int32_t n_out_blocks;
+  const int32_t *kv_len;
+  const int32_t *first;
+  const int32_t *block_table;
+  const int32_t *out_table;
+  const void *c_pool;
+  const void *r_pool;
+  int64_t c_page_stride;
+  int64_t c_token_stride;
+  int64_t r_page_stride;
+  int64_t r_token_stride;
+  const void *w_uk;
+  const void *w_uv;
+  int64_t w_uk_head_stride;
+  int64_t w_uv_head_stride;
+  void *k_pool;
+  void *v_pool;
+  int64_t k_page_stride;
+  int64_t k_token_stride;
+  int64_t k_head_stride;
+  int64_t v_page_stride;
+  int64_t v_token_stride;
+  int64_t v_head_stride;
+  uint32_t *status_dev;
+} csa_latent_expand_args;
+
+CSA_API csa_status_t csa_latent_expand(csa_latent_expand_args *args, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * csa_attn_mass - the attention weight that every cached position received.
+ *
+ *   mass_out[b,j] = decay * mass[b,j] + sum over the call's rows t of request b that
+ *                   see j, and heads h, of e^{softmax_scale q[t,h] . k_j - lse[t,h]}
+ * for every position j < min(kv_len[b], 128 max_blocks), seen or not; entries behind
+ * are left as they were.  decay == 0 does not read mass (which may be NULL), whatever it
+ * holds.  mass_out may be mass.  What a row sees, the head groups, pages and padding
+ * are those of csa_paged_attn, whose lse (sink included) is the one meant; any other
+ * FP32 reference will do.  A row and head of lse -inf adds nothing.  Weights and sums
+ * are FP32, added in an order that depends on the arguments alone.  Positions that a
+ * row does not see add nothing for it, whatever they hold.
+ *
+ * q bf16 [n_rows, n_heads, head_dim], row-strided; lse f32 [n_rows, n_heads]; k_pool
+ * bf16 [n_blocks, 128, n_kv_heads, head_dim] with strides as in csa_kv_append; mass,
+ * mass_out f32 [n_req, 128 max_blocks] with row strides in bytes (0: dense; multiples
+ * of 4).  Supported: at most 2^24 rows and 2^24 - 1 pages a request; head_dim 64 or 128;
+ * n_kv_heads a divisor of n_heads, n_heads / n_kv_heads <= 128.  decay finite, >= 0.
+ * The workspace is used as csa_paged_attn's is.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;
+  int32_t n_rows;
+  int32_t n_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t causal;
+  int32_t window;
+  float softmax_scale;
+  float decay;
+  int32_t n_req;
+  int32_t max_blocks;
+  int32_t n_blocks;
+  const void *q;
+  int64_t q_row_stride;
+  const float *lse;
+  const int32_t *row_req;
+  const int32_t *row_pos;
+  const int32_t *kv_len;
+  const int32_t *block_table;
+  const void *k_pool;
+  int64_t k_page_stride;
+  int64_t k_token_stride;
+  int64_t k_head_stride;
+  const float *mass;
+  float *mass_out;
+  int64_t mass_row_stride;
+  int64_t mass_out_row_stride;
+  uint32_t *status_dev;
+  void *workspace;
+  size_t workspace_bytes;
+} csa_attn_mass_args;
+
+CSA_API csa_status_t csa_attn_mass(csa_attn_mass_args *args, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * csa_kv_evict - cuts paged caches to their heaviest positions, in place.
+ *
+ * Request b keeps n = min(L, budget[b]) of its L = min(kv_len[b], 128 max_blocks)
+ * positions: those of the largest mass[b,j], ties going to the lowest j.  The first
+ * `first` and the last `recent` positions count as +inf; a NaN counts as less than
+ * anything.  Kept positions before n stay where they are; the others go, in ascending
+ * order, to the slots before n that evicted positions leave, so that slots 0 .. n - 1
+ * hold the kept ones and as few rows as possible move.  kv_len_out[b] = n (kv_len_out
+ * may be kv_len).  Keys hold their rotation, so attention over the cut cache goes by
+ * slots: rows at slot n on (row_pos of csa_paged_attn) see all that was kept.
+ * mass_out[b,d] (or NULL) gets the mass of what slot d holds now (mass_out may be
+ * mass); slot_src[b,d] (or NULL) its old position.  d < n; entries behind, and the
+ * rows of slots n on, are left as they were.  A move whose source or destination page
+ * is outside the pool raises CSA_DEV_BAD_BLOCK and is not made (mass_out and slot_src
+ * are).  Pages that are cut must be one request's alone.
+ *
+ * mass f32 [n_req, 128 max_blocks] and mass_out alike, row strides in bytes (0:
+ * dense; multiples of 4); slot_src i32 [n_req, 128 max_blocks] dense; kv_len, budget
+ * i32 [n_req] (below 0: 0).  k_pool bf16 [n_blocks, 128, n_heads, k_dim], v_pool bf16
+ * [n_blocks, 128, n_heads, v_dim] or NULL, strides as in csa_kv_append (a latent
+ * cache: one head, c as k of 512 and r as v of 64).  k_dim, v_dim multiples of 8, 8
+ * .. 512; max_blocks < 2^24; first, recent >= 0.  The workspace is used as
+ * csa_paged_attn's is.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint32_t struct_size;
+  int32_t n_req;
+  int32_t max_blocks;
+  int32_t n_blocks;
+  int32_t n_heads;
+  int32_t k_dim;
+  int32_t v_dim;
+  int32_t first;
+  int32_t recent;
+  const float *mass;
+  int64_t mass_row_stride;
+  const int32_t *kv_len;
+  const int32_t *budget;
+  const int32_t *block_table;
+  void *k_pool;
+  void *v_pool;
+  int64_t k_page_stride;
+  int64_t k_token_stride;
+  int64_t k_head_stride;
+  int64_t v_page_stride;
+  int64_t v_token_stride;
+  int64_t v_head_stride;
+  int32_t *kv_len_out;
+  float *mass_out;
+  int64_t mass_out_row_stride;
+  int32_t *slot_src;
+  uint32_t *status_dev;
+  void *workspace;
+  size_t workspace_bytes;
+} csa_kv_evict_args;
+
+CSA_API csa_status_t csa_kv_evict(csa_kv_evict_args *args, csa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Library information and measurement hooks (no counterpart on the pages).
@@ -791,7 +1057,14 @@ typedef enum {
   CSA_K_KV_APPEND = 10,
   CSA_K_PAGED_ATTN = 11,    /* csa_paged_attn: the attention itself */
   CSA_K_PAGED_MERGE = 12,   /* csa_paged_attn: joining the parts of split rows */
-  CSA_K_COUNT = 13
+  CSA_K_LATENT_ATTN = 13,   /* csa_latent_attn: the attention itself */
+  CSA_K_LATENT_JOIN = 14,   /* csa_latent_attn: joining the parts of split rows */
+  CSA_K_LATENT_EXPAND = 15,
+  CSA_K_ATTN_MASS = 16,     /* csa_attn_mass: the weights */
+  CSA_K_MASS_JOIN = 17,     /* csa_attn_mass: joining partial sums */
+  CSA_K_EVICT_PLAN = 18,    /* csa_kv_evict: what stays and what moves where */
+  CSA_K_EVICT_MOVE = 19,    /* csa_kv_evict: the moves */
+  CSA_K_COUNT = 20
 } csa_kernel_id_t;
 
 /* Time every launch of kernel `kernel_id` (up to `max_launches` launches)

@@ -81,13 +81,13 @@ def visible(p, kv_len, causal=True, window=0):
 
 def paged_attention(q, row_req, row_pos, k_pool, v_pool, table, kv_len, scale, *, causal=True,
                     window=0, sink=None):
-    """out [rows, heads, dim], lse [rows, heads], and spread, the sum of
+    """out [rows, heads, the values' dim], lse [rows, heads], and spread, the sum of
     p_j |v_j| (what a relative error of the probabilities can move out by).
     Positions on unmapped pages are not seen."""
-    T, H, D = q.shape
+    T, H, _ = q.shape
     nb, _, KH, _ = k_pool.shape
     G = H // KH
-    out, spread = np.zeros((T, H, D)), np.zeros((T, H, D))
+    out, spread = np.zeros((2, T, H, v_pool.shape[-1]))
     lse = np.full((T, H), -np.inf)
     for t in range(T):
         b = int(row_req[t])
@@ -111,3 +111,63 @@ def paged_attention(q, row_req, row_pos, k_pool, v_pool, table, kv_len, scale, *
             spread[t, h] = w @ np.abs(v[:, h // G]) / L
             lse[t, h] = m + math.log(L)
     return out, lse, spread
+
+
+def latent_attention(q, q_rope, row_req, row_pos, c_pool, r_pool, table, kv_len, scale, **kw):
+    """Attention over latents: keys [c, r] and values c, shared by all heads.
+    out [rows, heads, 512], lse and spread as in ``paged_attention``."""
+    x = np.concatenate([q, q_rope], -1)
+    k = np.concatenate([c_pool, r_pool], -1)[:, :, None]
+    return paged_attention(x, row_req, row_pos, k, c_pool[:, :, None], table, kv_len, scale, **kw)
+
+
+def latent_expand(c, r, w_uk, w_uv):
+    """Keys [n, heads, 192] and values [n, heads, 128] of latents c [n, 512] and
+    rotated keys r [n, 64]."""
+    k = np.stack([c @ w.T for w in w_uk], 1)
+    v = np.stack([c @ w.T for w in w_uv], 1)
+    return np.concatenate([k, np.repeat(r[:, None], k.shape[1], 1)], -1), v
+
+
+def attention_mass(q, lse, row_req, row_pos, k_pool, table, kv_len, scale, *, mass=None, decay=0.0,
+                   causal=True, window=0):
+    """Per request the new masses of its positions (a list of arrays)."""
+    T, H, _ = q.shape
+    nb, _, KH, _ = k_pool.shape
+    lens = [max(0, min(int(n), table.shape[1] * PAGE)) for n in kv_len]
+    out = [decay * np.asarray(mass[b][:n], dtype=np.float64) if decay else np.zeros(n)
+           for b, n in enumerate(lens)]
+    for t in range(T):
+        b = int(row_req[t])
+        if b < 0 or b >= len(lens):
+            continue
+        lo, hi = visible(int(row_pos[t]), lens[b], causal, window)
+        for j in range(lo, max(lo, hi)):
+            page = int(table[b][j // PAGE])
+            if not 0 <= page < nb:
+                continue
+            for h in range(H):
+                if lse[t, h] != -np.inf:
+                    x = scale * float(k_pool[page, j % PAGE, h * KH // H] @ q[t, h])
+                    out[b][j] += math.exp(x - lse[t, h])
+    return out
+
+
+def evict(mass, kv_len, budget, first=0, recent=0):
+    """The old position of every kept slot: kept positions before the cut stay,
+    the others fill the slots of evicted ones in order."""
+    L, n = max(0, int(kv_len)), max(0, min(int(kv_len), int(budget)))
+
+    def heavier(j):  # sorted ascending by (-mass, position)
+        m = float(mass[j])
+        if j < first or j >= L - recent:
+            m = math.inf
+        return (0, -m, j) if m == m else (1, 0.0, j)
+
+    kept = sorted(sorted(range(L), key=heavier)[:n])
+    src, spare = list(range(n)), iter([j for j in kept if j >= n])
+    stays = set(kept)
+    for j in range(n):
+        if j not in stays:
+            src[j] = next(spare)
+    return src

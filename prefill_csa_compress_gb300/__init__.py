@@ -6,7 +6,9 @@ The four calls of the path -- ``csa_compress``, ``csa_index_topk``,
 the hand-written kernels of ``libcsa.so`` (declared in ``include/csa.h``).
 The rows around them -- ``csa_rope_table``, ``csa_qk_norm_rope``,
 ``csa_kv_append`` -- and the attention over caches of separate keys and values,
-``csa_paged_attn``, are in the same library.
+``csa_paged_attn``, are in the same library; so are attention over latent caches in
+both its forms -- ``csa_latent_attn``, ``csa_latent_expand`` -- and the eviction from
+caches by accumulated attention weight -- ``csa_attn_mass``, ``csa_kv_evict``.
 There is no CPU fallback: without the built library every call raises.
 """
 
@@ -31,6 +33,12 @@ from ._binding import (  # noqa: F401
     prof_read,
     status_string,
     version,
+)
+from ._cache import (  # noqa: F401
+    csa_attn_mass,
+    csa_kv_evict,
+    csa_latent_attn,
+    csa_latent_expand,
 )
 from ._paged import (  # noqa: F401
     csa_kv_append,

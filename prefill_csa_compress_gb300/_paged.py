@@ -72,6 +72,7 @@ class PagedAttnArgs(ctypes.Structure):
         ("k_head_stride", c_int64), ("v_page_stride", c_int64), ("v_token_stride", c_int64),
         ("v_head_stride", c_int64), ("sink", c_void_p), ("out", c_void_p), ("lse", c_void_p),
         ("status_dev", c_void_p), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+        ("v_dim", c_int32),
     ]
 
 
@@ -116,6 +117,8 @@ def _rows(t, name, shape):
     row stride in bytes."""
     _want(t, name, torch.bfloat16, shape)
     n, h, d = t.shape
+    if t.numel() == 0:  # (strides of an empty tensor say nothing)
+        return h * d * 2
     if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     if n <= 1:
@@ -361,6 +364,8 @@ def csa_paged_attn(*, q, row_req, row_pos, k_pool, v_pool, block_table, kv_len, 
                    status=None, workspace=None, stream=None, prepare=False):
     """Attention of the rows of ``q`` [rows, heads, dim] over paged keys and
     values [pages, 128, kv_heads, dim] (``include/csa.h``: csa_paged_attn).
+    Keys of 192 channels go with values, and an ``out``, of 128 (the expanded form
+    of latent attention).
     Returns the workspace, which a later call of the same sizes may be given;
     calls that overlap need one each.  ``mode`` (CSA_MODE_*) names the kernel;
     left to itself the call takes the rows as spread evenly over the block
@@ -371,7 +376,9 @@ def csa_paged_attn(*, q, row_req, row_pos, k_pool, v_pool, block_table, kv_len, 
     n, h, d = (int(x) for x in q.shape)
     a.n_rows, a.n_heads, a.head_dim = (_int32(x, "q") for x in (n, h, d))
     _want(k_pool, "k_pool", torch.bfloat16, (None, PAGE, None, d))
-    _want(v_pool, "v_pool", torch.bfloat16, tuple(k_pool.shape))
+    dv = 128 if d == 192 else d
+    _want(v_pool, "v_pool", torch.bfloat16, tuple(k_pool.shape[:3]) + (dv,))
+    a.v_dim = _int32(dv, "v_pool")
     a.n_blocks, a.n_kv_heads = _int32(k_pool.shape[0], "pools"), _int32(k_pool.shape[2], "pools")
     if a.n_kv_heads < 1 or h % a.n_kv_heads:
         raise ValueError(f"{h} query heads do not divide among {a.n_kv_heads} key/value heads")
@@ -382,7 +389,7 @@ def csa_paged_attn(*, q, row_req, row_pos, k_pool, v_pool, block_table, kv_len, 
     _dense(kv_len, "kv_len", torch.int32, (a.n_req,))
     _dense(row_req, "row_req", torch.int32, (n,))
     _dense(row_pos, "row_pos", torch.int32, (n,))
-    _dense(out, "out", torch.bfloat16, (n, h, d))
+    _dense(out, "out", torch.bfloat16, (n, h, dv))
     for name, x, dtype, shape in (("lse", lse, torch.float32, (n, h)),
                                   ("sink", sink, torch.float32, (h,)),
                                   ("status", status, torch.int32, (1,)),

@@ -2,55 +2,13 @@
 // argument checks and kernel dispatch.  No entry point synchronises or
 // allocates device memory.
 #include <cmath>
-#include <utility>
 #include <cstring>
 
+#include "api_checks.cuh"
 #include "csa_internal.cuh"
 
 namespace csa {
 namespace {
-
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-csa_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
-
-bool has_size(const void *args, size_t size) {
-  uint32_t got = 0;
-  if (args) memcpy(&got, args, sizeof(got));
-  return args && got >= size;
-}
-
-// A row stride in bytes, 0 meaning dense.
-bool row_stride(int64_t *s, int64_t row_bytes) {
-  if (*s == 0) *s = row_bytes;
-  return *s % 16 == 0 && *s >= row_bytes && *s <= (int64_t(1) << 40);
-}
-
-// A pool's strides in bytes made explicit (0: dense); false unless they are
-// multiples of 16 that keep every (page, token, head) slot apart: sorted, each
-// spans at least what the smaller ones reach over.
-bool pool_strides(int64_t *page, int64_t *token, int64_t *head, int64_t n_pages, int64_t n_heads,
-                  int64_t bytes) {
-  if (*head == 0) *head = bytes;
-  if (*token == 0) *token = n_heads * bytes;
-  if (*page == 0) *page = kBlock * *token;
-  int64_t st[3] = {*page, *token, *head}, n[3] = {n_pages, kBlock, n_heads};
-  for (int i = 0; i < 3; ++i)
-    if (st[i] % 16 != 0 || st[i] < bytes || st[i] >= (int64_t(1) << 40)) return false;
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 3; ++j)
-      if (st[j] < st[i]) {
-        std::swap(st[i], st[j]);
-        std::swap(n[i], n[j]);
-      }
-  __int128 reach = bytes;  // (to 2^71: 2^31 pages, 2^40 bytes apart)
-  for (int i = 0; i < 3; ++i) {
-    if (n[i] == 1) continue;
-    if (st[i] < reach) return false;
-    reach += (__int128)st[i] * (n[i] - 1);
-  }
-  return true;
-}
 
 // head_dim, rotation and norm arguments that csa_qk_norm_rope and
 // csa_kv_append share.
@@ -165,15 +123,18 @@ CSA_API csa_status_t csa_kv_append(csa_kv_append_args *user, csa_stream_t stream
 }
 
 CSA_API csa_status_t csa_paged_attn(csa_paged_attn_args *user, csa_stream_t stream) {
-  if (!has_size(user, sizeof(csa_paged_attn_args))) return CSA_ERR_INVALID_ARG;
-  csa_paged_attn_args a = *user;
+  if (!has_size(user, offsetof(csa_paged_attn_args, v_dim))) return CSA_ERR_INVALID_ARG;
+  csa_paged_attn_args a = {};
+  memcpy(&a, user, user->struct_size < sizeof(a) ? user->struct_size : sizeof(a));
+  if (user->struct_size < sizeof(a) || a.v_dim == 0) a.v_dim = a.head_dim;
   if (a.n_rows < 0 || a.n_req <= 0 || a.max_blocks <= 0 || a.n_blocks <= 0)
     return CSA_ERR_INVALID_ARG;
   if (a.n_rows > (1 << 24)) return CSA_ERR_UNSUPPORTED;
   if (a.max_blocks > (1 << 24) || a.n_heads < 1 || a.n_kv_heads < 1 || a.n_heads > 65536 ||
       a.n_heads % a.n_kv_heads)
     return CSA_ERR_INVALID_ARG;
-  if ((a.head_dim != 64 && a.head_dim != 128) || a.n_heads / a.n_kv_heads > 128)
+  const bool same = (a.head_dim == 64 || a.head_dim == 128) && a.v_dim == a.head_dim;
+  if (!(same || (a.head_dim == 192 && a.v_dim == 128)) || a.n_heads / a.n_kv_heads > 128)
     return CSA_ERR_UNSUPPORTED;
   if ((a.causal != 0 && a.causal != 1) || a.window < 0 || a.mode < CSA_MODE_AUTO ||
       a.mode > CSA_MODE_PREFILL)
@@ -184,7 +145,7 @@ CSA_API csa_status_t csa_paged_attn(csa_paged_attn_args *user, csa_stream_t stre
   if (!pool_strides(&a.k_page_stride, &a.k_token_stride, &a.k_head_stride, a.n_blocks,
                     a.n_kv_heads, bytes) ||
       !pool_strides(&a.v_page_stride, &a.v_token_stride, &a.v_head_stride, a.n_blocks,
-                    a.n_kv_heads, bytes))
+                    a.n_kv_heads, (int64_t)a.v_dim * 2))
     return CSA_ERR_INVALID_ARG;
   const size_t need = paged_attn_workspace(a);
   if (!a.workspace) {

@@ -140,7 +140,8 @@ bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims
 // caches' lengths: max_blocks stands for them.  Results do not depend on the choice but
 // for rounding.
 bool use_decode(const csa_paged_attn_args &a, int sms) {
-  if (a.mode == CSA_MODE_PREFILL || a.n_rows > paged::kDecodeRows) return false;
+  if (a.mode == CSA_MODE_PREFILL || a.n_rows > paged::kDecodeRows || a.v_dim != a.head_dim)
+    return false;
   if (a.mode == CSA_MODE_DECODE) return true;
   const int per = (int)(((long long)a.n_rows + a.n_req - 1) / a.n_req);
   const long long items = paged_decode_items(a, per);
@@ -163,7 +164,7 @@ Layout layout(const csa_paged_attn_args &a, int sms) {
   L.parts = paged_chunk_parts(a, sms);
   if (L.parts > 1) {
     const size_t rows = (size_t)a.n_rows * a.n_heads * L.parts;
-    L.ml = align_up(rows * a.head_dim * sizeof(float), 256);
+    L.ml = align_up(rows * a.v_dim * sizeof(float), 256);
     L.total = L.ml + align_up(rows * sizeof(float2), 256);
   }
   return L;
@@ -176,12 +177,13 @@ namespace paged {
 bool encode_pools(const csa_paged_attn_args &a, CUtensorMap *k, CUtensorMap *v) {
   const cuuint64_t dims[4] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_kv_heads, (cuuint64_t)kBlock,
                               (cuuint64_t)a.n_blocks};
+  const cuuint64_t v_dims[4] = {(cuuint64_t)a.v_dim, dims[1], dims[2], dims[3]};
   const cuuint32_t box[4] = {64, 1, (cuuint32_t)kBlock, 1};
   const cuuint64_t ks[3] = {(cuuint64_t)a.k_head_stride, (cuuint64_t)a.k_token_stride,
                             (cuuint64_t)a.k_page_stride};
   const cuuint64_t vs[3] = {(cuuint64_t)a.v_head_stride, (cuuint64_t)a.v_token_stride,
                             (cuuint64_t)a.v_page_stride};
-  return encode(k, a.k_pool, 4, dims, ks, box) && encode(v, a.v_pool, 4, dims, vs, box);
+  return encode(k, a.k_pool, 4, dims, ks, box) && encode(v, a.v_pool, 4, v_dims, vs, box);
 }
 
 bool encode_q(const csa_paged_attn_args &a, int rows, CUtensorMap *q) {

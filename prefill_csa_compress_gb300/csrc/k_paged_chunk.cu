@@ -59,13 +59,27 @@ constexpr int PC_BAR_START = 9;  // named barriers: 1 .. 8 are the softmax warps
 constexpr int PC_META = 8;  // pages described ahead (the ring holds at most 4 of them)
 constexpr float kLift = 7.f;  // log2 of the room below P = 2, where a reference moves
 
-template <int D>
+// Keys of DK channels, values of D.
+template <int DK, int D>
 struct Cfg {
-  static constexpr int CHUNKS = D / 64;                // 128-byte column groups of a row
-  static constexpr int TILE = CHUNKS * 16384;          // bytes of a 128-row tile
-  static constexpr int STAGES = D == 128 ? 5 : 8;      // K and V tiles in flight
+  static constexpr int CHUNKS = DK / 64;               // 128-byte column groups of a row of K
+  static constexpr int V_CHUNKS = D / 64;              // and of V
+  static constexpr int TILE = CHUNKS * 16384;          // bytes of a 128-row tile of K
+  static constexpr int V_TILE = V_CHUNKS * 16384;
+  // K and V tiles in flight.  Where both have a size, they take the stages in turn;
+  // else (SPLIT) K has stages 0 and 1 and V stage 2, and K is asked for a page
+  // ahead of V, since V's stage is free later.
+  static constexpr bool SPLIT = DK != D;
+  static constexpr int STAGES = SPLIT ? 3 : (D == 128 ? 5 : 8);
   static constexpr int OFF_KV = 2 * TILE;
-  static constexpr int OFF_MISC = OFF_KV + STAGES * TILE;
+  static constexpr int OFF_MISC = OFF_KV + (SPLIT ? 2 * TILE + V_TILE : STAGES * TILE);
+  // the stage of a page's K or V, and its turn there
+  __device__ static __forceinline__ int stage(int kv, uint32_t page) {
+    return SPLIT ? (kv ? 2 : (int)(page & 1)) : (int)((2 * page + kv) % STAGES);
+  }
+  __device__ static __forceinline__ uint32_t turn(int kv, uint32_t page) {
+    return SPLIT ? (kv ? page : page >> 1) : (2 * page + kv) / STAGES;
+  }
   // Tensor memory columns: buffers of 128 for S (with P over it), then O.  Two
   // buffers, one a tile, or with room for a third (ROTATE) three that the tiles
   // take in turn, so that a tile's next logits do not wait for its product.
@@ -96,7 +110,8 @@ struct Misc {
 // All of it but for a few hundred bytes, so nothing is set aside for aligning
 // the start: a kernel without static shared memory gets it 1024-byte aligned,
 // and one that did not would stop before touching it.
-static_assert(Cfg<128>::OFF_MISC + sizeof(Misc) <= 227 * 1024, "shared memory");
+static_assert(Cfg<128, 128>::OFF_MISC + sizeof(Misc) <= 227 * 1024, "shared memory");
+static_assert(Cfg<192, 128>::OFF_MISC + sizeof(Misc) <= 227 * 1024, "shared memory");
 
 // Bounded wait that also gives up when another role has.
 __device__ __forceinline__ bool pc_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
@@ -252,17 +267,24 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p_tmem, uint64_t v
                "r"(p_tmem), "l"(v), "r"(idesc), "r"(freed), "r"(done)
                : "memory");
 }
-// S = Q K^T over D / 16 steps; `full` also gets a plain arrival, which hands on
+// S = Q K^T over DK / 16 steps; `full` also gets a plain arrival, which hands on
 // what this warp has seen (the page's description).
-template <int D>
+template <int DK>
 __device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc,
                                          uint32_t full, uint32_t freed) {
 #define PC_QK_END_PTX                                                                      \
   PC_COMMIT_PTX "[%4];\n\t{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%4];\n\t}\n\t" \
   PC_COMMIT_IF_PTX(5) "}"
-  if constexpr (D == 64)
+  if constexpr (DK == 64)
     asm volatile(PC_BEGIN_PTX "setp.ne.b32 p, 0, 0;\n\t" PC_QK_PTX(0, 0) PC_QK_PTX(0, 1)
                      PC_QK_PTX(0, 2) PC_QK_PTX(0, 3) PC_QK_END_PTX ::"r"(d),
+                 "l"(q), "l"(k), "r"(idesc), "r"(full), "r"(freed)
+                 : "memory");
+  else if constexpr (DK == 192)
+    asm volatile(PC_BEGIN_PTX "setp.ne.b32 p, 0, 0;\n\t" PC_QK_PTX(0, 0) PC_QK_PTX(0, 1)
+                     PC_QK_PTX(0, 2) PC_QK_PTX(0, 3) PC_QK_PTX(1, 0) PC_QK_PTX(1, 1)
+                         PC_QK_PTX(1, 2) PC_QK_PTX(1, 3) PC_QK_PTX(2, 0) PC_QK_PTX(2, 1)
+                             PC_QK_PTX(2, 2) PC_QK_PTX(2, 3) PC_QK_END_PTX ::"r"(d),
                  "l"(q), "l"(k), "r"(idesc), "r"(full), "r"(freed)
                  : "memory");
   else
@@ -309,13 +331,13 @@ struct ChunkGrid {
   int n_parts;    // parts of a tile's pages
 };
 
-template <int D>
+template <int DK, int D>
 __global__ void __launch_bounds__(PC_THREADS, 1)
     paged_chunk_kernel(csa_paged_attn_args a, Parts parts, ChunkGrid G,
                        const __grid_constant__ CUtensorMap qmap,
                        const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
-  using C = Cfg<D>;
+  using C = Cfg<DK, D>;
   extern __shared__ __align__(1024) uint8_t sm[];
   Misc *M = reinterpret_cast<Misc *>(sm + C::OFF_MISC);
   tc::griddep_wait();
@@ -364,7 +386,31 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     if (!single) read_rows(a, t0, n_rows, W);
     bool counting = true, many = false, ok = true;
     int total = 0, valid = 0, skip = 0, n_pages = 0, left = 0;
-    uint32_t it = 0;  // tiles loaded
+    uint32_t n_k = 0, n_v = 0;  // tiles loaded
+    int behind = 0;             // the page before
+    // The next K or V, of page `phys`, once its stage is free; describe() runs in one
+    // lane before it is handed on.
+    auto load = [&](int kv, int phys, auto &&describe) {
+      uint32_t &n = kv ? n_v : n_k;
+      const int st = C::stage(kv, n);
+      if (!pc_wait_warp(&M->kv_empty[st], (C::turn(kv, n) & 1) ^ 1, abort, a.status_dev))
+        return false;
+      if (lane == 0) {
+        describe();
+        uint8_t *dst = sm + C::OFF_KV + st * C::TILE;
+        if (phys >= 0 && phys < a.n_blocks) {
+          tc::mbar_arrive_expect_tx(&M->kv_full[st], kv ? C::V_TILE : C::TILE);
+          for (int c = 0; c < (kv ? C::V_CHUNKS : C::CHUNKS); ++c)
+            paged::tma_load_4d(dst + c * 16384, kv ? &vmap : &kmap, c * 64, kvh, 0, phys,
+                               &M->kv_full[st]);
+        } else {
+          tc::mbar_arrive(&M->kv_full[st]);
+        }
+      }
+      __syncwarp();
+      ++n;
+      return true;
+    };
     for (int r = 0; ok;) {
       if (r >= n_rows || (!counting && left == 0)) {
         if (!counting) break;
@@ -403,39 +449,24 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         const int phys = __shfl_sync(0xffffffffu, entry, i & 31);
         const bool there = phys >= 0 && phys < a.n_blocks;
         const int base = (pg0 + i) * kBlock;
-        // K, then V
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int st = it % C::STAGES;
-          ok = pc_wait_warp(&M->kv_empty[st], ((it / C::STAGES) & 1) ^ 1, abort, a.status_dev);
-          if (!ok) break;
-          if (lane == 0) {
-            if (kv == 0) {
-              Page &P = M->page[(it >> 1) % PC_META];
-              P.base = base;
-              P.req = R.req;
-              P.r0 = r0;
-              P.r1 = there ? R.end : r0;  // an unmapped page is seen by no row
-              P.mixed = many || !there || base < R.all_lo || R.all_hi - base < kBlock;
-              P.lo = there ? max(R.lo - base, 0) : 0;
-              P.hi = there ? min(R.hi - base, kBlock) : 0;
-              if (!there) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
-            }
-            uint8_t *dst = sm + C::OFF_KV + st * C::TILE;
-            if (there) {
-              tc::mbar_arrive_expect_tx(&M->kv_full[st], C::TILE);
-              for (int c = 0; c < C::CHUNKS; ++c)
-                paged::tma_load_4d(dst + c * 16384, kv ? &vmap : &kmap, c * 64, kvh, 0, phys,
-                                   &M->kv_full[st]);
-            } else {
-              tc::mbar_arrive(&M->kv_full[st]);
-            }
-          }
-          __syncwarp();
-        }
-        if (it == 2) tc::bar_sync(PC_BAR_START, PC_THREADS);  // n_it, barriers
+        // K, then V (SPLIT: V of the page before)
+        ok = load(0, phys, [&] {
+          Page &P = M->page[n_k % PC_META];
+          P.base = base;
+          P.req = R.req;
+          P.r0 = r0;
+          P.r1 = there ? R.end : r0;  // an unmapped page is seen by no row
+          P.mixed = many || !there || base < R.all_lo || R.all_hi - base < kBlock;
+          P.lo = there ? max(R.lo - base, 0) : 0;
+          P.hi = there ? min(R.hi - base, kBlock) : 0;
+          if (!there) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
+        });
+        if (C::SPLIT ? n_k > 1 : true) ok = ok && load(1, C::SPLIT ? behind : phys, [] {});
+        behind = phys;
+        if (n_k == 1 && ok) tc::bar_sync(PC_BAR_START, PC_THREADS);  // n_it, barriers
       }
     }
+    if (C::SPLIT && n_k > 0 && ok) load(1, behind, [] {});
     if (n_pages == 0) {
       // q has landed before the others put their zeros where it goes
       pc_wait_warp(&M->q_full, 0, abort, a.status_dev);
@@ -444,8 +475,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     // whatever was asked for has landed before the CTA retires
     if (*abort) {
       tc::mbar_wait(&M->q_full, 0, 50000000ull);
-      for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
-        tc::mbar_wait(&M->kv_full[k % C::STAGES], (k / C::STAGES) & 1, 50000000ull);
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t n = kv ? n_v : n_k;
+        const uint32_t held = C::SPLIT ? 2 - kv : (C::STAGES + 1) / 2;
+        for (uint32_t k = n > held ? n - held : 0; k < n; ++k)
+          tc::mbar_wait(&M->kv_full[C::stage(kv, k)], C::turn(kv, k) & 1, 50000000ull);
+      }
     }
   } else {
     if (warp == PC_MMA) tc::tmem_alloc(&M->tmem, 512);
@@ -474,18 +509,18 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       const uint64_t dv = tc::desc_sw128_mn(kvs, 16384, 1024);
       const uint32_t bar_s = tc::smem_u32(M->s_full), bar_pv = tc::smem_u32(M->pv_done),
                      bar_kv = tc::smem_u32(M->kv_empty);
-      int sk = 0, sv = 1;  // stages of the next K and V
+      int sk = 0, sv = C::stage(1, 0);  // stages of the next K and V
       // The next logits, page qj of tile qs into buffer qb.
       int qj = 0, qs = 0, qb = 0;
       auto next_s = [&] {
         if (C::ROTATE && qs == 0 && !pc_wait(&M->kv_full[sk], (qj >> 2) & 1, abort, a.status_dev))
           return false;
-        issue_qk<D>(tmem + qb * 128, dq + qs * (C::TILE >> 4), dk + sk * (C::TILE >> 4), idesc_s,
+        issue_qk<DK>(tmem + qb * 128, dq + qs * (C::TILE >> 4), dk + sk * (C::TILE >> 4), idesc_s,
                     bar_s + 8 * qb, qs == n_sub - 1 ? bar_kv + 8 * sk : 0);
         if (++qs == n_sub) {
           qs = 0;
           ++qj;
-          sk = sk + 2 >= C::STAGES ? sk + 2 - C::STAGES : sk + 2;
+          sk = C::SPLIT ? sk ^ 1 : (sk + 2 >= C::STAGES ? sk + 2 - C::STAGES : sk + 2);
         }
         qb = C::ROTATE ? (qb == 2 ? 0 : qb + 1) : qs;
         return true;
@@ -510,7 +545,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           }
           if (qj < n_it) ok = next_s();  // over P, or over the P before it
         }
-        sv = sv + 2 >= C::STAGES ? sv + 2 - C::STAGES : sv + 2;
+        if (!C::SPLIT) sv = sv + 2 >= C::STAGES ? sv + 2 - C::STAGES : sv + 2;
       }
       for (int s = 0; s < n_sub && ok; ++s) tc::mma_commit(&M->o_full[s]);
       // every issued MMA has completed before tensor memory is released
@@ -522,12 +557,11 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     // ================================================================ V on mixed pages
     bool ok = true;
     for (int j = 0; j < n_it && ok; ++j) {
-      const uint32_t ik = 2 * j, iv = ik + 1;
-      const int sv = iv % C::STAGES;
+      const int sv = C::stage(1, j);
       // in the order of the loads: only then does a stage's parity tell this
       // load from the stage's one before
       if (j == 0) ok = pc_wait_warp(&M->kv_full[0], 0, abort, a.status_dev);
-      ok = ok && pc_wait_warp(&M->kv_full[sv], (iv / C::STAGES) & 1, abort, a.status_dev);
+      ok = ok && pc_wait_warp(&M->kv_full[sv], C::turn(1, j) & 1, abort, a.status_dev);
       if (!ok) break;
       Page &P = M->page[j % PC_META];
       if (P.mixed) {
@@ -539,7 +573,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           uint4 *p = reinterpret_cast<uint4 *>(v + row * 128);
           uint32_t bad = 0;
 #pragma unroll
-          for (int c = 0; c < C::CHUNKS; ++c) {
+          for (int c = 0; c < C::V_CHUNKS; ++c) {
             uint4 w[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) w[q] = p[c * 1024 + ((q + lane) & 7)];
@@ -549,7 +583,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
                      paged::not_finite2(w[q].z) | paged::not_finite2(w[q].w);
           }
           if (bad) {
-            for (int c = 0; c < C::CHUNKS; ++c)
+            for (int c = 0; c < C::V_CHUNKS; ++c)
               for (int q = 0; q < 8; ++q) p[c * 1024 + q] = make_uint4(0, 0, 0, 0);
             wrote = true;
           }
@@ -559,7 +593,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         if (wrote) tc::fence_async_shared();
       }
       if (j + 1 < n_it)  // the MMA warp waits once for both
-        ok = pc_wait_warp(&M->kv_full[(ik + 2) % C::STAGES], ((ik + 2) / C::STAGES) & 1, abort,
+        ok = pc_wait_warp(&M->kv_full[C::stage(0, j + 1)], C::turn(0, j + 1) & 1, abort,
                           a.status_dev);
       __syncwarp();
       if (lane == 0 && ok) tc::mbar_arrive(&M->ready[j & 3]);
@@ -825,9 +859,9 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   if (warp == PC_MMA) tc::tmem_dealloc(tmem, 512);
 }
 
-template <int D>
+template <int DK, int D>
 cudaError_t launch(const csa_paged_attn_args &a, const Parts &parts, cudaStream_t s) {
-  using C = Cfg<D>;
+  using C = Cfg<DK, D>;
   const int g = a.n_heads / a.n_kv_heads;
   ChunkGrid G;
   G.rows_tile = 128 / g;
@@ -842,15 +876,15 @@ cudaError_t launch(const csa_paged_attn_args &a, const Parts &parts, cudaStream_
   static bool attr[64] = {};
   if (dev < 0 || dev >= 64 || !attr[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(
-        paged_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        paged_chunk_kernel<DK, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr[dev] = true;
   }
   const long long grid = (long long)G.n_tiles * a.n_kv_heads * G.n_parts;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   launch_begin(CSA_K_PAGED_ATTN, s);
-  const cudaError_t e = launch_kernel(paged_chunk_kernel<D>, dim3((unsigned)grid), dim3(PC_THREADS),
-                                      smem, s, 0, false, a, parts, G, qmap, kmap, vmap);
+  const cudaError_t e = launch_kernel(paged_chunk_kernel<DK, D>, dim3((unsigned)grid),
+                                      dim3(PC_THREADS), smem, s, 0, false, a, parts, G, qmap, kmap, vmap);
   launch_end(CSA_K_PAGED_ATTN, s);
   return e;
 }
@@ -891,7 +925,8 @@ int paged_chunk_parts(const csa_paged_attn_args &a, int sms) {
 
 cudaError_t launch_paged_chunk(const csa_paged_attn_args &a, const Parts &parts, int /*sms*/,
                                cudaStream_t s) {
-  return a.head_dim == 64 ? launch<64>(a, parts, s) : launch<128>(a, parts, s);
+  if (a.head_dim == 192) return launch<192, 128>(a, parts, s);
+  return a.head_dim == 64 ? launch<64, 64>(a, parts, s) : launch<128, 128>(a, parts, s);
 }
 
 }  // namespace csa

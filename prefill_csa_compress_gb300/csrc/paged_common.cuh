@@ -14,7 +14,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // Positions [lo, hi) that a row at position p sees in a cache of kv_len; neither is
 // negative, so that a page's first position can be taken off both.
-__device__ __forceinline__ void visible_range(const csa_paged_attn_args &a, int kv_len, int p,
+template <typename Args>  // (of the calls that read a paged cache)
+__device__ __forceinline__ void visible_range(const Args &a, int kv_len, int p,
                                               int &lo, int &hi) {
   const int len = min(kv_len, a.max_blocks < 0x7FFFFFFF / kBlock ? a.max_blocks * kBlock : 0x7FFFFFFF);
   hi = max(a.causal && p < len ? p + 1 : len, 0);
