@@ -1,85 +1,808 @@
-// Absorbed latent attention over a paged latent cache (csa_latent_attn).
+// Absorbed latent attention over a paged latent cache (csa_latent_attn): tcgen05
+// tiles of up to 64 (row, head) pairs against 64 positions.
+//
+// A position is one row of 576 channels, key and value at once: the logits take all of
+// it, the values are its first 512.  With the heads of a row stacked under it, an item of
+// R rows x G heads (R G <= 64) of one request does
+//   S[m, j]  = q_m . (c_j, r_j)      64 x 64 x 576, both operands K-major
+//   O^T[:, m] += c^T P^T             512 x pairs x 64: the latents as they lie are the
+//                                    M-major operand, P through shared memory
+// so a tile is fetched once for both products, and O^T takes 4 x 64 columns of tensor
+// memory beside two buffers of S.  P = 2^(S scale log2(e) - ref), one reference a pair,
+// which moves (and O^T is rescaled) only when some P reaches 2; it is set so that the
+// largest is 2^-7, so that is seldom.
+//
+// Roles: warp 0 loads (TMA, nine boxes of 64 channels a tile, each with a barrier of its
+// own, two tiles in flight; a box is asked for again as soon as its last product is
+// done); warp 1 issues whichever product can go on, P's first, since that frees the
+// loads; warps 4 .. 11 do the softmax, two warps 16 pairs, and the outputs.
+//
+// Calls of up to 512 rows: all tiles of all items are one list, cut into equal shares,
+// one per SM, so that ragged contexts load every SM alike; a cut item leaves parts that
+// latent_join_kernel puts together in order.  More rows: a CTA takes R rows whole.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
+#include "attn_common.cuh"
 #include "cache_common.cuh"
 #include "paged_common.cuh"
+#include "tc.cuh"
 
 namespace csa {
 namespace {
 
-// One CTA a (row, head): 256 positions at a time, a thread a logit, then two
-// output channels a thread.
-__global__ void __launch_bounds__(256) latent_attn_kernel(csa_latent_attn_args a) {
-  __shared__ float q[kLatent + kRopeDim], p[256], red[8];
-  __shared__ long long at[256];
-  const int t = blockIdx.x / a.n_heads, h = blockIdx.x % a.n_heads, tid = threadIdx.x;
-  const int b = a.row_req[t];
-  if (b >= a.n_req && tid == 0) flag(a.status_dev, CSA_DEV_BAD_POS);
-  if (b < 0 || b >= a.n_req) return;
-  int lo, hi;
-  paged::visible_range(a, a.kv_len[b], a.row_pos[t], lo, hi);
-  const __nv_bfloat16 *qp = reinterpret_cast<const __nv_bfloat16 *>(
-      static_cast<const uint8_t *>(a.q) + t * a.q_row_stride + h * a.q_head_stride);
-  const __nv_bfloat16 *rp = reinterpret_cast<const __nv_bfloat16 *>(
-      static_cast<const uint8_t *>(a.q_rope) + t * a.q_rope_row_stride + h * a.q_rope_head_stride);
-  for (int i = tid; i < kLatent + kRopeDim; i += 256)
-    q[i] = __bfloat162float(i < kLatent ? qp[i] : rp[i - kLatent]);
-  __syncthreads();
-  const float sl2 = a.softmax_scale * paged::kLog2e;
-  float m = -INFINITY, l = 0.f, o[2] = {};
-  for (int j0 = lo; j0 < hi; j0 += 256) {
-    const int j = j0 + tid;
-    const long long row =
-        j < hi ? page_row(a.block_table, a.max_blocks, a.n_blocks, b, j, a.status_dev) : -1;
-    float x = -INFINITY;
-    if (row >= 0) {
-      const __nv_bfloat16 *c = reinterpret_cast<const __nv_bfloat16 *>(
-          static_cast<const uint8_t *>(a.c_pool) + pool_offset(row, a.c_page_stride, a.c_token_stride));
-      const __nv_bfloat16 *r = reinterpret_cast<const __nv_bfloat16 *>(
-          static_cast<const uint8_t *>(a.r_pool) + pool_offset(row, a.r_page_stride, a.r_token_stride));
-      float s = 0.f;
-      for (int i = 0; i < kLatent; ++i) s += q[i] * __bfloat162float(c[i]);
-      for (int i = 0; i < kRopeDim; ++i) s += q[kLatent + i] * __bfloat162float(r[i]);
-      x = s * sl2;
+constexpr int LA_THREADS = 384;
+constexpr int LA_LOAD = 0, LA_MMA = 1, LA_SOFT0 = 4;  // first warps
+constexpr int LA_PAIRS = 64, LA_KEYS = 64;
+constexpr int LA_BOXES = 9;                   // of 64 channels; the last is the rotated key
+constexpr int LA_BOX = LA_KEYS * 128;         // bytes (of 64 pairs or 64 positions)
+constexpr int LA_TILE = LA_BOXES * LA_BOX;
+constexpr int LA_ROWS = 512;                  // of a call whose tiles are cut into shares
+constexpr int OFF_KV = LA_TILE, OFF_P = OFF_KV + 2 * LA_TILE, OFF_MISC = OFF_P + LA_BOX;
+constexpr int BAR_SOFT = 1;                   // named barrier of the softmax warps
+constexpr int O_COL = 0, S_COL = 256;         // tensor memory
+constexpr float kLift = 7.f;                  // log2 of the room below P = 2
+
+// A CTA's run of tiles of one item.
+struct Seg {
+  int t, nr;    // rows
+  int sub;      // group of 64 heads
+  int tile, n;  // first tile (of 64 positions) and how many
+  int slot;     // where its part goes, -1: the item is whole
+};
+constexpr int LA_NEAR = 6;  // segments kept in shared memory; the rest in the workspace
+
+struct Misc {
+  uint64_t q_full, q_empty, pv_done, p_full, o_free, drained, s_full[2];
+  uint64_t full[2][LA_BOXES], empty[2][5];  // (rotated keys last, pairs of boxes before)
+  uint32_t tmem;
+  int abort;
+  int n_seg, n_tiles;
+  int there[2];                // the tile's page is in the pool
+  uint32_t bad[2];             // positions of a tile with values that are not finite
+  Seg near_[LA_NEAR];
+  float top[2][LA_PAIRS], f[LA_PAIRS];
+};
+static_assert(OFF_MISC + sizeof(Misc) <= 227 * 1024, "shared memory");
+
+struct Parts {
+  float *o;      // [slots][64][512]
+  float2 *ml;    // [slots][64]
+  int4 *cut;     // [CTAs]: an item that the CTA begins and does not end: row, rows, sub, last CTA
+  Seg *far_;     // [CTAs][n_far]: a CTA's segments behind those in shared memory
+  int n_far;
+};
+
+struct Shape {
+  int gt, R, subs;  // heads and rows of an item, head groups
+  int n16;          // pairs, rounded up to 16
+  int shares;       // 1: the list of tiles is cut into shares
+};
+
+__device__ __forceinline__ bool la_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                        uint32_t *status) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = tc::global_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*abort) return false;
+      if (tc::global_ns() - t0 > 2000000000ull) {
+        *abort = 1;
+        flag(status, CSA_DEV_TIMEOUT);
+        return false;
+      }
     }
-    float mx = x;
-    for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, k));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
+  }
+}
+
+// 32 columns of 16 lanes: thread i holds columns 2 (i % 4) + {0, 1} of every group of
+// eight, of lane i / 4 (x[4 g], x[4 g + 1]) and of lane i / 4 + 8 (x[4 g + 2], ...).
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&x)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
+
+// The CTA's rows while its segments are found, where the tiles land afterwards.
+struct Plan {
+  long long *before;  // tiles of all items of earlier rows
+  int *req, *lo, *hi, *tiles, *first, *nr;
+  uint32_t *starts;   // a bit a row that differs from the one before it in its request
+  __device__ Plan(uint8_t *at, int n) {
+    before = reinterpret_cast<long long *>(at);
+    req = reinterpret_cast<int *>(before + n + 1);
+    lo = req + n, hi = lo + n, tiles = hi + n, first = tiles + n, nr = first + n;
+    starts = reinterpret_cast<uint32_t *>(nr + n);
+  }
+};
+
+__global__ void __launch_bounds__(LA_THREADS, 1)
+    latent_attn_kernel(csa_latent_attn_args a, Parts parts, Shape H,
+                       const __grid_constant__ CUtensorMap qmap,
+                       const __grid_constant__ CUtensorMap qrmap,
+                       const __grid_constant__ CUtensorMap cmap,
+                       const __grid_constant__ CUtensorMap rmap) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  Misc *M = reinterpret_cast<Misc *>(sm + OFF_MISC);
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tc::smem_u32(sm) & 1023u) {
+    if (tid == 0) flag(a.status_dev, CSA_DEV_TIMEOUT);
+    return;
+  }
+  volatile int *abort = &M->abort;
+  Seg *far_ = parts.far_ + (long long)blockIdx.x * parts.n_far;
+
+  // ================================================================ the CTA's segments
+  // rows [row0, row0 + n): all of the call, or this CTA's own
+  const int own = H.shares ? 0 : (int)(gridDim.x - 1 - blockIdx.x);
+  const int row0 = H.shares ? 0 : own / H.subs * H.R;
+  const int n = H.shares ? a.n_rows : min(H.R, a.n_rows - row0);
+  const int subs = H.shares ? H.subs : 1, sub0 = H.shares ? 0 : own % H.subs;
+  {
+    const Plan plan(sm + OFF_KV, n);
+    for (int r = tid; r < ((n + 31) & ~31); r += LA_THREADS) {
+      int b = -1, lo = 0, hi = 0;
+      if (r < n) {
+        b = a.row_req[row0 + r];
+        if (b >= a.n_req) {
+          if ((H.shares ? blockIdx.x : sub0) == 0) flag(a.status_dev, CSA_DEV_BAD_POS);
+          b = -1;
+        }
+        if (b >= 0) paged::visible_range(a, a.kv_len[b], a.row_pos[row0 + r], lo, hi);
+        plan.req[r] = b, plan.lo[r] = lo, plan.hi[r] = hi;
+      }
+      const bool start = r < n && (r == 0 || a.row_req[row0 + r - 1] != a.row_req[row0 + r]);
+      const uint32_t bits = __ballot_sync(0xffffffffu, start);
+      if (lane == 0) plan.starts[r >> 5] = bits;
+    }
+    if (tid == 0) {
+      tc::mbar_init(&M->q_full, 1);
+      tc::mbar_init(&M->q_empty, 1);
+      tc::mbar_init(&M->pv_done, 1);
+      tc::mbar_init(&M->p_full, 8);
+      tc::mbar_init(&M->o_free, 8);
+      tc::mbar_init(&M->drained, 1);
+      for (int i = 0; i < 2; ++i) {
+        tc::mbar_init(&M->s_full[i], 2);
+        for (int c = 0; c < LA_BOXES; ++c) tc::mbar_init(&M->full[i][c], 1);
+        for (int c = 0; c < 5; ++c) tc::mbar_init(&M->empty[i][c], 1);
+      }
+      M->abort = 0;
+      M->bad[0] = M->bad[1] = 0;
+      tc::mbar_fence_init();
+    }
     __syncthreads();
-    mx = m;
-    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, red[k]);
-    const float f = m == mx ? 1.f : exp2f(m - mx);
-    m = mx;
-    // (round the probabilities as the product with the latents takes them)
-    p[tid] = row < 0 || x == -INFINITY ? 0.f : exp2f(x - (m == -INFINITY ? 0.f : m));
-    at[tid] = row;
+    for (int r = tid; r < n; r += LA_THREADS) {
+      const int b = plan.req[r];
+      int w = r >> 5;
+      uint32_t bits = plan.starts[w] & (0xffffffffu >> (31 - (r & 31)));
+      while (bits == 0) bits = plan.starts[--w];  // (row 0 starts a run)
+      const int run = w * 32 + 31 - __clz(bits);
+      int tiles = 0, first = 0, k = 0;
+      if (b >= 0 && (r - run) % H.R == 0) {
+        int lo = 0x7FFFFFFF, hi = 0;
+        for (; k < H.R && r + k < n && plan.req[r + k] == b; ++k)
+          if (plan.lo[r + k] < plan.hi[r + k]) {
+            lo = min(lo, plan.lo[r + k]);
+            hi = max(hi, plan.hi[r + k]);
+          }
+        if (lo < hi) {
+          first = lo / LA_KEYS;
+          tiles = (hi - 1) / LA_KEYS - first + 1;
+        }
+      }
+      plan.tiles[r] = tiles, plan.first[r] = first, plan.nr[r] = k;
+    }
     __syncthreads();
-    l *= f, o[0] *= f, o[1] *= f;
-    for (int k = 0; k < 256 && j0 + k < hi; ++k) {
-      if (at[k] < 0) continue;
-      const __nv_bfloat162 c = reinterpret_cast<const __nv_bfloat162 *>(
-          static_cast<const uint8_t *>(a.c_pool) +
-          pool_offset(at[k], a.c_page_stride, a.c_token_stride))[tid];
-      l += p[k];
-      const float pr = round_bf16(p[k]);
-      o[0] += pr * __low2float(c), o[1] += pr * __high2float(c);
+    if (warp == 0) {
+      long long sum = 0;
+      for (int r0 = 0; r0 < n; r0 += 32) {
+        const int r = r0 + lane;
+        const long long mine = r < n ? (long long)plan.tiles[r] * subs : 0;
+        long long x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (r < n) plan.before[r] = sum + x - mine;
+        sum += __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (lane == 0) plan.before[n] = sum;
+      __syncwarp();
+      if (lane == 0) {
+        const long long W = sum, N = H.shares ? (W < gridDim.x ? W : gridDim.x) : 1;
+        const long long c = H.shares ? blockIdx.x : 0;
+        int n_seg = 0, n_tiles = 0;
+        int4 cut = make_int4(-1, 0, 0, 0);
+        if (W > 0 && c < N) {
+          const long long w0 = c * W / N, w1 = (c + 1) * W / N;
+          n_tiles = (int)(w1 - w0);
+          int l = 0, h = n;
+          while (h - l > 1) {
+            const int mid = (l + h) >> 1;
+            if (plan.before[mid] <= w0)
+              l = mid;
+            else
+              h = mid;
+          }
+          for (long long w = w0; w < w1;) {
+            while (plan.tiles[l] == 0) ++l;
+            const int P = plan.tiles[l], sub = (int)((w - plan.before[l]) / P);
+            const int pa = (int)(w - plan.before[l] - (long long)sub * P);
+            const int pb = (int)min((long long)P, pa + (w1 - w));
+            Seg s;
+            s.t = row0 + l, s.nr = plan.nr[l], s.sub = sub0 + sub;
+            s.tile = plan.first[l] + pa, s.n = pb - pa;
+            s.slot = pa > 0 ? 2 * (int)c : (pb < P ? 2 * (int)c + 1 : -1);
+            if (pa == 0 && pb < P)
+              cut = make_int4(s.t, s.nr, s.sub, (int)(((w + P) * N - 1) / W));
+            if (n_seg < LA_NEAR)
+              M->near_[n_seg] = s;
+            else
+              far_[n_seg] = s;
+            ++n_seg;
+            w += pb - pa;
+            if (pb == P && sub == subs - 1) ++l;
+          }
+        }
+        M->n_seg = n_seg, M->n_tiles = n_tiles;
+        if (H.shares) parts.cut[c] = cut;
+      }
+    }
+    // rows of items that see nothing
+    for (int r = H.shares ? (int)blockIdx.x : 0; r < n; r += H.shares ? (int)gridDim.x : 1) {
+      if (plan.nr[r] == 0 || plan.tiles[r] != 0) continue;
+      const int h0 = H.shares ? 0 : sub0 * H.gt, h1 = H.shares ? a.n_heads : min(a.n_heads, h0 + H.gt);
+      for (int k = 0; k < plan.nr[r]; ++k) {
+        const long long at = (long long)(row0 + r + k) * a.n_heads;
+        for (int i = tid; i < (h1 - h0) * (kLatent / 8); i += LA_THREADS)
+          reinterpret_cast<uint4 *>(a.out)[(at + h0) * (kLatent / 8) + i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+          for (int h = h0 + tid; h < h1; h += LA_THREADS)
+            a.lse[at + h] = a.sink ? a.sink[h] : -INFINITY;
+      }
     }
     __syncthreads();
   }
-  const paged::Joined J = paged::finish(m, l, a.sink ? a.sink[h] : -INFINITY);
-  const bool zero = m == -INFINITY && l == 0.f;
-  reinterpret_cast<__nv_bfloat162 *>(a.out)[((long long)t * a.n_heads + h) * (kLatent / 2) + tid] =
-      zero ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(o[0] * J.inv, o[1] * J.inv);
-  if (a.lse && tid == 0) a.lse[(long long)t * a.n_heads + h] = J.lse;
+  const int n_seg = M->n_seg, n_tiles = M->n_tiles;
+  if (n_seg == 0) return;
+  auto seg_at = [&](int i) { return i < LA_NEAR ? M->near_[i] : far_[i]; };
+  if (warp == LA_MMA) tc::tmem_alloc(&M->tmem, 512);
+  tc::fence_async_shared();  // (the plan was where the tiles land)
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = __reduce_or_sync(0xffffffffu, M->tmem);
+
+  if (warp == LA_LOAD) {
+    // ================================================================ loads
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t it = 0, n_q = 0;
+      for (int s = 0; s < n_seg && ok; ++s) {
+        const Seg g = seg_at(s);
+        const int32_t *table = a.block_table + (long long)a.row_req[g.t] * a.max_blocks;
+        int phys = table[g.tile >> 1];
+        ok = la_wait(&M->q_empty, (s & 1) ^ 1, abort, a.status_dev);
+        if (!ok) break;
+        ++n_q;
+        tc::mbar_arrive_expect_tx(&M->q_full, LA_BOXES * 128 * H.gt * H.R);
+        tc::tma_load_3d(sm + 8 * LA_BOX, &qrmap, 0, g.sub * H.gt, g.t, &M->q_full);
+        for (int c = 0; c < 8; ++c)
+          tc::tma_load_3d(sm + c * LA_BOX, &qmap, c * 64, g.sub * H.gt, g.t, &M->q_full);
+        for (int i = 0; i < g.n && ok; ++i, ++it) {
+          const int st = it & 1, tile = g.tile + i;
+          const uint32_t par = ((it >> 1) & 1) ^ 1;
+          const int next = i + 1 < g.n ? table[(tile + 1) >> 1] : 0;
+          const bool there = phys >= 0 && phys < a.n_blocks;
+          uint8_t *dst = sm + OFF_KV + st * LA_TILE;
+          ok = la_wait(&M->empty[st][4], par, abort, a.status_dev);
+          if (!ok) break;
+          if (!there) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
+          M->there[st] = there;
+          if (there) {
+            tc::mbar_arrive_expect_tx(&M->full[st][8], LA_BOX);
+            tc::tma_load_3d(dst + 8 * LA_BOX, &rmap, 0, (tile & 1) * LA_KEYS, phys, &M->full[st][8]);
+          } else {
+            tc::mbar_arrive(&M->full[st][8]);
+          }
+          for (int c = 0; c < 8; ++c) {
+            if ((c & 1) == 0) ok = la_wait(&M->empty[st][c >> 1], par, abort, a.status_dev);
+            if (!ok) break;
+            if (there) {
+              tc::mbar_arrive_expect_tx(&M->full[st][c], LA_BOX);
+              tc::tma_load_3d(dst + c * LA_BOX, &cmap, c * 64, (tile & 1) * LA_KEYS, phys,
+                              &M->full[st][c]);
+            } else {
+              tc::mbar_arrive(&M->full[st][c]);
+            }
+          }
+          phys = next;
+        }
+      }
+      // whatever was asked for has landed before the CTA retires
+      if (!ok || *abort) {
+        if (n_q > 0) tc::mbar_wait(&M->q_full, (n_q - 1) & 1, 50000000ull);
+        for (uint32_t k = it > 1 ? it - 2 : 0; k <= it; ++k)
+          for (int c = 0; c < LA_BOXES; ++c)
+            tc::mbar_wait(&M->full[k & 1][c], (k >> 1) & 1, 5000000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == LA_MMA) {
+    // ================================================================ MMA
+    if (tc::elect_one()) {
+      constexpr uint32_t idesc_s = tc::idesc_bf16_f32(LA_PAIRS, LA_KEYS);
+      const uint32_t idesc_o = tc::idesc_bf16_f32(128, H.n16) | (1u << 15);  // c^T is M-major
+      const uint32_t base = tc::smem_u32(sm);
+      const uint64_t dq = tc::desc_sw128(base), dk = tc::desc_sw128(base + OFF_KV);
+      const uint64_t dv = tc::desc_sw128_mn(base + OFF_KV, LA_BOX, 1024);
+      const uint64_t dp = tc::desc_sw128(base + OFF_P);
+      // the next box of logits (tile sj, its segment ss ending before tile s_end), and
+      // the next product (tile pj, segment ps)
+      int sj = 0, sc = 0, ss = 0, s_end = seg_at(0).n;
+      int pj = 0, ps = 0, p_end = s_end;
+      bool q_here = false, first = true;
+      uint32_t idle = 0;
+      uint64_t t0 = 0;
+      while (pj < n_tiles) {
+        bool moved = false;
+        if (pj < sj && tc::mbar_test_wait(&M->p_full, pj & 1) &&
+            (!first || ps == 0 || tc::mbar_test_wait(&M->o_free, (ps - 1) & 1))) {
+          tc::tc_fence_after();
+          const int st = pj & 1;
+#pragma unroll 1
+          for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc::mma_bf16(tmem + O_COL + b * 64, dv + ((st * LA_TILE + 2 * b * LA_BOX) >> 4) + k * 128,
+                           dp + k * 2, idesc_o, !(first && k == 0));
+            tc::mma_commit(&M->empty[st][b]);
+          }
+          tc::mma_commit(&M->pv_done);
+          first = false;
+          if (++pj == p_end && pj < n_tiles) {
+            p_end += seg_at(++ps).n;
+            first = true;
+          }
+          moved = true;
+        }
+        if (sj < n_tiles && sj - pj < 2) {
+          if (!q_here) q_here = tc::mbar_test_wait(&M->q_full, ss & 1);
+          const int st = sj & 1, c = sc == 0 ? 8 : sc - 1;
+          if (q_here && tc::mbar_test_wait(&M->full[st][c], (sj >> 1) & 1)) {
+            tc::tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc::mma_bf16(tmem + S_COL + st * 64, dq + ((c * LA_BOX) >> 4) + k * 2,
+                           dk + ((st * LA_TILE + c * LA_BOX) >> 4) + k * 2, idesc_s,
+                           !(sc == 0 && k == 0));
+            if (++sc == LA_BOXES) {
+              sc = 0;
+              tc::mma_commit(&M->s_full[st]);
+              tc::mbar_arrive(&M->s_full[st]);  // hands on what the loads were told
+              tc::mma_commit(&M->empty[st][4]);
+              if (++sj == s_end) {
+                tc::mma_commit(&M->q_empty);
+                q_here = false;
+                if (sj < n_tiles) s_end += seg_at(++ss).n;
+              }
+            }
+            moved = true;
+          }
+        }
+        if (moved) {
+          idle = 0;
+        } else if ((++idle & 255u) == 0) {
+          if (*abort) break;
+          const uint64_t now = tc::global_ns();
+          if (idle == 256u)
+            t0 = now;
+          else if (now - t0 > 2000000000ull) {
+            *abort = 1;
+            flag(a.status_dev, CSA_DEV_TIMEOUT);
+            break;
+          }
+        }
+      }
+      // every issued MMA has completed before tensor memory is released
+      tc::mma_commit(&M->drained);
+      tc::mbar_wait(&M->drained, 0, 100000000ull);
+    }
+    __syncwarp();
+  } else if (warp >= LA_SOFT0) {
+    // ================================================================ softmax and outputs
+    const int qd = warp & 3, half = (warp - LA_SOFT0) >> 2;
+    const int ma = 16 * qd + (lane >> 2), fc = (lane & 3) * 2;  // pairs ma, ma + 8
+    const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+    const float sl2 = a.softmax_scale * paged::kLog2e;
+    uint8_t *P = sm + OFF_P;
+    uint32_t it = 0;
+    auto wait = [&](uint64_t *bar, uint32_t turn) {
+      return (bool)__all_sync(0xffffffffu, la_wait(bar, turn & 1, abort, a.status_dev));
+    };
+    // ok: no wait of this warp gave up; given_up: some warp's did
+    bool ok = true, given_up = false;
+    for (int s = 0; s < n_seg && !given_up; ++s) {
+      const Seg g = seg_at(s);
+      const int b = a.row_req[g.t], len = a.kv_len[b];
+      // what the item's rows see: all of them, and this thread's two
+      int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = 0;
+      int lo[2] = {0, 0}, hi[2] = {0, 0};
+      for (int r = 0; r < g.nr; ++r) {
+        int l, h;
+        paged::visible_range(a, len, a.row_pos[g.t + r], l, h);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int m = ma + 8 * e;
+          if (m / H.gt == r && g.sub * H.gt + m % H.gt < a.n_heads) lo[e] = l, hi[e] = h;
+        }
+        if (l >= h) {
+          all_hi = 0;
+          continue;
+        }
+        all_lo = max(all_lo, l), all_hi = min(all_hi, h);
+        any_lo = min(any_lo, l), any_hi = max(any_hi, h);
+      }
+      float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int i = 0; i < g.n; ++i, ++it) {
+        const int st = it & 1, base = (g.tile + i) * LA_KEYS;
+        ok = wait(&M->s_full[st], it >> 1) && ok;
+        const bool there = ok && M->there[st];
+        const bool mixed = !there || base < all_lo || all_hi - base < LA_KEYS;
+        tc::tc_fence_after();
+        float x[16];
+        tmem_ld_16x32(tmem + S_COL + st * 64 + 32 * half + lane_off, x);
+        if (mixed) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int e = (k >> 1) & 1, j = base + 32 * half + (k >> 2) * 8 + fc + (k & 1);
+            if (!there || j < lo[e] || j >= hi[e]) x[k] = -INFINITY;
+          }
+        }
+        float p[16];
+        uint32_t w[8];
+        for (bool move = i == 0;;) {
+          if (move) {
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < 16; ++k) top[(k >> 1) & 1] = fmaxf(top[(k >> 1) & 1], x[k]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+              top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+              if ((lane & 3) == 0) M->top[half][ma + 8 * e] = top[e] * sl2;
+            }
+            tc::bar_sync(BAR_SOFT, 256);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float t = fmaxf(M->top[0][ma + 8 * e], M->top[1][ma + 8 * e]);
+              float f = 1.f;
+              if (t > ref[e] + 1.f && hi[e] > lo[e]) {
+                f = ref[e] == -INFINITY ? 1.f : exp2f(ref[e] - (t + kLift));
+                ref[e] = t + kLift;
+                l[e] *= f;
+              }
+              if (half == 0 && (lane & 3) == 0) M->f[ma + 8 * e] = f;
+            }
+            if (i > 0) {
+              // O^T of all pairs, once the product before is complete
+              ok = wait(&M->pv_done, it - 1) && ok;
+              tc::bar_sync(BAR_SOFT, 256);
+              tc::tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < 128; c += 32) {
+                if ((c & 63) >= H.n16) continue;
+                const uint32_t at = tmem + O_COL + half * 128 + c + lane_off;
+                float o[32];
+                tc::tmem_ld32(at, o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= M->f[(c & 63) + k];
+                tc::tmem_st32(at, o);
+              }
+              tc::tmem_wait_st();
+              tc::tc_fence_before();
+            }
+            // (the next reading of top and f is behind this barrier)
+            tc::bar_sync(BAR_SOFT, 256);
+          }
+          uint32_t any = 0;
+          const float r0[2] = {ref[0] == -INFINITY ? 1e30f : -ref[0],
+                               ref[1] == -INFINITY ? 1e30f : -ref[1]};
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            const int e = (k >> 1) & 1;
+            p[k] = attn::exp2_sfu(fmaf(x[k], sl2, r0[e]));
+            p[k + 1] = attn::exp2_sfu(fmaf(x[k + 1], sl2, r0[e]));
+            w[k >> 1] = attn::pack2(p[k], p[k + 1]);
+            if (hi[e] > lo[e]) any |= w[k >> 1];
+          }
+          // (a wait that gave up is known to all of them from here: every thread takes
+          // the same way past the barriers)
+          if (!tc::bar_or(BAR_SOFT, 256, !ok || (!move && (any & 0x40004000u)))) break;
+          if (tc::bar_or(BAR_SOFT, 256, !ok)) {
+            given_up = true;
+            break;
+          }
+          if (move) break;
+          move = true;
+        }
+        if (given_up) break;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) l[(k >> 1) & 1] += p[k];
+        if (mixed) {
+          // Positions that not every row sees: latents that are not finite become zero
+          // (zero times them is not zero), and rows that see them NaN.
+          uint8_t *kv = sm + OFF_KV + st * LA_TILE;
+          const int key = (tid - LA_SOFT0 * 32) >> 2, j = base + key;
+          if (!there || j < all_lo || j >= all_hi) {
+            bool zero = !there || j < any_lo || j >= any_hi, bad = false;
+            uint4 *row = reinterpret_cast<uint4 *>(kv + key * 128 + 2 * (lane & 3) * LA_BOX);
+            if (!zero) {
+              uint32_t odd = 0;
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {
+                const uint4 v = row[(u >> 3) * (LA_BOX / 16) + ((u + key) & 7)];
+                odd |= paged::not_finite2(v.x) | paged::not_finite2(v.y) | paged::not_finite2(v.z) |
+                       paged::not_finite2(v.w);
+              }
+              zero = bad = odd != 0;
+            }
+            if (zero)
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                row[(u >> 3) * (LA_BOX / 16) + ((u + key) & 7)] = make_uint4(0, 0, 0, 0);
+            if (bad) atomicOr(&M->bad[key >> 5], 1u << (key & 31));
+          }
+          tc::bar_sync(BAR_SOFT, 256);
+          const uint32_t bad[2] = {M->bad[0], M->bad[1]};
+          if (bad[0] | bad[1]) {
+            for (int k = 0; k < LA_KEYS; ++k)
+              if (bad[k >> 5] >> (k & 31) & 1u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (base + k >= lo[e] && base + k < hi[e]) l[e] = NAN;
+            tc::bar_sync(BAR_SOFT, 256);
+            if (tid == LA_SOFT0 * 32) M->bad[0] = M->bad[1] = 0;
+          }
+        }
+        // P goes where the product before read its own
+        if (it > 0) ok = wait(&M->pv_done, it - 1) && ok;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int m = ma + 8 * (k & 1), chunk = 4 * half + (k >> 1);
+          *reinterpret_cast<uint32_t *>(P + m * 128 + ((chunk ^ (m & 7)) << 4) + fc * 2) = w[k];
+        }
+        tc::fence_async_shared();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&M->p_full);
+      }
+      // ---- the item's outputs, or its part
+      if (given_up) break;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        if ((lane & 3) == 0) M->top[half][ma + 8 * e] = l[e];
+      }
+      tc::bar_sync(BAR_SOFT, 256);
+      if (half == 0 && (lane & 3) == 0)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int m = ma + 8 * e, r = m / H.gt, h = g.sub * H.gt + m % H.gt;
+          const float sum = M->top[0][m] + M->top[1][m];
+          float f = 0.f;
+          if (r < g.nr && h < a.n_heads) {
+            const long long row = (long long)(g.t + r) * a.n_heads + h;
+            if (g.slot >= 0) {
+              parts.ml[(long long)g.slot * LA_PAIRS + m] = make_float2(ref[e], sum);
+            } else {
+              const paged::Joined J = paged::finish(ref[e], sum, a.sink ? a.sink[h] : -INFINITY);
+              f = ref[e] == -INFINITY && sum == 0.f ? 0.f : J.inv;
+              if (a.lse) a.lse[row] = J.lse;
+            }
+          }
+          M->f[m] = f;
+        }
+      ok = wait(&M->pv_done, it - 1) && ok;
+      if (tc::bar_or(BAR_SOFT, 256, !ok)) break;
+      tc::tc_fence_after();
+#pragma unroll 1
+      for (int blk = 2 * half; blk < 2 * half + 2; ++blk) {
+        const int d = blk * 128 + 32 * qd + lane;
+#pragma unroll 1
+        for (int c = 0; c < H.n16; c += 32) {
+          float o[32];
+          tc::tmem_ld32(tmem + O_COL + blk * 64 + c + lane_off, o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const int m = c + k, r = m / H.gt, h = g.sub * H.gt + m % H.gt;
+            if (r >= g.nr || h >= a.n_heads) continue;
+            if (g.slot >= 0) {
+              parts.o[((long long)g.slot * LA_PAIRS + m) * kLatent + d] = o[k];
+            } else {
+              const float f = M->f[m];  // (0: the row saw nothing)
+              static_cast<__nv_bfloat16 *>(a.out)[((long long)(g.t + r) * a.n_heads + h) * kLatent + d] =
+                  __float2bfloat16_rn(f == 0.f ? 0.f : o[k] * f);
+            }
+          }
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&M->o_free);
+      tc::bar_sync(BAR_SOFT, 256);  // (before top and f are written again)
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == LA_MMA) tc::tmem_dealloc(tmem, 512);
+}
+
+// The pairs of items that were cut: CTA (m, c) joins pair m of the item that CTA c of
+// the attention began and did not end, parts in order.
+__global__ void __launch_bounds__(128)
+    latent_join_kernel(csa_latent_attn_args a, Parts parts, Shape H, int n_ctas) {
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  const int c = blockIdx.y, m = blockIdx.x, tid = threadIdx.x;
+  const int4 it = parts.cut[c];
+  if (it.x < 0 || it.w >= n_ctas) return;
+  const int r = m / H.gt, h = it.z * H.gt + m % H.gt;
+  if (r >= it.y || h >= a.n_heads) return;
+  const int n = it.w - c + 1;
+  auto slot = [&](int s) { return (2ll * (c + s) + (s == 0 ? 1 : 0)) * LA_PAIRS + m; };
+  float ref = -INFINITY;
+  for (int s = 0; s < n; ++s) ref = fmaxf(ref, parts.ml[slot(s)].x);
+  float acc[4] = {}, l = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const float2 ml = parts.ml[slot(s)];
+    const float4 o = reinterpret_cast<const float4 *>(parts.o + slot(s) * kLatent)[tid];
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;                     // nothing was seen there
+    const float w = ml.x == -INFINITY ? ml.y : exp2f(ml.x - ref);       // (l is NaN there)
+    l += w * ml.y;
+    acc[0] += w * o.x, acc[1] += w * o.y, acc[2] += w * o.z, acc[3] += w * o.w;
+  }
+  const paged::Joined J = paged::finish(ref, l, a.sink ? a.sink[h] : -INFINITY);
+  const bool zero = ref == -INFINITY && l == 0.f;
+  const long long row = (long long)(it.x + r) * a.n_heads + h;
+  __nv_bfloat162 out[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    out[e] = zero ? __floats2bfloat162_rn(0.f, 0.f)
+                  : __floats2bfloat162_rn(acc[2 * e] * J.inv, acc[2 * e + 1] * J.inv);
+  reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * kLatent)[tid] =
+      *reinterpret_cast<const uint2 *>(out);
+  if (a.lse && tid == 0) a.lse[row] = J.lse;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    sms = 152;
+  return sms;
+}
+
+Shape shape_of(const csa_latent_attn_args &a) {
+  Shape H;
+  H.gt = a.n_heads < LA_PAIRS ? a.n_heads : LA_PAIRS;
+  H.R = LA_PAIRS / H.gt;
+  H.subs = (a.n_heads + LA_PAIRS - 1) / LA_PAIRS;
+  H.n16 = (H.gt * H.R + 15) / 16 * 16;
+  H.shares = a.n_rows <= LA_ROWS;
+  return H;
+}
+
+// CTAs of a call whose rows are taken whole.
+long long blocks_of(const csa_latent_attn_args &a, const Shape &H) {
+  return (long long)((a.n_rows + H.R - 1) / H.R) * H.subs;
+}
+
+struct Layout {
+  size_t ml, cut, far_, total;
+  int n_far;
+};
+Layout layout(const csa_latent_attn_args &a, int sms) {
+  Layout L{0, 0, 0, 0, 0};
+  const Shape H = shape_of(a);
+  if (!H.shares) {  // a CTA that takes its rows whole has as many segments as rows, at most
+    L.n_far = H.R > LA_NEAR ? H.R : 0;
+    L.total = align_up((size_t)blocks_of(a, H) * L.n_far * sizeof(Seg), 256);
+    return L;
+  }
+  L.n_far = 2 * LA_ROWS;
+  const size_t slots = 2 * (size_t)sms * LA_PAIRS;
+  L.ml = align_up(slots * kLatent * sizeof(float), 256);
+  L.cut = L.ml + align_up(slots * sizeof(float2), 256);
+  L.far_ = L.cut + align_up(sms * sizeof(int4), 256);
+  L.total = L.far_ + align_up((size_t)sms * L.n_far * sizeof(Seg), 256);
+  return L;
+}
+
+bool encode(CUtensorMap *map, const void *base, const cuuint64_t (&dims)[3], int64_t s1, int64_t s2,
+            const cuuint32_t (&box)[3]) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void *f = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  const cuuint64_t strides[2] = {(cuuint64_t)s1, (cuuint64_t)s2};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  memset(map, 0, sizeof(*map));
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
-size_t latent_attn_workspace(const csa_latent_attn_args &) { return 0; }
+size_t latent_attn_workspace(const csa_latent_attn_args &a) { return layout(a, sm_count()).total; }
 
 cudaError_t launch_latent_attn(const csa_latent_attn_args &a, cudaStream_t s) {
+  const int sms = sm_count();
+  const Shape H = shape_of(a);
+  const Layout L = layout(a, sms);
+  uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+  const Parts parts{reinterpret_cast<float *>(ws), reinterpret_cast<float2 *>(ws + L.ml),
+                    reinterpret_cast<int4 *>(ws + L.cut), reinterpret_cast<Seg *>(ws + L.far_),
+                    L.n_far};
+  CUtensorMap qmap, qrmap, cmap, rmap;
+  const cuuint64_t rows = a.n_rows, heads = a.n_heads, pages = a.n_blocks;
+  const cuuint32_t qbox[3] = {64, (cuuint32_t)H.gt, (cuuint32_t)H.R}, kbox[3] = {64, LA_KEYS, 1};
+  if (!encode(&qmap, a.q, {kLatent, heads, rows}, a.q_head_stride, a.q_row_stride, qbox) ||
+      !encode(&qrmap, a.q_rope, {kRopeDim, heads, rows}, a.q_rope_head_stride, a.q_rope_row_stride,
+              qbox) ||
+      !encode(&cmap, a.c_pool, {kLatent, kBlock, pages}, a.c_token_stride, a.c_page_stride, kbox) ||
+      !encode(&rmap, a.r_pool, {kRopeDim, kBlock, pages}, a.r_token_stride, a.r_page_stride, kbox))
+    return cudaErrorInvalidValue;
+  const size_t smem = OFF_MISC + sizeof(Misc);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static bool attr[64] = {};
+  if (dev < 0 || dev >= 64 || !attr[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        latent_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr[dev] = true;
+  }
+  const long long grid = H.shares ? sms : blocks_of(a, H);
   launch_begin(CSA_K_LATENT_ATTN, s);
-  latent_attn_kernel<<<a.n_rows * a.n_heads, 256, 0, s>>>(a);
+  cudaError_t e = launch_kernel(latent_attn_kernel, dim3((unsigned)grid), dim3(LA_THREADS), smem, s,
+                                0, false, a, parts, H, qmap, qrmap, cmap, rmap);
   launch_end(CSA_K_LATENT_ATTN, s);
-  return cudaGetLastError();
+  if (e != cudaSuccess || !H.shares) return e != cudaSuccess ? e : cudaGetLastError();
+  launch_begin(CSA_K_LATENT_JOIN, s);
+  e = launch_kernel(latent_join_kernel, dim3(H.gt * H.R, (unsigned)sms), dim3(128), 0, s, 0, false,
+                    a, parts, H, sms);
+  launch_end(CSA_K_LATENT_JOIN, s);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace csa
