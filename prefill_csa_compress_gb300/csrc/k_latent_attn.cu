@@ -6,16 +6,18 @@
 // R rows x G heads (R G <= 64) of one request does
 //   S[m, j]  = q_m . (c_j, r_j)      64 x 64 x 576, both operands K-major
 //   O^T[:, m] += c^T P^T             512 x pairs x 64: the latents as they lie are the
-//                                    M-major operand, P through shared memory
+//                                    M-major operand, P in shared memory
 // so a tile is fetched once for both products, and O^T takes 4 x 64 columns of tensor
 // memory beside two buffers of S.  P = 2^(S scale log2(e) - ref), one reference a pair,
 // which moves (and O^T is rescaled) only when some P reaches 2; it is set so that the
 // largest is 2^-7, so that is seldom.
 //
-// Roles: warp 0 loads (TMA, nine boxes of 64 channels a tile, each with a barrier of its
-// own, two tiles in flight; a box is asked for again as soon as its last product is
-// done); warp 1 issues whichever product can go on, P's first, since that frees the
-// loads; warps 4 .. 11 do the softmax, two warps 16 pairs, and the outputs.
+// P goes over the tile's rotated keys, so that a tile's logits and its product are all
+// that has to be complete before its shared memory is loaded again.
+//
+// Roles: warp 0 loads (TMA, nine boxes of 64 channels a tile, pairs with a barrier of their
+// own, two tiles in flight; boxes are asked for again as soon as their last product is
+// done); warp 1 issues the logits, warp 2 the products; warps 4 .. 11 do the softmax, two warps 16 pairs, and the outputs.
 //
 // Calls of up to 512 rows: all tiles of all items are one list, cut into equal shares,
 // one per SM, so that ragged contexts load every SM alike; a cut item leaves parts that
@@ -40,7 +42,7 @@ constexpr int LA_BOXES = 9;                   // of 64 channels; the last is the
 constexpr int LA_BOX = LA_KEYS * 128;         // bytes (of 64 pairs or 64 positions)
 constexpr int LA_TILE = LA_BOXES * LA_BOX;
 constexpr int LA_ROWS = 512;                  // of a call whose tiles are cut into shares
-constexpr int OFF_KV = LA_TILE, OFF_P = OFF_KV + 2 * LA_TILE, OFF_MISC = OFF_P + LA_BOX;
+constexpr int OFF_KV = LA_TILE, OFF_MISC = OFF_KV + 2 * LA_TILE;
 constexpr int BAR_SOFT = 1;                   // named barrier of the softmax warps
 constexpr int O_COL = 0, S_COL = 256;         // tensor memory
 constexpr float kLift = 7.f;                  // log2 of the room below P = 2
@@ -48,23 +50,27 @@ constexpr float kLift = 7.f;                  // log2 of the room below P = 2
 // A CTA's run of tiles of one item.
 struct Seg {
   int t, nr;    // rows
+  int req;      // of this request
   int sub;      // group of 64 heads
   int tile, n;  // first tile (of 64 positions) and how many
   int slot;     // where its part goes, -1: the item is whole
 };
-constexpr int LA_NEAR = 6;  // segments kept in shared memory; the rest in the workspace
+constexpr int LA_AHEAD = 4;  // tiles that L2 is asked for before they are loaded
+constexpr int LA_NEAR = 64;  // segments kept in shared memory; the rest in the workspace
 
 struct Misc {
-  uint64_t q_full, q_empty, pv_done, p_full, o_free, drained, s_full[2];
-  uint64_t full[2][LA_BOXES], empty[2][5];  // (rotated keys last, pairs of boxes before)
+  uint64_t q_full, q_empty, pv_done, p_full, o_free, drained[2], s_full[2];
+  uint64_t full[2][4], empty[2][4];  // pairs of boxes of a tile; the rotated keys with the last
   uint32_t tmem;
   int abort;
-  int n_seg, n_tiles;
+  int n_seg;
   int there[2];                // the tile's page is in the pool
   uint32_t bad[2];             // positions of a tile with values that are not finite
   Seg near_[LA_NEAR];
   float top[2][LA_PAIRS], f[LA_PAIRS];
+  uint32_t row[LA_PAIRS];      // a pair's (row, head) in lse, kNone: it has none
 };
+constexpr uint32_t kNone = 0xFFFFFFFFu;
 static_assert(OFF_MISC + sizeof(Misc) <= 227 * 1024, "shared memory");
 
 struct Parts {
@@ -117,6 +123,33 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&x)[16]) {
   for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
 }
 
+// A box of a tensor map into L2.
+__device__ __forceinline__ void prefetch_3d(const void *tmap, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+// Four MMAs over 64 of K, the operands' descriptors AS and BS sixteen bytes further on
+// each; acc = 0: the first overwrites.  One statement, for one elected lane: a loop of
+// single ones takes 80 cycles each to issue, these the 32 or 48 that they run for.
+template <int AS, int BS>
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 q, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.u64 x, %1, %5;\n\tadd.u64 y, %2, %6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+      "add.u64 x, %1, 2 * %5;\n\tadd.u64 y, %2, 2 * %6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+      "add.u64 x, %1, 3 * %5;\n\tadd.u64 y, %2, 3 * %6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(AS), "n"(BS)
+      : "memory");
+}
+
 // The CTA's rows while its segments are found, where the tiles land afterwards.
 struct Plan {
   long long *before;  // tiles of all items of earlier rows
@@ -145,6 +178,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     if (tid == 0) flag(a.status_dev, CSA_DEV_TIMEOUT);
     return;
   }
+  if (warp == LA_MMA) tc::tmem_alloc(&M->tmem, 512);
+  if (warp == LA_SOFT0 && lane < 4)
+    paged::prefetch_map(lane == 0 ? &qmap : (lane == 1 ? &qrmap : (lane == 2 ? &cmap : &rmap)));
   volatile int *abort = &M->abort;
   Seg *far_ = parts.far_ + (long long)blockIdx.x * parts.n_far;
 
@@ -177,11 +213,11 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       tc::mbar_init(&M->pv_done, 1);
       tc::mbar_init(&M->p_full, 8);
       tc::mbar_init(&M->o_free, 8);
-      tc::mbar_init(&M->drained, 1);
       for (int i = 0; i < 2; ++i) {
+        tc::mbar_init(&M->drained[i], 1);
         tc::mbar_init(&M->s_full[i], 2);
-        for (int c = 0; c < LA_BOXES; ++c) tc::mbar_init(&M->full[i][c], 1);
-        for (int c = 0; c < 5; ++c) tc::mbar_init(&M->empty[i][c], 1);
+        for (int c = 0; c < 4; ++c) tc::mbar_init(&M->full[i][c], 1);
+        for (int c = 0; c < 4; ++c) tc::mbar_init(&M->empty[i][c], 1);
       }
       M->abort = 0;
       M->bad[0] = M->bad[1] = 0;
@@ -229,11 +265,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       if (lane == 0) {
         const long long W = sum, N = H.shares ? (W < gridDim.x ? W : gridDim.x) : 1;
         const long long c = H.shares ? blockIdx.x : 0;
-        int n_seg = 0, n_tiles = 0;
+        int n_seg = 0;
         int4 cut = make_int4(-1, 0, 0, 0);
         if (W > 0 && c < N) {
           const long long w0 = c * W / N, w1 = (c + 1) * W / N;
-          n_tiles = (int)(w1 - w0);
           int l = 0, h = n;
           while (h - l > 1) {
             const int mid = (l + h) >> 1;
@@ -248,7 +283,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
             const int pa = (int)(w - plan.before[l] - (long long)sub * P);
             const int pb = (int)min((long long)P, pa + (w1 - w));
             Seg s;
-            s.t = row0 + l, s.nr = plan.nr[l], s.sub = sub0 + sub;
+            s.t = row0 + l, s.nr = plan.nr[l], s.req = plan.req[l], s.sub = sub0 + sub;
             s.tile = plan.first[l] + pa, s.n = pb - pa;
             s.slot = pa > 0 ? 2 * (int)c : (pb < P ? 2 * (int)c + 1 : -1);
             if (pa == 0 && pb < P)
@@ -262,7 +297,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
             if (pb == P && sub == subs - 1) ++l;
           }
         }
-        M->n_seg = n_seg, M->n_tiles = n_tiles;
+        M->n_seg = n_seg;
         if (H.shares) parts.cut[c] = cut;
       }
     }
@@ -281,10 +316,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     }
     __syncthreads();
   }
-  const int n_seg = M->n_seg, n_tiles = M->n_tiles;
-  if (n_seg == 0) return;
+  const int n_seg = M->n_seg;
   auto seg_at = [&](int i) { return i < LA_NEAR ? M->near_[i] : far_[i]; };
-  if (warp == LA_MMA) tc::tmem_alloc(&M->tmem, 512);
   tc::fence_async_shared();  // (the plan was where the tiles land)
   tc::tc_fence_before();
   __syncthreads();
@@ -298,8 +331,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       uint32_t it = 0, n_q = 0;
       for (int s = 0; s < n_seg && ok; ++s) {
         const Seg g = seg_at(s);
-        const int32_t *table = a.block_table + (long long)a.row_req[g.t] * a.max_blocks;
-        int phys = table[g.tile >> 1];
+        const int32_t *table = a.block_table + (long long)g.req * a.max_blocks;
+        const int end = g.tile + g.n;
+        int asked = g.tile + 1, phys = table[g.tile >> 1];  // (prefetches keep to the segment)
         ok = la_wait(&M->q_empty, (s & 1) ^ 1, abort, a.status_dev);
         if (!ok) break;
         ++n_q;
@@ -313,26 +347,28 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
           const int next = i + 1 < g.n ? table[(tile + 1) >> 1] : 0;
           const bool there = phys >= 0 && phys < a.n_blocks;
           uint8_t *dst = sm + OFF_KV + st * LA_TILE;
-          ok = la_wait(&M->empty[st][4], par, abort, a.status_dev);
-          if (!ok) break;
-          if (!there) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
-          M->there[st] = there;
-          if (there) {
-            tc::mbar_arrive_expect_tx(&M->full[st][8], LA_BOX);
-            tc::tma_load_3d(dst + 8 * LA_BOX, &rmap, 0, (tile & 1) * LA_KEYS, phys, &M->full[st][8]);
-          } else {
-            tc::mbar_arrive(&M->full[st][8]);
-          }
-          for (int c = 0; c < 8; ++c) {
-            if ((c & 1) == 0) ok = la_wait(&M->empty[st][c >> 1], par, abort, a.status_dev);
+          for (int c = 0; c < 4; ++c) {
+            ok = la_wait(&M->empty[st][c], par, abort, a.status_dev);
             if (!ok) break;
+            if (c == 0) M->there[st] = there;
             if (there) {
-              tc::mbar_arrive_expect_tx(&M->full[st][c], LA_BOX);
-              tc::tma_load_3d(dst + c * LA_BOX, &cmap, c * 64, (tile & 1) * LA_KEYS, phys,
-                              &M->full[st][c]);
+              uint64_t *bar = &M->full[st][c];
+              tc::mbar_arrive_expect_tx(bar, c == 3 ? 3 * LA_BOX : 2 * LA_BOX);
+              for (int e = 2 * c; e < 2 * c + 2; ++e)
+                tc::tma_load_3d(dst + e * LA_BOX, &cmap, e * 64, (tile & 1) * LA_KEYS, phys, bar);
+              if (c == 3)
+                tc::tma_load_3d(dst + 8 * LA_BOX, &rmap, 0, (tile & 1) * LA_KEYS, phys, bar);
             } else {
               tc::mbar_arrive(&M->full[st][c]);
             }
+          }
+          if (!there) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
+          for (; asked < min(tile + LA_AHEAD, end); ++asked) {
+            const int pg = table[asked >> 1];
+            if (asked < tile + 2 || pg < 0 || pg >= a.n_blocks) continue;
+            for (int c = 0; c < 8; ++c)
+              prefetch_3d(&cmap, c * 64, (asked & 1) * LA_KEYS, pg);
+            prefetch_3d(&rmap, 0, (asked & 1) * LA_KEYS, pg);
           }
           phys = next;
         }
@@ -341,90 +377,79 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       if (!ok || *abort) {
         if (n_q > 0) tc::mbar_wait(&M->q_full, (n_q - 1) & 1, 50000000ull);
         for (uint32_t k = it > 1 ? it - 2 : 0; k <= it; ++k)
-          for (int c = 0; c < LA_BOXES; ++c)
+          for (int c = 0; c < 4; ++c)
             tc::mbar_wait(&M->full[k & 1][c], (k >> 1) & 1, 5000000ull);
       }
     }
     __syncwarp();
   } else if (warp == LA_MMA) {
-    // ================================================================ MMA
+    // ================================================================ logits
+    // (In order: a tile is loaded again only after its product, so its arrival also says
+    // that the softmax has read the logits before in this buffer and that nothing reads
+    // the P before.)
     if (tc::elect_one()) {
-      constexpr uint32_t idesc_s = tc::idesc_bf16_f32(LA_PAIRS, LA_KEYS);
-      const uint32_t idesc_o = tc::idesc_bf16_f32(128, H.n16) | (1u << 15);  // c^T is M-major
+      constexpr uint32_t idesc = tc::idesc_bf16_f32(LA_PAIRS, LA_KEYS);
       const uint32_t base = tc::smem_u32(sm);
       const uint64_t dq = tc::desc_sw128(base), dk = tc::desc_sw128(base + OFF_KV);
-      const uint64_t dv = tc::desc_sw128_mn(base + OFF_KV, LA_BOX, 1024);
-      const uint64_t dp = tc::desc_sw128(base + OFF_P);
-      // the next box of logits (tile sj, its segment ss ending before tile s_end), and
-      // the next product (tile pj, segment ps)
-      int sj = 0, sc = 0, ss = 0, s_end = seg_at(0).n;
-      int pj = 0, ps = 0, p_end = s_end;
-      bool q_here = false, first = true;
-      uint32_t idle = 0;
-      uint64_t t0 = 0;
-      while (pj < n_tiles) {
-        bool moved = false;
-        if (pj < sj && tc::mbar_test_wait(&M->p_full, pj & 1) &&
-            (!first || ps == 0 || tc::mbar_test_wait(&M->o_free, (ps - 1) & 1))) {
-          tc::tc_fence_after();
-          const int st = pj & 1;
-#pragma unroll 1
-          for (int b = 0; b < 4; ++b) {
+      bool ok = true;
+      int it = 0;
+      for (int s = 0; s < n_seg && ok; ++s) {
+        const int end = it + seg_at(s).n;
+        ok = la_wait(&M->q_full, s & 1, abort, a.status_dev);
+        for (; it < end && ok; ++it) {
+          const int st = it & 1;
+          const uint32_t d = tmem + S_COL + st * 64;
+          const uint64_t k = dk + ((st * LA_TILE) >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_bf16(tmem + O_COL + b * 64, dv + ((st * LA_TILE + 2 * b * LA_BOX) >> 4) + k * 128,
-                           dp + k * 2, idesc_o, !(first && k == 0));
-            tc::mma_commit(&M->empty[st][b]);
-          }
-          tc::mma_commit(&M->pv_done);
-          first = false;
-          if (++pj == p_end && pj < n_tiles) {
-            p_end += seg_at(++ps).n;
-            first = true;
-          }
-          moved = true;
-        }
-        if (sj < n_tiles && sj - pj < 2) {
-          if (!q_here) q_here = tc::mbar_test_wait(&M->q_full, ss & 1);
-          const int st = sj & 1, c = sc == 0 ? 8 : sc - 1;
-          if (q_here && tc::mbar_test_wait(&M->full[st][c], (sj >> 1) & 1)) {
+          for (int c = 0; c < 4; ++c) {
+            ok = ok && la_wait(&M->full[st][c], (it >> 1) & 1, abort, a.status_dev);
+            if (!ok) break;
             tc::tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_bf16(tmem + S_COL + st * 64, dq + ((c * LA_BOX) >> 4) + k * 2,
-                           dk + ((st * LA_TILE + c * LA_BOX) >> 4) + k * 2, idesc_s,
-                           !(sc == 0 && k == 0));
-            if (++sc == LA_BOXES) {
-              sc = 0;
-              tc::mma_commit(&M->s_full[st]);
-              tc::mbar_arrive(&M->s_full[st]);  // hands on what the loads were told
-              tc::mma_commit(&M->empty[st][4]);
-              if (++sj == s_end) {
-                tc::mma_commit(&M->q_empty);
-                q_here = false;
-                if (sj < n_tiles) s_end += seg_at(++ss).n;
-              }
-            }
-            moved = true;
+            for (int e = 2 * c; e < (c == 3 ? 9 : 2 * c + 2); ++e)
+              mma4<2, 2>(d, dq + ((e * LA_BOX) >> 4), k + ((e * LA_BOX) >> 4), idesc, e > 0);
           }
+          if (!ok) break;
+          tc::mma_commit(&M->s_full[st]);
+          tc::mbar_arrive(&M->s_full[st]);  // hands on what the loads were told
         }
-        if (moved) {
-          idle = 0;
-        } else if ((++idle & 255u) == 0) {
-          if (*abort) break;
-          const uint64_t now = tc::global_ns();
-          if (idle == 256u)
-            t0 = now;
-          else if (now - t0 > 2000000000ull) {
-            *abort = 1;
-            flag(a.status_dev, CSA_DEV_TIMEOUT);
-            break;
-          }
-        }
+        if (ok) tc::mma_commit(&M->q_empty);
       }
       // every issued MMA has completed before tensor memory is released
-      tc::mma_commit(&M->drained);
-      tc::mbar_wait(&M->drained, 0, 100000000ull);
+      tc::mma_commit(&M->drained[0]);
+      tc::mbar_wait(&M->drained[0], 0, 100000000ull);
+    }
+    __syncwarp();
+  } else if (warp == LA_MMA + 1) {
+    // ================================================================ products
+    // (A warp of their own: one that issues both has to ask which is ready, and each
+    // question costs it a hundred cycles.)
+    if (tc::elect_one()) {
+      const uint32_t idesc = tc::idesc_bf16_f32(128, H.n16) | (1u << 15);  // c^T is M-major
+      const uint32_t base = tc::smem_u32(sm);
+      const uint64_t dv = tc::desc_sw128_mn(base + OFF_KV, LA_BOX, 1024);
+      const uint64_t dp = tc::desc_sw128(base + OFF_KV + 8 * LA_BOX);
+      bool ok = true;
+      int it = 0;
+      for (int s = 0; s < n_seg && ok; ++s) {
+        const int n_it = seg_at(s).n;
+        if (s > 0) ok = la_wait(&M->o_free, (s - 1) & 1, abort, a.status_dev);
+        for (int i = 0; i < n_it && ok; ++i, ++it) {
+          ok = la_wait(&M->p_full, it & 1, abort, a.status_dev);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint64_t at = ((it & 1) * LA_TILE) >> 4;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            mma4<128, 2>(tmem + O_COL + b * 64, dv + at + ((2 * b * LA_BOX) >> 4), dp + at, idesc,
+                         i > 0);
+            tc::mma_commit(&M->empty[it & 1][b]);
+          }
+          tc::mma_commit(&M->pv_done);
+        }
+      }
+      tc::mma_commit(&M->drained[1]);
+      tc::mbar_wait(&M->drained[1], 0, 100000000ull);
     }
     __syncwarp();
   } else if (warp >= LA_SOFT0) {
@@ -433,7 +458,6 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     const int ma = 16 * qd + (lane >> 2), fc = (lane & 3) * 2;  // pairs ma, ma + 8
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     const float sl2 = a.softmax_scale * paged::kLog2e;
-    uint8_t *P = sm + OFF_P;
     uint32_t it = 0;
     auto wait = [&](uint64_t *bar, uint32_t turn) {
       return (bool)__all_sync(0xffffffffu, la_wait(bar, turn & 1, abort, a.status_dev));
@@ -442,18 +466,23 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     bool ok = true, given_up = false;
     for (int s = 0; s < n_seg && !given_up; ++s) {
       const Seg g = seg_at(s);
-      const int b = a.row_req[g.t], len = a.kv_len[b];
+      const int len = a.kv_len[g.req];
       // what the item's rows see: all of them, and this thread's two
       int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = 0;
       int lo[2] = {0, 0}, hi[2] = {0, 0};
+      if (tid < LA_SOFT0 * 32 + LA_PAIRS) {
+        const int m = tid - LA_SOFT0 * 32, r = m / H.gt, h = g.sub * H.gt + m % H.gt;
+        M->row[m] = r < g.nr && h < a.n_heads ? (uint32_t)(g.t + r) * a.n_heads + h : kNone;
+      }
+      const int my_r[2] = {ma / H.gt, (ma + 8) / H.gt};
+      const bool my[2] = {g.sub * H.gt + ma % H.gt < a.n_heads,
+                          g.sub * H.gt + (ma + 8) % H.gt < a.n_heads};
       for (int r = 0; r < g.nr; ++r) {
         int l, h;
         paged::visible_range(a, len, a.row_pos[g.t + r], l, h);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int m = ma + 8 * e;
-          if (m / H.gt == r && g.sub * H.gt + m % H.gt < a.n_heads) lo[e] = l, hi[e] = h;
-        }
+        for (int e = 0; e < 2; ++e)
+          if (my_r[e] == r && my[e]) lo[e] = l, hi[e] = h;
         if (l >= h) {
           all_hi = 0;
           continue;
@@ -583,8 +612,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
             if (tid == LA_SOFT0 * 32) M->bad[0] = M->bad[1] = 0;
           }
         }
-        // P goes where the product before read its own
-        if (it > 0) ok = wait(&M->pv_done, it - 1) && ok;
+        // P goes over the tile's rotated keys, which nothing reads any more
+        uint8_t *P = sm + OFF_KV + st * LA_TILE + 8 * LA_BOX;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int m = ma + 8 * (k & 1), chunk = 4 * half + (k >> 1);
@@ -607,11 +636,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       if (half == 0 && (lane & 3) == 0)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int m = ma + 8 * e, r = m / H.gt, h = g.sub * H.gt + m % H.gt;
+          const int m = ma + 8 * e;
           const float sum = M->top[0][m] + M->top[1][m];
           float f = 0.f;
-          if (r < g.nr && h < a.n_heads) {
-            const long long row = (long long)(g.t + r) * a.n_heads + h;
+          const uint32_t row = M->row[m];
+          if (row != kNone) {
+            const int h = g.sub * H.gt + m % H.gt;
             if (g.slot >= 0) {
               parts.ml[(long long)g.slot * LA_PAIRS + m] = make_float2(ref[e], sum);
             } else {
@@ -632,16 +662,24 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         for (int c = 0; c < H.n16; c += 32) {
           float o[32];
           tc::tmem_ld32(tmem + O_COL + blk * 64 + c + lane_off, o);
+          if (g.slot >= 0) {
+            float *to = parts.o + ((long long)g.slot * LA_PAIRS + c) * kLatent + d;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int m = c + k, r = m / H.gt, h = g.sub * H.gt + m % H.gt;
-            if (r >= g.nr || h >= a.n_heads) continue;
-            if (g.slot >= 0) {
-              parts.o[((long long)g.slot * LA_PAIRS + m) * kLatent + d] = o[k];
-            } else {
-              const float f = M->f[m];  // (0: the row saw nothing)
-              static_cast<__nv_bfloat16 *>(a.out)[((long long)(g.t + r) * a.n_heads + h) * kLatent + d] =
-                  __float2bfloat16_rn(f == 0.f ? 0.f : o[k] * f);
+            for (int k = 0; k < 32; ++k)
+              if (M->row[c + k] != kNone) to[k * kLatent] = o[k];
+          } else {
+            // two pairs at a time: even lanes store two channels of the first, odd ones
+            // of the second
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float f0 = M->f[c + k], f1 = M->f[c + k + 1];  // (0: the row saw nothing)
+              const uint32_t both = attn::pack2(f0 == 0.f ? 0.f : o[k] * f0, f1 == 0.f ? 0.f : o[k + 1] * f1);
+              const uint32_t other = __shfl_xor_sync(0xffffffffu, both, 1);
+              const uint32_t row = M->row[c + k + (lane & 1)];
+              if (row != kNone)
+                *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                              (long long)row * kLatent + (d & ~1)) =
+                    lane & 1 ? __byte_perm(other, both, 0x7632) : __byte_perm(both, other, 0x5410);
             }
           }
         }
@@ -672,17 +710,34 @@ __global__ void __launch_bounds__(128)
   if (r >= it.y || h >= a.n_heads) return;
   const int n = it.w - c + 1;
   auto slot = [&](int s) { return (2ll * (c + s) + (s == 0 ? 1 : 0)) * LA_PAIRS + m; };
-  float ref = -INFINITY;
-  for (int s = 0; s < n; ++s) ref = fmaxf(ref, parts.ml[slot(s)].x);
-  float acc[4] = {}, l = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) {
-    const float2 ml = parts.ml[slot(s)];
-    const float4 o = reinterpret_cast<const float4 *>(parts.o + slot(s) * kLatent)[tid];
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;                     // nothing was seen there
-    const float w = ml.x == -INFINITY ? ml.y : exp2f(ml.x - ref);       // (l is NaN there)
-    l += w * ml.y;
-    acc[0] += w * o.x, acc[1] += w * o.y, acc[2] += w * o.z, acc[3] += w * o.w;
+  // 16 parts at a time, statistics and outputs asked for together: what this takes is
+  // the way to memory.  The sums move to a larger reference as it comes.
+  float ref = -INFINITY, acc[4] = {}, l = 0.f;
+  for (int s0 = 0; s0 < n; s0 += 16) {
+    float2 ml[16];
+    float4 o[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (s0 + k >= n) break;
+      ml[k] = parts.ml[slot(s0 + k)];
+      o[k] = reinterpret_cast<const float4 *>(parts.o + slot(s0 + k) * kLatent)[tid];
+    }
+    float top = ref;
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (s0 + k < n) top = fmaxf(top, ml[k].x);
+    const float f = ref == -INFINITY ? 0.f : exp2f(ref - top);
+    if (ref != -INFINITY) l *= f;  // (l is NaN where a logit was)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] *= f;
+    ref = top;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (s0 + k >= n || (ml[k].x == -INFINITY && ml[k].y == 0.f)) continue;  // nothing seen there
+      const float w = ml[k].x == -INFINITY ? ml[k].y : exp2f(ml[k].x - ref);
+      l += w * ml[k].y;
+      acc[0] += w * o[k].x, acc[1] += w * o[k].y, acc[2] += w * o[k].z, acc[3] += w * o[k].w;
+    }
   }
   const paged::Joined J = paged::finish(ref, l, a.sink ? a.sink[h] : -INFINITY);
   const bool zero = ref == -INFINITY && l == 0.f;
