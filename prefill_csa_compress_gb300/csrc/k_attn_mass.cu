@@ -1,75 +1,569 @@
-// The attention weight that every cached position received (csa_attn_mass).
+// The attention weight that every cached position received (csa_attn_mass): tcgen05
+// tiles of one page of 128 positions against up to 128 (row, head) pairs.
+//
+//   S^T[j, n] = k_j . q_n          (128 x N x D, both operands K-major)
+//   mass[j]  += sum_n 2^(S^T[j, n] scale log2(e) - lse_n log2(e))
+// A lane of tensor memory is a position, so a thread adds up its position's weights
+// over all columns, and no sum crosses threads but at the end (in an order that the
+// arguments fix: no atomics).
+//
+// A CTA takes a page of a request, some of its key heads and a share of the rows that
+// see it (heads and rows are split only as far as there are too few pages to fill the
+// GPU; mass_join_kernel then adds the parts in order).  A step is one key head and one
+// tile of consecutive rows with their heads stacked under them.  Roles:
+//   warp 0       loads (TMA): a page's keys once a head, the queries of every step;
+//   warp 1       issues the MMAs;
+//   warp 2       walks the rows, leaves out tiles that do not see the page and
+//                describes each step to the rest: references and bounds a column;
+//   warps 4..11  the exponentials and the sums, two warps 32 positions, 32 columns in turn.
+// Two CTAs an SM.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstddef>
+#include <cstring>
+
+#include "attn_common.cuh"
 #include "cache_common.cuh"
 #include "paged_common.cuh"
+#include "tc.cuh"
 
 namespace csa {
 namespace {
 
-// One CTA a page of a request, a thread a position.
-template <int D>
-__global__ void __launch_bounds__(128) attn_mass_kernel(csa_attn_mass_args a) {
-  const int b = blockIdx.y, j = blockIdx.x * kBlock + threadIdx.x;
-  if (blockIdx.x == 0 && b == 0)
-    for (int t = threadIdx.x; t < a.n_rows; t += 128)
-      if (a.row_req[t] >= a.n_req) flag(a.status_dev, CSA_DEV_BAD_POS);
-  if (j >= a.kv_len[b]) return;
-  const int page = a.block_table[(long long)b * a.max_blocks + blockIdx.x];
-  const bool there = page >= 0 && page < a.n_blocks;
-  bool read = false;
-  float sum = 0.f;
-  const float sl2 = a.softmax_scale * paged::kLog2e;
-  const int g = a.n_heads / a.n_kv_heads;
-  for (int kh = 0; kh < a.n_kv_heads; ++kh) {
-    float k[D];
-    if (there) {
-      const __nv_bfloat16 *kp = reinterpret_cast<const __nv_bfloat16 *>(
-          static_cast<const uint8_t *>(a.k_pool) + page * a.k_page_stride +
-          threadIdx.x * a.k_token_stride + kh * a.k_head_stride);
-#pragma unroll
-      for (int i = 0; i < D; ++i) k[i] = __bfloat162float(kp[i]);
-    }
-    for (int t = 0; t < a.n_rows; ++t) {
-      if (a.row_req[t] != b) continue;
-      int lo, hi;
-      paged::visible_range(a, a.kv_len[b], a.row_pos[t], lo, hi);
-      if (j < lo || j >= hi) continue;
-      read = true;
-      if (!there) continue;
-      for (int h = kh * g; h < kh * g + g; ++h) {
-        const float lse = a.lse[(long long)t * a.n_heads + h];
-        if (lse == -INFINITY) continue;
-        const __nv_bfloat16 *q = reinterpret_cast<const __nv_bfloat16 *>(
-                                     static_cast<const uint8_t *>(a.q) + t * a.q_row_stride) +
-                                 h * D;
-        float x = 0.f;
-#pragma unroll
-        for (int i = 0; i < D; ++i) x += k[i] * __bfloat162float(q[i]);
-        sum += exp2f(x * sl2 - lse * paged::kLog2e);
+constexpr int AM_THREADS = 384;
+constexpr int AM_LOAD = 0, AM_MMA = 1, AM_WALK = 2, AM_SUM0 = 4;  // first warps
+constexpr int AM_STEPS = 4;   // steps described ahead
+constexpr int AM_RING = 4;    // stages of keys and of queries, at most
+constexpr int AM_BAR = 1;     // named barrier of the summing warps
+
+struct Step {
+  int t0, kvh;         // its rows start here; key head, < 0: no more steps
+  int new_k, last_k;   // the head's first step, its last
+  int mixed;           // some column does not see all of the page
+};
+
+struct Misc {
+  uint64_t k_full[AM_RING], k_empty[AM_RING], q_full[AM_RING], q_empty[AM_RING];
+  uint64_t s_full[2], s_empty[2], m_full[AM_STEPS], m_empty[AM_STEPS], drained;
+  uint32_t tmem;
+  int abort;
+  int vmin, vmax;      // rows of the request that see the page
+  Step step[AM_STEPS];
+  alignas(16) float lse[AM_STEPS][128];  // (read four at a time)
+  int2 see[AM_STEPS][128];  // a column's positions of the page [x, y)
+  float sum[128];
+};
+
+static_assert(offsetof(Misc, lse) % 16 == 0 && offsetof(Misc, see) % 8 == 0, "vector reads");
+
+// How the host splits a call, and its shared memory.
+struct Split {
+  int tr, n;          // rows of a step and its columns, rounded up to 32
+  int kv, rows;       // parts by key heads (heads_per each) and by rows
+  int heads_per;
+  int k_stages, q_stages;
+  int q_bytes;        // of a stage (a whole number of 1024)
+};
+
+__device__ __forceinline__ bool am_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                        uint32_t *status) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = tc::global_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*abort) return false;
+      if (tc::global_ns() - t0 > 2000000000ull) {
+        *abort = 1;
+        flag(status, CSA_DEV_TIMEOUT);
+        return false;
       }
     }
   }
-  if (read && !there) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
-  float *out = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.mass_out) +
-                                         b * a.mass_out_row_stride) + j;
+}
+
+// Four MMAs over 64 of K in one statement (an elected lane); acc = 0: the first overwrites.
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 q, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.u64 x, %1, 2;\n\tadd.u64 y, %2, 2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+      "add.u64 x, %1, 4;\n\tadd.u64 y, %2, 4;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+      "add.u64 x, %1, 6;\n\tadd.u64 y, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(AM_THREADS, 2)
+    attn_mass_kernel(csa_attn_mass_args a, float *parts, Split G,
+                     const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ CUtensorMap kmap) {
+  constexpr int BOXES = D / 64, K_TILE = BOXES * 16384;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint8_t *ks = sm, *qs = sm + G.k_stages * K_TILE;
+  Misc *M = reinterpret_cast<Misc *>(qs + G.q_stages * G.q_bytes);
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tc::smem_u32(sm) & 1023u) {
+    if (tid == 0) flag(a.status_dev, CSA_DEV_TIMEOUT);
+    return;
+  }
+  // key heads fastest, then rows, requests, pages: the first pages, which the most rows
+  // see, first
+  int u = blockIdx.x;
+  const int kv_part = u % G.kv;
+  u /= G.kv;
+  const int row_part = u % G.rows;
+  u /= G.rows;
+  const int b = u % a.n_req, page = u / a.n_req;
+  const int len = min(a.kv_len[b], a.max_blocks * kBlock), base = page * kBlock;
+  if (b == 0 && page == 0 && kv_part == 0 && row_part == 0)
+    for (int t = tid; t < a.n_rows; t += AM_THREADS)
+      if (a.row_req[t] >= a.n_req) flag(a.status_dev, CSA_DEV_BAD_POS);
+  if (base >= len) return;
+  const int phys = a.block_table[(long long)b * a.max_blocks + page];
+  const bool there = phys >= 0 && phys < a.n_blocks;
+  if (tid == 0) {
+    for (int i = 0; i < AM_RING; ++i) {
+      tc::mbar_init(&M->k_full[i], 1);
+      tc::mbar_init(&M->k_empty[i], 1);
+      tc::mbar_init(&M->q_full[i], 1);
+      tc::mbar_init(&M->q_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&M->s_full[i], 1);
+      tc::mbar_init(&M->s_empty[i], 8);
+    }
+    for (int i = 0; i < AM_STEPS; ++i) {
+      tc::mbar_init(&M->m_full[i], 1);
+      tc::mbar_init(&M->m_empty[i], 10);  // loads, MMA, eight warps of sums
+    }
+    tc::mbar_init(&M->drained, 1);
+    M->abort = 0;
+    M->vmin = 0x7FFFFFFF, M->vmax = -1;
+    tc::mbar_fence_init();
+    paged::prefetch_map(&qmap);
+    paged::prefetch_map(&kmap);
+  }
+  if (warp == AM_MMA) tc::tmem_alloc(&M->tmem, 256);
+  const int g = a.n_heads / a.n_kv_heads;
+  // columns that no query fills are zero, and their references +inf
+  {
+    const int tail = (G.n - G.tr * g) * 8, per = G.q_bytes / BOXES;
+    for (int i = tid; i < tail * BOXES * G.q_stages; i += AM_THREADS)
+      reinterpret_cast<uint4 *>(qs + i / tail * per + G.tr * g * 128)[i % tail] = make_uint4(0, 0, 0, 0);
+    tc::fence_async_shared();
+  }
+  __syncthreads();
+  // the rows that see some of the page
+  {
+    int v0 = 0x7FFFFFFF, v1 = -1;
+#pragma unroll 4
+    for (int t = tid; t < a.n_rows; t += AM_THREADS) {
+      const int req = a.row_req[t], pos = a.row_pos[t];
+      int lo, hi;
+      paged::visible_range(a, len, pos, lo, hi);
+      if (req == b && max(lo, base) < min(hi, base + kBlock)) v0 = min(v0, t), v1 = t;
+    }
+    v0 = __reduce_min_sync(0xffffffffu, v0);
+    v1 = __reduce_max_sync(0xffffffffu, v1);
+    if (lane == 0 && v1 >= 0) {
+      atomicMin(&M->vmin, v0);
+      atomicMax(&M->vmax, v1);
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = __reduce_or_sync(0xffffffffu, M->tmem);
+  volatile int *abort = &M->abort;
+  const int kv0 = kv_part * G.heads_per, kv1 = min(a.n_kv_heads, kv0 + G.heads_per);
+  // this part's tiles of rows
+  const int vmin = M->vmin, n_all = M->vmax < 0 ? 0 : (M->vmax - vmin) / G.tr + 1;
+  const int tile0 = (int)((long long)n_all * row_part / G.rows);
+  const int tile1 = there ? (int)((long long)n_all * (row_part + 1) / G.rows) : tile0;
+  if (!there && n_all > 0 && tid == 0) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
+
+  if (warp == AM_WALK) {
+    // ================================================================ the steps
+    // four columns a lane: row and head within the tile
+    int r[4], h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = 32 * i + lane;
+      r[i] = n / g, h[i] = n % g;
+      if (r[i] >= G.tr) r[i] = -1;
+    }
+    uint32_t it = 0;
+    bool ok = true;
+    for (int kvh = kv0; kvh < kv1 && ok; ++kvh) {
+      // asked for a tile ahead
+      int req[4], pos[4];
+      float lse[4];
+      auto ask = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = vmin + tile * G.tr + r[i];
+          const bool in = r[i] >= 0 && t < a.n_rows && tile < tile1;
+          req[i] = in ? a.row_req[t] : -1;
+          pos[i] = in ? a.row_pos[t] : 0;
+          lse[i] = in ? a.lse[(long long)t * a.n_heads + kvh * g + h[i]] : INFINITY;
+        }
+      };
+      // a step is published when the next one is known, or that there is none
+      int pending = -1, first = 1;
+      float p_lse[4];
+      int2 p_see[4];
+      bool p_mixed = false;
+      auto publish = [&](bool last) {
+        const int st = it % AM_STEPS;
+        ok = __all_sync(0xffffffffu, am_wait(&M->m_empty[st], ((it / AM_STEPS) & 1) ^ 1, abort,
+                                             a.status_dev));
+        if (!ok) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          M->lse[st][32 * i + lane] = p_lse[i];
+          M->see[st][32 * i + lane] = p_see[i];
+        }
+        if (lane == 0) {
+          Step &S = M->step[st];
+          S.t0 = pending, S.kvh = kvh, S.new_k = first, S.last_k = last, S.mixed = p_mixed;
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&M->m_full[st]);
+        ++it;
+        first = 0;
+      };
+      ask(tile0);
+      for (int tile = tile0; tile < tile1 && ok; ++tile) {
+        bool any = false, mixed = false;
+        float x[4];
+        int2 see[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int lo, hi;
+          paged::visible_range(a, len, pos[i], lo, hi);
+          lo = max(lo - base, 0), hi = min(hi - base, kBlock);
+          if (req[i] != b || lo >= hi || lse[i] == -INFINITY) lo = hi = 0;
+          any = any || lo < hi;
+          const bool row = r[i] >= 0 && vmin + tile * G.tr + r[i] < a.n_rows;
+          mixed = mixed || (row && (lo > 0 || hi < kBlock));
+          x[i] = lse[i] * paged::kLog2e, see[i] = make_int2(lo, hi);
+        }
+        ask(tile + 1);
+        any = __any_sync(0xffffffffu, any);
+        mixed = __any_sync(0xffffffffu, mixed);
+        if (!any) continue;
+        if (pending >= 0) publish(false);
+        pending = vmin + tile * G.tr, p_mixed = mixed;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p_lse[i] = x[i], p_see[i] = see[i];
+      }
+      if (pending >= 0 && ok) publish(true);
+    }
+    if (ok) {
+      const int st = it % AM_STEPS;
+      if (__all_sync(0xffffffffu, am_wait(&M->m_empty[st], ((it / AM_STEPS) & 1) ^ 1, abort,
+                                          a.status_dev)) &&
+          lane == 0) {
+        M->step[st].kvh = -1;
+        tc::mbar_arrive(&M->m_full[st]);
+      }
+    }
+    __syncwarp();
+  } else if (warp == AM_LOAD) {
+    // ================================================================ loads
+    if (lane == 0) {
+      uint32_t nk = 0, nq = 0;
+      bool ok = true;
+      for (uint32_t it = 0;; ++it) {
+        const int st = it % AM_STEPS;
+        ok = am_wait(&M->m_full[st], (it / AM_STEPS) & 1, abort, a.status_dev);
+        if (!ok) break;
+        const Step S = M->step[st];
+        tc::mbar_arrive(&M->m_empty[st]);
+        if (S.kvh < 0) break;
+        if (S.new_k) {
+          const int s = nk % G.k_stages;
+          ok = am_wait(&M->k_empty[s], ((nk / G.k_stages) & 1) ^ 1, abort, a.status_dev);
+          if (!ok) break;
+          tc::mbar_arrive_expect_tx(&M->k_full[s], K_TILE);
+          for (int c = 0; c < BOXES; ++c)
+            paged::tma_load_4d(ks + s * K_TILE + c * 16384, &kmap, c * 64, S.kvh, 0, phys,
+                               &M->k_full[s]);
+          ++nk;
+        }
+        const int s = nq % G.q_stages;
+        ok = am_wait(&M->q_empty[s], ((nq / G.q_stages) & 1) ^ 1, abort, a.status_dev);
+        if (!ok) break;
+        tc::mbar_arrive_expect_tx(&M->q_full[s], BOXES * 128 * g * G.tr);
+        for (int c = 0; c < BOXES; ++c)
+          tc::tma_load_3d(qs + s * G.q_bytes + c * (G.q_bytes / BOXES), &qmap, c * 64, S.kvh * g,
+                          S.t0, &M->q_full[s]);
+        ++nq;
+      }
+      // whatever was asked for has landed before the CTA retires
+      if (!ok) {
+        for (uint32_t k = nk > (uint32_t)G.k_stages ? nk - G.k_stages : 0; k < nk; ++k)
+          tc::mbar_wait(&M->k_full[k % G.k_stages], (k / G.k_stages) & 1, 50000000ull);
+        for (uint32_t k = nq > (uint32_t)G.q_stages ? nq - G.q_stages : 0; k < nq; ++k)
+          tc::mbar_wait(&M->q_full[k % G.q_stages], (k / G.q_stages) & 1, 50000000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == AM_MMA) {
+    // ================================================================ MMA
+    if (tc::elect_one()) {
+      const uint32_t idesc = tc::idesc_bf16_f32(128, G.n);
+      const uint64_t dk = tc::desc_sw128(tc::smem_u32(ks)), dq = tc::desc_sw128(tc::smem_u32(qs));
+      uint32_t nk = 0, nq = 0;
+      bool ok = true;
+      for (uint32_t it = 0;; ++it) {
+        const int st = it % AM_STEPS;
+        ok = am_wait(&M->m_full[st], (it / AM_STEPS) & 1, abort, a.status_dev);
+        if (!ok) break;
+        const Step S = M->step[st];
+        tc::mbar_arrive(&M->m_empty[st]);
+        if (S.kvh < 0) break;
+        const int sk = nk % G.k_stages, sq = nq % G.q_stages, buf = it & 1;
+        ok = (!S.new_k || am_wait(&M->k_full[sk], (nk / G.k_stages) & 1, abort, a.status_dev)) &&
+             am_wait(&M->s_empty[buf], ((it >> 1) & 1) ^ 1, abort, a.status_dev) &&
+             am_wait(&M->q_full[sq], (nq / G.q_stages) & 1, abort, a.status_dev);
+        if (!ok) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < BOXES; ++c)
+          mma4(tmem + buf * 128, dk + ((sk * K_TILE + c * 16384) >> 4),
+               dq + ((sq * G.q_bytes + c * (G.q_bytes / BOXES)) >> 4), idesc, c > 0);
+        tc::mma_commit(&M->s_full[buf]);
+        tc::mma_commit(&M->q_empty[sq]);
+        ++nq;
+        if (S.last_k) {
+          tc::mma_commit(&M->k_empty[sk]);
+          ++nk;
+        }
+      }
+      // every issued MMA has completed before tensor memory is released
+      tc::mma_commit(&M->drained);
+      tc::mbar_wait(&M->drained, 0, 100000000ull);
+    }
+    __syncwarp();
+  } else if (warp >= AM_SUM0) {
+    // ================================================================ exponentials and sums
+    const int qd = warp & 3, grp = (warp - AM_SUM0) >> 2, j = qd * 32 + lane;
+    const uint32_t ts = tmem + ((uint32_t)(qd * 32) << 16);
+    const float sl2 = a.softmax_scale * paged::kLog2e;
+    float total = 0.f;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t turn) {
+      return (bool)__all_sync(0xffffffffu, am_wait(bar, turn & 1, abort, a.status_dev));
+    };
+    for (uint32_t it = 0;; ++it) {
+      const int st = it % AM_STEPS, buf = it & 1;
+      ok = wait(&M->m_full[st], it / AM_STEPS);
+      if (!ok || M->step[st].kvh < 0) break;
+      const bool mixed = M->step[st].mixed;
+      ok = wait(&M->s_full[buf], it >> 1);
+      if (!ok) break;
+      tc::tc_fence_after();
+      float2 sums[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll 1
+      for (int c = 32 * grp; c < G.n; c += 64) {
+        float x[32];
+        tc::tmem_ld32(ts + buf * 128 + c, x);
+        const float4 *lse = reinterpret_cast<const float4 *>(M->lse[st] + c);
+        if (!mixed) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 r = lse[i >> 2];
+            float2 y = tc::ffma2(make_float2(x[i], x[i + 1]), make_float2(sl2, sl2),
+                                 make_float2(-r.x, -r.y));
+            float2 z = tc::ffma2(make_float2(x[i + 2], x[i + 3]), make_float2(sl2, sl2),
+                                 make_float2(-r.z, -r.w));
+            y.x = attn::exp2_sfu(y.x), y.y = attn::exp2_sfu(y.y);
+            z.x = attn::exp2_sfu(z.x), z.y = attn::exp2_sfu(z.y);
+            sums[0] = tc::ffma2(y, make_float2(1.f, 1.f), sums[0]);
+            sums[1] = tc::ffma2(z, make_float2(1.f, 1.f), sums[1]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int2 see = M->see[st][c + i];
+            const float y = attn::exp2_sfu(fmaf(x[i], sl2, -M->lse[st][c + i]));
+            if (j >= see.x && j < see.y) sums[i & 1].x += y;
+          }
+        }
+      }
+      total += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&M->s_empty[buf]);
+        tc::mbar_arrive(&M->m_empty[st]);
+      }
+    }
+    // the two halves of the columns, then the position's mass or its part
+    if (grp == 1) M->sum[j] = total;
+    if (!tc::bar_or(AM_BAR, 256, !ok) && grp == 0 && base + j < len) {
+      total += M->sum[j];
+      const long long col = base + j;
+      if (parts) {
+        const long long cols = (long long)a.max_blocks * kBlock;
+        parts[((long long)(kv_part * G.rows + row_part) * a.n_req + b) * cols + col] = total;
+      } else {
+        if (a.decay != 0.f)
+          total += a.decay * reinterpret_cast<const float *>(
+                                 reinterpret_cast<const uint8_t *>(a.mass) + b * a.mass_row_stride)[col];
+        reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.mass_out) +
+                                  b * a.mass_out_row_stride)[col] = total;
+      }
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == AM_MMA) tc::tmem_dealloc(tmem, 256);
+}
+
+// mass_out from the parts, in order.
+__global__ void __launch_bounds__(256)
+    mass_join_kernel(csa_attn_mass_args a, const float *parts, int n_parts) {
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  const long long cols = (long long)a.max_blocks * kBlock;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int b = (int)(i / cols), j = (int)(i - b * cols);
+  if (b >= a.n_req || j >= a.kv_len[b]) return;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < n_parts; ++s) sum += parts[((long long)s * a.n_req + b) * cols + j];
   if (a.decay != 0.f)
     sum += a.decay * reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(a.mass) +
                                                      b * a.mass_row_stride)[j];
-  *out = sum;
+  reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.mass_out) + b * a.mass_out_row_stride)[j] = sum;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    sms = 152;
+  return sms;
+}
+
+// Rows of a step: what a request has on average, as far as 128 columns go (the host
+// does not know how rows are spread).  Parts: as many as make four CTAs for each place
+// on the GPU, by key heads first (they share nothing), then by rows.
+Split split_of(const csa_attn_mass_args &a) {
+  Split G;
+  const int g = a.n_heads / a.n_kv_heads;
+  const long long per = a.n_rows > 0 ? ((long long)a.n_rows + a.n_req - 1) / a.n_req : 1;
+  const int most = 128 / g;
+  G.tr = per < most ? (int)per : most;
+  G.n = (G.tr * g + 31) / 32 * 32;
+  const long long pages = (long long)a.n_req * a.max_blocks;
+  const long long want = (4ll * 2 * sm_count() + pages - 1) / pages;
+  G.kv = (int)(want < a.n_kv_heads ? want : a.n_kv_heads);
+  G.heads_per = (a.n_kv_heads + G.kv - 1) / G.kv;
+  G.kv = (a.n_kv_heads + G.heads_per - 1) / G.heads_per;
+  const long long left = (want + G.kv - 1) / G.kv, tiles = (per + G.tr - 1) / G.tr;
+  const long long row_parts = left < tiles / 8 ? left : tiles / 8;  // (at least eight tiles each)
+  G.rows = (int)(row_parts < 1 ? 1 : (row_parts > 16 ? 16 : row_parts));
+  // 112 KB a CTA: two of queries at least, keys in what is left
+  const int k_tile = a.head_dim * 256, boxes = a.head_dim / 64;
+  G.q_bytes = boxes * (int)align_up((size_t)G.n * 128, 1024);
+  const int room = 227 * 512 - 1024 - (int)sizeof(Misc);
+  G.q_stages = G.n > 64 ? 2 : 4;
+  G.k_stages = (room - G.q_stages * G.q_bytes) / k_tile;
+  if (G.k_stages > AM_RING) G.k_stages = AM_RING;
+  return G;
+}
+
+bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void *f = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  memset(map, 0, sizeof(*map));
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims,
+                  strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  dims[0] == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const csa_attn_mass_args &a, float *parts, const Split &G,
+                   const CUtensorMap &qmap, const CUtensorMap &kmap, cudaStream_t s) {
+  const size_t smem = G.k_stages * D * 256 + G.q_stages * G.q_bytes + sizeof(Misc);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static bool attr[64] = {};
+  if (dev < 0 || dev >= 64 || !attr[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        attn_mass_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 512);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr[dev] = true;
+  }
+  const long long grid = (long long)a.n_req * a.max_blocks * G.kv * G.rows;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  return launch_kernel(attn_mass_kernel<D>, dim3((unsigned)grid), dim3(AM_THREADS), smem, s, 0,
+                       false, a, parts, G, qmap, kmap);
 }
 
 }  // namespace
 
-size_t attn_mass_workspace(const csa_attn_mass_args &) { return 0; }
+size_t attn_mass_workspace(const csa_attn_mass_args &a) {
+  const Split G = split_of(a);
+  const size_t n = (size_t)G.kv * G.rows;
+  return n == 1 ? 0 : align_up(n * a.n_req * a.max_blocks * kBlock * sizeof(float), 256);
+}
 
 cudaError_t launch_attn_mass(const csa_attn_mass_args &a, cudaStream_t s) {
+  const Split G = split_of(a);
+  const int n_parts = G.kv * G.rows, g = a.n_heads / a.n_kv_heads;
+  float *parts = n_parts > 1 ? static_cast<float *>(a.workspace) : nullptr;
+  CUtensorMap qmap, kmap;
+  const cuuint64_t rows = a.n_rows > 0 ? a.n_rows : 1;
+  const cuuint64_t qd[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_heads, rows};
+  const cuuint64_t qs[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)a.q_row_stride};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)g, (cuuint32_t)G.tr};
+  const cuuint64_t kd[4] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_kv_heads, kBlock,
+                            (cuuint64_t)a.n_blocks};
+  const cuuint64_t kst[3] = {(cuuint64_t)a.k_head_stride, (cuuint64_t)a.k_token_stride,
+                             (cuuint64_t)a.k_page_stride};
+  const cuuint32_t kb[4] = {64, 1, kBlock, 1};
+  // (without rows nothing is loaded: any address will do for the queries)
+  if (!encode(&qmap, a.n_rows > 0 ? a.q : a.k_pool, 3, qd, qs, qb) ||
+      !encode(&kmap, a.k_pool, 4, kd, kst, kb))
+    return cudaErrorInvalidValue;
   launch_begin(CSA_K_ATTN_MASS, s);
-  const dim3 grid(a.max_blocks, a.n_req);
-  if (a.head_dim == 64)
-    attn_mass_kernel<64><<<grid, 128, 0, s>>>(a);
-  else
-    attn_mass_kernel<128><<<grid, 128, 0, s>>>(a);
+  cudaError_t e = a.head_dim == 64 ? launch<64>(a, parts, G, qmap, kmap, s)
+                                   : launch<128>(a, parts, G, qmap, kmap, s);
   launch_end(CSA_K_ATTN_MASS, s);
-  return cudaGetLastError();
+  if (e != cudaSuccess || n_parts == 1) return e != cudaSuccess ? e : cudaGetLastError();
+  launch_begin(CSA_K_MASS_JOIN, s);
+  // (a call that is split has too few pages to come near a grid's limit)
+  const long long all = (long long)a.n_req * a.max_blocks * kBlock;
+  e = launch_kernel(mass_join_kernel, dim3((unsigned)((all + 255) / 256)), dim3(256), 0, s, 0, false,
+                    a, (const float *)parts, n_parts);
+  launch_end(CSA_K_MASS_JOIN, s);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace csa
