@@ -11,11 +11,11 @@
 // see it (heads and rows are split only as far as there are too few pages to fill the
 // GPU; mass_join_kernel then adds the parts in order).  A step is one key head and one
 // tile of consecutive rows with their heads stacked under them.  Roles:
-//   warp 0       loads (TMA): a page's keys once a head, the queries of every step;
-//   warp 1       issues the MMAs;
-//   warp 2       walks the rows, leaves out tiles that do not see the page and
-//                describes each step to the rest: references and bounds a column;
-//   warps 4..11  the exponentials and the sums, two warps 32 positions, 32 columns in turn.
+//   warps 0..7  the exponentials and the sums, two warps 32 positions, 32 columns in turn;
+//   warp 8      loads (TMA): a page's keys once a head, the queries of every step;
+//   warp 9      issues the MMAs;
+//   warp 10     walks the rows, leaves out tiles that do not see the page and
+//               describes each step to the rest: references and bounds a column.
 // Two CTAs an SM.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -31,8 +31,8 @@
 namespace csa {
 namespace {
 
-constexpr int AM_THREADS = 384;
-constexpr int AM_LOAD = 0, AM_MMA = 1, AM_WALK = 2, AM_SUM0 = 4;  // first warps
+constexpr int AM_THREADS = 352;
+constexpr int AM_LOAD = 8, AM_MMA = 9, AM_WALK = 10;  // warps; 0 .. 7 add up
 constexpr int AM_STEPS = 4;   // steps described ahead
 constexpr int AM_RING = 4;    // stages of keys and of queries, at most
 constexpr int AM_BAR = 1;     // named barrier of the summing warps
@@ -50,7 +50,7 @@ struct Misc {
   int abort;
   int vmin, vmax;      // rows of the request that see the page
   Step step[AM_STEPS];
-  alignas(16) float lse[AM_STEPS][128];  // (read four at a time)
+  alignas(16) float lse[AM_STEPS][128];  // a column's -lse log2(e) (read four at a time)
   int2 see[AM_STEPS][128];  // a column's positions of the page [x, y)
   float sum[128];
 };
@@ -130,6 +130,16 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
   if (base >= len) return;
   const int phys = a.block_table[(long long)b * a.max_blocks + page];
   const bool there = phys >= 0 && phys < a.n_blocks;
+  // the keys are asked for while the rows are found (behind a window no row may see them)
+  if (warp == 0 && there && a.window == 0)
+    for (int i = lane; i < BOXES * G.heads_per; i += 32) {
+      const int h = kv_part * G.heads_per + i / BOXES;
+      if (h < a.n_kv_heads)
+        asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];" ::"l"(
+                         reinterpret_cast<uint64_t>(&kmap)),
+                     "r"(i % BOXES * 64), "r"(h), "r"(0), "r"(phys)
+                     : "memory");
+    }
   if (tid == 0) {
     for (int i = 0; i < AM_RING; ++i) {
       tc::mbar_init(&M->k_full[i], 1);
@@ -138,7 +148,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
       tc::mbar_init(&M->q_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&M->s_full[i], 1);
+      tc::mbar_init(&M->s_full[i], 2);
       tc::mbar_init(&M->s_empty[i], 8);
     }
     for (int i = 0; i < AM_STEPS; ++i) {
@@ -255,7 +265,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
           any = any || lo < hi;
           const bool row = r[i] >= 0 && vmin + tile * G.tr + r[i] < a.n_rows;
           mixed = mixed || (row && (lo > 0 || hi < kBlock));
-          x[i] = lse[i] * paged::kLog2e, see[i] = make_int2(lo, hi);
+          x[i] = -lse[i] * paged::kLog2e, see[i] = make_int2(lo, hi);
         }
         ask(tile + 1);
         any = __any_sync(0xffffffffu, any);
@@ -331,7 +341,13 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
         if (!ok) break;
         const Step S = M->step[st];
         tc::mbar_arrive(&M->m_empty[st]);
-        if (S.kvh < 0) break;
+        if (S.kvh < 0) {  // (no logits: both arrivals are plain)
+          if (am_wait(&M->s_empty[it & 1], ((it >> 1) & 1) ^ 1, abort, a.status_dev)) {
+            tc::mbar_arrive(&M->s_full[it & 1]);
+            tc::mbar_arrive(&M->s_full[it & 1]);
+          }
+          break;
+        }
         const int sk = nk % G.k_stages, sq = nq % G.q_stages, buf = it & 1;
         ok = (!S.new_k || am_wait(&M->k_full[sk], (nk / G.k_stages) & 1, abort, a.status_dev)) &&
              am_wait(&M->s_empty[buf], ((it >> 1) & 1) ^ 1, abort, a.status_dev) &&
@@ -343,6 +359,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
           mma4(tmem + buf * 128, dk + ((sk * K_TILE + c * 16384) >> 4),
                dq + ((sq * G.q_bytes + c * (G.q_bytes / BOXES)) >> 4), idesc, c > 0);
         tc::mma_commit(&M->s_full[buf]);
+        tc::mbar_arrive(&M->s_full[buf]);  // hands on the step's description
         tc::mma_commit(&M->q_empty[sq]);
         ++nq;
         if (S.last_k) {
@@ -355,9 +372,9 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
       tc::mbar_wait(&M->drained, 0, 100000000ull);
     }
     __syncwarp();
-  } else if (warp >= AM_SUM0) {
+  } else {
     // ================================================================ exponentials and sums
-    const int qd = warp & 3, grp = (warp - AM_SUM0) >> 2, j = qd * 32 + lane;
+    const int qd = warp & 3, grp = warp >> 2, j = qd * 32 + lane;
     const uint32_t ts = tmem + ((uint32_t)(qd * 32) << 16);
     const float sl2 = a.softmax_scale * paged::kLog2e;
     float total = 0.f;
@@ -367,11 +384,9 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
     };
     for (uint32_t it = 0;; ++it) {
       const int st = it % AM_STEPS, buf = it & 1;
-      ok = wait(&M->m_full[st], it / AM_STEPS);
+      ok = wait(&M->s_full[buf], it >> 1);
       if (!ok || M->step[st].kvh < 0) break;
       const bool mixed = M->step[st].mixed;
-      ok = wait(&M->s_full[buf], it >> 1);
-      if (!ok) break;
       tc::tc_fence_after();
       float2 sums[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll 1
@@ -380,23 +395,22 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
         tc::tmem_ld32(ts + buf * 128 + c, x);
         const float4 *lse = reinterpret_cast<const float4 *>(M->lse[st] + c);
         if (!mixed) {
+          const float2 one = make_float2(1.f, 1.f), scale = make_float2(sl2, sl2);
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             const float4 r = lse[i >> 2];
-            float2 y = tc::ffma2(make_float2(x[i], x[i + 1]), make_float2(sl2, sl2),
-                                 make_float2(-r.x, -r.y));
-            float2 z = tc::ffma2(make_float2(x[i + 2], x[i + 3]), make_float2(sl2, sl2),
-                                 make_float2(-r.z, -r.w));
+            float2 y = tc::ffma2(make_float2(x[i], x[i + 1]), scale, make_float2(r.x, r.y));
+            float2 z = tc::ffma2(make_float2(x[i + 2], x[i + 3]), scale, make_float2(r.z, r.w));
             y.x = attn::exp2_sfu(y.x), y.y = attn::exp2_sfu(y.y);
             z.x = attn::exp2_sfu(z.x), z.y = attn::exp2_sfu(z.y);
-            sums[0] = tc::ffma2(y, make_float2(1.f, 1.f), sums[0]);
-            sums[1] = tc::ffma2(z, make_float2(1.f, 1.f), sums[1]);
+            sums[0] = tc::ffma2(y, one, sums[0]);
+            sums[1] = tc::ffma2(z, one, sums[1]);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int2 see = M->see[st][c + i];
-            const float y = attn::exp2_sfu(fmaf(x[i], sl2, -M->lse[st][c + i]));
+            const float y = attn::exp2_sfu(fmaf(x[i], sl2, M->lse[st][c + i]));
             if (j >= see.x && j < see.y) sums[i & 1].x += y;
           }
         }
