@@ -1,64 +1,290 @@
-// Keys and values of every head from a paged latent cache (csa_latent_expand).
+// Keys and values of every head from a paged latent cache (csa_latent_expand): a
+// tcgen05 product of one page of latents with the heads' up-projections.
+//
+//   D[j, n] = c_j . w_n    (128 positions x 256 channels of a head x 512, K-major both)
+// A CTA keeps a page (128 KB) in shared memory and goes through some of the heads: a
+// head's 256 rows of 512 stream past in eight pieces of 64 columns (32 KB), three in
+// flight, and its 256 columns of sums take half of tensor memory, so that one head is
+// written while the next one is computed.  Roles:
+//   warp 0       loads (TMA): the page's latents, then the pieces of the weights;
+//   warp 1       issues the MMAs (N = 256);
+//   warps 4..11  round the sums to BF16 and store them, two warps 32 positions: key
+//                channels and the rotated key (which all heads share, held in registers),
+//                or value channels.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
+#include "attn_common.cuh"
 #include "cache_common.cuh"
+#include "paged_common.cuh"
+#include "tc.cuh"
 
 namespace csa {
 namespace {
 
-constexpr int LE_POS = 16;
+constexpr int LE_THREADS = 384;
+constexpr int LE_LOAD = 0, LE_MMA = 1, LE_OUT0 = 4;  // first warps
+constexpr int LE_BOX = 16384;                        // 64 columns of 128 rows
+constexpr int LE_STAGES = 3;                         // pieces of the weights in flight
+constexpr int LE_PIECE = 2 * LE_BOX;                 // 64 columns of a head's keys and values
+constexpr int LE_OFF_W = 8 * LE_BOX, LE_OFF_MISC = LE_OFF_W + LE_STAGES * LE_PIECE;
 
-// One CTA: 16 positions of one page, one head; a thread an output channel.
-__global__ void __launch_bounds__(256) latent_expand_kernel(csa_latent_expand_args a) {
-  __shared__ float c[LE_POS][kLatent];
-  const int h = blockIdx.x, piece = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int j0 = piece * LE_POS;
-  const int lo = max(a.first ? a.first[b] : 0, j0);
-  const int hi = (int)min((long long)min(a.kv_len[b], j0 + LE_POS), (long long)a.max_blocks * kBlock);
+struct Misc {
+  uint64_t c_full[8], w_full[LE_STAGES], w_empty[LE_STAGES], d_full[2], d_empty[2], drained;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(LE_OFF_MISC + sizeof(Misc) <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ bool le_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                        uint32_t *status) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = tc::global_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*abort) return false;
+      if (tc::global_ns() - t0 > 2000000000ull) {
+        *abort = 1;
+        flag(status, CSA_DEV_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// Four MMAs over 64 of K in one statement (an elected lane); acc = 0: the first overwrites.
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 q, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.u64 x, %1, 2;\n\tadd.u64 y, %2, 2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+      "add.u64 x, %1, 4;\n\tadd.u64 y, %2, 4;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+      "add.u64 x, %1, 6;\n\tadd.u64 y, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__global__ void __launch_bounds__(LE_THREADS, 1)
+    latent_expand_kernel(csa_latent_expand_args a, int heads_per, int parts,
+                         const __grid_constant__ CUtensorMap cmap,
+                         const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  Misc *M = reinterpret_cast<Misc *>(sm + LE_OFF_MISC);
+  tc::griddep_wait();
+  tc::griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tc::smem_u32(sm) & 1023u) {
+    if (tid == 0) flag(a.status_dev, CSA_DEV_TIMEOUT);
+    return;
+  }
+  // pages fastest: CTAs that run together read the same weights
+  const long long pages = (long long)a.n_req * a.max_blocks;
+  const int part = (int)(blockIdx.x / pages);
+  const long long u = blockIdx.x - part * pages;
+  const int b = (int)(u / a.max_blocks), page = (int)(u - (long long)b * a.max_blocks);
+  const int h0 = part * heads_per, h1 = min(a.n_heads, h0 + heads_per);
+  // positions [lo, hi) of the page
+  const int base = page * kBlock;
+  const int lo = max((a.first ? max(a.first[b], 0) : 0) - base, 0);
+  const int hi = min(max(a.kv_len[b], 0) - base, kBlock);
   if (lo >= hi) return;
-  const long long src = page_row(a.block_table, a.max_blocks, a.n_blocks, b, j0, a.status_dev);
-  const long long dst = page_row(a.out_table, a.out_max_blocks, a.n_out_blocks, b, j0, a.status_dev);
-  if (src < 0 || dst < 0) return;
-  const uint8_t *cp = static_cast<const uint8_t *>(a.c_pool) +
-                      pool_offset(src, a.c_page_stride, a.c_token_stride);
-  for (int i = tid; i < (hi - j0) * kLatent; i += 256)
-    c[i / kLatent][i % kLatent] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(
-        cp + (i / kLatent) * a.c_token_stride)[i % kLatent]);
+  const int src = a.block_table[u];
+  const int dst = page < a.out_max_blocks ? a.out_table[(long long)b * a.out_max_blocks + page] : -1;
+  if (src < 0 || src >= a.n_blocks || dst < 0 || dst >= a.n_out_blocks) {
+    if (tid == 0) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 8; ++i) tc::mbar_init(&M->c_full[i], 1);
+    for (int i = 0; i < LE_STAGES; ++i) {
+      tc::mbar_init(&M->w_full[i], 1);
+      tc::mbar_init(&M->w_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&M->d_full[i], 1);
+      tc::mbar_init(&M->d_empty[i], 8);
+    }
+    tc::mbar_init(&M->drained, 1);
+    M->abort = 0;
+    tc::mbar_fence_init();
+  }
+  if (warp == LE_MMA) tc::tmem_alloc(&M->tmem, 512);
+  tc::tc_fence_before();
   __syncthreads();
-  const bool key = tid < kNope;
-  const __nv_bfloat16 *w =
-      reinterpret_cast<const __nv_bfloat16 *>(
-          static_cast<const uint8_t *>(key ? a.w_uk : a.w_uv) +
-          h * (key ? a.w_uk_head_stride : a.w_uv_head_stride)) +
-      (tid & 127) * kLatent;
-  float s[LE_POS] = {};
-  for (int k = 0; k < kLatent; ++k) {
-    const float x = __bfloat162float(w[k]);
+  tc::tc_fence_after();
+  const uint32_t tmem = __reduce_or_sync(0xffffffffu, M->tmem);
+  volatile int *abort = &M->abort;
+
+  if (warp == LE_LOAD) {
+    // ================================================================ loads
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      int n_c = 0;
+      for (int h = h0; h < h1 && ok; ++h)
+        for (int c = 0; c < 8; ++c, ++it) {
+          const int st = it % LE_STAGES;
+          ok = le_wait(&M->w_empty[st], ((it / LE_STAGES) & 1) ^ 1, abort, a.status_dev);
+          if (!ok) break;
+          if (h == h0) {
+            tc::mbar_arrive_expect_tx(&M->c_full[c], LE_BOX);
+            tc::tma_load_3d(sm + c * LE_BOX, &cmap, c * 64, 0, src, &M->c_full[c]);
+            ++n_c;
+          }
+          uint8_t *w = sm + LE_OFF_W + st * LE_PIECE;
+          tc::mbar_arrive_expect_tx(&M->w_full[st], LE_PIECE);
+          tc::tma_load_3d(w, &kmap, c * 64, 0, h, &M->w_full[st]);
+          tc::tma_load_3d(w + LE_BOX, &vmap, c * 64, 0, h, &M->w_full[st]);
+        }
+      // whatever was asked for has landed before the CTA retires
+      if (!ok) {
+        for (int c = 0; c < n_c; ++c) tc::mbar_wait(&M->c_full[c], 0, 50000000ull);
+        for (uint32_t k = it > LE_STAGES ? it - LE_STAGES : 0; k < it; ++k)
+          tc::mbar_wait(&M->w_full[k % LE_STAGES], (k / LE_STAGES) & 1, 50000000ull);
+      }
+    }
+    __syncwarp();
+  } else if (warp == LE_MMA) {
+    // ================================================================ MMA
+    if (tc::elect_one()) {
+      constexpr uint32_t idesc = tc::idesc_bf16_f32(128, 256);
+      const uint64_t dc = tc::desc_sw128(tc::smem_u32(sm));
+      const uint64_t dw = tc::desc_sw128(tc::smem_u32(sm) + LE_OFF_W);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int h = h0; h < h1 && ok; ++h) {
+        const int n = h - h0, buf = n & 1;
+        ok = le_wait(&M->d_empty[buf], ((n >> 1) & 1) ^ 1, abort, a.status_dev);
+        for (int c = 0; c < 8 && ok; ++c, ++it) {
+          const int st = it % LE_STAGES;
+          ok = (n > 0 || le_wait(&M->c_full[c], 0, abort, a.status_dev)) &&
+               le_wait(&M->w_full[st], (it / LE_STAGES) & 1, abort, a.status_dev);
+          if (!ok) break;
+          tc::tc_fence_after();
+          mma4(tmem + buf * 256, dc + ((c * LE_BOX) >> 4), dw + ((st * LE_PIECE) >> 4), idesc, c > 0);
+          tc::mma_commit(&M->w_empty[st]);
+        }
+        if (ok) tc::mma_commit(&M->d_full[buf]);
+      }
+      // every issued MMA has completed before tensor memory is released
+      tc::mma_commit(&M->drained);
+      tc::mbar_wait(&M->drained, 0, 100000000ull);
+    }
+    __syncwarp();
+  } else if (warp >= LE_OUT0) {
+    // ================================================================ outputs
+    // (a value's half: columns 128 and on of a head's sums)
+    const int qd = warp & 3, value = (warp - LE_OUT0) >> 2, j = qd * 32 + lane;
+    const bool mine = j >= lo && j < hi;
+    const uint32_t from = tmem + ((uint32_t)(qd * 32) << 16) + value * 128;
+    uint8_t *to = value ? static_cast<uint8_t *>(a.v_pool) + dst * a.v_page_stride + j * a.v_token_stride
+                        : static_cast<uint8_t *>(a.k_pool) + dst * a.k_page_stride + j * a.k_token_stride;
+    const long long hs = value ? a.v_head_stride : a.k_head_stride;
+    uint4 r[8];
+    if (!value && mine)
 #pragma unroll
-    for (int i = 0; i < LE_POS; ++i) s[i] += x * c[i][k];
-  }
-  uint8_t *kp = static_cast<uint8_t *>(a.k_pool) + pool_offset(dst, a.k_page_stride, a.k_token_stride) +
-                h * a.k_head_stride;
-  uint8_t *vp = static_cast<uint8_t *>(a.v_pool) + pool_offset(dst, a.v_page_stride, a.v_token_stride) +
-                h * a.v_head_stride;
-  const uint8_t *rp = static_cast<const uint8_t *>(a.r_pool) +
-                      pool_offset(src, a.r_page_stride, a.r_token_stride);
+      for (int i = 0; i < 8; ++i)
+        r[i] = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.r_pool) +
+                                               src * a.r_page_stride + j * a.r_token_stride)[i];
+    for (int h = h0; h < h1; ++h) {
+      const int n = h - h0, buf = n & 1;
+      if (!__all_sync(0xffffffffu, le_wait(&M->d_full[buf], (n >> 1) & 1, abort, a.status_dev))) break;
+      tc::tc_fence_after();
+      uint4 *out = reinterpret_cast<uint4 *>(to + h * hs);
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        float x[32];
+        tc::tmem_ld32(from + buf * 256 + c, x);
+        if (mine)
 #pragma unroll
-  for (int i = 0; i < LE_POS; ++i) {
-    if (j0 + i < lo || j0 + i >= hi) continue;
-    uint8_t *to = key ? kp + i * a.k_token_stride : vp + i * a.v_token_stride;
-    reinterpret_cast<__nv_bfloat16 *>(to)[tid & 127] = __float2bfloat16_rn(s[i]);
-    if (tid < kRopeDim)
-      reinterpret_cast<__nv_bfloat16 *>(kp + i * a.k_token_stride)[kNope + tid] =
-          reinterpret_cast<const __nv_bfloat16 *>(rp + i * a.r_token_stride)[tid];
+          for (int i = 0; i < 4; ++i)
+            out[c / 8 + i] = make_uint4(attn::pack2(x[8 * i], x[8 * i + 1]),
+                                        attn::pack2(x[8 * i + 2], x[8 * i + 3]),
+                                        attn::pack2(x[8 * i + 4], x[8 * i + 5]),
+                                        attn::pack2(x[8 * i + 6], x[8 * i + 7]));
+      }
+      if (!value && mine)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[kNope / 8 + i] = r[i];
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&M->d_empty[buf]);
+    }
   }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == LE_MMA) tc::tmem_dealloc(tmem, 512);
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    sms = 152;
+  return sms;
+}
+
+bool encode(CUtensorMap *map, const void *base, const cuuint64_t (&dims)[3], int64_t s1, int64_t s2) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void *f = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  const cuuint64_t strides[2] = {(cuuint64_t)s1, (cuuint64_t)s2};
+  const cuuint32_t ones[3] = {1, 1, 1}, box[3] = {64, 128, 1};
+  memset(map, 0, sizeof(*map));
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 cudaError_t launch_latent_expand(const csa_latent_expand_args &a, cudaStream_t s) {
+  CUtensorMap cmap, kmap, vmap;
+  const cuuint64_t pages = a.n_blocks, heads = a.n_heads;
+  if (!encode(&cmap, a.c_pool, {kLatent, kBlock, pages}, a.c_token_stride, a.c_page_stride) ||
+      !encode(&kmap, a.w_uk, {kLatent, kNope, heads}, kLatent * 2, a.w_uk_head_stride) ||
+      !encode(&vmap, a.w_uv, {kLatent, kValue, heads}, kLatent * 2, a.w_uv_head_stride))
+    return cudaErrorInvalidValue;
+  const size_t smem = LE_OFF_MISC + sizeof(Misc);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static bool attr[64] = {};
+  if (dev < 0 || dev >= 64 || !attr[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        latent_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr[dev] = true;
+  }
+  // heads of a CTA: as many as leave four CTAs for every SM, at least one
+  const int sms = sm_count();
+  const long long n_pages = (long long)a.n_req * a.max_blocks;
+  long long per = n_pages * a.n_heads / (4ll * sms);
+  per = per < 1 ? 1 : (per > a.n_heads ? a.n_heads : per);
+  const int parts = (int)((a.n_heads + per - 1) / per);
+  if (n_pages * parts > 0x7FFFFFFF) return cudaErrorInvalidValue;
   launch_begin(CSA_K_LATENT_EXPAND, s);
-  latent_expand_kernel<<<dim3(a.n_heads, a.max_blocks * (kBlock / LE_POS), a.n_req), 256, 0, s>>>(a);
+  const cudaError_t e =
+      launch_kernel(latent_expand_kernel, dim3((unsigned)(n_pages * parts)), dim3(LE_THREADS), smem, s,
+                    0, false, a, (int)per, parts, cmap, kmap, vmap);
   launch_end(CSA_K_LATENT_EXPAND, s);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace csa
