@@ -994,7 +994,7 @@ CSA_API csa_status_t csa_attn_mass(csa_attn_mass_args *args, csa_stream_t stream
  * i32 [n_req] (below 0: 0).  k_pool bf16 [n_blocks, 128, n_heads, k_dim], v_pool bf16
  * [n_blocks, 128, n_heads, v_dim] or NULL, strides as in csa_kv_append (a latent
  * cache: one head, c as k of 512 and r as v of 64).  k_dim, v_dim multiples of 8, 8
- * .. 512; max_blocks < 2^24; first, recent >= 0.  The workspace is used as
+ * .. 512; max_blocks < 2^23; first, recent >= 0.  The workspace is used as
  * csa_paged_attn's is.
  * ---------------------------------------------------------------------- */
 typedef struct {

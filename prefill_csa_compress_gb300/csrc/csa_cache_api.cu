@@ -143,7 +143,7 @@ CSA_API csa_status_t csa_kv_evict(csa_kv_evict_args *user, csa_stream_t stream) 
   if (a.n_req < 0 || a.max_blocks <= 0 || a.n_blocks <= 0 || a.n_heads < 1 || a.n_heads > 65536 ||
       a.first < 0 || a.recent < 0)
     return CSA_ERR_INVALID_ARG;
-  if (a.max_blocks >= kMaxPages) return CSA_ERR_UNSUPPORTED;
+  if (a.max_blocks >= kMaxPages / 2) return CSA_ERR_UNSUPPORTED;
   if (!a.v_pool) a.v_dim = 0, a.v_page_stride = a.v_token_stride = a.v_head_stride = 0;
   if (a.k_dim < 8 || a.k_dim > 512 || a.k_dim % 8 != 0 ||
       (a.v_pool && (a.v_dim < 8 || a.v_dim > 512 || a.v_dim % 8 != 0)))
