@@ -3,14 +3,14 @@
 //
 //   D[j, n] = c_j . w_n    (128 positions x 256 channels of a head x 512, K-major both)
 // A CTA keeps a page (128 KB) in shared memory and goes through some of the heads: a
-// head's 256 rows of 512 stream past in eight pieces of 64 columns (32 KB), three in
+// head's 256 rows of 512 stream past in eight pieces of 64 columns (32 KB), two in
 // flight, and its 256 columns of sums take half of tensor memory, so that one head is
 // written while the next one is computed.  Roles:
 //   warp 0       loads (TMA): the page's latents, then the pieces of the weights;
 //   warp 1       issues the MMAs (N = 256);
 //   warps 4..11  round the sums to BF16 and store them, two warps 32 positions: key
-//                channels and the rotated key (which all heads share, held in registers),
-//                or value channels.
+//                channels, or value channels.  The rotated key, which all heads share,
+//                is loaded once and stored from shared memory for every head.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -27,12 +27,14 @@ namespace {
 constexpr int LE_THREADS = 384;
 constexpr int LE_LOAD = 0, LE_MMA = 1, LE_OUT0 = 4;  // first warps
 constexpr int LE_BOX = 16384;                        // 64 columns of 128 rows
-constexpr int LE_STAGES = 3;                         // pieces of the weights in flight
+constexpr int LE_STAGES = 2;                         // pieces of the weights in flight
 constexpr int LE_PIECE = 2 * LE_BOX;                 // 64 columns of a head's keys and values
-constexpr int LE_OFF_W = 8 * LE_BOX, LE_OFF_MISC = LE_OFF_W + LE_STAGES * LE_PIECE;
+constexpr int LE_OUT = 2048;  // 32 channels of 32 positions, a warp's way to memory
+constexpr int LE_OFF_W = 8 * LE_BOX, LE_OFF_R = LE_OFF_W + LE_STAGES * LE_PIECE,
+              LE_OFF_OUT = LE_OFF_R + LE_BOX, LE_OFF_MISC = LE_OFF_OUT + 8 * LE_OUT;
 
 struct Misc {
-  uint64_t c_full[8], w_full[LE_STAGES], w_empty[LE_STAGES], d_full[2], d_empty[2], drained;
+  uint64_t r_full, c_full[8], w_full[LE_STAGES], w_empty[LE_STAGES], d_full[2], d_empty[2], drained;
   uint32_t tmem;
   int abort;
 };
@@ -71,11 +73,31 @@ __device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_
       : "memory");
 }
 
+// A box of shared memory into a pool [channels, heads, 128, pages], as a bulk group; until
+// the groups of this thread have been read, or are complete.
+__device__ __forceinline__ void store_4d(const void *tmap, int x, int y, int z, int w, const void *src) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+      "r"(x), "r"(y), "r"(z), "r"(w), "r"(tc::smem_u32(src))
+      : "memory");
+}
+__device__ __forceinline__ void stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void stores_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 __global__ void __launch_bounds__(LE_THREADS, 1)
     latent_expand_kernel(csa_latent_expand_args a, int heads_per, int parts,
                          const __grid_constant__ CUtensorMap cmap,
                          const __grid_constant__ CUtensorMap kmap,
-                         const __grid_constant__ CUtensorMap vmap) {
+                         const __grid_constant__ CUtensorMap vmap,
+                         const __grid_constant__ CUtensorMap rmap,
+                         const __grid_constant__ CUtensorMap k_out,
+                         const __grid_constant__ CUtensorMap kr_out,
+                         const __grid_constant__ CUtensorMap v_out) {
   extern __shared__ __align__(1024) uint8_t sm[];
   Misc *M = reinterpret_cast<Misc *>(sm + LE_OFF_MISC);
   tc::griddep_wait();
@@ -96,6 +118,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
   const int lo = max((a.first ? max(a.first[b], 0) : 0) - base, 0);
   const int hi = min(max(a.kv_len[b], 0) - base, kBlock);
   if (lo >= hi) return;
+  const bool full = lo == 0 && hi == kBlock;
   const int src = a.block_table[u];
   const int dst = page < a.out_max_blocks ? a.out_table[(long long)b * a.out_max_blocks + page] : -1;
   if (src < 0 || src >= a.n_blocks || dst < 0 || dst >= a.n_out_blocks) {
@@ -103,6 +126,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
     return;
   }
   if (tid == 0) {
+    tc::mbar_init(&M->r_full, 1);
     for (int i = 0; i < 8; ++i) tc::mbar_init(&M->c_full[i], 1);
     for (int i = 0; i < LE_STAGES; ++i) {
       tc::mbar_init(&M->w_full[i], 1);
@@ -129,6 +153,10 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
       uint32_t it = 0;
       bool ok = true;
       int n_c = 0;
+      if (full) {
+        tc::mbar_arrive_expect_tx(&M->r_full, LE_BOX);
+        tc::tma_load_3d(sm + LE_OFF_R, &rmap, 0, 0, src, &M->r_full);
+      }
       for (int h = h0; h < h1 && ok; ++h)
         for (int c = 0; c < 8; ++c, ++it) {
           const int st = it % LE_STAGES;
@@ -145,6 +173,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
           tc::tma_load_3d(w + LE_BOX, &vmap, c * 64, 0, h, &M->w_full[st]);
         }
       // whatever was asked for has landed before the CTA retires
+      if (full) tc::mbar_wait(&M->r_full, 0, 50000000ull);
       if (!ok) {
         for (int c = 0; c < n_c; ++c) tc::mbar_wait(&M->c_full[c], 0, 50000000ull);
         for (uint32_t k = it > LE_STAGES ? it - LE_STAGES : 0; k < it; ++k)
@@ -188,36 +217,57 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
     uint8_t *to = value ? static_cast<uint8_t *>(a.v_pool) + dst * a.v_page_stride + j * a.v_token_stride
                         : static_cast<uint8_t *>(a.k_pool) + dst * a.k_page_stride + j * a.k_token_stride;
     const long long hs = value ? a.v_head_stride : a.k_head_stride;
+    // A page that is written whole goes through shared memory, 32 channels of a warp's 32
+    // positions at a time (16-byte chunk c of row j at c ^ (j / 2) % 4), and by TMA; the
+    // rotated key straight from where it was loaded.  Else every thread stores its row.
+    uint8_t *box = sm + LE_OFF_OUT + (warp - LE_OUT0) * LE_OUT;
+    const bool rotated = full && warp == LE_OUT0;
     uint4 r[8];
-    if (!value && mine)
+    if (!full && !value && mine)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         r[i] = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.r_pool) +
                                                src * a.r_page_stride + j * a.r_token_stride)[i];
-    for (int h = h0; h < h1; ++h) {
+    bool ok = !rotated || __all_sync(0xffffffffu, le_wait(&M->r_full, 0, abort, a.status_dev));
+    for (int h = h0; h < h1 && ok; ++h) {
       const int n = h - h0, buf = n & 1;
-      if (!__all_sync(0xffffffffu, le_wait(&M->d_full[buf], (n >> 1) & 1, abort, a.status_dev))) break;
+      ok = __all_sync(0xffffffffu, le_wait(&M->d_full[buf], (n >> 1) & 1, abort, a.status_dev));
+      if (!ok) break;
       tc::tc_fence_after();
       uint4 *out = reinterpret_cast<uint4 *>(to + h * hs);
+      if (rotated && lane == 0) store_4d(&kr_out, kNope, h, 0, dst, sm + LE_OFF_R);
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         float x[32];
         tc::tmem_ld32(from + buf * 256 + c, x);
-        if (mine)
+        uint4 y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          y[i] = make_uint4(attn::pack2(x[8 * i], x[8 * i + 1]), attn::pack2(x[8 * i + 2], x[8 * i + 3]),
+                            attn::pack2(x[8 * i + 4], x[8 * i + 5]),
+                            attn::pack2(x[8 * i + 6], x[8 * i + 7]));
+        if (full) {
+          if (lane == 0) stores_read();
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            out[c / 8 + i] = make_uint4(attn::pack2(x[8 * i], x[8 * i + 1]),
-                                        attn::pack2(x[8 * i + 2], x[8 * i + 3]),
-                                        attn::pack2(x[8 * i + 4], x[8 * i + 5]),
-                                        attn::pack2(x[8 * i + 6], x[8 * i + 7]));
+            reinterpret_cast<uint4 *>(box + lane * 64)[i ^ ((lane >> 1) & 3)] = y[i];
+          tc::fence_async_shared();
+          __syncwarp();
+          if (lane == 0) store_4d(value ? &v_out : &k_out, c, h, qd * 32, dst, box);
+        } else if (mine) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[c / 8 + i] = y[i];
+        }
       }
-      if (!value && mine)
+      if (!full && !value && mine)
 #pragma unroll
         for (int i = 0; i < 8; ++i) out[kNope / 8 + i] = r[i];
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&M->d_empty[buf]);
     }
+    if (lane == 0) stores_done();
   }
 
   tc::tc_fence_before();
@@ -234,7 +284,8 @@ int sm_count() {
   return sms;
 }
 
-bool encode(CUtensorMap *map, const void *base, const cuuint64_t (&dims)[3], int64_t s1, int64_t s2) {
+bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     cudaDriverEntryPointQueryResult q;
     void *f = nullptr;
@@ -244,23 +295,47 @@ bool encode(CUtensorMap *map, const void *base, const cuuint64_t (&dims)[3], int
       f = nullptr;
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
   }();
-  const cuuint64_t strides[2] = {(cuuint64_t)s1, (cuuint64_t)s2};
-  const cuuint32_t ones[3] = {1, 1, 1}, box[3] = {64, 128, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
   memset(map, 0, sizeof(*map));
-  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
-                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides,
+                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [x, y, z], boxes of 64 x 128.
+bool encode_in(CUtensorMap *map, const void *base, cuuint64_t x, cuuint64_t y, cuuint64_t z,
+               int64_t s1, int64_t s2) {
+  const cuuint64_t dims[3] = {x, y, z}, strides[2] = {(cuuint64_t)s1, (cuuint64_t)s2};
+  const cuuint32_t box[3] = {64, 128, 1};
+  return encode(map, base, 3, dims, strides, box);
+}
+
+// A pool [pages, 128, heads, channels], boxes of `w` channels and `rows` positions of a head.
+bool encode_out(CUtensorMap *map, void *base, int channels, int heads, int pages, int64_t head,
+                int64_t token, int64_t page, int w, int rows) {
+  const cuuint64_t dims[4] = {(cuuint64_t)channels, (cuuint64_t)heads, kBlock, (cuuint64_t)pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)head, (cuuint64_t)token, (cuuint64_t)page};
+  const cuuint32_t box[4] = {(cuuint32_t)w, 1, (cuuint32_t)rows, 1};
+  return encode(map, base, 4, dims, strides, box);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_expand(const csa_latent_expand_args &a, cudaStream_t s) {
-  CUtensorMap cmap, kmap, vmap;
+  CUtensorMap cmap, kmap, vmap, rmap, k_out, kr_out, v_out;
   const cuuint64_t pages = a.n_blocks, heads = a.n_heads;
-  if (!encode(&cmap, a.c_pool, {kLatent, kBlock, pages}, a.c_token_stride, a.c_page_stride) ||
-      !encode(&kmap, a.w_uk, {kLatent, kNope, heads}, kLatent * 2, a.w_uk_head_stride) ||
-      !encode(&vmap, a.w_uv, {kLatent, kValue, heads}, kLatent * 2, a.w_uv_head_stride))
+  if (!encode_in(&cmap, a.c_pool, kLatent, kBlock, pages, a.c_token_stride, a.c_page_stride) ||
+      !encode_in(&kmap, a.w_uk, kLatent, kNope, heads, kLatent * 2, a.w_uk_head_stride) ||
+      !encode_in(&vmap, a.w_uv, kLatent, kValue, heads, kLatent * 2, a.w_uv_head_stride) ||
+      !encode_in(&rmap, a.r_pool, kRopeDim, kBlock, pages, a.r_token_stride, a.r_page_stride) ||
+      !encode_out(&k_out, a.k_pool, kNope + kRopeDim, a.n_heads, a.n_out_blocks, a.k_head_stride,
+                  a.k_token_stride, a.k_page_stride, 32, 32) ||
+      !encode_out(&kr_out, a.k_pool, kNope + kRopeDim, a.n_heads, a.n_out_blocks, a.k_head_stride,
+                  a.k_token_stride, a.k_page_stride, 64, 128) ||
+      !encode_out(&v_out, a.v_pool, kValue, a.n_heads, a.n_out_blocks, a.v_head_stride,
+                  a.v_token_stride, a.v_page_stride, 32, 32))
     return cudaErrorInvalidValue;
   const size_t smem = LE_OFF_MISC + sizeof(Misc);
   int dev = 0;
@@ -272,17 +347,22 @@ cudaError_t launch_latent_expand(const csa_latent_expand_args &a, cudaStream_t s
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr[dev] = true;
   }
-  // heads of a CTA: as many as leave four CTAs for every SM, at least one
+  // Parts of the heads: as many as make waves x (heads of a part + 1) smallest, a CTA's
+  // start and end being worth about one head.
   const int sms = sm_count();
   const long long n_pages = (long long)a.n_req * a.max_blocks;
-  long long per = n_pages * a.n_heads / (4ll * sms);
-  per = per < 1 ? 1 : (per > a.n_heads ? a.n_heads : per);
-  const int parts = (int)((a.n_heads + per - 1) / per);
+  int per = a.n_heads, parts = 1;
+  long long best = 0;
+  for (int p = 1; p <= a.n_heads && p <= 128; ++p) {
+    const long long k = (a.n_heads + p - 1) / p, n = (a.n_heads + k - 1) / k;
+    const long long cost = (n_pages * n + sms - 1) / sms * (k + 1);
+    if (p == 1 || cost < best) best = cost, per = (int)k, parts = (int)n;
+  }
   if (n_pages * parts > 0x7FFFFFFF) return cudaErrorInvalidValue;
   launch_begin(CSA_K_LATENT_EXPAND, s);
   const cudaError_t e =
       launch_kernel(latent_expand_kernel, dim3((unsigned)(n_pages * parts)), dim3(LE_THREADS), smem, s,
-                    0, false, a, (int)per, parts, cmap, kmap, vmap);
+                    0, false, a, per, parts, cmap, kmap, vmap, rmap, k_out, kr_out, v_out);
   launch_end(CSA_K_LATENT_EXPAND, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

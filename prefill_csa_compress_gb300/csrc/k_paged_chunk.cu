@@ -66,19 +66,26 @@ struct Cfg {
   static constexpr int V_CHUNKS = D / 64;              // and of V
   static constexpr int TILE = CHUNKS * 16384;          // bytes of a 128-row tile of K
   static constexpr int V_TILE = V_CHUNKS * 16384;
-  // K and V tiles in flight.  Where both have a size, they take the stages in turn;
-  // else (SPLIT) K has stages 0 and 1 and V stage 2, and K is asked for a page
-  // ahead of V, since V's stage is free later.
+  // K and V tiles in flight.  Where both have a size, they take the stages in turn.
+  // Else (SPLIT) K goes through a ring of four boxes of 64 columns, each handed back as
+  // soon as the last tile's logits have gone over it, and V has two stages: a page of K
+  // is 48 KB, and with two whole pages of it and one of V a page took 5,000 cycles,
+  // waiting for V (a prompt of 8192 rows of 64 heads: 1,170 us).
   static constexpr bool SPLIT = DK != D;
-  static constexpr int STAGES = SPLIT ? 3 : (D == 128 ? 5 : 8);
+  static constexpr int STAGES = D == 128 ? 5 : 8;
   static constexpr int OFF_KV = 2 * TILE;
-  static constexpr int OFF_MISC = OFF_KV + (SPLIT ? 2 * TILE + V_TILE : STAGES * TILE);
-  // the stage of a page's K or V, and its turn there
+  static constexpr int OFF_V = OFF_KV + 4 * 16384;  // SPLIT
+  static constexpr int OFF_MISC = SPLIT ? OFF_V + 2 * V_TILE : OFF_KV + STAGES * TILE;
+  // the barriers' stage of a page's K or V, its turn there, and its place; SPLIT: K boxes
+  // have stages 0 .. 3 (box c of page j is the ring's box CHUNKS j + c), V 4 and 5
   __device__ static __forceinline__ int stage(int kv, uint32_t page) {
-    return SPLIT ? (kv ? 2 : (int)(page & 1)) : (int)((2 * page + kv) % STAGES);
+    return SPLIT ? 4 + (int)(page & 1) : (int)((2 * page + kv) % STAGES);
   }
   __device__ static __forceinline__ uint32_t turn(int kv, uint32_t page) {
-    return SPLIT ? (kv ? page : page >> 1) : (2 * page + kv) / STAGES;
+    return SPLIT ? page >> 1 : (2 * page + kv) / STAGES;
+  }
+  __device__ static __forceinline__ int offset(int stage) {
+    return SPLIT ? OFF_V + (stage - 4) * V_TILE : OFF_KV + stage * TILE;
   }
   // Tensor memory columns: buffers of 128 for S (with P over it), then O.  Two
   // buffers, one a tile, or with room for a third (ROTATE) three that the tiles
@@ -280,19 +287,21 @@ __device__ __forceinline__ void issue_qk(uint32_t d, uint64_t q, uint64_t k, uin
                      PC_QK_PTX(0, 2) PC_QK_PTX(0, 3) PC_QK_END_PTX ::"r"(d),
                  "l"(q), "l"(k), "r"(idesc), "r"(full), "r"(freed)
                  : "memory");
-  else if constexpr (DK == 192)
-    asm volatile(PC_BEGIN_PTX "setp.ne.b32 p, 0, 0;\n\t" PC_QK_PTX(0, 0) PC_QK_PTX(0, 1)
-                     PC_QK_PTX(0, 2) PC_QK_PTX(0, 3) PC_QK_PTX(1, 0) PC_QK_PTX(1, 1)
-                         PC_QK_PTX(1, 2) PC_QK_PTX(1, 3) PC_QK_PTX(2, 0) PC_QK_PTX(2, 1)
-                             PC_QK_PTX(2, 2) PC_QK_PTX(2, 3) PC_QK_END_PTX ::"r"(d),
-                 "l"(q), "l"(k), "r"(idesc), "r"(full), "r"(freed)
-                 : "memory");
   else
     asm volatile(PC_BEGIN_PTX "setp.ne.b32 p, 0, 0;\n\t" PC_QK_PTX(0, 0) PC_QK_PTX(0, 1)
                      PC_QK_PTX(0, 2) PC_QK_PTX(0, 3) PC_QK_PTX(1, 0) PC_QK_PTX(1, 1)
                          PC_QK_PTX(1, 2) PC_QK_PTX(1, 3) PC_QK_END_PTX ::"r"(d),
                  "l"(q), "l"(k), "r"(idesc), "r"(full), "r"(freed)
                  : "memory");
+}
+
+// Four of its steps, over one box of K.
+__device__ __forceinline__ void issue_qk_box(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc,
+                                             uint32_t acc, uint32_t freed) {
+  asm volatile(PC_BEGIN_PTX "setp.ne.u32 p, %4, 0;\n\t" PC_QK_PTX(0, 0) PC_QK_PTX(0, 1)
+                   PC_QK_PTX(0, 2) PC_QK_PTX(0, 3) PC_COMMIT_IF_PTX(5) "}" ::"r"(d),
+               "l"(q), "l"(k), "r"(idesc), "r"(acc), "r"(freed)
+               : "memory");
 }
 
 // Bits below n of a word (none for n <= 0, all for n >= 32).
@@ -387,18 +396,38 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     bool counting = true, many = false, ok = true;
     int total = 0, valid = 0, skip = 0, n_pages = 0, left = 0;
     uint32_t n_k = 0, n_v = 0;  // tiles loaded
-    int behind = 0;             // the page before
-    // The next K or V, of page `phys`, once its stage is free; describe() runs in one
-    // lane before it is handed on.
+    // The next K or V, of page `phys`, once its stages are free; describe() runs in one
+    // lane before any of it is handed on.
     auto load = [&](int kv, int phys, auto &&describe) {
+      const bool there = phys >= 0 && phys < a.n_blocks;
+      if (C::SPLIT && kv == 0) {
+        for (int c = 0; c < C::CHUNKS; ++c) {
+          const uint32_t i = C::CHUNKS * n_k + c;
+          const int st = i & 3;
+          if (!pc_wait_warp(&M->kv_empty[st], ((i >> 2) & 1) ^ 1, abort, a.status_dev)) return false;
+          if (lane == 0) {
+            if (c == 0) describe();
+            if (there) {
+              tc::mbar_arrive_expect_tx(&M->kv_full[st], 16384);
+              paged::tma_load_4d(sm + C::OFF_KV + st * 16384, &kmap, c * 64, kvh, 0, phys,
+                                 &M->kv_full[st]);
+            } else {
+              tc::mbar_arrive(&M->kv_full[st]);
+            }
+          }
+          __syncwarp();
+        }
+        ++n_k;
+        return true;
+      }
       uint32_t &n = kv ? n_v : n_k;
       const int st = C::stage(kv, n);
       if (!pc_wait_warp(&M->kv_empty[st], (C::turn(kv, n) & 1) ^ 1, abort, a.status_dev))
         return false;
       if (lane == 0) {
         describe();
-        uint8_t *dst = sm + C::OFF_KV + st * C::TILE;
-        if (phys >= 0 && phys < a.n_blocks) {
+        uint8_t *dst = sm + C::offset(st);
+        if (there) {
           tc::mbar_arrive_expect_tx(&M->kv_full[st], kv ? C::V_TILE : C::TILE);
           for (int c = 0; c < (kv ? C::V_CHUNKS : C::CHUNKS); ++c)
             paged::tma_load_4d(dst + c * 16384, kv ? &vmap : &kmap, c * 64, kvh, 0, phys,
@@ -449,7 +478,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         const int phys = __shfl_sync(0xffffffffu, entry, i & 31);
         const bool there = phys >= 0 && phys < a.n_blocks;
         const int base = (pg0 + i) * kBlock;
-        // K, then V (SPLIT: V of the page before)
+        // K, then V
         ok = load(0, phys, [&] {
           Page &P = M->page[n_k % PC_META];
           P.base = base;
@@ -461,12 +490,10 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           P.hi = there ? min(R.hi - base, kBlock) : 0;
           if (!there) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
         });
-        if (C::SPLIT ? n_k > 1 : true) ok = ok && load(1, C::SPLIT ? behind : phys, [] {});
-        behind = phys;
+        ok = ok && load(1, phys, [] {});
         if (n_k == 1 && ok) tc::bar_sync(PC_BAR_START, PC_THREADS);  // n_it, barriers
       }
     }
-    if (C::SPLIT && n_k > 0 && ok) load(1, behind, [] {});
     if (n_pages == 0) {
       // q has landed before the others put their zeros where it goes
       pc_wait_warp(&M->q_full, 0, abort, a.status_dev);
@@ -475,9 +502,14 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     // whatever was asked for has landed before the CTA retires
     if (*abort) {
       tc::mbar_wait(&M->q_full, 0, 50000000ull);
-      for (int kv = 0; kv < 2; ++kv) {
+      if (C::SPLIT) {  // (the last four boxes of K; one that was not asked for times out)
+        const uint32_t n = C::CHUNKS * (n_k + 1);
+        for (uint32_t i = n > 6 ? n - 6 : 0; i < n; ++i)
+          tc::mbar_wait(&M->kv_full[i & 3], (i >> 2) & 1, 5000000ull);
+      }
+      for (int kv = C::SPLIT; kv < 2; ++kv) {
         const uint32_t n = kv ? n_v : n_k;
-        const uint32_t held = C::SPLIT ? 2 - kv : (C::STAGES + 1) / 2;
+        const uint32_t held = C::SPLIT ? 2 : (C::STAGES + 1) / 2;
         for (uint32_t k = n > held ? n - held : 0; k < n; ++k)
           tc::mbar_wait(&M->kv_full[C::stage(kv, k)], C::turn(kv, k) & 1, 50000000ull);
       }
@@ -506,27 +538,44 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       const uint32_t kvs = tc::smem_u32(sm) + C::OFF_KV;
       // descriptors of the first tiles; an address further on adds its sixteenths
       const uint64_t dq = tc::desc_sw128(tc::smem_u32(sm)), dk = tc::desc_sw128(kvs);
-      const uint64_t dv = tc::desc_sw128_mn(kvs, 16384, 1024);
+      const uint64_t dv = tc::desc_sw128_mn(C::SPLIT ? tc::smem_u32(sm) + C::OFF_V : kvs, 16384, 1024);
       const uint32_t bar_s = tc::smem_u32(M->s_full), bar_pv = tc::smem_u32(M->pv_done),
                      bar_kv = tc::smem_u32(M->kv_empty);
-      int sk = 0, sv = C::stage(1, 0);  // stages of the next K and V
+      int sk = 0, sv = C::SPLIT ? 0 : 1;  // stages of the next K (SPLIT: box) and V
+      uint32_t k_turn = 0;               // SPLIT: of that box
       // The next logits, page qj of tile qs into buffer qb.
       int qj = 0, qs = 0, qb = 0;
       auto next_s = [&] {
         if (C::ROTATE && qs == 0 && !pc_wait(&M->kv_full[sk], (qj >> 2) & 1, abort, a.status_dev))
           return false;
-        issue_qk<DK>(tmem + qb * 128, dq + qs * (C::TILE >> 4), dk + sk * (C::TILE >> 4), idesc_s,
-                    bar_s + 8 * qb, qs == n_sub - 1 ? bar_kv + 8 * sk : 0);
+        if constexpr (C::SPLIT) {
+          // the second tile goes over the same boxes and hands them back
+          int box = sk;
+          uint32_t turn = k_turn;
+#pragma unroll
+          for (int c = 0; c < C::CHUNKS; ++c) {
+            if (qs == 0 && !pc_wait(&M->kv_full[box], turn, abort, a.status_dev)) return false;
+            issue_qk_box(tmem + qb * 128, dq + qs * (C::TILE >> 4) + c * 1024, dk + box * 1024, idesc_s,
+                         c > 0, qs == n_sub - 1 ? bar_kv + 8 * box : 0);
+            if (++box == 4) box = 0, turn ^= 1;
+          }
+          tc::mma_commit(&M->s_full[qb]);
+          tc::mbar_arrive(&M->s_full[qb]);
+          if (qs == n_sub - 1) sk = box, k_turn = turn;
+        } else {
+          issue_qk<DK>(tmem + qb * 128, dq + qs * (C::TILE >> 4), dk + sk * (C::TILE >> 4), idesc_s,
+                       bar_s + 8 * qb, qs == n_sub - 1 ? bar_kv + 8 * sk : 0);
+        }
         if (++qs == n_sub) {
           qs = 0;
           ++qj;
-          sk = C::SPLIT ? sk ^ 1 : (sk + 2 >= C::STAGES ? sk + 2 - C::STAGES : sk + 2);
+          if (!C::SPLIT) sk = sk + 2 >= C::STAGES ? sk + 2 - C::STAGES : sk + 2;
         }
         qb = C::ROTATE ? (qb == 2 ? 0 : qb + 1) : qs;
         return true;
       };
       bool ok = pc_wait(&M->q_full, 0, abort, a.status_dev) &&
-                (C::ROTATE || pc_wait(&M->kv_full[0], 0, abort, a.status_dev));
+                (C::ROTATE || C::SPLIT || pc_wait(&M->kv_full[0], 0, abort, a.status_dev));
       for (int n = 0; n < (C::ROTATE ? n_sub + 1 : n_sub) && qj < n_it && ok; ++n) ok = next_s();
       int pb = 0;  // buffer of the next P, and the parity of its turn
       uint32_t turn = 0;
@@ -537,15 +586,15 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
           ok = pc_wait(&M->p_full[pb], turn, abort, a.status_dev);
           if (!ok) break;
           tc::tc_fence_after();
-          issue_pv(tmem + C::O_COL + s * D, tmem + pb * 128, dv + sv * (C::TILE >> 4), idesc_o,
-                   s == n_sub - 1 ? bar_kv + 8 * sv : 0, C::ROTATE ? bar_pv + 8 * s : 0);
+          issue_pv(tmem + C::O_COL + s * D, tmem + pb * 128, dv + sv * (C::V_TILE >> 4), idesc_o,
+                   s == n_sub - 1 ? bar_kv + 8 * (C::SPLIT ? 4 + sv : sv) : 0, C::ROTATE ? bar_pv + 8 * s : 0);
           if (++pb == (C::ROTATE ? 3 : n_sub)) {
             pb = 0;
             turn ^= 1;
           }
           if (qj < n_it) ok = next_s();  // over P, or over the P before it
         }
-        if (!C::SPLIT) sv = sv + 2 >= C::STAGES ? sv + 2 - C::STAGES : sv + 2;
+        sv = C::SPLIT ? sv ^ 1 : (sv + 2 >= C::STAGES ? sv + 2 - C::STAGES : sv + 2);
       }
       for (int s = 0; s < n_sub && ok; ++s) tc::mma_commit(&M->o_full[s]);
       // every issued MMA has completed before tensor memory is released
@@ -560,12 +609,12 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       const int sv = C::stage(1, j);
       // in the order of the loads: only then does a stage's parity tell this
       // load from the stage's one before
-      if (j == 0) ok = pc_wait_warp(&M->kv_full[0], 0, abort, a.status_dev);
+      if (j == 0 && !C::SPLIT) ok = pc_wait_warp(&M->kv_full[0], 0, abort, a.status_dev);
       ok = ok && pc_wait_warp(&M->kv_full[sv], C::turn(1, j) & 1, abort, a.status_dev);
       if (!ok) break;
       Page &P = M->page[j % PC_META];
       if (P.mixed) {
-        uint8_t *v = sm + C::OFF_KV + sv * C::TILE;
+        uint8_t *v = sm + C::offset(sv);
         bool wrote = false;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -592,7 +641,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
         }
         if (wrote) tc::fence_async_shared();
       }
-      if (j + 1 < n_it)  // the MMA warp waits once for both
+      if (j + 1 < n_it && !C::SPLIT)  // the MMA warp waits once for both
         ok = pc_wait_warp(&M->kv_full[C::stage(0, j + 1)], C::turn(0, j + 1) & 1, abort,
                           a.status_dev);
       __syncwarp();
