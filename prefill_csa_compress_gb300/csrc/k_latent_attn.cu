@@ -491,6 +491,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         any_lo = min(any_lo, l), any_hi = max(any_hi, h);
       }
       float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      // bits of a P of 2 or more, of rows that see something
+      const uint32_t big[2] = {hi[0] > lo[0] ? 0x40004000u : 0u, hi[1] > lo[1] ? 0x40004000u : 0u};
+      const float2 one = make_float2(1.f, 1.f);
       for (int i = 0; i < g.n; ++i, ++it) {
         const int st = it & 1, base = (g.tile + i) * LA_KEYS;
         ok = wait(&M->s_full[st], it >> 1) && ok;
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
             if (!there || j < lo[e] || j >= hi[e]) x[k] = -INFINITY;
           }
         }
-        float p[16];
+        float2 p[8];
         uint32_t w[8];
         for (bool move = i == 0;;) {
           if (move) {
@@ -556,16 +559,18 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
           const float r0[2] = {ref[0] == -INFINITY ? 1e30f : -ref[0],
                                ref[1] == -INFINITY ? 1e30f : -ref[1]};
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            const int e = (k >> 1) & 1;
-            p[k] = attn::exp2_sfu(fmaf(x[k], sl2, r0[e]));
-            p[k + 1] = attn::exp2_sfu(fmaf(x[k + 1], sl2, r0[e]));
-            w[k >> 1] = attn::pack2(p[k], p[k + 1]);
-            if (hi[e] > lo[e]) any |= w[k >> 1];
+          for (int k = 0; k < 8; ++k) {
+            const int e = k & 1;
+            float2 y = tc::ffma2(make_float2(x[2 * k], x[2 * k + 1]), make_float2(sl2, sl2),
+                                 make_float2(r0[e], r0[e]));
+            y.x = attn::exp2_sfu(y.x), y.y = attn::exp2_sfu(y.y);
+            p[k] = y;
+            w[k] = attn::pack2(y.x, y.y);
+            any |= w[k] & big[e];
           }
           // (a wait that gave up is known to all of them from here: every thread takes
           // the same way past the barriers)
-          if (!tc::bar_or(BAR_SOFT, 256, !ok || (!move && (any & 0x40004000u)))) break;
+          if (!tc::bar_or(BAR_SOFT, 256, !ok || (!move && any))) break;
           if (tc::bar_or(BAR_SOFT, 256, !ok)) {
             given_up = true;
             break;
@@ -574,8 +579,6 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
           move = true;
         }
         if (given_up) break;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) l[(k >> 1) & 1] += p[k];
         if (mixed) {
           // Positions that not every row sees: latents that are not finite become zero
           // (zero times them is not zero), and rows that see them NaN.
@@ -623,6 +626,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&M->p_full);
+        // (the sums while the product runs)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 y = tc::ffma2(tc::ffma2(p[e], one, p[2 + e]), one, tc::ffma2(p[4 + e], one, p[6 + e]));
+          l[e] += y.x + y.y;
+        }
       }
       // ---- the item's outputs, or its part
       if (given_up) break;
