@@ -1,13 +1,18 @@
 // Keys and values of every head from a paged latent cache (csa_latent_expand): a
-// tcgen05 product of one page of latents with the heads' up-projections.
+// tcgen05 product of two pages of latents with the heads' up-projections, by pairs of
+// CTAs.
 //
-//   D[j, n] = c_j . w_n    (128 positions x 256 channels of a head x 512, K-major both)
-// A CTA keeps a page (128 KB) in shared memory and goes through some of the heads: a
-// head's 256 rows of 512 stream past in eight pieces of 64 columns (32 KB), two in
-// flight, and its 256 columns of sums take half of tensor memory, so that one head is
-// written while the next one is computed.  Roles:
-//   warp 0       loads (TMA): the page's latents, then the pieces of the weights;
-//   warp 1       issues the MMAs (N = 256);
+//   D[j, n] = c_j . w_n    (256 positions x 256 channels of a head x 512, K-major both)
+// Each CTA of a pair (cta_group::2) keeps its page of latents (128 KB) in shared memory
+// and the pair goes through some of the heads: of a head's 256 rows of 512 the first CTA
+// loads the keys' half and the second the values', in eight pieces of 64 columns (16 KB),
+// four in flight, and the tensor cores of both read both.  So every SM fetches 32 bytes
+// a cycle, where a CTA by itself needs 64 for the same rate, more than it can keep in
+// flight beside the latents (355 us for a prompt of 8192 and 128 heads).  A head's 256
+// columns of sums take half of tensor memory: one head is written while the next one is
+// computed.  Roles, in each CTA:
+//   warp 0       loads (TMA): the page's latents, its half of the weights' pieces;
+//   warp 1       of the first CTA: issues the MMAs of the pair (256 x 256 x 16);
 //   warps 4..11  round the sums to BF16 and store them, two warps 32 positions: key
 //                channels, or value channels.  The rotated key, which all heads share,
 //                is loaded once and stored from shared memory for every head.
@@ -27,10 +32,9 @@ namespace {
 constexpr int LE_THREADS = 384;
 constexpr int LE_LOAD = 0, LE_MMA = 1, LE_OUT0 = 4;  // first warps
 constexpr int LE_BOX = 16384;                        // 64 columns of 128 rows
-constexpr int LE_STAGES = 2;                         // pieces of the weights in flight
-constexpr int LE_PIECE = 2 * LE_BOX;                 // 64 columns of a head's keys and values
+constexpr int LE_STAGES = 4;                         // pieces of the weights in flight
 constexpr int LE_OUT = 2048;  // 32 channels of 32 positions, a warp's way to memory
-constexpr int LE_OFF_W = 8 * LE_BOX, LE_OFF_R = LE_OFF_W + LE_STAGES * LE_PIECE,
+constexpr int LE_OFF_W = 8 * LE_BOX, LE_OFF_R = LE_OFF_W + LE_STAGES * LE_BOX,
               LE_OFF_OUT = LE_OFF_R + LE_BOX, LE_OFF_MISC = LE_OFF_OUT + 8 * LE_OUT;
 
 struct Misc {
@@ -57,18 +61,50 @@ __device__ __forceinline__ bool le_wait(uint64_t *bar, uint32_t parity, volatile
   }
 }
 
+// ---- the pair: addresses of the first CTA's barriers, arrivals there, loads that
+// complete there, commits that arrive at both
+
+__device__ __forceinline__ uint32_t first_cta(const uint64_t *bar) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(tc::smem_u32(bar)));
+  return r;
+}
+__device__ __forceinline__ void arrive_first(const uint64_t *bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(first_cta(bar))
+               : "memory");
+}
+__device__ __forceinline__ void load_pair_3d(void *dst, const void *tmap, int x, int y, int z,
+                                             const uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(first_cta(bar))
+      : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(tc::smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
 // Four MMAs over 64 of K in one statement (an elected lane); acc = 0: the first overwrites.
 __device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "setp.eq.b32 q, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
       "add.u64 x, %1, 2;\n\tadd.u64 y, %2, 2;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, q;\n\t"
       "add.u64 x, %1, 4;\n\tadd.u64 y, %2, 4;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, q;\n\t"
       "add.u64 x, %1, 6;\n\tadd.u64 y, %2, 6;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, q;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
@@ -90,7 +126,7 @@ __device__ __forceinline__ void stores_done() {
 }
 
 __global__ void __launch_bounds__(LE_THREADS, 1)
-    latent_expand_kernel(csa_latent_expand_args a, int heads_per, int parts,
+    latent_expand_kernel(csa_latent_expand_args a, int heads_per,
                          const __grid_constant__ CUtensorMap cmap,
                          const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap,
@@ -108,23 +144,34 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
     return;
   }
   // pages fastest: CTAs that run together read the same weights
-  const long long pages = (long long)a.n_req * a.max_blocks;
-  const int part = (int)(blockIdx.x / pages);
-  const long long u = blockIdx.x - part * pages;
-  const int b = (int)(u / a.max_blocks), page = (int)(u - (long long)b * a.max_blocks);
+  const int rank = blockIdx.x & 1, pairs_req = (a.max_blocks + 1) / 2;
+  const long long pairs = (long long)a.n_req * pairs_req;
+  const int part = (int)((blockIdx.x >> 1) / pairs);
+  const long long u = (blockIdx.x >> 1) - part * pairs;
+  const int b = (int)(u / pairs_req), page0 = 2 * (int)(u - (long long)b * pairs_req);
   const int h0 = part * heads_per, h1 = min(a.n_heads, h0 + heads_per);
-  // positions [lo, hi) of the page
-  const int base = page * kBlock;
-  const int lo = max((a.first ? max(a.first[b], 0) : 0) - base, 0);
-  const int hi = min(max(a.kv_len[b], 0) - base, kBlock);
-  if (lo >= hi) return;
-  const bool full = lo == 0 && hi == kBlock;
-  const int src = a.block_table[u];
-  const int dst = page < a.out_max_blocks ? a.out_table[(long long)b * a.out_max_blocks + page] : -1;
-  if (src < 0 || src >= a.n_blocks || dst < 0 || dst >= a.n_out_blocks) {
-    if (tid == 0) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
-    return;
+  // positions [lo, hi) of either page, and where they are and go; both CTAs know both
+  int lo[2], hi[2], src[2], dst[2];
+  bool on[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int page = page0 + e;
+    lo[e] = hi[e] = src[e] = dst[e] = 0;
+    on[e] = false;
+    if (page >= a.max_blocks) continue;
+    const int base = page * kBlock;
+    lo[e] = max((a.first ? max(a.first[b], 0) : 0) - base, 0);
+    hi[e] = min(max(a.kv_len[b], 0) - base, kBlock);
+    if (lo[e] >= hi[e]) continue;
+    src[e] = a.block_table[(long long)b * a.max_blocks + page];
+    dst[e] = page < a.out_max_blocks ? a.out_table[(long long)b * a.out_max_blocks + page] : -1;
+    on[e] = src[e] >= 0 && src[e] < a.n_blocks && dst[e] >= 0 && dst[e] < a.n_out_blocks;
+    if (!on[e] && tid == 0) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
   }
+  if (!on[0] && !on[1]) return;
+  const bool mine_on = on[rank];
+  const int my_lo = lo[rank], my_hi = mine_on ? hi[rank] : my_lo, my_src = src[rank], my_dst = dst[rank];
+  const bool full = mine_on && my_lo == 0 && my_hi == kBlock;
   if (tid == 0) {
     tc::mbar_init(&M->r_full, 1);
     for (int i = 0; i < 8; ++i) tc::mbar_init(&M->c_full[i], 1);
@@ -134,15 +181,23 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&M->d_full[i], 1);
-      tc::mbar_init(&M->d_empty[i], 8);
+      tc::mbar_init(&M->d_empty[i], 16);  // eight warps of either CTA
     }
     tc::mbar_init(&M->drained, 1);
     M->abort = 0;
     tc::mbar_fence_init();
   }
-  if (warp == LE_MMA) tc::tmem_alloc(&M->tmem, 512);
+  __syncthreads();
+  if (warp == LE_MMA) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     tc::smem_u32(&M->tmem)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
   tc::tc_fence_before();
   __syncthreads();
+  cluster_sync();  // the other CTA's barriers are there
   tc::tc_fence_after();
   const uint32_t tmem = __reduce_or_sync(0xffffffffu, M->tmem);
   volatile int *abort = &M->abort;
@@ -152,10 +207,9 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      int n_c = 0;
       if (full) {
         tc::mbar_arrive_expect_tx(&M->r_full, LE_BOX);
-        tc::tma_load_3d(sm + LE_OFF_R, &rmap, 0, 0, src, &M->r_full);
+        tc::tma_load_3d(sm + LE_OFF_R, &rmap, 0, 0, my_src, &M->r_full);
       }
       for (int h = h0; h < h1 && ok; ++h)
         for (int c = 0; c < 8; ++c, ++it) {
@@ -163,28 +217,20 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
           ok = le_wait(&M->w_empty[st], ((it / LE_STAGES) & 1) ^ 1, abort, a.status_dev);
           if (!ok) break;
           if (h == h0) {
-            tc::mbar_arrive_expect_tx(&M->c_full[c], LE_BOX);
-            tc::tma_load_3d(sm + c * LE_BOX, &cmap, c * 64, 0, src, &M->c_full[c]);
-            ++n_c;
+            if (rank == 0) tc::mbar_arrive_expect_tx(&M->c_full[c], LE_BOX * (on[0] + on[1]));
+            if (mine_on) load_pair_3d(sm + c * LE_BOX, &cmap, c * 64, 0, my_src, &M->c_full[c]);
           }
-          uint8_t *w = sm + LE_OFF_W + st * LE_PIECE;
-          tc::mbar_arrive_expect_tx(&M->w_full[st], LE_PIECE);
-          tc::tma_load_3d(w, &kmap, c * 64, 0, h, &M->w_full[st]);
-          tc::tma_load_3d(w + LE_BOX, &vmap, c * 64, 0, h, &M->w_full[st]);
+          if (rank == 0) tc::mbar_arrive_expect_tx(&M->w_full[st], 2 * LE_BOX);
+          load_pair_3d(sm + LE_OFF_W + st * LE_BOX, rank ? &vmap : &kmap, c * 64, 0, h, &M->w_full[st]);
         }
       // whatever was asked for has landed before the CTA retires
       if (full) tc::mbar_wait(&M->r_full, 0, 50000000ull);
-      if (!ok) {
-        for (int c = 0; c < n_c; ++c) tc::mbar_wait(&M->c_full[c], 0, 50000000ull);
-        for (uint32_t k = it > LE_STAGES ? it - LE_STAGES : 0; k < it; ++k)
-          tc::mbar_wait(&M->w_full[k % LE_STAGES], (k / LE_STAGES) & 1, 50000000ull);
-      }
     }
     __syncwarp();
   } else if (warp == LE_MMA) {
     // ================================================================ MMA
-    if (tc::elect_one()) {
-      constexpr uint32_t idesc = tc::idesc_bf16_f32(128, 256);
+    if (rank == 0 && tc::elect_one()) {
+      constexpr uint32_t idesc = tc::idesc_bf16_f32(256, 256);
       const uint64_t dc = tc::desc_sw128(tc::smem_u32(sm));
       const uint64_t dw = tc::desc_sw128(tc::smem_u32(sm) + LE_OFF_W);
       uint32_t it = 0;
@@ -198,13 +244,20 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
                le_wait(&M->w_full[st], (it / LE_STAGES) & 1, abort, a.status_dev);
           if (!ok) break;
           tc::tc_fence_after();
-          mma4(tmem + buf * 256, dc + ((c * LE_BOX) >> 4), dw + ((st * LE_PIECE) >> 4), idesc, c > 0);
-          tc::mma_commit(&M->w_empty[st]);
+          mma4(tmem + buf * 256, dc + ((c * LE_BOX) >> 4), dw + ((st * LE_BOX) >> 4), idesc, c > 0);
+          commit_pair(&M->w_empty[st]);
         }
-        if (ok) tc::mma_commit(&M->d_full[buf]);
+        if (ok) commit_pair(&M->d_full[buf]);
       }
-      // every issued MMA has completed before tensor memory is released
-      tc::mma_commit(&M->drained);
+      // What was asked for has landed, and every issued MMA has completed, before the
+      // pair retires.  (Where a wait gave up, loads of the stages may be under way still.)
+      if (!ok)
+        for (int k = 0; k < 2 * LE_STAGES; ++k)
+          tc::mbar_wait(&M->w_full[k % LE_STAGES], (it / LE_STAGES + k / LE_STAGES) & 1, 5000000ull);
+      asm volatile(
+          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+              tc::smem_u32(&M->drained))
+          : "memory");
       tc::mbar_wait(&M->drained, 0, 100000000ull);
     }
     __syncwarp();
@@ -212,10 +265,10 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
     // ================================================================ outputs
     // (a value's half: columns 128 and on of a head's sums)
     const int qd = warp & 3, value = (warp - LE_OUT0) >> 2, j = qd * 32 + lane;
-    const bool mine = j >= lo && j < hi;
+    const bool mine = j >= my_lo && j < my_hi;
     const uint32_t from = tmem + ((uint32_t)(qd * 32) << 16) + value * 128;
-    uint8_t *to = value ? static_cast<uint8_t *>(a.v_pool) + dst * a.v_page_stride + j * a.v_token_stride
-                        : static_cast<uint8_t *>(a.k_pool) + dst * a.k_page_stride + j * a.k_token_stride;
+    uint8_t *to = value ? static_cast<uint8_t *>(a.v_pool) + my_dst * a.v_page_stride + j * a.v_token_stride
+                        : static_cast<uint8_t *>(a.k_pool) + my_dst * a.k_page_stride + j * a.k_token_stride;
     const long long hs = value ? a.v_head_stride : a.k_head_stride;
     // A page that is written whole goes through shared memory, 32 channels of a warp's 32
     // positions at a time (16-byte chunk c of row j at c ^ (j / 2) % 4), and by TMA; the
@@ -227,7 +280,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         r[i] = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.r_pool) +
-                                               src * a.r_page_stride + j * a.r_token_stride)[i];
+                                               my_src * a.r_page_stride + j * a.r_token_stride)[i];
     bool ok = !rotated || __all_sync(0xffffffffu, le_wait(&M->r_full, 0, abort, a.status_dev));
     for (int h = h0; h < h1 && ok; ++h) {
       const int n = h - h0, buf = n & 1;
@@ -235,7 +288,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
       if (!ok) break;
       tc::tc_fence_after();
       uint4 *out = reinterpret_cast<uint4 *>(to + h * hs);
-      if (rotated && lane == 0) store_4d(&kr_out, kNope, h, 0, dst, sm + LE_OFF_R);
+      if (rotated && lane == 0) store_4d(&kr_out, kNope, h, 0, my_dst, sm + LE_OFF_R);
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         float x[32];
@@ -254,7 +307,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
             reinterpret_cast<uint4 *>(box + lane * 64)[i ^ ((lane >> 1) & 3)] = y[i];
           tc::fence_async_shared();
           __syncwarp();
-          if (lane == 0) store_4d(value ? &v_out : &k_out, c, h, qd * 32, dst, box);
+          if (lane == 0) store_4d(value ? &v_out : &k_out, c, h, qd * 32, my_dst, box);
         } else if (mine) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) out[c / 8 + i] = y[i];
@@ -265,15 +318,18 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
         for (int i = 0; i < 8; ++i) out[kNope / 8 + i] = r[i];
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&M->d_empty[buf]);
+      if (lane == 0) arrive_first(&M->d_empty[buf]);
     }
     if (lane == 0) stores_done();
   }
 
   tc::tc_fence_before();
   __syncthreads();
+  cluster_sync();  // neither CTA goes while the other's products or arrivals need it
   tc::tc_fence_after();
-  if (warp == LE_MMA) tc::tmem_dealloc(tmem, 512);
+  if (warp == LE_MMA)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
 }
 
 int sm_count() {
@@ -349,20 +405,20 @@ cudaError_t launch_latent_expand(const csa_latent_expand_args &a, cudaStream_t s
   }
   // Parts of the heads: as many as make waves x (heads of a part + 1) smallest, a CTA's
   // start and end being worth about one head.
-  const int sms = sm_count();
-  const long long n_pages = (long long)a.n_req * a.max_blocks;
+  const int places = sm_count() / 2;
+  const long long n_pairs = (long long)a.n_req * ((a.max_blocks + 1) / 2);
   int per = a.n_heads, parts = 1;
   long long best = 0;
   for (int p = 1; p <= a.n_heads && p <= 128; ++p) {
     const long long k = (a.n_heads + p - 1) / p, n = (a.n_heads + k - 1) / k;
-    const long long cost = (n_pages * n + sms - 1) / sms * (k + 1);
+    const long long cost = (n_pairs * n + places - 1) / places * (k + 1);
     if (p == 1 || cost < best) best = cost, per = (int)k, parts = (int)n;
   }
-  if (n_pages * parts > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  if (2 * n_pairs * parts > 0x7FFFFFFF) return cudaErrorInvalidValue;
   launch_begin(CSA_K_LATENT_EXPAND, s);
   const cudaError_t e =
-      launch_kernel(latent_expand_kernel, dim3((unsigned)(n_pages * parts)), dim3(LE_THREADS), smem, s,
-                    0, false, a, per, parts, cmap, kmap, vmap, rmap, k_out, kr_out, v_out);
+      launch_kernel(latent_expand_kernel, dim3((unsigned)(2 * n_pairs * parts)), dim3(LE_THREADS), smem,
+                    s, 2, false, a, per, cmap, kmap, vmap, rmap, k_out, kr_out, v_out);
   launch_end(CSA_K_LATENT_EXPAND, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
