@@ -74,11 +74,11 @@ __device__ __forceinline__ void arrive_first(const uint64_t *bar) {
                : "memory");
 }
 __device__ __forceinline__ void load_pair_3d(void *dst, const void *tmap, int x, int y, int z,
-                                             const uint64_t *bar) {
+                                             const uint64_t *bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(first_cta(bar))
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(first_cta(bar)), "l"(policy)
       : "memory");
 }
 __device__ __forceinline__ void commit_pair(uint64_t *bar) {
@@ -110,16 +110,13 @@ __device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_
 }
 
 // A box of shared memory into a pool [channels, heads, 128, pages], as a bulk group; until
-// the groups of this thread have been read, or are complete.
+// the groups of this thread are complete.
 __device__ __forceinline__ void store_4d(const void *tmap, int x, int y, int z, int w, const void *src) {
   asm volatile(
       "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n\t"
       "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(tmap)),
       "r"(x), "r"(y), "r"(z), "r"(w), "r"(tc::smem_u32(src))
       : "memory");
-}
-__device__ __forceinline__ void stores_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 __device__ __forceinline__ void stores_done() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -131,9 +128,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
                          const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ CUtensorMap rmap,
-                         const __grid_constant__ CUtensorMap k_out,
-                         const __grid_constant__ CUtensorMap kr_out,
-                         const __grid_constant__ CUtensorMap v_out) {
+                         const __grid_constant__ CUtensorMap kr_out) {
   extern __shared__ __align__(1024) uint8_t sm[];
   Misc *M = reinterpret_cast<Misc *>(sm + LE_OFF_MISC);
   tc::griddep_wait();
@@ -205,6 +200,8 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
   if (warp == LE_LOAD) {
     // ================================================================ loads
     if (lane == 0) {
+      // (weights and latents are read again, what is written is not)
+      const uint64_t keep = tc::l2_evict_last();
       uint32_t it = 0;
       bool ok = true;
       if (full) {
@@ -218,10 +215,11 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
           if (!ok) break;
           if (h == h0) {
             if (rank == 0) tc::mbar_arrive_expect_tx(&M->c_full[c], LE_BOX * (on[0] + on[1]));
-            if (mine_on) load_pair_3d(sm + c * LE_BOX, &cmap, c * 64, 0, my_src, &M->c_full[c]);
+            if (mine_on) load_pair_3d(sm + c * LE_BOX, &cmap, c * 64, 0, my_src, &M->c_full[c], keep);
           }
           if (rank == 0) tc::mbar_arrive_expect_tx(&M->w_full[st], 2 * LE_BOX);
-          load_pair_3d(sm + LE_OFF_W + st * LE_BOX, rank ? &vmap : &kmap, c * 64, 0, h, &M->w_full[st]);
+          load_pair_3d(sm + LE_OFF_W + st * LE_BOX, rank ? &vmap : &kmap, c * 64, 0, h, &M->w_full[st],
+                       keep);
         }
       // whatever was asked for has landed before the CTA retires
       if (full) tc::mbar_wait(&M->r_full, 0, 50000000ull);
@@ -267,13 +265,16 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
     const int qd = warp & 3, value = (warp - LE_OUT0) >> 2, j = qd * 32 + lane;
     const bool mine = j >= my_lo && j < my_hi;
     const uint32_t from = tmem + ((uint32_t)(qd * 32) << 16) + value * 128;
-    uint8_t *to = value ? static_cast<uint8_t *>(a.v_pool) + my_dst * a.v_page_stride + j * a.v_token_stride
-                        : static_cast<uint8_t *>(a.k_pool) + my_dst * a.k_page_stride + j * a.k_token_stride;
+    const long long ts = value ? a.v_token_stride : a.k_token_stride;
+    uint8_t *to = value ? static_cast<uint8_t *>(a.v_pool) + my_dst * a.v_page_stride
+                        : static_cast<uint8_t *>(a.k_pool) + my_dst * a.k_page_stride;
     const long long hs = value ? a.v_head_stride : a.k_head_stride;
-    // A page that is written whole goes through shared memory, 32 channels of a warp's 32
-    // positions at a time (16-byte chunk c of row j at c ^ (j / 2) % 4), and by TMA; the
-    // rotated key straight from where it was loaded.  Else every thread stores its row.
-    uint8_t *box = sm + LE_OFF_OUT + (warp - LE_OUT0) * LE_OUT;
+    // 32 channels at a time a warp turns its 32 positions through shared memory (16-byte
+    // chunk c of row j at c ^ (j / 2) % 4), so that four lanes store 64 bytes of a row
+    // (by TMA instead, a store's buffer was free again after 1,500 cycles, behind the
+    // loads: 7,000 a head).  The rotated key of a page that is written whole goes by TMA,
+    // straight from where it was loaded, else from registers.
+    uint4 *box = reinterpret_cast<uint4 *>(sm + LE_OFF_OUT + (warp - LE_OUT0) * LE_OUT);
     const bool rotated = full && warp == LE_OUT0;
     uint4 r[8];
     if (!full && !value && mine)
@@ -287,40 +288,36 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
       ok = __all_sync(0xffffffffu, le_wait(&M->d_full[buf], (n >> 1) & 1, abort, a.status_dev));
       if (!ok) break;
       tc::tc_fence_after();
-      uint4 *out = reinterpret_cast<uint4 *>(to + h * hs);
+      uint8_t *out = to + h * hs;
       if (rotated && lane == 0) store_4d(&kr_out, kNope, h, 0, my_dst, sm + LE_OFF_R);
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         float x[32];
         tc::tmem_ld32(from + buf * 256 + c, x);
-        uint4 y[4];
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          y[i] = make_uint4(attn::pack2(x[8 * i], x[8 * i + 1]), attn::pack2(x[8 * i + 2], x[8 * i + 3]),
-                            attn::pack2(x[8 * i + 4], x[8 * i + 5]),
-                            attn::pack2(x[8 * i + 6], x[8 * i + 7]));
-        if (full) {
-          if (lane == 0) stores_read();
-          __syncwarp();
+          box[lane * 4 + (i ^ ((lane >> 1) & 3))] =
+              make_uint4(attn::pack2(x[8 * i], x[8 * i + 1]), attn::pack2(x[8 * i + 2], x[8 * i + 3]),
+                         attn::pack2(x[8 * i + 4], x[8 * i + 5]),
+                         attn::pack2(x[8 * i + 6], x[8 * i + 7]));
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4 *>(box + lane * 64)[i ^ ((lane >> 1) & 3)] = y[i];
-          tc::fence_async_shared();
-          __syncwarp();
-          if (lane == 0) store_4d(value ? &v_out : &k_out, c, h, qd * 32, my_dst, box);
-        } else if (mine) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) out[c / 8 + i] = y[i];
+        for (int i = 0; i < 4; ++i) {
+          const int row = i * 8 + (lane >> 2), q = lane & 3, at = qd * 32 + row;
+          const uint4 y = box[row * 4 + (q ^ ((row >> 1) & 3))];
+          if (at >= my_lo && at < my_hi)
+            reinterpret_cast<uint4 *>(out + at * ts)[c / 8 + q] = y;
         }
       }
       if (!full && !value && mine)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[kNope / 8 + i] = r[i];
+        for (int i = 0; i < 8; ++i) reinterpret_cast<uint4 *>(out + j * ts)[kNope / 8 + i] = r[i];
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_first(&M->d_empty[buf]);
     }
-    if (lane == 0) stores_done();
+    if (rotated && lane == 0) stores_done();
   }
 
   tc::tc_fence_before();
@@ -354,8 +351,7 @@ bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims
   const cuuint32_t ones[4] = {1, 1, 1, 1};
   memset(map, 0, sizeof(*map));
   return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides,
-                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -368,30 +364,21 @@ bool encode_in(CUtensorMap *map, const void *base, cuuint64_t x, cuuint64_t y, c
   return encode(map, base, 3, dims, strides, box);
 }
 
-// A pool [pages, 128, heads, channels], boxes of `w` channels and `rows` positions of a head.
-bool encode_out(CUtensorMap *map, void *base, int channels, int heads, int pages, int64_t head,
-                int64_t token, int64_t page, int w, int rows) {
-  const cuuint64_t dims[4] = {(cuuint64_t)channels, (cuuint64_t)heads, kBlock, (cuuint64_t)pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)head, (cuuint64_t)token, (cuuint64_t)page};
-  const cuuint32_t box[4] = {(cuuint32_t)w, 1, (cuuint32_t)rows, 1};
-  return encode(map, base, 4, dims, strides, box);
-}
-
 }  // namespace
 
 cudaError_t launch_latent_expand(const csa_latent_expand_args &a, cudaStream_t s) {
-  CUtensorMap cmap, kmap, vmap, rmap, k_out, kr_out, v_out;
+  CUtensorMap cmap, kmap, vmap, rmap, kr_out;
   const cuuint64_t pages = a.n_blocks, heads = a.n_heads;
+  // the rotated keys' place in a page of one head of k_pool
+  const cuuint64_t out_dims[4] = {kNope + kRopeDim, heads, kBlock, (cuuint64_t)a.n_out_blocks};
+  const cuuint64_t out_strides[3] = {(cuuint64_t)a.k_head_stride, (cuuint64_t)a.k_token_stride,
+                                     (cuuint64_t)a.k_page_stride};
+  const cuuint32_t out_box[4] = {kRopeDim, 1, kBlock, 1};
   if (!encode_in(&cmap, a.c_pool, kLatent, kBlock, pages, a.c_token_stride, a.c_page_stride) ||
       !encode_in(&kmap, a.w_uk, kLatent, kNope, heads, kLatent * 2, a.w_uk_head_stride) ||
       !encode_in(&vmap, a.w_uv, kLatent, kValue, heads, kLatent * 2, a.w_uv_head_stride) ||
       !encode_in(&rmap, a.r_pool, kRopeDim, kBlock, pages, a.r_token_stride, a.r_page_stride) ||
-      !encode_out(&k_out, a.k_pool, kNope + kRopeDim, a.n_heads, a.n_out_blocks, a.k_head_stride,
-                  a.k_token_stride, a.k_page_stride, 32, 32) ||
-      !encode_out(&kr_out, a.k_pool, kNope + kRopeDim, a.n_heads, a.n_out_blocks, a.k_head_stride,
-                  a.k_token_stride, a.k_page_stride, 64, 128) ||
-      !encode_out(&v_out, a.v_pool, kValue, a.n_heads, a.n_out_blocks, a.v_head_stride,
-                  a.v_token_stride, a.v_page_stride, 32, 32))
+      !encode(&kr_out, a.k_pool, 4, out_dims, out_strides, out_box))
     return cudaErrorInvalidValue;
   const size_t smem = LE_OFF_MISC + sizeof(Misc);
   int dev = 0;
@@ -418,7 +405,7 @@ cudaError_t launch_latent_expand(const csa_latent_expand_args &a, cudaStream_t s
   launch_begin(CSA_K_LATENT_EXPAND, s);
   const cudaError_t e =
       launch_kernel(latent_expand_kernel, dim3((unsigned)(2 * n_pairs * parts)), dim3(LE_THREADS), smem,
-                    s, 2, false, a, per, cmap, kmap, vmap, rmap, k_out, kr_out, v_out);
+                    s, 2, false, a, per, cmap, kmap, vmap, rmap, kr_out);
   launch_end(CSA_K_LATENT_EXPAND, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
