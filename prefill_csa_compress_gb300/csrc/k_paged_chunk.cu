@@ -49,6 +49,21 @@
 #include "tc.cuh"
 
 namespace csa {
+
+// CTAs that share a tile's requests where keys and values differ in width (such calls
+// have no kernel for few rows): as many as a tile has runs of one request's rows on
+// average, which the host does not know but by the number of requests; 16 at most.  A
+// CTA without a run costs a microsecond or two, two runs in one twice the time (5
+// requests of up to 511 rows of 20 heads over 2000 positions: 80 us with one CTA a tile).
+static int paged_chunk_runs(const csa_paged_attn_args &a) {
+  if (a.v_dim == a.head_dim || a.n_req <= 1) return 1;
+  const int rows = 2 * (128 / (a.n_heads / a.n_kv_heads));
+  const long long per = ((long long)a.n_rows + a.n_req - 1) / a.n_req;
+  long long runs = per >= rows ? 2 : (rows + per - 1) / (per > 0 ? per : 1) + 1;
+  if (runs > a.n_req) runs = a.n_req;
+  return (int)(runs < 16 ? runs : 16);
+}
+
 namespace {
 
 using paged::Parts;
@@ -112,6 +127,7 @@ struct Misc {
   int abort;
   int n_it;  // pages this CTA works through
   Page page[PC_META];
+  uint32_t own[8];  // SPLIT: the CTA's rows whose run is its own
   float top[2][2][128];  // a pair's largest logit, or sum, of each half
 };
 // All of it but for a few hundred bytes, so nothing is set aside for aligning
@@ -338,6 +354,7 @@ struct ChunkGrid {
   int n_tiles;    // row tiles (of 2 R rows)
   int rows_tile;  // R
   int n_parts;    // parts of a tile's pages
+  int n_runs;     // CTAs that share a tile's requests (SPLIT; else 1)
 };
 
 template <int DK, int D>
@@ -362,7 +379,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
   // see the most) first
   const int kvh = blockIdx.x % a.n_kv_heads;
   const int part = blockIdx.x / a.n_kv_heads % G.n_parts;
-  const int tile = G.n_tiles - 1 - blockIdx.x / a.n_kv_heads / G.n_parts;
+  const int run_part = C::SPLIT ? blockIdx.x / a.n_kv_heads / G.n_parts % G.n_runs : 0;
+  const int tile = G.n_tiles - 1 - blockIdx.x / a.n_kv_heads / G.n_parts / (C::SPLIT ? G.n_runs : 1);
   const int g = a.n_heads / a.n_kv_heads;
   const int t0 = tile * 2 * G.rows_tile;
   const int n_rows = min(2 * G.rows_tile, a.n_rows - t0);
@@ -395,6 +413,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     if (!single) read_rows(a, t0, n_rows, W);
     bool counting = true, many = false, ok = true;
     int total = 0, valid = 0, skip = 0, n_pages = 0, left = 0;
+    int idx = 0;       // of the next run that has a request
+    uint32_t own = 0;  // lane i: the CTA's own among rows 32 i ..
     uint32_t n_k = 0, n_v = 0;  // tiles loaded
     // The next K or V, of page `phys`, once its stages are free; describe() runs in one
     // lane before any of it is handed on.
@@ -444,6 +464,8 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       if (r >= n_rows || (!counting && left == 0)) {
         if (!counting) break;
         counting = false;
+        idx = 0;
+        if (C::SPLIT && lane < 8) M->own[lane] = own;
         skip = (int)((long long)total * part / G.n_parts);
         left = n_pages = (int)((long long)total * (part + 1) / G.n_parts) - skip;
         many = valid > 1;
@@ -456,8 +478,11 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
       r = R.end;
       if (counting && R.req >= a.n_req && lane == 0) flag(a.status_dev, CSA_DEV_BAD_POS);
       if (R.req < 0 || R.req >= a.n_req) continue;
+      // (the CTAs of a tile take its runs in turn)
+      if (C::SPLIT && idx++ % G.n_runs != run_part) continue;
       const int np = run_pages(R);
       if (counting) {
+        own |= below(R.end - 32 * lane) & ~below(r0 - 32 * lane);
         total += np;
         ++valid;
         continue;
@@ -660,7 +685,7 @@ __global__ void __launch_bounds__(PC_THREADS, 1)
     int req = -1, lo = 0, hi = 0;
     if (m < G.rows_tile * g && rr < n_rows) {
       req = a.row_req[t];
-      if (req >= a.n_req) req = -1;
+      if (req >= a.n_req || (C::SPLIT && !(M->own[rr >> 5] >> (rr & 31) & 1u))) req = -1;
       if (req >= 0) paged::visible_range(a, a.kv_len[req], a.row_pos[t], lo, hi);
     }
     const float sink = req >= 0 && a.sink ? a.sink[h] : -INFINITY;
@@ -916,6 +941,7 @@ cudaError_t launch(const csa_paged_attn_args &a, const Parts &parts, cudaStream_
   G.rows_tile = 128 / g;
   G.n_tiles = (a.n_rows + 2 * G.rows_tile - 1) / (2 * G.rows_tile);
   G.n_parts = parts.n;
+  G.n_runs = paged_chunk_runs(a);
   CUtensorMap qmap, kmap, vmap;
   if (!paged::encode_q(a, G.rows_tile, &qmap) || !paged::encode_pools(a, &kmap, &vmap))
     return cudaErrorInvalidValue;
@@ -929,7 +955,7 @@ cudaError_t launch(const csa_paged_attn_args &a, const Parts &parts, cudaStream_
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr[dev] = true;
   }
-  const long long grid = (long long)G.n_tiles * a.n_kv_heads * G.n_parts;
+  const long long grid = (long long)G.n_tiles * a.n_kv_heads * G.n_parts * G.n_runs;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   launch_begin(CSA_K_PAGED_ATTN, s);
   const cudaError_t e = launch_kernel(paged_chunk_kernel<DK, D>, dim3((unsigned)grid),
@@ -948,7 +974,8 @@ cudaError_t launch(const csa_paged_attn_args &a, const Parts &parts, cudaStream_
 // 64 parts 22, 17, 16, 19 us.  The rule takes 3, 19 and 32.)
 int paged_chunk_parts(const csa_paged_attn_args &a, int sms) {
   const int rows = 2 * (128 / (a.n_heads / a.n_kv_heads));
-  const long long items = (long long)((a.n_rows + rows - 1) / rows) * a.n_kv_heads;
+  const int shared = paged_chunk_runs(a);
+  const long long items = (long long)((a.n_rows + rows - 1) / rows) * a.n_kv_heads * shared;
   long long pages = a.max_blocks;
   if (a.window > 0) {
     const long long seen = ((long long)a.window + rows + kBlock - 1) / kBlock + 1;
@@ -957,7 +984,7 @@ int paged_chunk_parts(const csa_paged_attn_args &a, int sms) {
   // the requests that a CTA's rows may belong to, each with pages of its own
   const long long per = ((long long)a.n_rows + a.n_req - 1) / a.n_req;
   const long long runs = per >= rows ? 1 : (rows + per - 1) / (per > 0 ? per : 1);
-  pages *= runs < a.n_req ? runs : a.n_req;
+  pages *= ((runs < a.n_req ? runs : a.n_req) + shared - 1) / shared;
   int best = 1;
   double cost = 1e30;
   for (int p = 1; p <= 64 && p <= pages; ++p) {
