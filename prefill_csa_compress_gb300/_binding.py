@@ -27,6 +27,8 @@ KERNEL_IDS = {
     "compress_gate": 0, "compress_pool": 1, "compress_fused": 2, "index_score": 3,
     "index_topk": 4, "attn_decode": 5, "attn_prefill": 6, "dequant": 7,
     "rope_table": 8, "norm_rope": 9, "kv_append": 10, "paged_attn": 11, "paged_merge": 12,
+    "latent_attn": 13, "latent_join": 14, "latent_expand": 15, "attn_mass": 16, "mass_join": 17,
+    "evict_plan": 18, "evict_move": 19,
 }
 
 
