@@ -17,11 +17,14 @@
 //
 // Roles: warp 0 loads (TMA, nine boxes of 64 channels a tile, pairs with a barrier of their
 // own, two tiles in flight; boxes are asked for again as soon as their last product is
-// done); warp 1 issues the logits, warp 2 the products; warps 4 .. 11 do the softmax, two warps 16 pairs, and the outputs.
+// done); warp 1 issues the logits, warp 2 the products; warp 3 looks up what the rows of
+// the next item see; warps 4 .. 11 do the softmax, two warps 16 pairs, and the outputs.
 //
-// Calls of up to 512 rows: all tiles of all items are one list, cut into equal shares,
-// one per SM, so that ragged contexts load every SM alike; a cut item leaves parts that
-// latent_join_kernel puts together in order.  More rows: a CTA takes R rows whole.
+// Calls of up to 16 items an SM (and 4096 rows): all tiles of all items are one list, cut
+// into equal shares, one per SM, so that ragged contexts load every SM alike; a cut item
+// leaves parts that latent_join_kernel puts together in order.  More: a CTA takes R rows
+// whole.  (993 rows of 32 heads over windows of 4096, 3.3 items an SM, take 350 us in
+// either way.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -41,7 +44,7 @@ constexpr int LA_PAIRS = 64, LA_KEYS = 64;
 constexpr int LA_BOXES = 9;                   // of 64 channels; the last is the rotated key
 constexpr int LA_BOX = LA_KEYS * 128;         // bytes (of 64 pairs or 64 positions)
 constexpr int LA_TILE = LA_BOXES * LA_BOX;
-constexpr int LA_ROWS = 512;                  // of a call whose tiles are cut into shares
+constexpr int LA_ROWS = 4096;                 // of a call whose tiles are cut into shares
 constexpr int OFF_KV = LA_TILE, OFF_MISC = OFF_KV + 2 * LA_TILE;
 constexpr int BAR_SOFT = 1;                   // named barrier of the softmax warps
 constexpr int O_COL = 0, S_COL = 256;         // tensor memory
@@ -55,11 +58,11 @@ struct Seg {
   int tile, n;  // first tile (of 64 positions) and how many
   int slot;     // where its part goes, -1: the item is whole
 };
-constexpr int LA_AHEAD = 4;  // tiles that L2 is asked for before they are loaded
+constexpr int LA_AHEAD = 3;  // tiles that L2 is asked for before they are loaded
 constexpr int LA_NEAR = 64;  // segments kept in shared memory; the rest in the workspace
 
 struct Misc {
-  uint64_t q_full, q_empty, pv_done, p_full, o_free, drained[2], s_full[2];
+  uint64_t q_full, q_empty, pv_done, p_full, o_free, drained[2], s_full[2], info[2], info_free[2];
   uint64_t full[2][4], empty[2][4];  // pairs of boxes of a tile; the rotated keys with the last
   uint32_t tmem;
   int abort;
@@ -67,8 +70,11 @@ struct Misc {
   int there[2];                // the tile's page is in the pool
   uint32_t bad[2];             // positions of a tile with values that are not finite
   Seg near_[LA_NEAR];
-  float top[2][LA_PAIRS], f[LA_PAIRS];
-  uint32_t row[LA_PAIRS];      // a pair's (row, head) in lse, kNone: it has none
+  int2 see[2][LA_PAIRS];       // what a pair sees (segments in turn)
+  int4 all[2];                 // positions that all rows see [x, y), that some do [z, w)
+  float top[2][LA_PAIRS];
+  alignas(8) float f[LA_PAIRS];  // (read two at a time)
+  uint32_t row[2][LA_PAIRS];   // a pair's (row, head) in lse, kNone: it has none
 };
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 static_assert(OFF_MISC + sizeof(Misc) <= 227 * 1024, "shared memory");
@@ -150,18 +156,39 @@ __device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_
       : "memory");
 }
 
+// 16 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&x)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
+
 // The CTA's rows while its segments are found, where the tiles land afterwards.
 struct Plan {
   long long *before;  // tiles of all items of earlier rows
   int *req, *lo, *hi, *tiles, *first, *nr;
   uint32_t *starts;   // a bit a row that differs from the one before it in its request
+  int *run;           // a word of these: the row that starts the run its first row is in
   __device__ Plan(uint8_t *at, int n) {
     before = reinterpret_cast<long long *>(at);
     req = reinterpret_cast<int *>(before + n + 1);
     lo = req + n, hi = lo + n, tiles = hi + n, first = tiles + n, nr = first + n;
     starts = reinterpret_cast<uint32_t *>(nr + n);
+    run = reinterpret_cast<int *>(starts + (n + 31) / 32);
   }
+  static constexpr int bytes(int n) { return 8 * (n + 1) + 24 * n + (n + 31) / 32 * 8; }
 };
+
+static_assert(Plan::bytes(LA_ROWS) <= 2 * LA_TILE, "the list of rows");
 
 __global__ void __launch_bounds__(LA_THREADS, 1)
     latent_attn_kernel(csa_latent_attn_args a, Parts parts, Shape H,
@@ -215,6 +242,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       tc::mbar_init(&M->o_free, 8);
       for (int i = 0; i < 2; ++i) {
         tc::mbar_init(&M->drained[i], 1);
+        tc::mbar_init(&M->info[i], 1);
+        tc::mbar_init(&M->info_free[i], 8);
         tc::mbar_init(&M->s_full[i], 2);
         for (int c = 0; c < 4; ++c) tc::mbar_init(&M->full[i][c], 1);
         for (int c = 0; c < 4; ++c) tc::mbar_init(&M->empty[i][c], 1);
@@ -224,12 +253,29 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       tc::mbar_fence_init();
     }
     __syncthreads();
+    if (n > 32) {
+      if (warp == 0) {
+        int last = 0;
+        for (int w0 = 0; w0 * 32 < n; w0 += 32) {
+          const int w = w0 + lane;
+          const uint32_t bits = w * 32 < n ? plan.starts[w] : 0;
+          int x = bits ? w * 32 + 31 - __clz(bits) : -1;  // the word's last start
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x = max(x, y);
+          }
+          const int before = __shfl_up_sync(0xffffffffu, x, 1);
+          if (w * 32 < n) plan.run[w] = max(last, lane ? before : -1);
+          last = max(last, __shfl_sync(0xffffffffu, x, 31));
+        }
+      }
+      __syncthreads();
+    }
     for (int r = tid; r < n; r += LA_THREADS) {
       const int b = plan.req[r];
-      int w = r >> 5;
-      uint32_t bits = plan.starts[w] & (0xffffffffu >> (31 - (r & 31)));
-      while (bits == 0) bits = plan.starts[--w];  // (row 0 starts a run)
-      const int run = w * 32 + 31 - __clz(bits);
+      const uint32_t bits = plan.starts[r >> 5] & (0xffffffffu >> (31 - (r & 31)));
+      const int run = bits ? (r & ~31) + 31 - __clz(bits) : plan.run[r >> 5];
       int tiles = 0, first = 0, k = 0;
       if (b >= 0 && (r - run) % H.R == 0) {
         int lo = 0x7FFFFFFF, hi = 0;
@@ -452,6 +498,54 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       tc::mbar_wait(&M->drained[1], 0, 100000000ull);
     }
     __syncwarp();
+  } else if (warp == LA_MMA + 2) {
+    // ================================================================ what the rows see
+    // (a segment ahead: the softmax would wait for memory twice at every item's start)
+    for (int s = 0; s < n_seg; ++s) {
+      const Seg g = seg_at(s);
+      const int len = a.kv_len[g.req];
+      int pos[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) pos[e] = 32 * e + lane < g.nr ? a.row_pos[g.t + 32 * e + lane] : 0;
+      // (the tables of the segment before the last: its outputs are written)
+      if (!__all_sync(0xffffffffu, la_wait(&M->info_free[s & 1], ((s >> 1) & 1) ^ 1, abort,
+                                           a.status_dev)))
+        break;
+      int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = 0;
+      int2 see[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        int lo, hi;
+        paged::visible_range(a, len, pos[e], lo, hi);
+        if (32 * e + lane < g.nr) {
+          if (lo < hi) {
+            all_lo = max(all_lo, lo), all_hi = min(all_hi, hi);
+            any_lo = min(any_lo, lo), any_hi = max(any_hi, hi);
+          } else {
+            all_hi = 0;  // a row that sees nothing
+          }
+        }
+        see[e] = make_int2(lo, hi);
+      }
+      all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+      all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+      any_lo = __reduce_min_sync(0xffffffffu, any_lo);
+      any_hi = __reduce_max_sync(0xffffffffu, any_hi);
+      if (lane == 0) M->all[s & 1] = make_int4(all_lo, all_hi, any_lo, any_hi);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // pair m is row m / gt (a lane's register) and head m % gt
+        const int m = 32 * e + lane, r = m / H.gt, h = g.sub * H.gt + m % H.gt;
+        int2 x, y;
+        x.x = __shfl_sync(0xffffffffu, see[0].x, r & 31), x.y = __shfl_sync(0xffffffffu, see[0].y, r & 31);
+        y.x = __shfl_sync(0xffffffffu, see[1].x, r & 31), y.y = __shfl_sync(0xffffffffu, see[1].y, r & 31);
+        const bool in = r < g.nr && h < a.n_heads;
+        M->see[s & 1][m] = in ? (r < 32 ? x : y) : make_int2(0, 0);
+        M->row[s & 1][m] = in ? (uint32_t)(g.t + r) * a.n_heads + h : kNone;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&M->info[s & 1]);
+    }
   } else if (warp >= LA_SOFT0) {
     // ================================================================ softmax and outputs
     const int qd = warp & 3, half = (warp - LA_SOFT0) >> 2;
@@ -466,30 +560,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     bool ok = true, given_up = false;
     for (int s = 0; s < n_seg && !given_up; ++s) {
       const Seg g = seg_at(s);
-      const int len = a.kv_len[g.req];
-      // what the item's rows see: all of them, and this thread's two
-      int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = 0;
-      int lo[2] = {0, 0}, hi[2] = {0, 0};
-      if (tid < LA_SOFT0 * 32 + LA_PAIRS) {
-        const int m = tid - LA_SOFT0 * 32, r = m / H.gt, h = g.sub * H.gt + m % H.gt;
-        M->row[m] = r < g.nr && h < a.n_heads ? (uint32_t)(g.t + r) * a.n_heads + h : kNone;
-      }
-      const int my_r[2] = {ma / H.gt, (ma + 8) / H.gt};
-      const bool my[2] = {g.sub * H.gt + ma % H.gt < a.n_heads,
-                          g.sub * H.gt + (ma + 8) % H.gt < a.n_heads};
-      for (int r = 0; r < g.nr; ++r) {
-        int l, h;
-        paged::visible_range(a, len, a.row_pos[g.t + r], l, h);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (my_r[e] == r && my[e]) lo[e] = l, hi[e] = h;
-        if (l >= h) {
-          all_hi = 0;
-          continue;
-        }
-        all_lo = max(all_lo, l), all_hi = min(all_hi, h);
-        any_lo = min(any_lo, l), any_hi = max(any_hi, h);
-      }
+      // what the item's rows see: all of them, some, and this thread's two
+      ok = wait(&M->info[s & 1], s >> 1) && ok;
+      const int4 all = M->all[s & 1];
+      const int all_lo = all.x, all_hi = all.y, any_lo = all.z, any_hi = all.w;
+      const int2 see[2] = {M->see[s & 1][ma], M->see[s & 1][ma + 8]};
+      const int lo[2] = {see[0].x, see[1].x}, hi[2] = {see[0].y, see[1].y};
       float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       // bits of a P of 2 or more, of rows that see something
       const uint32_t big[2] = {hi[0] > lo[0] ? 0x40004000u : 0u, hi[1] > lo[1] ? 0x40004000u : 0u};
@@ -582,30 +658,38 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         if (mixed) {
           // Positions that not every row sees: latents that are not finite become zero
           // (zero times them is not zero), and rows that see them NaN.
-          uint8_t *kv = sm + OFF_KV + st * LA_TILE;
-          const int key = (tid - LA_SOFT0 * 32) >> 2, j = base + key;
-          if (!there || j < all_lo || j >= all_hi) {
-            bool zero = !there || j < any_lo || j >= any_hi, bad = false;
-            uint4 *row = reinterpret_cast<uint4 *>(kv + key * 128 + 2 * (lane & 3) * LA_BOX);
-            if (!zero) {
+          // Four positions of a warp at a time, eight lanes a row of a box.
+#pragma unroll 1
+          for (int key4 = 4 * (warp - LA_SOFT0); key4 < LA_KEYS; key4 += 32) {
+            const int key = key4 + (lane >> 3), j = base + key;
+            const bool part = !there || j < all_lo || j >= all_hi;
+            if (!__any_sync(0xffffffffu, part)) continue;
+            bool zero = part && (!there || j < any_lo || j >= any_hi);
+            const bool look = part && !zero;
+            uint4 *row = reinterpret_cast<uint4 *>(sm + OFF_KV + st * LA_TILE + key * 128) + (lane & 7);
+            if (__any_sync(0xffffffffu, look)) {
               uint32_t odd = 0;
-#pragma unroll
-              for (int u = 0; u < 16; ++u) {
-                const uint4 v = row[(u >> 3) * (LA_BOX / 16) + ((u + key) & 7)];
+#pragma unroll 4
+              for (int u = 0; u < 8; ++u) {
+                const uint4 v = row[u * (LA_BOX / 16)];
                 odd |= paged::not_finite2(v.x) | paged::not_finite2(v.y) | paged::not_finite2(v.z) |
                        paged::not_finite2(v.w);
               }
-              zero = bad = odd != 0;
+#pragma unroll
+              for (int o = 1; o < 8; o <<= 1) odd |= __shfl_xor_sync(0xffffffffu, odd, o);
+              if (look && odd) {
+                zero = true;
+                if ((lane & 7) == 0) atomicOr(&M->bad[key >> 5], 1u << (key & 31));
+              }
             }
             if (zero)
-#pragma unroll
-              for (int u = 0; u < 16; ++u)
-                row[(u >> 3) * (LA_BOX / 16) + ((u + key) & 7)] = make_uint4(0, 0, 0, 0);
-            if (bad) atomicOr(&M->bad[key >> 5], 1u << (key & 31));
+#pragma unroll 4
+              for (int u = 0; u < 8; ++u) row[u * (LA_BOX / 16)] = make_uint4(0, 0, 0, 0);
           }
           tc::bar_sync(BAR_SOFT, 256);
           const uint32_t bad[2] = {M->bad[0], M->bad[1]};
           if (bad[0] | bad[1]) {
+#pragma unroll 1
             for (int k = 0; k < LA_KEYS; ++k)
               if (bad[k >> 5] >> (k & 31) & 1u)
 #pragma unroll
@@ -648,7 +732,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
           const int m = ma + 8 * e;
           const float sum = M->top[0][m] + M->top[1][m];
           float f = 0.f;
-          const uint32_t row = M->row[m];
+          const uint32_t row = M->row[s & 1][m];
           if (row != kNone) {
             const int h = g.sub * H.gt + m % H.gt;
             if (g.slot >= 0) {
@@ -667,27 +751,29 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
 #pragma unroll 1
       for (int blk = 2 * half; blk < 2 * half + 2; ++blk) {
         const int d = blk * 128 + 32 * qd + lane;
+        // (16 pairs at a time: more take registers from the tiles' loop, 304 -> 317 us for
+        // 4 x 2 rows of 128 heads at 131,072 positions)
 #pragma unroll 1
-        for (int c = 0; c < H.n16; c += 32) {
-          float o[32];
-          tc::tmem_ld32(tmem + O_COL + blk * 64 + c + lane_off, o);
+        for (int c = 0; c < H.n16; c += 16) {
+          float o[16];
+          tmem_ld16(tmem + O_COL + blk * 64 + c + lane_off, o);
           if (g.slot >= 0) {
             float *to = parts.o + ((long long)g.slot * LA_PAIRS + c) * kLatent + d;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (M->row[c + k] != kNone) to[k * kLatent] = o[k];
+            for (int k = 0; k < 16; ++k)
+              if (M->row[s & 1][c + k] != kNone) to[k * kLatent] = o[k];
           } else {
             // two pairs at a time: even lanes store two channels of the first, odd ones
             // of the second
+            __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.out) + (d & ~1);
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const float f0 = M->f[c + k], f1 = M->f[c + k + 1];  // (0: the row saw nothing)
-              const uint32_t both = attn::pack2(f0 == 0.f ? 0.f : o[k] * f0, f1 == 0.f ? 0.f : o[k + 1] * f1);
+            for (int k = 0; k < 16; k += 2) {
+              const float2 f = *reinterpret_cast<const float2 *>(M->f + c + k);  // (0: saw nothing)
+              const uint32_t both = attn::pack2(f.x == 0.f ? 0.f : o[k] * f.x, f.y == 0.f ? 0.f : o[k + 1] * f.y);
               const uint32_t other = __shfl_xor_sync(0xffffffffu, both, 1);
-              const uint32_t row = M->row[c + k + (lane & 1)];
+              const uint32_t row = M->row[s & 1][c + k + (lane & 1)];
               if (row != kNone)
-                *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                              (long long)row * kLatent + (d & ~1)) =
+                *reinterpret_cast<uint32_t *>(to + (long long)row * kLatent) =
                     lane & 1 ? __byte_perm(other, both, 0x7632) : __byte_perm(both, other, 0x5410);
             }
           }
@@ -695,7 +781,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       }
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&M->o_free);
+      if (lane == 0) {
+        tc::mbar_arrive(&M->o_free);
+        tc::mbar_arrive(&M->info_free[s & 1]);
+      }
       tc::bar_sync(BAR_SOFT, 256);  // (before top and f are written again)
     }
   }
@@ -769,19 +858,19 @@ int sm_count() {
   return sms;
 }
 
+// CTAs of a call whose rows are taken whole.
+long long blocks_of(const csa_latent_attn_args &a, const Shape &H) {
+  return (long long)((a.n_rows + H.R - 1) / H.R) * H.subs;
+}
+
 Shape shape_of(const csa_latent_attn_args &a) {
   Shape H;
   H.gt = a.n_heads < LA_PAIRS ? a.n_heads : LA_PAIRS;
   H.R = LA_PAIRS / H.gt;
   H.subs = (a.n_heads + LA_PAIRS - 1) / LA_PAIRS;
   H.n16 = (H.gt * H.R + 15) / 16 * 16;
-  H.shares = a.n_rows <= LA_ROWS;
+  H.shares = a.n_rows <= LA_ROWS && blocks_of(a, H) <= 16ll * sm_count();
   return H;
-}
-
-// CTAs of a call whose rows are taken whole.
-long long blocks_of(const csa_latent_attn_args &a, const Shape &H) {
-  return (long long)((a.n_rows + H.R - 1) / H.R) * H.subs;
 }
 
 struct Layout {
@@ -796,7 +885,8 @@ Layout layout(const csa_latent_attn_args &a, int sms) {
     L.total = align_up((size_t)blocks_of(a, H) * L.n_far * sizeof(Seg), 256);
     return L;
   }
-  L.n_far = 2 * LA_ROWS;
+  const long long items = (long long)a.n_rows * H.subs;  // (of a CTA, at most)
+  L.n_far = items > LA_NEAR ? (int)items : 0;
   const size_t slots = 2 * (size_t)sms * LA_PAIRS;
   L.ml = align_up(slots * kLatent * sizeof(float), 256);
   L.cut = L.ml + align_up(slots * sizeof(float2), 256);

@@ -41,6 +41,12 @@ def test_latent_attention_single_heads_of_many_requests():
     Latent([(i, n - 1) for i, n in enumerate(lens[:500])], lens[:500], 2, seed=4).check()
 
 
+def test_latent_attention_rows_taken_whole():
+    """More items than are cut into shares, and more rows."""
+    Latent(chunk(0, 5, 2500) + chunk(1, 0, 3), [2505, 3], 33, window=3, seed=8).check()
+    Latent(chunk(0, 5, 4200) + chunk(1, 0, 3), [4205, 3], 2, window=2, seed=9, sink=True).check()
+
+
 def test_latent_attention_rows_in_any_order():
     rows = [(0, 205), (0, 3), (0, 205), (1, 9), (0, 130), (0, 64), (1, 400), (1, 0), (0, 63)]
     Latent(rows, [206, 401], 10, seed=5).check()
