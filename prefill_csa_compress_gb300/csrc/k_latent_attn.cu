@@ -20,11 +20,16 @@
 // done); warp 1 issues the logits, warp 2 the products; warp 3 looks up what the rows of
 // the next item see; warps 4 .. 11 do the softmax, two warps 16 pairs, and the outputs.
 //
-// Calls of up to 16 items an SM (and 4096 rows): all tiles of all items are one list, cut
-// into equal shares, one per SM, so that ragged contexts load every SM alike; a cut item
-// leaves parts that latent_join_kernel puts together in order.  More: a CTA takes R rows
-// whole.  (993 rows of 32 heads over windows of 4096, 3.3 items an SM, take 350 us in
-// either way.)
+// Few items: all tiles of all items are one list, cut into equal shares, one per SM, so
+// that ragged contexts load every SM alike; a cut item leaves parts that
+// latent_join_kernel puts together in order.  Many: a CTA takes R rows whole.
+//
+// What bounds it: a tile takes 2,200 cycles, 1,920 of them the tensor cores' (36 products
+// of 64 x 64 x 16 at 32 cycles, 16 of 128 x 64 x 16 at 48: an SM reads 128 bytes of shared
+// memory a cycle, so that half of their rate is the most with 64 pairs; 128 pairs would
+// fill tensor memory with O alone).  4 x 2 rows of 128 heads at 131,072 positions: 304 us,
+// 0.96 PFLOP/s; 32 rows of 16 heads, contexts to 16,384: 80 us, 4.8 TB/s, 12 of them the
+// start (the list, the first loads) and 8 the join; one row of 128 heads over 1001: 20 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -294,9 +299,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     __syncthreads();
     if (warp == 0) {
       long long sum = 0;
+      int most = 0, items = 0;  // tiles of the longest item; items
       for (int r0 = 0; r0 < n; r0 += 32) {
         const int r = r0 + lane;
-        const long long mine = r < n ? (long long)plan.tiles[r] * subs : 0;
+        const int tiles = r < n ? plan.tiles[r] : 0;
+        const long long mine = (long long)tiles * subs;
+        most = max(most, tiles);
+        items += __popc(__ballot_sync(0xffffffffu, tiles > 0)) * subs;
         long long x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -307,9 +316,15 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         sum += __shfl_sync(0xffffffffu, x, 31);
       }
       if (lane == 0) plan.before[n] = sum;
+      most = __reduce_max_sync(0xffffffffu, most);
       __syncwarp();
       if (lane == 0) {
-        const long long W = sum, N = H.shares ? (W < gridDim.x ? W : gridDim.x) : 1;
+        const long long W = sum;
+        long long N = H.shares ? (W < gridDim.x ? W : gridDim.x) : 1;
+        // Items of one length: whole shares an item, so that the items of one cache (its
+        // rows, its head groups) go over the same tiles at the same time and L2 serves
+        // all but the first, where that leaves at most an eighth of the SMs out.
+        if (items > 0 && W == (long long)items * most && N > items && N % items * 8 <= N) N -= N % items;
         const long long c = H.shares ? blockIdx.x : 0;
         int n_seg = 0;
         int4 cut = make_int4(-1, 0, 0, 0);
@@ -869,7 +884,14 @@ Shape shape_of(const csa_latent_attn_args &a) {
   H.R = LA_PAIRS / H.gt;
   H.subs = (a.n_heads + LA_PAIRS - 1) / LA_PAIRS;
   H.n16 = (H.gt * H.R + 15) / 16 * 16;
-  H.shares = a.n_rows <= LA_ROWS && blocks_of(a, H) <= 16ll * sm_count();
+  // Whole rows where one request's items fill the SMs in their last round too (its rows
+  // then go over the same tiles at the same time: 600 rows of 16 heads over 8000 positions
+  // 147 us, in shares 175), and where there are many items of several (2000 rows of 32
+  // heads, 4 requests over 2000: 160 against 185); else shares (1200 rows of 8 heads, 3
+  // ragged requests to 4000: 80 us against 97).
+  const long long items = blocks_of(a, H), sms = sm_count(), rounds = (items + sms - 1) / sms;
+  const bool filled = a.n_req == 1 && items * 10 >= rounds * sms * 9;
+  H.shares = !filled && (a.n_rows <= 512 || (a.n_rows <= LA_ROWS && items <= 2 * sms));
   return H;
 }
 
