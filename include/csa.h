@@ -783,7 +783,9 @@ CSA_API csa_status_t csa_paged_attn(csa_paged_attn_args *args, csa_stream_t stre
  *  - expanded (csa_latent_expand, then csa_paged_attn with keys of 192 and values
  *    of 128): 640 operations a pair and 131,072 a position and head to expand.
  * The absorbed form is the one for few rows over long caches, the expanded one for
- * prompts.
+ * prompts.  One request, 64 heads over 8192 positions, 1 / 64 / 256 / 1024 / 8192 rows:
+ * absorbed 30 / 92 / 281 / 981 / 4277 us; expanding 120 us, once, and then 61 / 65 / 87 /
+ * 240 / 939 us.
  *
  * The pools are BF16: c_pool [n_blocks, 128, 512], r_pool [n_blocks, 128, 64], with
  * page and token strides in bytes (0: dense; multiples of 16), so one pool of rows of

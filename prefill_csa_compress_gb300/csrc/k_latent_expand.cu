@@ -16,6 +16,9 @@
 //   warps 4..11  round the sums to BF16 and store them, two warps 32 positions: key
 //                channels, or value channels.  The rotated key, which all heads share,
 //                is loaded once and stored from shared memory for every head.
+// A prompt of 8192 and 128 heads: 246 us (1.12 PFLOP/s), 159 without its stores; filling
+// the 671 MB that it writes takes 168, so what is left is how far the two overlap.  2 x 1500
+// positions, 32 heads: 29 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

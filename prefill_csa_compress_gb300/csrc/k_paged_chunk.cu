@@ -3,7 +3,7 @@
 //
 // With the query heads of a group stacked under their row, a tile of R rows x G
 // heads (R G <= 128) reads one key/value head:
-//   S[m, c] = q_m . k_c      (128 x 128 x D, both operands K-major)
+//   S[m, c] = q_m . k_c      (128 x 128 x DK, both operands K-major)
 //   O[m, :] += P[m, c] v_c   (128 x D x 128, P from tensor memory, V MN-major)
 // with P = 2^(S scale log2(e) - ref_m).  A page is exactly one key tile, so a
 // page costs one block-table look-up and D / 64 TMA boxes for K and V each.
@@ -32,6 +32,12 @@
 // Rows of several requests in one CTA take turns: a page of another request is
 // masked for the whole row.
 //
+// Keys of 192 channels with values of 128 (the expanded form of latent attention) take
+// 48 KB a page and 96 KB of queries, so K comes in boxes (Cfg), and the requests of a
+// tile are shared among CTAs (paged_chunk_runs): a prompt of 8192 rows of 64 heads takes
+// 1,052 us (1.31 PFLOP/s; 2,560 cycles of MMAs a page), 5 ragged requests of up to 511 rows of 20
+// heads over 2000 positions 68.
+//
 // What bounds it is the chain of one tile.  D = 128: 2,900 cycles a page for both
 // tiles, where their MMAs take 2,048 -- the softmax of a tile 1,500 (reading the
 // logits 300, the probabilities 700, the barrier 250, storing them 200), its MMAs
@@ -54,7 +60,8 @@ namespace csa {
 // have no kernel for few rows): as many as a tile has runs of one request's rows on
 // average, which the host does not know but by the number of requests; 16 at most.  A
 // CTA without a run costs a microsecond or two, two runs in one twice the time (5
-// requests of up to 511 rows of 20 heads over 2000 positions: 80 us with one CTA a tile).
+// requests of up to 511 rows of 20 heads over 2000 positions: 80 us with one CTA a tile, 68
+// with two).
 static int paged_chunk_runs(const csa_paged_attn_args &a) {
   if (a.v_dim == a.head_dim || a.n_req <= 1) return 1;
   const int rows = 2 * (128 / (a.n_heads / a.n_kv_heads));
