@@ -9,6 +9,15 @@ constexpr int kLatent = CSA_LATENT_DIM;
 constexpr int kNope = CSA_NOPE_DIM;
 constexpr int kValue = CSA_VALUE_DIM;
 
+// SMs of the current device.
+inline int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+    sms = 152;
+  return sms;
+}
+
 // Absorbed latent attention (k_latent_attn.cu).
 size_t latent_attn_workspace(const csa_latent_attn_args &a);
 cudaError_t launch_latent_attn(const csa_latent_attn_args &a, cudaStream_t s);

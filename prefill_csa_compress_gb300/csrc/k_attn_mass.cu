@@ -26,16 +26,10 @@
 // run), with the tensor cores 40 % busy, the exponentials' unit 42 %, issue 55 %.  Set aside:
 // exponentials on the FMA pipe (a quarter of them: 347 us), 16 columns at a time with the
 // next ones on their way (317), three or four groups of warps (312, 483 with spills).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <cstddef>
-#include <cstring>
 
 #include "attn_common.cuh"
-#include "cache_common.cuh"
-#include "paged_common.cuh"
-#include "tc.cuh"
+#include "cache_tiles.cuh"
 
 namespace csa {
 namespace {
@@ -76,39 +70,6 @@ struct Split {
   int k_stages, q_stages;
   int q_bytes;        // of a stage (a whole number of 1024)
 };
-
-__device__ __forceinline__ bool am_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                        uint32_t *status) {
-  if (tc::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = tc::global_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0) {
-      if (*abort) return false;
-      if (tc::global_ns() - t0 > 2000000000ull) {
-        *abort = 1;
-        flag(status, CSA_DEV_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
-
-// Four MMAs over 64 of K in one statement (an elected lane); acc = 0: the first overwrites.
-__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "setp.eq.b32 q, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "add.u64 x, %1, 2;\n\tadd.u64 y, %2, 2;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
-      "add.u64 x, %1, 4;\n\tadd.u64 y, %2, 4;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
-      "add.u64 x, %1, 6;\n\tadd.u64 y, %2, 6;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
 
 // A box of a tensor map into L2.
 __device__ __forceinline__ void prefetch_4d(const void *tmap, int x, int y, int z, int w) {
@@ -273,7 +234,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
         bool p_mixed = false;
         auto publish = [&](bool last) {
           const int st = it % AM_STEPS;
-          ok = __all_sync(0xffffffffu, am_wait(&M->m_empty[st], ((it / AM_STEPS) & 1) ^ 1, abort,
+          ok = __all_sync(0xffffffffu, cache::wait(&M->m_empty[st], ((it / AM_STEPS) & 1) ^ 1, abort,
                                                a.status_dev));
           if (!ok) return;
 #pragma unroll
@@ -326,7 +287,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
       if (page + 1 < page1) phys = table[page + 1];
       if (!ok) break;
       const int st = it % AM_STEPS;  // the page is done
-      ok = __all_sync(0xffffffffu, am_wait(&M->m_empty[st], ((it / AM_STEPS) & 1) ^ 1, abort,
+      ok = __all_sync(0xffffffffu, cache::wait(&M->m_empty[st], ((it / AM_STEPS) & 1) ^ 1, abort,
                                            a.status_dev));
       if (ok && lane == 0) {
         Step &S = M->step[st];
@@ -343,7 +304,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
       bool ok = true;
       for (uint32_t it = 0;; ++it) {
         const int st = it % AM_STEPS;
-        ok = am_wait(&M->m_full[st], (it / AM_STEPS) & 1, abort, a.status_dev);
+        ok = cache::wait(&M->m_full[st], (it / AM_STEPS) & 1, abort, a.status_dev);
         if (!ok) break;
         const Step S = M->step[st];
         tc::mbar_arrive(&M->m_empty[st]);
@@ -353,7 +314,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
         }
         if (S.new_k) {
           const int s = nk % G.k_stages;
-          ok = am_wait(&M->k_empty[s], ((nk / G.k_stages) & 1) ^ 1, abort, a.status_dev);
+          ok = cache::wait(&M->k_empty[s], ((nk / G.k_stages) & 1) ^ 1, abort, a.status_dev);
           if (!ok) break;
           tc::mbar_arrive_expect_tx(&M->k_full[s], K_TILE);
           for (int c = 0; c < BOXES; ++c)
@@ -362,7 +323,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
           ++nk;
         }
         const int s = nq % G.q_stages;
-        ok = am_wait(&M->q_empty[s], ((nq / G.q_stages) & 1) ^ 1, abort, a.status_dev);
+        ok = cache::wait(&M->q_empty[s], ((nq / G.q_stages) & 1) ^ 1, abort, a.status_dev);
         if (!ok) break;
         tc::mbar_arrive_expect_tx(&M->q_full[s], BOXES * 128 * g * G.tr);
         for (int c = 0; c < BOXES; ++c)
@@ -388,12 +349,12 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
       bool ok = true;
       for (uint32_t it = 0;; ++it) {
         const int st = it % AM_STEPS;
-        ok = am_wait(&M->m_full[st], (it / AM_STEPS) & 1, abort, a.status_dev);
+        ok = cache::wait(&M->m_full[st], (it / AM_STEPS) & 1, abort, a.status_dev);
         if (!ok) break;
         const Step S = M->step[st];
         tc::mbar_arrive(&M->m_empty[st]);
         if (S.kvh < 0) {  // (no logits: both arrivals are plain)
-          ok = am_wait(&M->s_empty[it & 1], ((it >> 1) & 1) ^ 1, abort, a.status_dev);
+          ok = cache::wait(&M->s_empty[it & 1], ((it >> 1) & 1) ^ 1, abort, a.status_dev);
           if (!ok) break;
           tc::mbar_arrive(&M->s_full[it & 1]);
           tc::mbar_arrive(&M->s_full[it & 1]);
@@ -401,14 +362,14 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
           continue;
         }
         const int sk = nk % G.k_stages, sq = nq % G.q_stages, buf = it & 1;
-        ok = (!S.new_k || am_wait(&M->k_full[sk], (nk / G.k_stages) & 1, abort, a.status_dev)) &&
-             am_wait(&M->s_empty[buf], ((it >> 1) & 1) ^ 1, abort, a.status_dev) &&
-             am_wait(&M->q_full[sq], (nq / G.q_stages) & 1, abort, a.status_dev);
+        ok = (!S.new_k || cache::wait(&M->k_full[sk], (nk / G.k_stages) & 1, abort, a.status_dev)) &&
+             cache::wait(&M->s_empty[buf], ((it >> 1) & 1) ^ 1, abort, a.status_dev) &&
+             cache::wait(&M->q_full[sq], (nq / G.q_stages) & 1, abort, a.status_dev);
         if (!ok) break;
         tc::tc_fence_after();
 #pragma unroll
         for (int c = 0; c < BOXES; ++c)
-          mma4(tmem + buf * 128, dk + ((sk * K_TILE + c * 16384) >> 4),
+          cache::mma4<2, 2>(tmem + buf * 128, dk + ((sk * K_TILE + c * 16384) >> 4),
                dq + ((sq * G.q_bytes + c * (G.q_bytes / BOXES)) >> 4), idesc, c > 0);
         tc::mma_commit(&M->s_full[buf]);
         tc::mbar_arrive(&M->s_full[buf]);  // hands on the step's description
@@ -433,7 +394,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
     uint32_t outs0 = 0, outs1 = 0;  // pages done, by the step's parity
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t turn) {
-      return (bool)__all_sync(0xffffffffu, am_wait(bar, turn & 1, abort, a.status_dev));
+      return (bool)__all_sync(0xffffffffu, cache::wait(bar, turn & 1, abort, a.status_dev));
     };
     for (uint32_t it = 0;; ++it) {
       const int st = it % AM_STEPS, buf = it & 1;
@@ -526,14 +487,6 @@ __global__ void __launch_bounds__(256)
   reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.mass_out) + b * a.mass_out_row_stride)[j] = sum;
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    sms = 152;
-  return sms;
-}
-
 // Rows of a step: what a request has on average, as far as 128 columns go (the host
 // does not know how rows are spread).  Parts: as many as make four CTAs for each place
 // on the GPU, by key heads first (they share nothing), then by rows.
@@ -565,26 +518,6 @@ Split split_of(const csa_attn_mass_args &a) {
   G.k_stages = (room - G.q_stages * G.q_bytes) / k_tile;
   if (G.k_stages > AM_RING) G.k_stages = AM_RING;
   return G;
-}
-
-bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
-            const cuuint64_t *strides, const cuuint32_t *box) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    cudaDriverEntryPointQueryResult q;
-    void *f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
-  memset(map, 0, sizeof(*map));
-  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims,
-                  strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  dims[0] == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
-                                : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
@@ -629,8 +562,11 @@ cudaError_t launch_attn_mass(const csa_attn_mass_args &a, cudaStream_t s) {
                              (cuuint64_t)a.k_page_stride};
   const cuuint32_t kb[4] = {64, 1, kBlock, 1};
   // (without rows nothing is loaded: any address will do for the queries)
-  if (!encode(&qmap, a.n_rows > 0 ? a.q : a.k_pool, 3, qd, qs, qb) ||
-      !encode(&kmap, a.k_pool, 4, kd, kst, kb))
+  // (heads of 64: the line beside theirs is another head's)
+  const auto l2 = a.head_dim == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                   : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+  if (!cache::encode(&qmap, a.n_rows > 0 ? a.q : a.k_pool, 3, qd, qs, qb, l2) ||
+      !cache::encode(&kmap, a.k_pool, 4, kd, kst, kb, l2))
     return cudaErrorInvalidValue;
   launch_begin(CSA_K_ATTN_MASS, s);
   cudaError_t e = a.head_dim == 64 ? launch<64>(a, parts, G, qmap, kmap, s)

@@ -255,14 +255,6 @@ __global__ void __launch_bounds__(32 * EV_MOVE_WARPS)
   }
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    sms = 152;
-  return sms;
-}
-
 }  // namespace
 
 size_t kv_evict_workspace(const csa_kv_evict_args &a) {

@@ -27,18 +27,11 @@
 // What bounds it: a tile takes 2,200 cycles, 1,920 of them the tensor cores' (36 products
 // of 64 x 64 x 16 at 32 cycles, 16 of 128 x 64 x 16 at 48: an SM reads 128 bytes of shared
 // memory a cycle, so that half of their rate is the most with 64 pairs; 128 pairs would
-// fill tensor memory with O alone).  4 x 2 rows of 128 heads at 131,072 positions: 304 us,
-// 0.96 PFLOP/s; 32 rows of 16 heads, contexts to 16,384: 80 us, 4.8 TB/s, 12 of them the
+// fill tensor memory with O alone).  4 x 2 rows of 128 heads at 131,072 positions: 291 us,
+// 1.00 PFLOP/s; 32 rows of 16 heads, contexts to 16,384: 80 us, 4.8 TB/s, 12 of them the
 // start (the list, the first loads) and 8 the join; one row of 128 heads over 1001: 20 us.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <cstring>
-
 #include "attn_common.cuh"
-#include "cache_common.cuh"
-#include "paged_common.cuh"
-#include "tc.cuh"
+#include "cache_tiles.cuh"
 
 namespace csa {
 namespace {
@@ -98,23 +91,6 @@ struct Shape {
   int shares;       // 1: the list of tiles is cut into shares
 };
 
-__device__ __forceinline__ bool la_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                        uint32_t *status) {
-  if (tc::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = tc::global_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0) {
-      if (*abort) return false;
-      if (tc::global_ns() - t0 > 2000000000ull) {
-        *abort = 1;
-        flag(status, CSA_DEV_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
-
 // 32 columns of 16 lanes: thread i holds columns 2 (i % 4) + {0, 1} of every group of
 // eight, of lane i / 4 (x[4 g], x[4 g + 1]) and of lane i / 4 + 8 (x[4 g + 2], ...).
 __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&x)[16]) {
@@ -140,25 +116,6 @@ __device__ __forceinline__ void prefetch_3d(const void *tmap, int x, int y, int 
                    reinterpret_cast<uint64_t>(tmap)),
                "r"(x), "r"(y), "r"(z)
                : "memory");
-}
-
-// Four MMAs over 64 of K, the operands' descriptors AS and BS sixteen bytes further on
-// each; acc = 0: the first overwrites.  One statement, for one elected lane: a loop of
-// single ones takes 80 cycles each to issue, these the 32 or 48 that they run for.
-template <int AS, int BS>
-__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "setp.eq.b32 q, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "add.u64 x, %1, %5;\n\tadd.u64 y, %2, %6;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
-      "add.u64 x, %1, 2 * %5;\n\tadd.u64 y, %2, 2 * %6;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t"
-      "add.u64 x, %1, 3 * %5;\n\tadd.u64 y, %2, 3 * %6;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(AS), "n"(BS)
-      : "memory");
 }
 
 // 16 consecutive columns of this thread's lane.
@@ -395,7 +352,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         const int32_t *table = a.block_table + (long long)g.req * a.max_blocks;
         const int end = g.tile + g.n;
         int asked = g.tile + 1, phys = table[g.tile >> 1];  // (prefetches keep to the segment)
-        ok = la_wait(&M->q_empty, (s & 1) ^ 1, abort, a.status_dev);
+        ok = cache::wait(&M->q_empty, (s & 1) ^ 1, abort, a.status_dev);
         if (!ok) break;
         ++n_q;
         tc::mbar_arrive_expect_tx(&M->q_full, LA_BOXES * 128 * H.gt * H.R);
@@ -409,7 +366,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
           const bool there = phys >= 0 && phys < a.n_blocks;
           uint8_t *dst = sm + OFF_KV + st * LA_TILE;
           for (int c = 0; c < 4; ++c) {
-            ok = la_wait(&M->empty[st][c], par, abort, a.status_dev);
+            ok = cache::wait(&M->empty[st][c], par, abort, a.status_dev);
             if (!ok) break;
             if (c == 0) M->there[st] = there;
             if (there) {
@@ -456,19 +413,19 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       int it = 0;
       for (int s = 0; s < n_seg && ok; ++s) {
         const int end = it + seg_at(s).n;
-        ok = la_wait(&M->q_full, s & 1, abort, a.status_dev);
+        ok = cache::wait(&M->q_full, s & 1, abort, a.status_dev);
         for (; it < end && ok; ++it) {
           const int st = it & 1;
           const uint32_t d = tmem + S_COL + st * 64;
           const uint64_t k = dk + ((st * LA_TILE) >> 4);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            ok = ok && la_wait(&M->full[st][c], (it >> 1) & 1, abort, a.status_dev);
+            ok = ok && cache::wait(&M->full[st][c], (it >> 1) & 1, abort, a.status_dev);
             if (!ok) break;
             tc::tc_fence_after();
 #pragma unroll
             for (int e = 2 * c; e < (c == 3 ? 9 : 2 * c + 2); ++e)
-              mma4<2, 2>(d, dq + ((e * LA_BOX) >> 4), k + ((e * LA_BOX) >> 4), idesc, e > 0);
+              cache::mma4<2, 2>(d, dq + ((e * LA_BOX) >> 4), k + ((e * LA_BOX) >> 4), idesc, e > 0);
           }
           if (!ok) break;
           tc::mma_commit(&M->s_full[st]);
@@ -494,15 +451,15 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       int it = 0;
       for (int s = 0; s < n_seg && ok; ++s) {
         const int n_it = seg_at(s).n;
-        if (s > 0) ok = la_wait(&M->o_free, (s - 1) & 1, abort, a.status_dev);
+        if (s > 0) ok = cache::wait(&M->o_free, (s - 1) & 1, abort, a.status_dev);
         for (int i = 0; i < n_it && ok; ++i, ++it) {
-          ok = la_wait(&M->p_full, it & 1, abort, a.status_dev);
+          ok = cache::wait(&M->p_full, it & 1, abort, a.status_dev);
           if (!ok) break;
           tc::tc_fence_after();
           const uint64_t at = ((it & 1) * LA_TILE) >> 4;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            mma4<128, 2>(tmem + O_COL + b * 64, dv + at + ((2 * b * LA_BOX) >> 4), dp + at, idesc,
+            cache::mma4<128, 2>(tmem + O_COL + b * 64, dv + at + ((2 * b * LA_BOX) >> 4), dp + at, idesc,
                          i > 0);
             tc::mma_commit(&M->empty[it & 1][b]);
           }
@@ -523,7 +480,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) pos[e] = 32 * e + lane < g.nr ? a.row_pos[g.t + 32 * e + lane] : 0;
       // (the tables of the segment before the last: its outputs are written)
-      if (!__all_sync(0xffffffffu, la_wait(&M->info_free[s & 1], ((s >> 1) & 1) ^ 1, abort,
+      if (!__all_sync(0xffffffffu, cache::wait(&M->info_free[s & 1], ((s >> 1) & 1) ^ 1, abort,
                                            a.status_dev)))
         break;
       int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = 0;
@@ -569,7 +526,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     const float sl2 = a.softmax_scale * paged::kLog2e;
     uint32_t it = 0;
     auto wait = [&](uint64_t *bar, uint32_t turn) {
-      return (bool)__all_sync(0xffffffffu, la_wait(bar, turn & 1, abort, a.status_dev));
+      return (bool)__all_sync(0xffffffffu, cache::wait(bar, turn & 1, abort, a.status_dev));
     };
     // ok: no wait of this warp gave up; given_up: some warp's did
     bool ok = true, given_up = false;
@@ -865,14 +822,6 @@ __global__ void __launch_bounds__(128)
   if (a.lse && tid == 0) a.lse[row] = J.lse;
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    sms = 152;
-  return sms;
-}
-
 // CTAs of a call whose rows are taken whole.
 long long blocks_of(const csa_latent_attn_args &a, const Shape &H) {
   return (long long)((a.n_rows + H.R - 1) / H.R) * H.subs;
@@ -917,24 +866,11 @@ Layout layout(const csa_latent_attn_args &a, int sms) {
   return L;
 }
 
+// [x, y, z] of the given strides (bytes).
 bool encode(CUtensorMap *map, const void *base, const cuuint64_t (&dims)[3], int64_t s1, int64_t s2,
             const cuuint32_t (&box)[3]) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    cudaDriverEntryPointQueryResult q;
-    void *f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
   const cuuint64_t strides[2] = {(cuuint64_t)s1, (cuuint64_t)s2};
-  const cuuint32_t ones[3] = {1, 1, 1};
-  memset(map, 0, sizeof(*map));
-  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
-                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return cache::encode(map, base, 3, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
 }  // namespace

@@ -19,15 +19,8 @@
 // A prompt of 8192 and 128 heads: 246 us (1.12 PFLOP/s), 159 without its stores; filling
 // the 671 MB that it writes takes 168, so what is left is how far the two overlap.  2 x 1500
 // positions, 32 heads: 29 us.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <cstring>
-
 #include "attn_common.cuh"
-#include "cache_common.cuh"
-#include "paged_common.cuh"
-#include "tc.cuh"
+#include "cache_tiles.cuh"
 
 namespace csa {
 namespace {
@@ -46,23 +39,6 @@ struct Misc {
   int abort;
 };
 static_assert(LE_OFF_MISC + sizeof(Misc) <= 227 * 1024, "shared memory");
-
-__device__ __forceinline__ bool le_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                        uint32_t *status) {
-  if (tc::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = tc::global_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0) {
-      if (*abort) return false;
-      if (tc::global_ns() - t0 > 2000000000ull) {
-        *abort = 1;
-        flag(status, CSA_DEV_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
 
 // ---- the pair: addresses of the first CTA's barriers, arrivals there, loads that
 // complete there, commits that arrive at both
@@ -94,22 +70,6 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
-}
-
-// Four MMAs over 64 of K in one statement (an elected lane); acc = 0: the first overwrites.
-__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "setp.eq.b32 q, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "add.u64 x, %1, 2;\n\tadd.u64 y, %2, 2;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, q;\n\t"
-      "add.u64 x, %1, 4;\n\tadd.u64 y, %2, 4;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, q;\n\t"
-      "add.u64 x, %1, 6;\n\tadd.u64 y, %2, 6;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, q;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
 }
 
 // A box of shared memory into a pool [channels, heads, 128, pages], as a bulk group; until
@@ -214,7 +174,7 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
       for (int h = h0; h < h1 && ok; ++h)
         for (int c = 0; c < 8; ++c, ++it) {
           const int st = it % LE_STAGES;
-          ok = le_wait(&M->w_empty[st], ((it / LE_STAGES) & 1) ^ 1, abort, a.status_dev);
+          ok = cache::wait(&M->w_empty[st], ((it / LE_STAGES) & 1) ^ 1, abort, a.status_dev);
           if (!ok) break;
           if (h == h0) {
             if (rank == 0) tc::mbar_arrive_expect_tx(&M->c_full[c], LE_BOX * (on[0] + on[1]));
@@ -238,14 +198,14 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
       bool ok = true;
       for (int h = h0; h < h1 && ok; ++h) {
         const int n = h - h0, buf = n & 1;
-        ok = le_wait(&M->d_empty[buf], ((n >> 1) & 1) ^ 1, abort, a.status_dev);
+        ok = cache::wait(&M->d_empty[buf], ((n >> 1) & 1) ^ 1, abort, a.status_dev);
         for (int c = 0; c < 8 && ok; ++c, ++it) {
           const int st = it % LE_STAGES;
-          ok = (n > 0 || le_wait(&M->c_full[c], 0, abort, a.status_dev)) &&
-               le_wait(&M->w_full[st], (it / LE_STAGES) & 1, abort, a.status_dev);
+          ok = (n > 0 || cache::wait(&M->c_full[c], 0, abort, a.status_dev)) &&
+               cache::wait(&M->w_full[st], (it / LE_STAGES) & 1, abort, a.status_dev);
           if (!ok) break;
           tc::tc_fence_after();
-          mma4(tmem + buf * 256, dc + ((c * LE_BOX) >> 4), dw + ((st * LE_BOX) >> 4), idesc, c > 0);
+          cache::mma4_pair<2, 2>(tmem + buf * 256, dc + ((c * LE_BOX) >> 4), dw + ((st * LE_BOX) >> 4), idesc, c > 0);
           commit_pair(&M->w_empty[st]);
         }
         if (ok) commit_pair(&M->d_full[buf]);
@@ -285,10 +245,10 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
       for (int i = 0; i < 8; ++i)
         r[i] = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.r_pool) +
                                                my_src * a.r_page_stride + j * a.r_token_stride)[i];
-    bool ok = !rotated || __all_sync(0xffffffffu, le_wait(&M->r_full, 0, abort, a.status_dev));
+    bool ok = !rotated || __all_sync(0xffffffffu, cache::wait(&M->r_full, 0, abort, a.status_dev));
     for (int h = h0; h < h1 && ok; ++h) {
       const int n = h - h0, buf = n & 1;
-      ok = __all_sync(0xffffffffu, le_wait(&M->d_full[buf], (n >> 1) & 1, abort, a.status_dev));
+      ok = __all_sync(0xffffffffu, cache::wait(&M->d_full[buf], (n >> 1) & 1, abort, a.status_dev));
       if (!ok) break;
       tc::tc_fence_after();
       uint8_t *out = to + h * hs;
@@ -332,39 +292,12 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
                  : "memory");
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-    sms = 152;
-  return sms;
-}
-
-bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
-            const cuuint64_t *strides, const cuuint32_t *box) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    cudaDriverEntryPointQueryResult q;
-    void *f = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
-  memset(map, 0, sizeof(*map));
-  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides,
-                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // [x, y, z], boxes of 64 x 128.
 bool encode_in(CUtensorMap *map, const void *base, cuuint64_t x, cuuint64_t y, cuuint64_t z,
                int64_t s1, int64_t s2) {
   const cuuint64_t dims[3] = {x, y, z}, strides[2] = {(cuuint64_t)s1, (cuuint64_t)s2};
   const cuuint32_t box[3] = {64, 128, 1};
-  return encode(map, base, 3, dims, strides, box);
+  return cache::encode(map, base, 3, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
 }  // namespace
@@ -381,7 +314,8 @@ cudaError_t launch_latent_expand(const csa_latent_expand_args &a, cudaStream_t s
       !encode_in(&kmap, a.w_uk, kLatent, kNope, heads, kLatent * 2, a.w_uk_head_stride) ||
       !encode_in(&vmap, a.w_uv, kLatent, kValue, heads, kLatent * 2, a.w_uv_head_stride) ||
       !encode_in(&rmap, a.r_pool, kRopeDim, kBlock, pages, a.r_token_stride, a.r_page_stride) ||
-      !encode(&kr_out, a.k_pool, 4, out_dims, out_strides, out_box))
+      !cache::encode(&kr_out, a.k_pool, 4, out_dims, out_strides, out_box,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
     return cudaErrorInvalidValue;
   const size_t smem = LE_OFF_MISC + sizeof(Misc);
   int dev = 0;
