@@ -56,6 +56,7 @@ struct Seg {
   int tile, n;  // first tile (of 64 positions) and how many
   int slot;     // where its part goes, -1: the item is whole
 };
+constexpr int LA_JOIN = 8;    // parts of a row that are asked for together
 constexpr int LA_AHEAD = 3;  // tiles that L2 is asked for before they are loaded
 constexpr int LA_NEAR = 64;  // segments kept in shared memory; the rest in the workspace
 
@@ -780,21 +781,21 @@ __global__ void __launch_bounds__(128)
   if (r >= it.y || h >= a.n_heads) return;
   const int n = it.w - c + 1;
   auto slot = [&](int s) { return (2ll * (c + s) + (s == 0 ? 1 : 0)) * LA_PAIRS + m; };
-  // 16 parts at a time, statistics and outputs asked for together: what this takes is
+  // LA_JOIN parts at a time, statistics and outputs asked for together: what this takes is
   // the way to memory.  The sums move to a larger reference as it comes.
   float ref = -INFINITY, acc[4] = {}, l = 0.f;
-  for (int s0 = 0; s0 < n; s0 += 16) {
-    float2 ml[16];
-    float4 o[16];
+  for (int s0 = 0; s0 < n; s0 += LA_JOIN) {
+    float2 ml[LA_JOIN];
+    float4 o[LA_JOIN];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
+    for (int k = 0; k < LA_JOIN; ++k) {
       if (s0 + k >= n) break;
       ml[k] = parts.ml[slot(s0 + k)];
       o[k] = reinterpret_cast<const float4 *>(parts.o + slot(s0 + k) * kLatent)[tid];
     }
     float top = ref;
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
+    for (int k = 0; k < LA_JOIN; ++k)
       if (s0 + k < n) top = fmaxf(top, ml[k].x);
     const float f = ref == -INFINITY ? 0.f : exp2f(ref - top);
     if (ref != -INFINITY) l *= f;  // (l is NaN where a logit was)
@@ -802,7 +803,7 @@ __global__ void __launch_bounds__(128)
     for (int e = 0; e < 4; ++e) acc[e] *= f;
     ref = top;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
+    for (int k = 0; k < LA_JOIN; ++k) {
       if (s0 + k >= n || (ml[k].x == -INFINITY && ml[k].y == 0.f)) continue;  // nothing seen there
       const float w = ml[k].x == -INFINITY ? ml[k].y : exp2f(ml[k].x - ref);
       l += w * ml[k].y;
