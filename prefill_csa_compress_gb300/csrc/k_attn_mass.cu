@@ -1,31 +1,37 @@
 // The attention weight that every cached position received (csa_attn_mass): tcgen05
-// tiles of one page of 128 positions against up to 128 (row, head) pairs.
+// tiles of two pages of 128 positions against up to 128 (row, head) pairs.
 //
-//   S^T[j, n] = k_j . q_n          (128 x N x D, both operands K-major)
+//   S^T[j, n] = k_j . q_n          (2 x 128 x N x D, both operands K-major)
 //   mass[j]  += sum_n 2^(S^T[j, n] scale log2(e) - lse_n log2(e))
 // A lane of tensor memory is a position, so a thread adds up its position's weights
 // over all columns, and no sum crosses threads but at the end (in an order that the
 // arguments fix: no atomics).
 //
-// A CTA takes a page of a request (up to eight, one after the other, in large calls), some
-// of its key heads and a share of the rows that see it (heads and rows are split only as far as there are too few pages to fill the
-// GPU; mass_join_kernel then adds the parts in order).  A step is one key head and one
-// tile of consecutive rows with their heads stacked under them.  Roles:
-//   warps 0..7  the exponentials and the sums, two warps 32 positions, 32 columns in turn;
-//   warp 8      loads (TMA): a page's keys once a head, the queries of every step;
-//   warp 9      issues the MMAs;
-//   warp 10     walks the rows, leaves out tiles that do not see the page and
-//               describes each step to the rest: references and bounds a column.
-// Two CTAs an SM.
+// A CTA takes two pages of a request (up to eight such pairs, one after the other, in large
+// calls), some of its key heads and a share of the rows that see them (heads and rows are
+// split only as far as there are too few pages to fill the GPU; mass_join_kernel then adds
+// the parts in order).  A step is one key head and one tile of consecutive rows with their
+// heads stacked under them; its queries serve both pages, which halves what a prompt
+// fetches from L2.  One CTA an SM.  Roles:
+//   warps 0..15  the exponentials and the sums, eight warps a page, two of them 32
+//                positions, 32 columns in turn; each page's logits have buffers and
+//                barriers of their own, so that one page's warps wait for tensor memory
+//                while the other's compute (with common ones a prompt 11 us more);
+//   warp 16      loads (TMA): the pages' keys once a head, the queries of every step;
+//   warp 17      issues the MMAs;
+//   warp 18      walks the rows, leaves out tiles that do not see the pages and
+//                describes each step to the rest: references and bounds a column.
 //
 // What bounds it.  Decode (32 rows over ragged contexts to 16,384, 64 heads on 8 of 128):
-// 132 us, 5.2 TB/s, the pages' way through two stages a CTA.  A prompt of 8192 rows of 32
-// heads on 8: 303 us, 0.92 PFLOP/s; a step takes a CTA 2,200 cycles, 1,750 of them the
-// sums' own latency (four columns: a read of shared memory, two FMAs, four exponentials, two
-// additions in a chain; the first columns are there after 300 to 700 while other products
-// run), with the tensor cores 40 % busy, the exponentials' unit 42 %, issue 55 %.  Set aside:
-// exponentials on the FMA pipe (a quarter of them: 347 us), 16 columns at a time with the
-// next ones on their way (317), three or four groups of warps (312, 483 with spills).
+// 120 us, 5.7 TB/s, the pages' way through three stages of a CTA.  A prompt of 8192 rows of
+// 32 heads on 8: 260 us, 1.07 PFLOP/s; a step takes a CTA some 1,850 cycles, of which the
+// products fill 1,024 (they read shared memory at its full rate) and the exponentials 1,024
+// of their unit; between them stand the issuing lane's waits and the sums' latency.  Set
+// aside: one page a CTA and two CTAs an SM (prompt 303 us, decode 132); runtime divisions
+// by the number of stages in the issuing lane (300); all of a warp's logits in registers
+// and the buffer free before the exponentials (328); with one page, exponentials on the FMA
+// pipe (a quarter of them: 347), 16 columns at a time with the next ones on their way
+// (317), three or four groups of warps (312, 483 with spills).
 #include <cstddef>
 
 #include "attn_common.cuh"
@@ -34,37 +40,46 @@
 namespace csa {
 namespace {
 
-constexpr int AM_THREADS = 352;
-constexpr int AM_LOAD = 8, AM_MMA = 9, AM_WALK = 10;  // warps; 0 .. 7 add up
+constexpr int AM_THREADS = 608;
+constexpr int AM_LOAD = 16, AM_MMA = 17, AM_WALK = 18;  // warps; 0 .. 15 add up
+constexpr int AM_PAIR = 2 * kBlock;  // positions of two pages
 constexpr int AM_STEPS = 4;   // steps described ahead
 constexpr int AM_RING = 4;    // stages of keys and of queries, at most
 
+// (One read for what the issuing lane needs: it goes through every step by itself, and
+// each access that it waits for is time without products.)
 struct Step {
-  int t0, kvh;         // its rows start here; key head, < 0: no products, the page is done
-  int new_k, last_k;   // the head's first step, its last
-  int mixed;           // some column does not see all of the page
-  int page, phys;      // of the request, and in the pool
-  int last;            // kvh < 0: no more steps
+  int t0;        // its rows start here
+  int kvh;       // key head, < 0: no products, the pages are done
+  int flags;     // NEW_K, ...; from SEEN on bit p: page p is there and some column sees some
+                 // of it, from MIXED on: some column does not see all of it
+  int page;      // of the request the first
+  int phys[2];   // in the pool, -1: it is not there
+  int pad[2];
 };
+constexpr int NEW_K = 1, LAST_K = 2, NO_MORE = 4;  // the head's first step, its last; kvh < 0
+constexpr int SEEN = 3, MIXED = 5;                 // shifts
 
 struct Misc {
   uint64_t k_full[AM_RING], k_empty[AM_RING], q_full[AM_RING], q_empty[AM_RING];
-  uint64_t s_full[2], s_empty[2], x_full[2], m_full[AM_STEPS], m_empty[AM_STEPS], drained;
+  uint64_t s_full[2][2], s_empty[2][2], x_full[2][2], m_full[AM_STEPS], m_empty[AM_STEPS], drained;
   uint32_t tmem;
   int abort;
   int vmin, vmax;      // rows of the request that see some of the pages
-  Step step[AM_STEPS];
+  alignas(16) Step step[AM_STEPS];
   alignas(16) float lse[AM_STEPS][128];  // a column's -lse log2(e) (read four at a time)
-  int2 see[AM_STEPS][128];  // a column's positions of the page [x, y)
-  float sum[2][128];   // (by the step's parity)
+  int2 see[AM_STEPS][128];  // a column's positions of the pages [x, y)
+  float sum[2][2][128];     // (by the step's parity, and the page)
 };
 
-static_assert(offsetof(Misc, lse) % 16 == 0 && offsetof(Misc, see) % 8 == 0, "vector reads");
+static_assert(offsetof(Misc, step) % 16 == 0 && sizeof(Step) % 16 == 0 &&
+                  offsetof(Misc, lse) % 16 == 0 && offsetof(Misc, see) % 8 == 0,
+              "vector reads");
 
 // How the host splits a call, and its shared memory.
 struct Split {
   int tr, n;          // rows of a step and its columns, rounded up to 32
-  int pages;          // of a request that a CTA takes one after the other
+  int pairs;          // of pages of a request that a CTA takes one after the other
   int kv, rows;       // parts by key heads (heads_per each) and by rows
   int heads_per;
   int k_stages, q_stages;
@@ -79,8 +94,8 @@ __device__ __forceinline__ void prefetch_4d(const void *tmap, int x, int y, int 
                : "memory");
 }
 
-// A position's mass, or its part.  (A function, since in the loop it costs registers: 308
-// against 302 us for a prompt.)
+// A position's mass, or its part.  (A function, since in the loop it costs registers: with
+// one page a CTA 308 against 302 us for a prompt.)
 __device__ __noinline__ void put_mass(const csa_attn_mass_args &a, float *parts, long long part, int b,
                                       int col, float sum) {
   if (parts) {
@@ -94,13 +109,13 @@ __device__ __noinline__ void put_mass(const csa_attn_mass_args &a, float *parts,
 }
 
 template <int D>
-__global__ void __launch_bounds__(AM_THREADS, 2)
+__global__ void __launch_bounds__(AM_THREADS, 1)
     attn_mass_kernel(const __grid_constant__ csa_attn_mass_args a, float *parts, Split G,
                      const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ CUtensorMap kmap) {
-  constexpr int BOXES = D / 64, K_TILE = BOXES * 16384;
+  constexpr int BOXES = D / 64, K_TILE = BOXES * 16384;  // (of a page; a stage has two)
   extern __shared__ __align__(1024) uint8_t sm[];
-  uint8_t *ks = sm, *qs = sm + G.k_stages * K_TILE;
+  uint8_t *ks = sm, *qs = sm + G.k_stages * 2 * K_TILE;
   Misc *M = reinterpret_cast<Misc *>(qs + G.q_stages * G.q_bytes);
   tc::griddep_wait();
   tc::griddep_launch_dependents();
@@ -116,23 +131,27 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
   u /= G.kv;
   const int row_part = u % G.rows;
   u /= G.rows;
-  const int b = u % a.n_req, page0 = u / a.n_req * G.pages;
+  const int b = u % a.n_req, pair0 = u / a.n_req * G.pairs;
   const int len = min(a.kv_len[b], a.max_blocks * kBlock);
-  if (b == 0 && page0 == 0 && kv_part == 0 && row_part == 0)
+  if (b == 0 && pair0 == 0 && kv_part == 0 && row_part == 0)
     for (int t = tid; t < a.n_rows; t += AM_THREADS)
       if (a.row_req[t] >= a.n_req) flag(a.status_dev, CSA_DEV_BAD_POS);
-  if ((long long)page0 * kBlock >= len) return;
-  const int page1 = min(page0 + G.pages, (len - 1) / kBlock + 1);
+  if ((long long)pair0 * AM_PAIR >= len) return;
+  const int pair1 = min(pair0 + G.pairs, (len - 1) / AM_PAIR + 1);
   const int32_t *table = a.block_table + (long long)b * a.max_blocks;
-  // the first page's keys are asked for while the rows are found (behind a window no row
-  // may see them; later pages asked for ahead make it slower, 132 -> 160 us for 32 rows)
-  if (warp == 0 && a.window == 0) {
-    const int phys = table[page0];
-    if (phys >= 0 && phys < a.n_blocks)
+  // a page's place in the pool; -1: it has no position, or none there
+  auto place = [&](int page) {
+    const int phys = (long long)page * kBlock < len ? table[page] : -1;
+    return phys >= 0 && phys < a.n_blocks ? phys : -1;
+  };
+  // the first pages' keys are asked for while the rows are found (behind a window no row
+  // may see them; later pages asked for ahead make it slower)
+  if (warp < 2 && a.window == 0) {
+    const int phys = place(2 * pair0 + warp);
+    if (phys >= 0)
       for (int i = lane; i < BOXES * G.heads_per; i += 32) {
         const int h = kv_part * G.heads_per + i / BOXES;
-        if (h < a.n_kv_heads)
-          prefetch_4d(&kmap, i % BOXES * 64, h, 0, phys);
+        if (h < a.n_kv_heads) prefetch_4d(&kmap, i % BOXES * 64, h, 0, phys);
       }
   }
   if (tid == 0) {
@@ -143,13 +162,15 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
       tc::mbar_init(&M->q_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&M->s_full[i], 2);
-      tc::mbar_init(&M->s_empty[i], 8);
-      tc::mbar_init(&M->x_full[i], 4);
+      for (int p = 0; p < 2; ++p) {
+        tc::mbar_init(&M->s_full[i][p], 2);
+        tc::mbar_init(&M->s_empty[i][p], 8);
+        tc::mbar_init(&M->x_full[i][p], 4);
+      }
     }
     for (int i = 0; i < AM_STEPS; ++i) {
       tc::mbar_init(&M->m_full[i], 1);
-      tc::mbar_init(&M->m_empty[i], 10);  // loads, MMA, eight warps of sums
+      tc::mbar_init(&M->m_empty[i], 18);  // loads, MMA, sixteen warps of sums
     }
     tc::mbar_init(&M->drained, 1);
     M->abort = 0;
@@ -158,7 +179,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
     paged::prefetch_map(&qmap);
     paged::prefetch_map(&kmap);
   }
-  if (warp == AM_MMA) tc::tmem_alloc(&M->tmem, 256);
+  if (warp == AM_MMA) tc::tmem_alloc(&M->tmem, 512);
   const int g = a.n_heads / a.n_kv_heads;
   // columns that no query fills are zero, and their references +inf
   {
@@ -171,13 +192,13 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
   // the rows that see some of the pages
   {
     int v0 = 0x7FFFFFFF, v1 = -1;
-    const int end = min(len, page1 < a.max_blocks ? page1 * kBlock : len);
+    const int from = pair0 * AM_PAIR, end = (long long)pair1 * AM_PAIR < len ? pair1 * AM_PAIR : len;
 #pragma unroll 4
     for (int t = tid; t < a.n_rows; t += AM_THREADS) {
       const int req = a.row_req[t], pos = a.row_pos[t];
       int lo, hi;
       paged::visible_range(a, len, pos, lo, hi);
-      if (req == b && max(lo, page0 * kBlock) < min(hi, end)) v0 = min(v0, t), v1 = t;
+      if (req == b && max(lo, from) < min(hi, end)) v0 = min(v0, t), v1 = t;
     }
     v0 = __reduce_min_sync(0xffffffffu, v0);
     v1 = __reduce_max_sync(0xffffffffu, v1);
@@ -209,10 +230,10 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
     }
     uint32_t it = 0;
     bool ok = true;
-    int phys = table[page0];
-    for (int page = page0; page < page1 && ok; ++page) {
-      const int base = page * kBlock;
-      const bool there = phys >= 0 && phys < a.n_blocks;
+    int phys[2] = {place(2 * pair0), place(2 * pair0 + 1)};
+    for (int pair = pair0; pair < pair1 && ok; ++pair) {
+      const int base = pair * AM_PAIR;
+      const int there = (phys[0] >= 0) + 2 * (phys[1] >= 0);
       for (int kvh = kv0; kvh < kv1 && ok; ++kvh) {
         // asked for a tile ahead
         int req[4], pos[4];
@@ -231,7 +252,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
         int pending = -1, first = 1;
         float p_lse[4];
         int2 p_see[4];
-        bool p_mixed = false;
+        int p_seen = 0, p_mixed = 0;
         auto publish = [&](bool last) {
           const int st = it % AM_STEPS;
           ok = __all_sync(0xffffffffu, cache::wait(&M->m_empty[st], ((it / AM_STEPS) & 1) ^ 1, abort,
@@ -244,8 +265,9 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
           }
           if (lane == 0) {
             Step &S = M->step[st];
-            S.t0 = pending, S.kvh = kvh, S.new_k = first, S.last_k = last, S.mixed = p_mixed;
-            S.page = page, S.phys = phys;
+            S.t0 = pending, S.kvh = kvh;
+            S.flags = (first ? NEW_K : 0) | (last ? LAST_K : 0) | p_seen << SEEN | p_mixed << MIXED;
+            S.page = 2 * pair, S.phys[0] = phys[0], S.phys[1] = phys[1];
           }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&M->m_full[st]);
@@ -254,44 +276,43 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
         };
         ask(tile0);
         for (int tile = tile0; tile < tile1 && ok; ++tile) {
-          bool any = false, mixed = false;
+          bool any[2] = {false, false}, part[2] = {false, false};
           float x[4];
           int2 see[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             int lo, hi;
             paged::visible_range(a, len, pos[i], lo, hi);
-            lo = max(lo - base, 0), hi = min(hi - base, kBlock);
+            lo = max(lo - base, 0), hi = min(hi - base, AM_PAIR);
             if (req[i] != b || lo >= hi || lse[i] == -INFINITY) lo = hi = 0;
-            any = any || lo < hi;
             const bool row = r[i] >= 0 && vmin + tile * G.tr + r[i] < a.n_rows;
-            mixed = mixed || (row && (lo > 0 || hi < kBlock));
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              any[p] = any[p] || max(lo, p * kBlock) < min(hi, p * kBlock + kBlock);
+              part[p] = part[p] || (row && (lo > p * kBlock || hi < p * kBlock + kBlock));
+            }
             x[i] = -lse[i] * paged::kLog2e, see[i] = make_int2(lo, hi);
           }
           ask(tile + 1);
-          any = __any_sync(0xffffffffu, any);
-          mixed = __any_sync(0xffffffffu, mixed);
-          if (!any) continue;
-          if (!there) {
-            if (lane == 0) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
-            break;
-          }
+          const int seen = __any_sync(0xffffffffu, any[0]) + 2 * __any_sync(0xffffffffu, any[1]);
+          const int mixed = __any_sync(0xffffffffu, part[0]) + 2 * __any_sync(0xffffffffu, part[1]);
+          if ((seen & ~there) && lane == 0) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
+          if (!(seen & there)) continue;
           if (pending >= 0) publish(false);
-          pending = vmin + tile * G.tr, p_mixed = mixed;
+          pending = vmin + tile * G.tr, p_seen = seen & there, p_mixed = mixed;
 #pragma unroll
           for (int i = 0; i < 4; ++i) p_lse[i] = x[i], p_see[i] = see[i];
         }
         if (pending >= 0 && ok) publish(true);
-        if (!there) break;
       }
-      if (page + 1 < page1) phys = table[page + 1];
+      if (pair + 1 < pair1) phys[0] = place(2 * pair + 2), phys[1] = place(2 * pair + 3);
       if (!ok) break;
-      const int st = it % AM_STEPS;  // the page is done
+      const int st = it % AM_STEPS;  // the pages are done
       ok = __all_sync(0xffffffffu, cache::wait(&M->m_empty[st], ((it / AM_STEPS) & 1) ^ 1, abort,
                                            a.status_dev));
       if (ok && lane == 0) {
         Step &S = M->step[st];
-        S.kvh = -1, S.page = page, S.last = page + 1 == page1;
+        S.kvh = -1, S.page = 2 * pair, S.flags = pair + 1 == pair1 ? NO_MORE : 0;
         tc::mbar_arrive(&M->m_full[st]);
       }
       ++it;
@@ -301,6 +322,8 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
     // ================================================================ loads
     if (lane == 0) {
       uint32_t nk = 0, nq = 0;
+      int sk = 0, sq = 0;               // stages
+      uint32_t k_turn = 1, q_turn = 1;  // parities
       bool ok = true;
       for (uint32_t it = 0;; ++it) {
         const int st = it % AM_STEPS;
@@ -309,27 +332,30 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
         const Step S = M->step[st];
         tc::mbar_arrive(&M->m_empty[st]);
         if (S.kvh < 0) {
-          if (S.last) break;
+          if (S.flags & NO_MORE) break;
           continue;
         }
-        if (S.new_k) {
-          const int s = nk % G.k_stages;
-          ok = cache::wait(&M->k_empty[s], ((nk / G.k_stages) & 1) ^ 1, abort, a.status_dev);
+        if (S.flags & NEW_K) {
+          ok = cache::wait(&M->k_empty[sk], k_turn, abort, a.status_dev);
           if (!ok) break;
-          tc::mbar_arrive_expect_tx(&M->k_full[s], K_TILE);
-          for (int c = 0; c < BOXES; ++c)
-            paged::tma_load_4d(ks + s * K_TILE + c * 16384, &kmap, c * 64, S.kvh, 0, S.phys,
-                               &M->k_full[s]);
+          // (every page that is there: a later step of the head may see it)
+          tc::mbar_arrive_expect_tx(&M->k_full[sk], K_TILE * ((S.phys[0] >= 0) + (S.phys[1] >= 0)));
+          for (int p = 0; p < 2; ++p)
+            if (S.phys[p] >= 0)
+              for (int c = 0; c < BOXES; ++c)
+                paged::tma_load_4d(ks + (2 * sk + p) * K_TILE + c * 16384, &kmap, c * 64, S.kvh, 0,
+                                   S.phys[p], &M->k_full[sk]);
           ++nk;
+          if (++sk == G.k_stages) sk = 0, k_turn ^= 1;
         }
-        const int s = nq % G.q_stages;
-        ok = cache::wait(&M->q_empty[s], ((nq / G.q_stages) & 1) ^ 1, abort, a.status_dev);
+        ok = cache::wait(&M->q_empty[sq], q_turn, abort, a.status_dev);
         if (!ok) break;
-        tc::mbar_arrive_expect_tx(&M->q_full[s], BOXES * 128 * g * G.tr);
+        tc::mbar_arrive_expect_tx(&M->q_full[sq], BOXES * 128 * g * G.tr);
         for (int c = 0; c < BOXES; ++c)
-          tc::tma_load_3d(qs + s * G.q_bytes + c * (G.q_bytes / BOXES), &qmap, c * 64, S.kvh * g,
-                          S.t0, &M->q_full[s]);
+          tc::tma_load_3d(qs + sq * G.q_bytes + c * (G.q_bytes / BOXES), &qmap, c * 64, S.kvh * g,
+                          S.t0, &M->q_full[sq]);
         ++nq;
+        if (++sq == G.q_stages) sq = 0, q_turn ^= 1;
       }
       // whatever was asked for has landed before the CTA retires
       if (!ok) {
@@ -345,39 +371,46 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
     if (tc::elect_one()) {
       const uint32_t idesc = tc::idesc_bf16_f32(128, G.n);
       const uint64_t dk = tc::desc_sw128(tc::smem_u32(ks)), dq = tc::desc_sw128(tc::smem_u32(qs));
-      uint32_t nk = 0, nq = 0;
+      int sk = 0, sq = 0;               // stages
+      uint32_t k_turn = 0, q_turn = 0;  // parities
       bool ok = true;
       for (uint32_t it = 0;; ++it) {
-        const int st = it % AM_STEPS;
+        const int st = it % AM_STEPS, buf = it & 1;
         ok = cache::wait(&M->m_full[st], (it / AM_STEPS) & 1, abort, a.status_dev);
         if (!ok) break;
-        const Step S = M->step[st];
+        const int4 S = *reinterpret_cast<const int4 *>(&M->step[st]);  // t0, kvh, flags, page
         tc::mbar_arrive(&M->m_empty[st]);
-        if (S.kvh < 0) {  // (no logits: both arrivals are plain)
-          ok = cache::wait(&M->s_empty[it & 1], ((it >> 1) & 1) ^ 1, abort, a.status_dev);
+        if (S.y >= 0)
+          ok = (!(S.z & NEW_K) || cache::wait(&M->k_full[sk], k_turn, abort, a.status_dev)) &&
+               cache::wait(&M->q_full[sq], q_turn, abort, a.status_dev);
+        if (!ok) break;
+        if (S.y >= 0) tc::tc_fence_after();
+        const uint64_t k = dk + ((sk * 2 * K_TILE) >> 4), q = dq + ((sq * G.q_bytes) >> 4);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          ok = ok && cache::wait(&M->s_empty[buf][p], ((it >> 1) & 1) ^ 1, abort, a.status_dev);
           if (!ok) break;
-          tc::mbar_arrive(&M->s_full[it & 1]);
-          tc::mbar_arrive(&M->s_full[it & 1]);
-          if (S.last) break;
+          tc::tc_fence_after();
+          if (S.z >> (SEEN + p) & 1)
+#pragma unroll
+            for (int c = 0; c < BOXES; ++c)
+              cache::mma4<2, 2>(tmem + buf * 256 + p * 128, k + ((p * K_TILE + c * 16384) >> 4),
+                                q + ((c * (G.q_bytes / BOXES)) >> 4), idesc, c > 0);
+          // (no logits: both arrivals are plain)
+          if (S.y >= 0) tc::mma_commit(&M->s_full[buf][p]);
+          else tc::mbar_arrive(&M->s_full[buf][p]);
+          tc::mbar_arrive(&M->s_full[buf][p]);  // hands on the step's description
+        }
+        if (!ok) break;
+        if (S.y < 0) {
+          if (S.z & NO_MORE) break;
           continue;
         }
-        const int sk = nk % G.k_stages, sq = nq % G.q_stages, buf = it & 1;
-        ok = (!S.new_k || cache::wait(&M->k_full[sk], (nk / G.k_stages) & 1, abort, a.status_dev)) &&
-             cache::wait(&M->s_empty[buf], ((it >> 1) & 1) ^ 1, abort, a.status_dev) &&
-             cache::wait(&M->q_full[sq], (nq / G.q_stages) & 1, abort, a.status_dev);
-        if (!ok) break;
-        tc::tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < BOXES; ++c)
-          cache::mma4<2, 2>(tmem + buf * 128, dk + ((sk * K_TILE + c * 16384) >> 4),
-               dq + ((sq * G.q_bytes + c * (G.q_bytes / BOXES)) >> 4), idesc, c > 0);
-        tc::mma_commit(&M->s_full[buf]);
-        tc::mbar_arrive(&M->s_full[buf]);  // hands on the step's description
         tc::mma_commit(&M->q_empty[sq]);
-        ++nq;
-        if (S.last_k) {
+        if (++sq == G.q_stages) sq = 0, q_turn ^= 1;
+        if (S.z & LAST_K) {
           tc::mma_commit(&M->k_empty[sk]);
-          ++nk;
+          if (++sk == G.k_stages) sk = 0, k_turn ^= 1;
         }
       }
       // every issued MMA has completed before tensor memory is released
@@ -387,8 +420,9 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
     __syncwarp();
   } else {
     // ================================================================ exponentials and sums
-    const int qd = warp & 3, grp = warp >> 2, j = qd * 32 + lane;
-    const uint32_t ts = tmem + ((uint32_t)(qd * 32) << 16);
+    const int qd = warp & 3, grp = (warp >> 2) & 1, pg = warp >> 3;
+    const int row = qd * 32 + lane, j = pg * kBlock + row;  // of the page, of both
+    const uint32_t ts = tmem + ((uint32_t)(qd * 32) << 16) + pg * 128;
     const float sl2 = a.softmax_scale * paged::kLog2e;
     float total = 0.f;
     uint32_t outs0 = 0, outs1 = 0;  // pages done, by the step's parity
@@ -398,39 +432,40 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
     };
     for (uint32_t it = 0;; ++it) {
       const int st = it % AM_STEPS, buf = it & 1;
-      ok = wait(&M->s_full[buf], it >> 1);
+      ok = wait(&M->s_full[buf][pg], it >> 1);
       if (!ok) break;
       if (M->step[st].kvh < 0) {
         // the two halves of the columns, then the position's mass or its part
-        const int col = M->step[st].page * kBlock + j;
-        const bool last = M->step[st].last != 0;
+        const long long col = (long long)M->step[st].page * kBlock + j;
+        const bool last = (M->step[st].flags & NO_MORE) != 0;
         if (grp == 1) {
-          M->sum[buf][j] = total;
+          M->sum[buf][pg][row] = total;
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&M->x_full[buf]);
+          if (lane == 0) tc::mbar_arrive(&M->x_full[buf][pg]);
         } else {
-          ok = wait(&M->x_full[buf], buf ? outs1++ : outs0++);
+          ok = wait(&M->x_full[buf][pg], buf ? outs1++ : outs0++);
           if (!ok) break;
         }
         if (grp == 0 && col < len)
-          put_mass(a, parts, (long long)(kv_part * G.rows + row_part) * a.n_req + b, b, col,
-                   total + M->sum[buf][j]);
+          put_mass(a, parts, (long long)(kv_part * G.rows + row_part) * a.n_req + b, b, (int)col,
+                   total + M->sum[buf][pg][row]);
         total = 0.f;
         __syncwarp();
         if (lane == 0) {
-          tc::mbar_arrive(&M->s_empty[buf]);
+          tc::mbar_arrive(&M->s_empty[buf][pg]);
           tc::mbar_arrive(&M->m_empty[st]);
         }
         if (last) break;
         continue;
       }
-      const bool mixed = M->step[st].mixed;
+      const int flags = M->step[st].flags;
+      const bool mixed = flags >> (MIXED + pg) & 1, seen = flags >> (SEEN + pg) & 1;
       tc::tc_fence_after();
       float2 sums[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll 1
-      for (int c = 32 * grp; c < G.n; c += 64) {
+      for (int c = 32 * grp; c < G.n && seen; c += 64) {
         float x[32];
-        tc::tmem_ld32(ts + buf * 128 + c, x);
+        tc::tmem_ld32(ts + buf * 256 + c, x);
         const float4 *lse = reinterpret_cast<const float4 *>(M->lse[st] + c);
         if (!mixed) {
           const float2 one = make_float2(1.f, 1.f), scale = make_float2(sl2, sl2);
@@ -457,7 +492,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        tc::mbar_arrive(&M->s_empty[buf]);
+        tc::mbar_arrive(&M->s_empty[buf][pg]);
         tc::mbar_arrive(&M->m_empty[st]);
       }
     }
@@ -466,7 +501,7 @@ __global__ void __launch_bounds__(AM_THREADS, 2)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (warp == AM_MMA) tc::tmem_dealloc(tmem, 256);
+  if (warp == AM_MMA) tc::tmem_dealloc(tmem, 512);
 }
 
 // mass_out from the parts, in order.
@@ -488,8 +523,12 @@ __global__ void __launch_bounds__(256)
 }
 
 // Rows of a step: what a request has on average, as far as 128 columns go (the host
-// does not know how rows are spread).  Parts: as many as make four CTAs for each place
-// on the GPU, by key heads first (they share nothing), then by rows.
+// does not know how rows are spread).  Parts, by key heads first (they share nothing), then
+// by rows: a CTA for each SM at least, and up to two where each still has 32 steps (4096
+// rows of 32 heads on 4 over 16,384: 505 us with one, 396 with two, 430 with four; 300 rows
+// over 32,768 95, 101 and 106, since a CTA's start is paid for each).  With a handful of
+// steps, as in decode, no second round for a few CTAs (one row over 32,768: 21 us with 256
+// CTAs, 15 with 128; 3 x 500 rows over ragged 4000, which have more steps, 60 for 46).
 Split split_of(const csa_attn_mass_args &a) {
   Split G;
   const int g = a.n_heads / a.n_kv_heads;
@@ -497,24 +536,29 @@ Split split_of(const csa_attn_mass_args &a) {
   const int most = 128 / g;
   G.tr = per < most ? (int)per : most;
   G.n = (G.tr * g + 31) / 32 * 32;
-  const long long pages = (long long)a.n_req * a.max_blocks;
-  const long long want = (4ll * 2 * sm_count() + pages - 1) / pages;
+  const long long pairs = (long long)a.n_req * ((a.max_blocks + 1) / 2);
+  const long long tiles = (per + G.tr - 1) / G.tr, steps = tiles * a.n_kv_heads, sms = sm_count();
+  const long long hi = (2 * sms + pairs - 1) / pairs, fit = steps / 32;
+  const long long lo = steps * pairs < 16 * sms ? (sms > pairs ? sms / pairs : 1)
+                                                : (sms + pairs - 1) / pairs;
+  const long long want = fit < lo ? lo : (fit < hi ? fit : hi);
   G.kv = (int)(want < a.n_kv_heads ? want : a.n_kv_heads);
   G.heads_per = (a.n_kv_heads + G.kv - 1) / G.kv;
   G.kv = (a.n_kv_heads + G.heads_per - 1) / G.heads_per;
-  const long long left = (want + G.kv - 1) / G.kv, tiles = (per + G.tr - 1) / G.tr;
+  const long long left = (want + G.kv - 1) / G.kv;
   const long long row_parts = left < tiles / 8 ? left : tiles / 8;  // (at least eight tiles each)
   G.rows = (int)(row_parts < 1 ? 1 : (row_parts > 16 ? 16 : row_parts));
-  // Several pages a CTA where that leaves six CTAs for each place: a CTA's start (the
-  // rows that see its pages, the first keys) is then paid once for them (32 rows over
-  // ragged contexts to 16384 of 64 heads on 8: one page 148 us, three 132).
-  const long long run = pages * G.kv * G.rows / (6ll * 2 * sm_count());
-  G.pages = (int)(run < 1 ? 1 : (run > 8 ? 8 : run));
-  // 112 KB a CTA: two of queries at least, keys in what is left
-  const int k_tile = a.head_dim * 256, boxes = a.head_dim / 64;
+  // Several pairs of pages a CTA where that leaves four CTAs for each SM: a CTA's start
+  // (the rows that see its pages, the first keys) is then paid once for them (the decode
+  // above 129 us in a graph with six, 116 with four, 133, 123 and 153 with three, two and one).
+  const long long run = pairs * G.kv * G.rows / (4 * sms);
+  G.pairs = (int)(run < 1 ? 1 : (run > 8 ? 8 : run));
+  // queries in two stages, keys in what is left (a prompt with four and one 1 % more
+  // than with two and two)
+  const int k_tile = 2 * a.head_dim * 256, boxes = a.head_dim / 64;
   G.q_bytes = boxes * (int)align_up((size_t)G.n * 128, 1024);
-  const int room = 227 * 512 - 1024 - (int)sizeof(Misc);
-  G.q_stages = G.n > 64 ? 2 : 4;
+  const int room = 227 * 1024 - 1024 - (int)sizeof(Misc);
+  G.q_stages = 2;
   G.k_stages = (room - G.q_stages * G.q_bytes) / k_tile;
   if (G.k_stages > AM_RING) G.k_stages = AM_RING;
   return G;
@@ -523,17 +567,18 @@ Split split_of(const csa_attn_mass_args &a) {
 template <int D>
 cudaError_t launch(const csa_attn_mass_args &a, float *parts, const Split &G,
                    const CUtensorMap &qmap, const CUtensorMap &kmap, cudaStream_t s) {
-  const size_t smem = G.k_stages * D * 256 + G.q_stages * G.q_bytes + sizeof(Misc);
+  const size_t smem = G.k_stages * D * 512 + G.q_stages * G.q_bytes + sizeof(Misc);
   int dev = 0;
   cudaGetDevice(&dev);
   static bool attr[64] = {};
   if (dev < 0 || dev >= 64 || !attr[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(
-        attn_mass_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 512);
+        attn_mass_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr[dev] = true;
   }
-  const long long grid = (long long)a.n_req * ((a.max_blocks + G.pages - 1) / G.pages) * G.kv * G.rows;
+  const long long grid = (long long)a.n_req * (((a.max_blocks + 1) / 2 + G.pairs - 1) / G.pairs) * G.kv *
+                         G.rows;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
   return launch_kernel(attn_mass_kernel<D>, dim3((unsigned)grid), dim3(AM_THREADS), smem, s, 0,
                        false, a, parts, G, qmap, kmap);
