@@ -220,6 +220,24 @@ def test_two_calls_at_once():
         assert np.array_equal(_np(o), w)
 
 
+@pytest.mark.parametrize("requests,step,window", [(400, 5, 0), (170, 12, 600)])
+def test_attention_mass_of_many_requests(requests, step, window):
+    """More pairs of pages than CTAs: several a CTA one after the other, with odd numbers
+    of pages, and requests that no row has."""
+    lens = [1 + step * b for b in range(requests)]
+    rows = [(b, lens[b] - 1) for b in range(requests) if b % 7] + chunk(requests - 1, 0, 40)
+    Mass(rows, lens, 4, 2, 64, seed=step, window=window).check(0.5)
+
+
+@pytest.mark.parametrize("gone", [[0], [1], [2], [0, 1], [1, 2], [0, 1, 2], [4]])
+@pytest.mark.parametrize("rows", [1, 80])
+def test_attention_mass_unmapped_pages(gone, rows):
+    """A page that is not there leaves the other page of its pair as it is."""
+    b = Mass(chunk(0, 600 - rows, rows), [600], 8, 2, 128, seed=len(gone))
+    b.table[0, gone] = -1
+    b.check(0.5, status=1)
+
+
 def test_attention_mass_captured_and_alike():
     b = Mass(chunk(0, 600, 300) + chunk(1, 40, 40), [900, 80], 16, 4, 128, seed=12)
     out = [torch.zeros_like(b.mass) for _ in range(2)]
