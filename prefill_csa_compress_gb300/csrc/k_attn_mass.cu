@@ -24,14 +24,15 @@
 //
 // What bounds it.  Decode (32 rows over ragged contexts to 16,384, 64 heads on 8 of 128):
 // 120 us, 5.7 TB/s, the pages' way through three stages of a CTA.  A prompt of 8192 rows of
-// 32 heads on 8: 260 us, 1.07 PFLOP/s; a step takes a CTA some 1,850 cycles, of which the
+// 32 heads on 8: 260 us, 1.07 PFLOP/s; a step takes a CTA some 1,900 cycles, of which the
 // products fill 1,024 (they read shared memory at its full rate) and the exponentials 1,024
 // of their unit; between them stand the issuing lane's waits and the sums' latency.  Set
 // aside: one page a CTA and two CTAs an SM (prompt 303 us, decode 132); runtime divisions
 // by the number of stages in the issuing lane (300); all of a warp's logits in registers
-// and the buffer free before the exponentials (328); with one page, exponentials on the FMA
-// pipe (a quarter of them: 347), 16 columns at a time with the next ones on their way
-// (317), three or four groups of warps (312, 483 with spills).
+// before its exponentials, as two reads of 32 columns or one of 64, the buffer given back
+// at once or at the end (2 to 20 % more); with one page, exponentials on the FMA pipe (a
+// quarter of them: 347), 16 columns at a time with the next ones on their way (317), three
+// or four groups of warps (312, 483 with spills).
 #include <cstddef>
 
 #include "attn_common.cuh"
