@@ -61,7 +61,11 @@ constexpr int LA_AHEAD = 3;  // tiles that L2 is asked for before they are loade
 constexpr int LA_NEAR = 64;  // segments kept in shared memory; the rest in the workspace
 
 struct Misc {
-  uint64_t q_full, q_empty, pv_done, p_full, o_free, drained[2], s_full[2], info[2], info_free[2];
+  uint64_t q_full, q_empty, p_full, o_free, drained[2], s_full[2], info[2], info_free[2];
+  // Products that are complete, tiles in turn: whoever waits for one knows only that the
+  // one two before is (its shared memory was loaded again), and a parity tells a phase from
+  // no more than the one before it.
+  uint64_t pv_done[2];
   uint64_t full[2][4], empty[2][4];  // pairs of boxes of a tile; the rotated keys with the last
   uint32_t tmem;
   int abort;
@@ -200,11 +204,11 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     if (tid == 0) {
       tc::mbar_init(&M->q_full, 1);
       tc::mbar_init(&M->q_empty, 1);
-      tc::mbar_init(&M->pv_done, 1);
       tc::mbar_init(&M->p_full, 8);
       tc::mbar_init(&M->o_free, 8);
       for (int i = 0; i < 2; ++i) {
         tc::mbar_init(&M->drained[i], 1);
+        tc::mbar_init(&M->pv_done[i], 1);
         tc::mbar_init(&M->info[i], 1);
         tc::mbar_init(&M->info_free[i], 8);
         tc::mbar_init(&M->s_full[i], 2);
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
                          i > 0);
             tc::mma_commit(&M->empty[it & 1][b]);
           }
-          tc::mma_commit(&M->pv_done);
+          tc::mma_commit(&M->pv_done[it & 1]);
         }
       }
       tc::mma_commit(&M->drained[1]);
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
             }
             if (i > 0) {
               // O^T of all pairs, once the product before is complete
-              ok = wait(&M->pv_done, it - 1) && ok;
+              ok = wait(&M->pv_done[(it - 1) & 1], (it - 1) >> 1) && ok;
               tc::bar_sync(BAR_SOFT, 256);
               tc::tc_fence_after();
 #pragma unroll 1
@@ -718,7 +722,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
           }
           M->f[m] = f;
         }
-      ok = wait(&M->pv_done, it - 1) && ok;
+      ok = wait(&M->pv_done[(it - 1) & 1], (it - 1) >> 1) && ok;
       if (tc::bar_or(BAR_SOFT, 256, !ok)) break;
       tc::tc_fence_after();
 #pragma unroll 1
