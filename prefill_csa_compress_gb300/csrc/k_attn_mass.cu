@@ -109,7 +109,28 @@ __device__ __noinline__ void put_mass(const csa_attn_mass_args &a, float *parts,
   reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.mass_out) + b * a.mass_out_row_stride)[col] = sum;
 }
 
-template <int D>
+// A position's sum where it is NaN, once more by the columns' bounds.
+__device__ __noinline__ float bounded_sum(uint32_t logits, const float *lse, const int2 *see, int c0,
+                                          int n, int j, float sl2, float sum) {
+  float again = 0.f;
+#pragma unroll 1
+  for (int c = c0; c < n; c += 64) {
+    float x[32];
+    tc::tmem_ld32(logits + c, x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (j >= see[c + i].x && j < see[c + i].y) again += attn::exp2_sfu(fmaf(x[i], sl2, lse[c + i]));
+  }
+  return sum == sum ? sum : again;
+}
+
+// Full: the rows of a step fill its columns.  Else some have no query and count on
+// 2^(0 k - inf) = 0, which a key that is not finite makes NaN, so that sums that come out
+// NaN are taken once more without them.  (In one kernel, asked for every step, a prompt
+// whose columns are full takes 265 us for 262; with such columns' logits set to zero 269;
+// by bounds from the first 256 -> 296 where 3 of 128 are empty.)  The last rows' tile,
+// which may be short in either, goes by bounds.
+template <int D, bool Full>
 __global__ void __launch_bounds__(AM_THREADS, 1)
     attn_mass_kernel(const __grid_constant__ csa_attn_mass_args a, float *parts, Split G,
                      const __grid_constant__ CUtensorMap qmap,
@@ -296,7 +317,9 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           }
           ask(tile + 1);
           const int seen = __any_sync(0xffffffffu, any[0]) + 2 * __any_sync(0xffffffffu, any[1]);
-          const int mixed = __any_sync(0xffffffffu, part[0]) + 2 * __any_sync(0xffffffffu, part[1]);
+          const int mixed = vmin + (tile + 1) * G.tr > a.n_rows
+                                ? 3
+                                : __any_sync(0xffffffffu, part[0]) + 2 * __any_sync(0xffffffffu, part[1]);
           if ((seen & ~there) && lane == 0) flag(a.status_dev, CSA_DEV_BAD_BLOCK);
           if (!(seen & there)) continue;
           if (pending >= 0) publish(false);
@@ -489,7 +512,10 @@ __global__ void __launch_bounds__(AM_THREADS, 1)
           }
         }
       }
-      total += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+      float sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+      if (!Full && __any_sync(0xffffffffu, sum != sum))
+        sum = bounded_sum(ts + buf * 256, M->lse[st], M->see[st], 32 * grp, seen ? G.n : 0, j, sl2, sum);
+      total += sum;
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -565,7 +591,7 @@ Split split_of(const csa_attn_mass_args &a) {
   return G;
 }
 
-template <int D>
+template <int D, bool Full>
 cudaError_t launch(const csa_attn_mass_args &a, float *parts, const Split &G,
                    const CUtensorMap &qmap, const CUtensorMap &kmap, cudaStream_t s) {
   const size_t smem = G.k_stages * D * 512 + G.q_stages * G.q_bytes + sizeof(Misc);
@@ -574,14 +600,14 @@ cudaError_t launch(const csa_attn_mass_args &a, float *parts, const Split &G,
   static bool attr[64] = {};
   if (dev < 0 || dev >= 64 || !attr[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(
-        attn_mass_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        attn_mass_kernel<D, Full>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr[dev] = true;
   }
   const long long grid = (long long)a.n_req * (((a.max_blocks + 1) / 2 + G.pairs - 1) / G.pairs) * G.kv *
                          G.rows;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  return launch_kernel(attn_mass_kernel<D>, dim3((unsigned)grid), dim3(AM_THREADS), smem, s, 0,
+  return launch_kernel(attn_mass_kernel<D, Full>, dim3((unsigned)grid), dim3(AM_THREADS), smem, s, 0,
                        false, a, parts, G, qmap, kmap);
 }
 
@@ -615,8 +641,11 @@ cudaError_t launch_attn_mass(const csa_attn_mass_args &a, cudaStream_t s) {
       !cache::encode(&kmap, a.k_pool, 4, kd, kst, kb, l2))
     return cudaErrorInvalidValue;
   launch_begin(CSA_K_ATTN_MASS, s);
-  cudaError_t e = a.head_dim == 64 ? launch<64>(a, parts, G, qmap, kmap, s)
-                                   : launch<128>(a, parts, G, qmap, kmap, s);
+  const bool full = G.n == G.tr * g;
+  cudaError_t e = a.head_dim == 64 ? full ? launch<64, true>(a, parts, G, qmap, kmap, s)
+                                          : launch<64, false>(a, parts, G, qmap, kmap, s)
+                  : full           ? launch<128, true>(a, parts, G, qmap, kmap, s)
+                                   : launch<128, false>(a, parts, G, qmap, kmap, s);
   launch_end(CSA_K_ATTN_MASS, s);
   if (e != cudaSuccess || n_parts == 1) return e != cudaSuccess ? e : cudaGetLastError();
   launch_begin(CSA_K_MASS_JOIN, s);

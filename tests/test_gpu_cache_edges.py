@@ -14,7 +14,7 @@ if not torch.cuda.is_available():  # pragma: no cover - collected on CPU machines
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import prefill_csa_compress_gb300 as csa  # noqa: E402
-from test_gpu_cache import DEV, SCALE, Latent, Mass, _bf, _i32, _np, chunk, compare, paged  # noqa: E402
+from test_gpu_cache import DEV, NAN, SCALE, Latent, Mass, _bf, _i32, _np, chunk, compare, paged  # noqa: E402
 
 
 # ---------------------------------------------------------------- shapes
@@ -236,6 +236,23 @@ def test_attention_mass_unmapped_pages(gone, rows):
     b = Mass(chunk(0, 600 - rows, rows), [600], 8, 2, 128, seed=len(gone))
     b.table[0, gone] = -1
     b.check(0.5, status=1)
+
+
+@pytest.mark.parametrize("rows,heads,kv_heads,dim", [(1, 8, 1, 128), (1, 8, 2, 64), (16, 8, 1, 128), (17, 8, 1, 64), (3, 21, 3, 64),
+                                                     (130, 4, 4, 64)])
+def test_attention_mass_infinite_keys(rows, heads, kv_heads, dim):
+    """A key that is not finite has its weight by the definition (e^-inf = 0, e^inf,
+    NaN), however the rows fill a tile; other positions keep their bits."""
+    b = Mass(chunk(0, 400 - rows, rows), [400], heads, kv_heads, dim, seed=rows)
+    b.q[..., 3] = -b.q[..., 3].abs() - 0.125  # against an infinite channel: all of one sign
+    want, got = torch.zeros_like(b.mass), torch.zeros_like(b.mass)
+    b.call(mass_out=want, decay=0.0)
+    for j, value in ((5, np.inf), (150, np.inf), (77, -np.inf), (200, NAN)):  # (all rows see them)
+        b.k[int(b.table[0, j // 128]), j % 128, :, 3] = value
+    b.call(mass_out=got, decay=0.0)
+    assert (got[0, [5, 150]] == 0).all() and torch.isposinf(got[0, 77]) and torch.isnan(got[0, 200])
+    rest = [j for j in range(400) if j not in (5, 150, 77, 200)]
+    assert torch.equal(got[0, rest], want[0, rest])
 
 
 def test_attention_mass_captured_and_alike():
