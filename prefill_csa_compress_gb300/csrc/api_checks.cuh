@@ -19,6 +19,10 @@ inline bool has_size(const void *args, size_t size) {
   return args && got >= size;
 }
 
+// What a size query answers: never 0, since a call without a workspace is taken for a
+// query, and a caller who allocates what it is told holds a pointer then.
+inline size_t query_bytes(size_t need) { return need < 256 ? 256 : need; }
+
 // A row stride in bytes, 0 meaning dense.
 inline bool row_stride(int64_t *s, int64_t row_bytes) {
   if (*s == 0) *s = row_bytes;

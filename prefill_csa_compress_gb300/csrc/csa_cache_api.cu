@@ -59,7 +59,7 @@ CSA_API csa_status_t csa_latent_attn(csa_latent_attn_args *user, csa_stream_t st
       !latent_pool_strides(&a.c_page_stride, &a.c_token_stride, &a.r_page_stride,
                            &a.r_token_stride, a.n_blocks))
     return CSA_ERR_INVALID_ARG;
-  const size_t need = latent_attn_workspace(a);
+  const size_t need = query_bytes(latent_attn_workspace(a));
   if (!a.workspace) {
     user->workspace_bytes = need;
     return CSA_OK;
@@ -119,7 +119,7 @@ CSA_API csa_status_t csa_attn_mass(csa_attn_mass_args *user, csa_stream_t stream
                     a.n_kv_heads, bytes) ||
       !float_row_stride(&a.mass_row_stride, cols) || !float_row_stride(&a.mass_out_row_stride, cols))
     return CSA_ERR_INVALID_ARG;
-  const size_t need = attn_mass_workspace(a);
+  const size_t need = query_bytes(attn_mass_workspace(a));
   if (!a.workspace) {
     user->workspace_bytes = need;
     return CSA_OK;
@@ -155,7 +155,7 @@ CSA_API csa_status_t csa_kv_evict(csa_kv_evict_args *user, csa_stream_t stream) 
                                  a.n_heads, (int64_t)a.v_dim * 2)) ||
       !float_row_stride(&a.mass_row_stride, cols) || !float_row_stride(&a.mass_out_row_stride, cols))
     return CSA_ERR_INVALID_ARG;
-  const size_t need = kv_evict_workspace(a);
+  const size_t need = query_bytes(kv_evict_workspace(a));
   if (!a.workspace) {
     user->workspace_bytes = need;
     return CSA_OK;

@@ -147,7 +147,7 @@ CSA_API csa_status_t csa_paged_attn(csa_paged_attn_args *user, csa_stream_t stre
       !pool_strides(&a.v_page_stride, &a.v_token_stride, &a.v_head_stride, a.n_blocks,
                     a.n_kv_heads, (int64_t)a.v_dim * 2))
     return CSA_ERR_INVALID_ARG;
-  const size_t need = paged_attn_workspace(a);
+  const size_t need = query_bytes(paged_attn_workspace(a));
   if (!a.workspace) {
     user->workspace_bytes = need;
     return CSA_OK;

@@ -59,6 +59,7 @@ struct Seg {
 constexpr int LA_JOIN = 8;    // parts of a row that are asked for together
 constexpr int LA_AHEAD = 3;  // tiles that L2 is asked for before they are loaded
 constexpr int LA_NEAR = 64;  // segments kept in shared memory; the rest in the workspace
+static_assert(LA_PAIRS <= LA_NEAR, "rows taken whole need no more");
 
 struct Misc {
   uint64_t q_full, q_empty, p_full, o_free, drained[2], s_full[2], info[2], info_free[2];
@@ -856,11 +857,7 @@ struct Layout {
 Layout layout(const csa_latent_attn_args &a, int sms) {
   Layout L{0, 0, 0, 0, 0};
   const Shape H = shape_of(a);
-  if (!H.shares) {  // a CTA that takes its rows whole has as many segments as rows, at most
-    L.n_far = H.R > LA_NEAR ? H.R : 0;
-    L.total = align_up((size_t)blocks_of(a, H) * L.n_far * sizeof(Seg), 256);
-    return L;
-  }
+  if (!H.shares) return L;  // (a CTA that takes its rows whole has no more segments than rows)
   const long long items = (long long)a.n_rows * H.subs;  // (of a CTA, at most)
   L.n_far = items > LA_NEAR ? (int)items : 0;
   const size_t slots = 2 * (size_t)sms * LA_PAIRS;

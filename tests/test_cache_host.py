@@ -161,6 +161,19 @@ def test_size_query(L, name, base):
         assert P._fn(name)(ctypes.byref(a), None) == INVALID
 
 
+@pytest.mark.parametrize("name,base", [
+    ("csa_latent_attn", dict(LATENT, n_rows=8192, n_heads=64, n_req=1)),  # rows taken whole
+    ("csa_latent_attn", dict(LATENT, n_rows=0)), ("csa_attn_mass", dict(MASS, n_req=64, max_blocks=128)),  # nothing split
+    ("csa_attn_mass", dict(MASS, n_rows=0, n_req=64, max_blocks=128)), ("csa_kv_evict", dict(EVICT, n_req=0)),
+    ("csa_paged_attn", dict(ATTN, n_rows=8192, n_heads=64, n_kv_heads=64)), ("csa_paged_attn", dict(ATTN, n_rows=0)),
+    ("csa_paged_attn", dict(ATTN, n_rows=8192, head_dim=64, v_dim=64, n_heads=64, n_kv_heads=64))])
+def test_size_query_is_never_zero(L, name, base):
+    """A call whose workspace is NULL is a size query: a caller who allocates the bytes it
+    is told has to hold a pointer then, also where nothing is split."""
+    a = _args(name, **dict(base, workspace=None, workspace_bytes=0))
+    assert P._fn(name)(ctypes.byref(a), None) == B.CSA_OK
+    assert a.workspace_bytes >= 256
+
 def test_paged_attention_struct_without_value_width(L):
     """A caller built before v_dim: its struct ends there, and values are as wide
     as keys."""
