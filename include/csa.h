@@ -925,7 +925,10 @@ CSA_API csa_status_t csa_latent_expand(csa_latent_expand_args *args, csa_stream_
  *   mass_out[b,j] = decay * mass[b,j] + sum over the call's rows t of request b that
  *                   see j, and heads h, of e^{softmax_scale q[t,h] . k_j - lse[t,h]}
  * for every position j < min(kv_len[b], 128 max_blocks), seen or not; entries behind
- * are left as they were.  decay == 0 does not read mass (which may be NULL), whatever it
+ * are left as they were.  So with a decay other than 0 the entry of a position that was
+ * published since the call before has to hold that position's start, 0; behind a cut
+ * (csa_kv_evict) the entries still hold weights of positions that are gone, and the
+ * caller clears them.  decay == 0 does not read mass (which may be NULL), whatever it
  * holds.  mass_out may be mass.  What a row sees, the head groups, pages and padding
  * are those of csa_paged_attn, whose lse (sink included) is the one meant; any other
  * FP32 reference will do.  A row and head of lse -inf adds nothing.  Weights and sums
@@ -987,7 +990,9 @@ CSA_API csa_status_t csa_attn_mass(csa_attn_mass_args *args, csa_stream_t stream
  * slots: rows at slot n on (row_pos of csa_paged_attn) see all that was kept.
  * mass_out[b,d] (or NULL) gets the mass of what slot d holds now (mass_out may be
  * mass); slot_src[b,d] (or NULL) its old position.  d < n; entries behind, and the
- * rows of slots n on, are left as they were.  A move whose source or destination page
+ * rows of slots n on, are left as they were: where mass_out goes on being added up by
+ * csa_attn_mass, its entries from n on have to be set to 0 before positions are
+ * published there.  A move whose source or destination page
  * is outside the pool raises CSA_DEV_BAD_BLOCK and is not made (mass_out and slot_src
  * are).  Pages that are cut must be one request's alone.
  *
@@ -996,7 +1001,8 @@ CSA_API csa_status_t csa_attn_mass(csa_attn_mass_args *args, csa_stream_t stream
  * i32 [n_req] (below 0: 0).  k_pool bf16 [n_blocks, 128, n_heads, k_dim], v_pool bf16
  * [n_blocks, 128, n_heads, v_dim] or NULL, strides as in csa_kv_append (a latent
  * cache: one head, c as k of 512 and r as v of 64).  k_dim, v_dim multiples of 8, 8
- * .. 512; max_blocks < 2^23; first, recent >= 0.  The workspace is used as
+ * .. 512; max_blocks < 2^23; first, recent >= 0.  What a latent cache is cut by comes
+ * from the caller: csa_attn_mass weighs keys of 64 and 128.  The workspace is used as
  * csa_paged_attn's is.
  * ---------------------------------------------------------------------- */
 typedef struct {

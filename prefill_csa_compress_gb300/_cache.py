@@ -224,7 +224,8 @@ def csa_attn_mass(*, q, lse, row_req, row_pos, k_pool, block_table, kv_len, mass
     ``q`` [rows, heads, dim] whose log-sums are ``lse`` [rows, heads], added to
     ``decay * mass`` [requests, 128 * pages a request] (``include/csa.h``:
     csa_attn_mass).  Without ``mass_out`` the sums replace ``mass``; ``decay`` 0 needs
-    no ``mass``."""
+    no ``mass``.  A position published since the last call starts from what its entry
+    holds: 0 in a buffer that began as zeros, but not behind a cut (csa_kv_evict)."""
     a, tensors = AttnMassArgs(), []
     a.struct_size = ctypes.sizeof(a)
     a.q_row_stride = _rows(q, "q", (None, None, None))
@@ -265,7 +266,8 @@ def csa_kv_evict(*, mass, kv_len, budget, block_table, k_pool, v_pool=None, kv_l
     (``include/csa.h``: csa_kv_evict).  The ``first`` and the last ``recent``
     positions stay as far as the budget goes.  ``kv_len_out`` (default: ``kv_len``
     itself) gets the new lengths, ``mass_out`` and ``slot_src`` each slot's mass and
-    old position.  Pools are BF16 [pages, 128, heads, dim] (one head: [pages, 128,
+    old position.  Entries of ``mass_out`` behind the new length keep what they held:
+    set them to 0 before new positions are published there and weighed.  Pools are BF16 [pages, 128, heads, dim] (one head: [pages, 128,
     dim] too), keys and values of widths of their own."""
     a, tensors = KvEvictArgs(), []
     a.struct_size = ctypes.sizeof(a)

@@ -313,6 +313,57 @@ def test_latent_cache_cut():
         assert (np.abs(_np(out)[r:r + 1] - o) <= tol).all()
 
 
+def test_weights_through_two_cuts():
+    """Attention, weights, eviction, publication, and again: every position's weight is its
+    own through two cuts, where the entries behind a cut are cleared before new positions
+    are published there."""
+    rng = np.random.default_rng(31)
+    heads, kvh, dim, decay = 8, 2, 64, 0.75
+    lens, budget, new = [520, 300], [250, 200], 3
+    table, total = paged(rng, lens)
+    k, v = _bf(rng, total, 128, kvh, dim), _bf(rng, total, 128, kvh, dim)
+    table_dev, kv_len, mass = _i32(table), _i32(lens), torch.zeros((2, table.shape[1] * 128), device=DEV)
+    slots = torch.arange(mass.shape[1], device=DEV)
+    want = [np.zeros(n) for n in lens]  # the weight of what each slot holds
+    for turn in range(3):
+        n = [int(x) for x in kv_len]
+        rows = [(b, n[b] - new + i) for b in range(2) for i in range(new)]
+        at = dict(row_req=_i32([r for r, _ in rows]), row_pos=_i32([p for _, p in rows]), block_table=table_dev, kv_len=kv_len)
+        q = _bf(rng, len(rows), heads, dim)
+        out, lse = torch.empty_like(q), torch.empty((len(rows), heads), device=DEV)
+        csa.csa_paged_attn(q=q, k_pool=k, v_pool=v, out=out, lse=lse, **at)
+        csa.csa_attn_mass(q=q, lse=lse, k_pool=k, mass=mass, decay=decay, **at)
+        torch.cuda.synchronize()
+        qn, kn, ln = _np(q), _np(k), _np(lse)
+        add = PO.attention_mass(qn, ln, [r for r, _ in rows], [p for _, p in rows], kn, table, n, dim ** -0.5)
+        # a logit is an FP32 sum of 64 products (64 2^-24 of the sum of their sizes, twice that
+        # for sums that are cut off, not rounded), its exponent and the reference are rounded,
+        # 24 weights and the decay added each turn
+        sizes = max((np.abs(kn[..., h, :]) @ np.abs(qn[:, 4 * h:4 * h + 4].reshape(-1, dim)).T).max() for h in range(kvh))
+        e = 2 * 64 * 2.0 ** -24 * sizes / 8 + 2.0 ** -20 * (1 + np.abs(ln).max()) + 32 * 2.0 ** -24
+        want = [decay * w + a for w, a in zip(want, add)]
+        for b in range(2):
+            tol = (turn + 1) * e * want[b]
+            assert (np.abs(_np(mass[b, :n[b]]) - want[b]) <= tol).all(), (turn, b)
+            if turn:  # (what the entries held behind the cut would show)
+                assert (decay * stale[b] > tol[n[b] - new:]).any()
+        before = mass.clone()
+        csa.csa_kv_evict(mass=mass, mass_out=mass, kv_len=kv_len, budget=_i32(budget), block_table=table_dev, k_pool=k, v_pool=v,
+                         first=2, recent=new)
+        left = [int(x) for x in kv_len]
+        assert left == budget
+        for b in range(2):
+            assert torch.equal(mass[b, left[b]:], before[b, left[b]:])  # of positions that are gone
+            want[b] = want[b][PO.evict(_np(before[b]), n[b], budget[b], 2, new)]
+        stale = [_np(before[b, left[b]:left[b] + new]) for b in range(2)]
+        mass.masked_fill_(slots >= kv_len[:, None], 0.0)
+        # new tokens at the slots behind the cut
+        pos = [(b, left[b] + i) for b in range(2) for i in range(new)]
+        csa.csa_kv_append(k=_bf(rng, len(pos), kvh, dim), v=_bf(rng, len(pos), kvh, dim), k_pool=k, v_pool=v,
+                          row_req=_i32([r for r, _ in pos]), row_pos=_i32([p for _, p in pos]), block_table=table_dev)
+        kv_len += new
+        want = [np.concatenate([w, np.zeros(new)]) for w in want]
+
 def test_launches_are_counted_and_timed():
     from prefill_csa_compress_gb300 import prof_disable, prof_enable, prof_read
 
