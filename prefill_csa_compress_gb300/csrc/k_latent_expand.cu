@@ -184,8 +184,11 @@ __global__ void __launch_bounds__(LE_THREADS, 1)
           load_pair_3d(sm + LE_OFF_W + st * LE_BOX, rank ? &vmap : &kmap, c * 64, 0, h, &M->w_full[st],
                        keep);
         }
-      // whatever was asked for has landed before the CTA retires
+      // Whatever was asked for has landed before the CTA retires, and the last stages have
+      // been handed back: the first CTA's commits arrive at the second's barriers too.
       if (full) tc::mbar_wait(&M->r_full, 0, 50000000ull);
+      for (uint32_t k = it > LE_STAGES ? it - LE_STAGES : 0; k < it && ok; ++k)
+        ok = cache::wait(&M->w_empty[k % LE_STAGES], (k / LE_STAGES) & 1, abort, a.status_dev);
     }
     __syncwarp();
   } else if (warp == LE_MMA) {
