@@ -1,5 +1,5 @@
-"""Absorbed latent attention on inputs whose logits are exact, so that a position
-counted twice or left out shows.
+"""Latent attention in both forms and accumulated weights on inputs whose logits are
+exact, so that a position counted twice or left out shows.
 
 With q of a few +-1 and keys of +-1 every logit is a small whole number, whatever the
 order of its sum, and softmax_scale = ln 2 makes each weight a power of two: rounding
@@ -11,7 +11,8 @@ exactly (multiples of the smallest weight, below 2^24 of them).  What is left:
  - FP32 sums of the weights: a thread adds a tile (64 positions; a page of 128) after
    another, 16 and fewer additions beside that: (n / 64 + 16) 2^-24;
  - out rounded once to BF16 (2^-8), lse a sum and a product of FP32 numbers (2^-22).
-Each check also shows, by the definition, that 64 positions less would not pass.
+Checks of the absorbed form also show, by the definition, that 64 positions less would
+not pass.
 """
 
 import math
@@ -28,7 +29,7 @@ if not torch.cuda.is_available():  # pragma: no cover - collected on CPU machines
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import prefill_csa_compress_gb300 as csa  # noqa: E402
-from test_gpu_cache import DEV, H8, Latent, _i32, _np, chunk  # noqa: E402
+from test_gpu_cache import DEV, H8, MASS_ROWS, Latent, Mass, _i32, _np, chunk, paged  # noqa: E402
 
 LN2 = float(np.float32(math.log(2.0)))
 
@@ -185,3 +186,84 @@ def test_latent_cache_cut_whole_logits():
             weight, sums = close(got[t:t + 1, h], gl[t:t + 1, h], o[None], np.array([ls]), (w @ np.abs(c0[at]))[None],
                                  np.zeros(1, bool), 3, len(kept))
             assert shows(x, c0[at], o, ls, weight, sums, 100)
+
+
+# ---------------------------------------------------------------- expanded
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(7, 7), (20, 20), (12, 4), (32, 1)])
+@pytest.mark.parametrize("rows,lens,kw", [
+    (chunk(0, 300, 140) + chunk(1, 5, 3) + [(-1, 2)] + chunk(2, 900, 50), [440, 8, 950], {}),
+    ([(b, 250 + b) for b in range(6)], [260] * 6, {}), ([(0, 3000)], [3001], {}),
+    (chunk(0, 500, 200), [700], dict(window=200))])
+def test_expanded_attention_whole_logits(heads, kv_heads, rows, lens, kw):
+    rng = np.random.default_rng(heads)
+    table, total = paged(rng, lens)
+    k, v = signs(rng, total, 128, kv_heads, 192), signs(rng, total, 128, kv_heads, 128)
+    q = sparse(rng, len(rows), heads, 192, 3, 1)
+    req, pos = (np.array([r[i] for r in rows]) for i in range(2))
+    out = torch.full((len(rows), heads, 128), 77.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((len(rows), heads), 77.0, device=DEV)
+    csa.csa_paged_attn(q=q, row_req=_i32(req), row_pos=_i32(pos), k_pool=k, v_pool=v, block_table=_i32(table),
+                       kv_len=_i32(lens), out=out, lse=lse, softmax_scale=LN2, **kw)
+    torch.cuda.synchronize()
+    o, ls, spread = PO.paged_attention(_np(q), req, pos, _np(k), _np(v), table, lens, LN2, **kw)
+    close(_np(out), _np(lse), o, ls, spread, req < 0, 3, max(lens))
+
+
+# ---------------------------------------------------------------- weights
+
+
+def seen_counts(b):
+    """How many (row, head) pairs see each position, a list of arrays."""
+    out = [np.zeros(max(int(n), 0)) for n in b.lens]
+    for r, p in zip(b.req, b.pos):
+        if 0 <= r < len(out):
+            lo, hi = PO.visible(int(p), len(out[r]), b.kw["causal"], b.kw["window"])
+            out[r][lo:hi] += b.q.shape[1]
+    return out
+
+
+@pytest.mark.parametrize("rows,lens,kw", [(r, n, {}) for r, n in MASS_ROWS] + [
+    (chunk(0, 0, 501) + chunk(1, 40, 333), [501, 373], {}), ([(0, 20000), (1, 300)], [20001, 301], {}),
+    (chunk(0, 400, 300), [700], dict(window=129)), (chunk(0, 400, 40) + chunk(1, 2, 1), [440, 3], dict(causal=False)),
+    ([(b, 40 * b) for b in range(200)], [40 * b + 1 for b in range(200)], {})])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(1, 1, 64), (8, 2, 128), (21, 3, 64), (128, 1, 128), (16, 16, 64)])
+def test_attention_mass_counts(rows, lens, kw, heads, kv_heads, dim):
+    """Queries of zero against references of zero: every weight is one, and a
+    position's sum the number of rows and heads that see it, exactly."""
+    b = Mass(rows, lens, heads, kv_heads, dim, seed=heads, **kw)
+    b.q.zero_()
+    b.lse.zero_()
+    out = torch.full_like(b.mass, 77.0)
+    b.call(mass_out=out, decay=0.0)
+    for r, want in enumerate(seen_counts(b)):
+        assert np.array_equal(_np(out[r, :len(want)]), want), r
+        assert (out[r, len(want):] == 77).all()
+
+
+def test_attention_mass_references_that_are_not_finite():
+    """A reference of -inf adds nothing, one of +inf zero; the other rows' and heads'
+    sums are right."""
+    b = Mass(chunk(0, 290, 4), [294], 4, 2, 64, seed=5)
+    b.lse[1] = float("-inf")
+    b.lse[2, 1] = float("inf")
+    b.lse[3] = float("inf")
+    out = torch.full_like(b.mass, 77.0)
+    assert b.call(mass_out=out, decay=0.0) == 0
+    q, k, lse = _np(b.q), _np(b.k), _np(b.lse)
+    want = PO.attention_mass(q, lse, b.req, b.pos, k, b.table, b.lens, 64 ** -0.5)[0]
+    # a logit is an FP32 sum of 64 products: 64 2^-24 of the sum of their sizes, the tensor
+    # cores' truncation counted as a rounding twice; the exponent's own roundings beside a
+    # reference of at most 16, the exponential, and sums of 16 weights
+    sizes = max(np.abs(k[b.table[0, j // 128], j % 128, h // 2]) @ np.abs(q[t, h])
+                for j in range(294) for t in (0, 2) for h in range(4))
+    assert np.abs(lse[np.isfinite(lse)]).max() < 16
+    e = 2 * 64 * 2.0 ** -24 * sizes / 8 + 2.0 ** -19 + 16 * 2.0 ** -24
+    assert np.isfinite(e) and e < 1e-3
+    got = _np(out[0, :294])
+    assert (np.abs(got - want) <= e * want).all() and (want[291:293] > 0).all()
+    # the definition without one of the pairs would not pass
+    lse[2, 0] = np.inf
+    less = PO.attention_mass(q, lse, b.req, b.pos, k, b.table, b.lens, 64 ** -0.5)[0]
+    assert (np.abs(less - want)[:293] > e * want[:293]).all()
