@@ -62,11 +62,16 @@ constexpr int LA_NEAR = 64;  // segments kept in shared memory; the rest in the 
 static_assert(LA_PAIRS <= LA_NEAR, "rows taken whole need no more");
 
 struct Misc {
-  uint64_t q_full, q_empty, p_full, o_free, drained[2], s_full[2], info[2], info_free[2];
+  uint64_t q_full, q_empty, o_free, drained[2], s_full[2], info[2], info_free[2];
   // Products that are complete, tiles in turn: whoever waits for one knows only that the
   // one two before is (its shared memory was loaded again), and a parity tells a phase from
   // no more than the one before it.
   uint64_t pv_done[2];
+  // P of a tile, tiles in turn: the softmax may be done with the next tile before the
+  // products' warp looks for this one (with one barrier it would have been overtaken by two
+  // phases and never see its own), but not with the one after, which is loaded behind this
+  // tile's product.
+  uint64_t p_full[2];
   uint64_t full[2][4], empty[2][4];  // pairs of boxes of a tile; the rotated keys with the last
   uint32_t tmem;
   int abort;
@@ -205,11 +210,11 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     if (tid == 0) {
       tc::mbar_init(&M->q_full, 1);
       tc::mbar_init(&M->q_empty, 1);
-      tc::mbar_init(&M->p_full, 8);
       tc::mbar_init(&M->o_free, 8);
       for (int i = 0; i < 2; ++i) {
         tc::mbar_init(&M->drained[i], 1);
         tc::mbar_init(&M->pv_done[i], 1);
+        tc::mbar_init(&M->p_full[i], 8);
         tc::mbar_init(&M->info[i], 1);
         tc::mbar_init(&M->info_free[i], 8);
         tc::mbar_init(&M->s_full[i], 2);
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         const int n_it = seg_at(s).n;
         if (s > 0) ok = cache::wait(&M->o_free, (s - 1) & 1, abort, a.status_dev);
         for (int i = 0; i < n_it && ok; ++i, ++it) {
-          ok = cache::wait(&M->p_full, it & 1, abort, a.status_dev);
+          ok = cache::wait(&M->p_full[it & 1], (it >> 1) & 1, abort, a.status_dev);
           if (!ok) break;
           tc::tc_fence_after();
           const uint64_t at = ((it & 1) * LA_TILE) >> 4;
@@ -687,7 +692,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         tc::fence_async_shared();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&M->p_full);
+        if (lane == 0) tc::mbar_arrive(&M->p_full[st]);
         // (the sums while the product runs)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {

@@ -156,6 +156,43 @@ def test_latent_attention_waits_for_every_product(rows, lens, heads):
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]), i
 
 
+@pytest.mark.parametrize("heads,rows_each", [(64, 200), (16, 700)])
+def test_latent_attention_beside_other_work(heads, rows_each):
+    """Rows taken whole while another stream's kernels come and go on the same SMs: no
+    role of a CTA outruns another, no wait gives up, every call has the same bits."""
+    lens = [rows_each + 40 * i for i in range(5)]
+    rows = [x for b, n in enumerate(lens) for x in chunk(b, n - rows_each, rows_each)]
+    b = Whole(rows, lens, heads, zero=True, seed=heads)
+    out = torch.empty((len(rows), heads, 512), dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty((len(rows), heads), device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    call = csa.csa_latent_attn(
+        q=b.q, q_rope=b.qr, row_req=_i32(b.req), row_pos=_i32(b.pos), c_pool=b.c, r_pool=b.r, block_table=_i32(b.table),
+        kv_len=_i32(b.lens), out=out, lse=lse, softmax_scale=LN2, status=st, prepare=True)
+    want = []  # equal weights: a row's output is the mean of what it sees
+    for r, n in enumerate(lens):
+        j = np.arange(n)
+        c = b.c[torch.as_tensor(b.table[r, j // 128], device=DEV), torch.as_tensor(j % 128, device=DEV)].double()
+        mean = c.cumsum(0) / torch.arange(1, n + 1, device=DEV)[:, None]
+        want.append(mean[n - rows_each:])
+    want = torch.cat(want)[:, None]
+    side = torch.cuda.Stream()
+    x = torch.randn(1 << 20, device=DEV)
+    torch.cuda.synchronize()
+    for i in range(150):
+        out.fill_(77)
+        lse.fill_(77)
+        with torch.cuda.stream(side):
+            torch.sort(x)
+        call()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0, i
+        if i == 0:
+            assert ((out.double() - want).abs() <= (H8 + 2.0 ** -18) * want.abs() + 1e-30).all()
+            first = out.clone(), lse.clone()
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), i
+
+
 @pytest.mark.parametrize("size", [32, 512])
 def test_latent_attention_whole_large_logits(size):
     """Logits of +-96 and +-1536 times ln 2: references move, only the largest count."""
