@@ -711,10 +711,13 @@ CSA_API csa_status_t csa_kv_append(csa_kv_append_args *args, csa_stream_t stream
  * overlap the inputs.  v_dim (0, or a struct_size that ends before it: head_dim) is
  * the values' width where it is not the keys': the expanded form of latent attention
  * has keys of 192 and values of 128 (csa_latent_expand), v_pool [.., v_dim], out
- * [n_rows, n_heads, v_dim]; such calls run as CSA_MODE_PREFILL whatever `mode` says.
+ * [n_rows, n_heads, v_dim]; such calls run as CSA_MODE_PREFILL whatever `mode` says, and
+ * take n_rows / n_req for the rows of a request (2000 rows of 64 heads over 2000 positions:
+ * 99 us, as the only one of 64 requests 223).
  * Supported: at most 2^24 rows and 2^24 pages a request;
- * head_dim = v_dim = 64 or 128, or head_dim 192 with v_dim 128; n_kv_heads a divisor of n_heads, n_heads / n_kv_heads <=
- * 128.  softmax_scale > 0, finite.  Tensors 16-byte aligned.
+ * head_dim = v_dim = 64 or 128, or head_dim 192 with v_dim 128; n_kv_heads a divisor of
+ * n_heads, n_heads / n_kv_heads <= 128.  softmax_scale > 0, finite.  Tensors 16-byte
+ * aligned.
  * `mode` (csa_mode_t) chooses between the kernel for few rows per request
  * (CSA_MODE_DECODE; calls of up to 512 rows, more run as CSA_MODE_PREFILL) and the
  * one for chunks (CSA_MODE_PREFILL).  Both compute the same function; they round
@@ -783,9 +786,9 @@ CSA_API csa_status_t csa_paged_attn(csa_paged_attn_args *args, csa_stream_t stre
  *  - expanded (csa_latent_expand, then csa_paged_attn with keys of 192 and values
  *    of 128): 640 operations a pair and 131,072 a position and head to expand.
  * The absorbed form is the one for few rows over long caches, the expanded one for
- * prompts.  One request, 64 heads over 8192 positions, 1 / 64 / 256 / 1024 / 8192 rows:
- * absorbed 30 / 92 / 281 / 981 / 4277 us; expanding 120 us, once, and then 61 / 65 / 87 /
- * 240 / 939 us.
+ * prompts.  One request, 64 heads over 8192 positions, 1 / 40 / 128 / 176 / 256 / 1024 /
+ * 8192 rows: absorbed 26 / 63 / 150 / 199 / 273 / 992 / 4305 us; expanding 120 to 141 us,
+ * once, and then 60 / 64 / 66 / 83 / 86 / 238 / 1012 us.
  *
  * The pools are BF16: c_pool [n_blocks, 128, 512], r_pool [n_blocks, 128, 64], with
  * page and token strides in bytes (0: dense; multiples of 16), so one pool of rows of
@@ -882,7 +885,10 @@ CSA_API csa_status_t csa_latent_attn(csa_latent_attn_args *args, csa_stream_t st
  * k_pool bf16 [n_out_blocks, 128, n_heads, 192], v_pool bf16 [n_out_blocks, 128,
  * n_heads, 128], page, token and head strides as in csa_kv_append.  block_table i32
  * [n_req, max_blocks], out_table i32 [n_req, out_max_blocks].  1 .. 65536 heads.
- * Tensors 16-byte aligned.  No workspace.
+ * Tensors 16-byte aligned.  No workspace.  How the heads are shared among CTAs goes by
+ * max_blocks, which the host knows, not by the lengths: 2 x 1500 positions of 32 heads take
+ * 31 us with a table as wide as they need, 45 with one four times and 48 with one 16 times
+ * as wide (8192 of 128 heads 246, 264, 277).
  * ---------------------------------------------------------------------- */
 typedef struct {
   uint32_t struct_size;
@@ -940,7 +946,13 @@ CSA_API csa_status_t csa_latent_expand(csa_latent_expand_args *args, csa_stream_
  * mass_out f32 [n_req, 128 max_blocks] with row strides in bytes (0: dense; multiples
  * of 4).  Supported: at most 2^24 rows and 2^24 - 1 pages a request; head_dim 64 or 128;
  * n_kv_heads a divisor of n_heads, n_heads / n_kv_heads <= 128.  decay finite, >= 0.
- * The workspace is used as csa_paged_attn's is.
+ * The workspace is used as csa_paged_attn's is.  How pages, heads and rows are shared
+ * among CTAs goes by max_blocks, not by the lengths, and by n_rows / n_req, not by how the
+ * rows are spread: a prompt of 8192 rows of 32 heads on 8 takes 259 us with a table as wide
+ * as it needs, 743 with one four times and 1941 with one 16 times as wide; 2000 rows of one
+ * request over 2000 positions 34 us by themselves, 502 as the only one of 64; 100 rows and
+ * 31 single tokens over 4000 180, 32 x 4 rows 68.  A chunk is best weighed in a call of its
+ * own, with its row of the tables.
  * ---------------------------------------------------------------------- */
 typedef struct {
   uint32_t struct_size;

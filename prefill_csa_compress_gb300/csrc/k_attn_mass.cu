@@ -23,8 +23,8 @@
 //                describes each step to the rest: references and bounds a column.
 //
 // What bounds it.  Decode (32 rows over ragged contexts to 16,384, 64 heads on 8 of 128):
-// 120 us, 5.7 TB/s, the pages' way through three stages of a CTA.  A prompt of 8192 rows of
-// 32 heads on 8: 260 us, 1.07 PFLOP/s; a step takes a CTA some 1,900 cycles, of which the
+// 121 us, 5.7 TB/s, the pages' way through three stages of a CTA.  A prompt of 8192 rows of
+// 32 heads on 8: 263 us, 1.05 PFLOP/s; a step takes a CTA some 1,900 cycles, of which the
 // products fill 1,024 (they read shared memory at its full rate) and the exponentials 1,024
 // of their unit; between them stand the issuing lane's waits and the sums' latency.  Set
 // aside: one page a CTA and two CTAs an SM (prompt 303 us, decode 132); runtime divisions
@@ -556,6 +556,9 @@ __global__ void __launch_bounds__(256)
 // over 32,768 95, 101 and 106, since a CTA's start is paid for each).  With a handful of
 // steps, as in decode, no second round for a few CTAs (one row over 32,768: 21 us with 256
 // CTAs, 15 with 128; 3 x 500 rows over ragged 4000, which have more steps, 60 for 46).
+// The host does not know the caches' lengths: the table's width stands for them, so that a
+// table much wider than its caches leaves SMs idle (the prompt above with 4 times the
+// columns it needs 743 us, with 16 times 1941).
 Split split_of(const csa_attn_mass_args &a) {
   Split G;
   const int g = a.n_heads / a.n_kv_heads;

@@ -26,10 +26,11 @@
 //
 // What bounds it: a tile takes 2,200 cycles, 1,920 of them the tensor cores' (36 products
 // of 64 x 64 x 16 at 32 cycles, 16 of 128 x 64 x 16 at 48: an SM reads 128 bytes of shared
-// memory a cycle, so that half of their rate is the most with 64 pairs; 128 pairs would
-// fill tensor memory with O alone).  4 x 2 rows of 128 heads at 131,072 positions: 291 us,
-// 1.00 PFLOP/s; 32 rows of 16 heads, contexts to 16,384: 80 us, 4.8 TB/s, 12 of them the
-// start (the list, the first loads) and 8 the join; one row of 128 heads over 1001: 20 us.
+// memory a cycle, so that half of their rate is the most with 64 pairs; the O of 128 would
+// fill the tensor memory of one CTA, not of two, but pairs of CTAs are not built).  4 x 2
+// rows of 128 heads at 131,072 positions: 295 us, 0.99 PFLOP/s; 32 rows of 16 heads,
+// contexts to 16,384: 81 us, 4.7 TB/s, 12 of them the start (the list, the first loads) and
+// 8 the join; one row of 128 heads over 1001: 20 us.
 #include "attn_common.cuh"
 #include "cache_tiles.cuh"
 

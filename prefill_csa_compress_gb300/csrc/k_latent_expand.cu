@@ -331,7 +331,8 @@ cudaError_t launch_latent_expand(const csa_latent_expand_args &a, cudaStream_t s
     if (dev >= 0 && dev < 64) attr[dev] = true;
   }
   // Parts of the heads: as many as make waves x (heads of a part + 1) smallest, a CTA's
-  // start and end being worth about one head.
+  // start and end being worth about one head.  (Every column of the tables counts as a page:
+  // the host does not know the lengths.)
   const int places = sm_count() / 2;
   const long long n_pairs = (long long)a.n_req * ((a.max_blocks + 1) / 2);
   int per = a.n_heads, parts = 1;
